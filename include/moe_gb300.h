@@ -501,6 +501,135 @@ moe_status moe_layer_backward(const moe_config* cfg, const moe_weights* w, const
                               const moe_outputs* fwd, const float* dy, const moe_grads* grads,
                               void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* moe_layer_backward with a further gradient of the router logits: dlogits [T][N] fp32
+ * (device; moe_balance_loss writes it), or NULL.  It is added to dz, the gradient through the
+ * coefficients, before dz is rounded to bf16 for dW_r = dz^T x and dx += dz W_r.  A dlogits
+ * without grads->dW_router returns MOE_ERR_INVALID_ARG. */
+moe_status moe_layer_backward_aux(const moe_config* cfg, const moe_weights* w, const void* x,
+                                  const moe_outputs* fwd, const float* dy, const float* dlogits,
+                                  const moe_grads* grads, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream);
+
+/* ---- The block around the layer ----------------------------------------------------------
+ * The operators a transformer block puts beside the MoE layer: the dense projections with
+ * their epilogue, the router's balance loss with its gradient, and residual dropout.  The pages
+ * stop at the layer (Eq. 80) and the loss value (Eq. 30); what each computes is given here. */
+
+/* Activation of a dense projection: identity, max(z, 0), z Phi(z) with the normal distribution
+ * function Phi, its tanh form z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))), z sigmoid(z). */
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_GELU = 2,
+  MOE_ACT_GELU_TANH = 3,
+  MOE_ACT_SILU = 4
+} moe_act;
+
+/* One dense projection z = x W^T + b, y = act(z) + r over T tokens.
+ * Rows may be strided: ldx, ldw, ldr, ldy are the elements between rows of x [T][in],
+ * W [out][in], the residual and y (and dy) [T][out]; 0 means dense rows.  Within a row
+ * elements are contiguous.  pre, dx and dW are dense.  Pointers are aligned to their element
+ * type.  Operand rows that start on 16-byte boundaries (base and stride) are read in place;
+ * others are first copied to aligned rows in the workspace, which costs one read and one write
+ * of that operand. */
+typedef struct moe_linear_config {
+  int64_t T;              /* tokens, 0..2^28 */
+  int32_t in_features;    /* 1..2^20 */
+  int32_t out_features;   /* 1..2^20 */
+  int32_t dtype;          /* moe_dtype of x and W: MOE_BF16 (MOE_F32: MOE_ERR_UNSUPPORTED) */
+  int32_t out_dtype;      /* moe_dtype of y, pre, the residual and dy */
+  int32_t act;            /* moe_act */
+  int32_t dx_dtype;       /* moe_dtype of dx */
+  int32_t dw_dtype;       /* moe_dtype of dW */
+  int64_t ldx, ldw, ldr, ldy;
+} moe_linear_config;
+
+/* Workspace bytes for moe_linear_forward and moe_linear_backward of this projection (host
+ * only).  The caller prepares the buffer with moe_workspace_init; moe_read_status reads its
+ * device status word. */
+moe_status moe_linear_workspace_size(const moe_linear_config* cfg, size_t* bytes);
+
+/* y = act(x W^T + b) + r.  x, W bf16 (device); bias [out] fp32 or NULL; residual
+ * [T][out] out_dtype or NULL; pre [T][out] out_dtype or NULL: z as the backward pass takes
+ * it; y [T][out] out_dtype.  Products accumulate in fp32; bias, activation and residual are
+ * applied in fp32 and y and pre are each rounded once.  y may be the residual itself (same
+ * address and stride); no other buffers may overlap.  T = 0 writes
+ * nothing.  Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED,
+ * MOE_ERR_MISALIGNED, MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_CUDA; on the device
+ * MOE_ERR_TIMEOUT. */
+moe_status moe_linear_forward(const moe_linear_config* cfg, const void* x, const void* W,
+                              const float* bias, const void* residual, void* pre, void* y,
+                              void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Gradients of moe_linear_forward for the upstream gradient dy [T][out] (out_dtype, stride
+ * ldy): with dz = dy act'(z) and z from pre (NULL allowed for MOE_ACT_NONE),
+ *   dx = dz W [T][in] (dx_dtype),  dW = dz^T x [out][in] (dw_dtype),  dbias = sum_t dz (fp32).
+ * The gradient of the residual is dy itself.  dx, dW and dbias may each be NULL (not computed);
+ * each is overwritten.  The matrix products take dz rounded to bf16 once (dy as it is, when
+ * act is none and dy is bf16) and accumulate in fp32; dbias sums the unrounded dz in a fixed
+ * order.  T = 0 writes dW = 0 and dbias = 0.  x is needed for dW only and W for dx only.
+ * Errors as above. */
+moe_status moe_linear_backward(const moe_linear_config* cfg, const void* x, const void* W,
+                               const void* pre, const void* dy, void* dx, void* dW, float* dbias,
+                               void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Dropout with a residual: rows x cols elements, element (row, col) numbered
+ * i = row cols + col whatever the strides.  The keep mask comes from a counter-based generator
+ * and is never stored: word i mod 4 of Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel
+ * random numbers: as easy as 1, 2, 3", 2011) at the counter (i div 4, offset), each as 64 bits
+ * low word first, under the 64-bit key seed; the element is kept when the word is at least
+ * round(p 2^32). */
+typedef struct moe_dropout_config {
+  int64_t rows, cols;      /* >= 0 */
+  double p;                /* probability of dropping, 0..1 */
+  int32_t x_dtype;         /* moe_dtype of x and dx */
+  int32_t residual_dtype;  /* moe_dtype of the residual */
+  int32_t y_dtype;         /* moe_dtype of y and dy */
+  int64_t ldx, ldr, ldy;   /* elements between rows; 0 = cols */
+} moe_dropout_config;
+
+/* y = r + keep x / (1 - p).  x, residual (NULL: 0) and y device; rng_state device [2]: seed,
+ * offset, read when the kernel runs, so that a captured graph takes new values at each replay.
+ * A dropped element's x is not looked at (an infinity or NaN there has no effect); p = 1
+ * drops everything.  y may be x or the residual itself where type and stride agree.
+ * Pointers aligned to their element type.  Errors: MOE_ERR_INVALID_ARG, MOE_ERR_MISALIGNED,
+ * MOE_ERR_CUDA. */
+moe_status moe_dropout_add(const moe_dropout_config* cfg, const void* x, const void* residual,
+                           const uint64_t* rng_state, void* y, cudaStream_t stream);
+
+/* dx = keep dy / (1 - p) with the mask of the same cfg and rng_state (the gradient of the
+ * residual is dy itself).  dy has y's type and stride, dx x's. */
+moe_status moe_dropout_backward(const moe_dropout_config* cfg, const void* dy,
+                                const uint64_t* rng_state, void* dx, cudaStream_t stream);
+
+/* Balance loss of a routed batch, its per-expert counts and its gradient (Section 10.5, Eq. 30
+ * and 38, taken per sequence; scores normalised as in Section 10.7.1).
+ * The T tokens are consecutive sequences of seq_len tokens (the last may be shorter; 0 = the
+ * whole batch as one), S = ceil(T / seq_len).  token_mask [T] (bytes, NULL = all valid): tokens
+ * whose byte is 0 count nowhere, whatever their logits hold, and get a zero gradient.  With
+ * V_s valid tokens in sequence s, V their sum and S' the sequences with V_s > 0,
+ *   C_si = requests of sequence s's valid tokens for expert i,  f_si = C_si / (K V_s),
+ *   P_si = mean over valid tokens of p_ti,  L_b = (1/S') sum_s N sum_i f_si P_si,
+ *   L_z = (1/V) sum_t (log sum_i exp z_ti)^2,  loss = coef_balance L_b + coef_z L_z,
+ * p the softmax, or sigmoid scores divided by their sum (cfg->score).  With f held fixed,
+ *   dlogits_ti = g [coef_balance N / (S' V_s) p_ti (f_si - sum_j f_sj p_tj) (1 - sigma_ti if sigmoid)
+ *                   + coef_z (2 / V) lse_t softmax_ti],   g = *grad_scale (NULL = 1).
+ * A valid token whose logits are all -infinity has p = 0 and no z-loss.  V = 0: everything is 0.
+ *   logits [T][N] fp32 and topk_idx [T][K] as moe_route wrote them (an index outside [0, N)
+ *   counts for no expert and leaves MOE_ERR_DEVICE_BOUNDS in the status word; -1 is an empty
+ *   slot and leaves nothing); grad_scale device fp32 or NULL.
+ * Out (device, each may be NULL): counts [S][N] int32, P [S][N], loss [3] = loss, L_b, L_z,
+ *   dlogits [T][N] fp32 (overwritten; not the logits themselves).  Deterministic.
+ * workspace: moe_balance_loss_workspace_size bytes, prepared by moe_workspace_init.  Errors:
+ * MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (S N > 2^20), MOE_ERR_MISALIGNED,
+ * MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_CUDA. */
+moe_status moe_balance_loss_workspace_size(const moe_config* cfg, int64_t seq_len, size_t* bytes);
+moe_status moe_balance_loss(const moe_config* cfg, const float* logits, const int32_t* topk_idx,
+                            const uint8_t* token_mask, int64_t seq_len, float coef_balance,
+                            float coef_z, const float* grad_scale, int32_t* counts, float* P,
+                            float* loss, float* dlogits, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream);
+
 /* Prepare a fresh workspace: zero its device status word (the first 256 bytes).  Call once
  * after allocating a workspace, before its first use.  Asynchronous on the stream. */
 moe_status moe_workspace_init(void* workspace, size_t workspace_bytes, cudaStream_t stream);

@@ -5,7 +5,10 @@ The compute path is the CUDA library ``libmoe_gb300.so`` (C ABI in
 requires the built library: there is no CPU fallback.
 """
 from ._native import (  # noqa: F401
-    STATS, MoEError, alloc_workspace, copy_config, library, make_config, make_outputs, make_weights,
+    ACTS, STATS, MoEError, alloc_balance_loss_workspace, alloc_linear_workspace, alloc_workspace,
+    copy_config, library, make_config, make_linear_config, make_outputs, make_weights,
+    moe_balance_loss, moe_balance_loss_workspace_size, moe_dropout_add, moe_dropout_backward,
+    moe_layer_backward_aux, moe_linear_backward, moe_linear_forward, moe_linear_workspace_size,
     moe_balance_stats, moe_bias_update, moe_combine,
     moe_grouped_swiglu, moe_layer_forward, moe_layer_forward_profiled, moe_merge_shared,
     moe_pack_weights, moe_packed_weights_size, pack_weights, moe_permute, moe_permute_noalloc,

@@ -25,6 +25,7 @@ NORMS = {"none": 0, "l1": 1, "softmax_selected": 2, "lp": 3}
 SHARED_MODES = {"none": 0, "const": 1, "gate": 2}
 CAP_POLICIES = {"none": 0, "per_expert": 1, "rank_wide": 2}
 H_FORMATS = {"bf16": 0, "f16": 1}
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 
 class MoEError(RuntimeError):
@@ -45,6 +46,19 @@ class moe_config(ctypes.Structure):
 class moe_weights(ctypes.Structure):
     _fields_ = [(n, c_void_p) for n in ("W_router", "router_bias", "selection_bias", "shared_gate_w",
                                         "W_gate", "W_up", "W_down", "Ws_gate", "Ws_up", "Ws_down")]
+
+
+class moe_linear_config(ctypes.Structure):
+    _fields_ = [("T", c_int64), ("in_features", c_int32), ("out_features", c_int32),
+                ("dtype", c_int32), ("out_dtype", c_int32), ("act", c_int32), ("dx_dtype", c_int32),
+                ("dw_dtype", c_int32), ("ldx", c_int64), ("ldw", c_int64), ("ldr", c_int64),
+                ("ldy", c_int64)]
+
+
+class moe_dropout_config(ctypes.Structure):
+    _fields_ = [("rows", c_int64), ("cols", c_int64), ("p", c_double), ("x_dtype", c_int32),
+                ("residual_dtype", c_int32), ("y_dtype", c_int32), ("ldx", c_int64), ("ldr", c_int64),
+                ("ldy", c_int64)]
 
 
 GRAD_FIELDS = ("dx", "dW_gate", "dW_up", "dW_down", "dWs_gate", "dWs_up", "dWs_down", "dW_router",
@@ -113,6 +127,17 @@ def _load():
         "moe_backward_workspace_size": ([C, POINTER(c_size_t)], c_int32),
         "moe_layer_backward": ([C, POINTER(moe_weights), P, POINTER(moe_outputs), P, POINTER(moe_grads),
                                 P, c_size_t, P], c_int32),
+        "moe_layer_backward_aux": ([C, POINTER(moe_weights), P, POINTER(moe_outputs), P, P,
+                                    POINTER(moe_grads), P, c_size_t, P], c_int32),
+        "moe_linear_workspace_size": ([POINTER(moe_linear_config), POINTER(c_size_t)], c_int32),
+        "moe_linear_forward": ([POINTER(moe_linear_config), P, P, P, P, P, P, P, c_size_t, P], c_int32),
+        "moe_linear_backward": ([POINTER(moe_linear_config), P, P, P, P, P, P, P, P, c_size_t, P],
+                                c_int32),
+        "moe_dropout_add": ([POINTER(moe_dropout_config), P, P, P, P, P], c_int32),
+        "moe_dropout_backward": ([POINTER(moe_dropout_config), P, P, P, P], c_int32),
+        "moe_balance_loss_workspace_size": ([C, c_int64, POINTER(c_size_t)], c_int32),
+        "moe_balance_loss": ([C, P, P, P, c_int64, c_float, c_float, P, P, P, P, P, P, c_size_t, P],
+                             c_int32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -393,3 +418,174 @@ def moe_layer_backward(cfg, weights: moe_weights, x, fwd_outputs: moe_outputs, d
         ctypes.byref(cfg), ctypes.byref(weights), _ptr(x), ctypes.byref(fwd_outputs), _ptr(dy),
         ctypes.byref(grads), _ptr(workspace), workspace.numel(), _stream(stream)))
 
+
+
+def moe_layer_backward_aux(cfg, weights: moe_weights, x, fwd_outputs: moe_outputs, dy, dlogits,
+                           grads: moe_grads, workspace, stream=None):
+    """moe_layer_backward with a further gradient of the router logits (fp32 [T][N])."""
+    _check("moe_layer_backward_aux", _lib.moe_layer_backward_aux(
+        ctypes.byref(cfg), ctypes.byref(weights), _ptr(x), ctypes.byref(fwd_outputs), _ptr(dy),
+        _ptr(dlogits), ctypes.byref(grads), _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+# ---- the block around the layer ------------------------------------------------------
+
+def make_linear_config(T, in_features, out_features, act="none", out_dtype="bf16", dx_dtype="bf16",
+                       dw_dtype="bf16", dtype="bf16", ldx=0, ldw=0, ldr=0, ldy=0) -> moe_linear_config:
+    """A ``moe_linear_config``; ``ld*`` are the elements between rows (0 = dense)."""
+    c = moe_linear_config()
+    c.T, c.in_features, c.out_features = int(T), int(in_features), int(out_features)
+    c.dtype, c.out_dtype = _enum(DTYPES, dtype), _enum(DTYPES, out_dtype)
+    c.dx_dtype, c.dw_dtype = _enum(DTYPES, dx_dtype), _enum(DTYPES, dw_dtype)
+    c.act = _enum(ACTS, act)
+    c.ldx, c.ldw, c.ldr, c.ldy = int(ldx), int(ldw), int(ldr), int(ldy)
+    return c
+
+
+_TORCH_DTYPES = {"torch.float32": 0, "torch.bfloat16": 1}
+
+
+def _dtype_of(t) -> int:
+    try:
+        return _TORCH_DTYPES[str(t.dtype)]
+    except KeyError:
+        raise ValueError(f"fp32 or bf16 tensors are expected, got {t.dtype}") from None
+
+
+def _on_device(name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor is expected")
+
+
+def _mat(name, t, rows, cols, ld, dtype):
+    """Pointer of a row-strided [rows][cols] matrix, checked against what the call assumes."""
+    if t is None:
+        return None
+    _on_device(name, t)
+    if tuple(t.shape) != (rows, cols) or _dtype_of(t) != dtype:
+        raise ValueError(f"{name}: expected [{rows}][{cols}] of "
+                         f"{'fp32' if dtype == 0 else 'bf16'}, got {tuple(t.shape)} {t.dtype}")
+    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) != (ld or cols)):
+        raise ValueError(f"{name}: strides {t.stride()} do not match a row stride of {ld or cols}")
+    return c_void_p(t.data_ptr())
+
+
+def _vec(name, t, n, dtype="torch.float32"):
+    if t is None:
+        return None
+    _on_device(name, t)
+    if t.numel() != n or not t.is_contiguous() or str(t.dtype) != dtype:
+        raise ValueError(f"{name}: expected {n} contiguous values of {dtype}, "
+                         f"got {tuple(t.shape)} {t.dtype}")
+    return c_void_p(t.data_ptr())
+
+
+def moe_linear_workspace_size(cfg: moe_linear_config) -> int:
+    n = c_size_t(0)
+    _check("moe_linear_workspace_size", _lib.moe_linear_workspace_size(ctypes.byref(cfg), ctypes.byref(n)))
+    return int(n.value)
+
+
+def alloc_linear_workspace(cfg: moe_linear_config, device="cuda", stream=None):
+    """A zero-status workspace (uint8 tensor) for moe_linear_forward and moe_linear_backward."""
+    import torch
+    ws = torch.empty(moe_linear_workspace_size(cfg), dtype=torch.uint8, device=device)
+    moe_workspace_init(ws, stream)
+    return ws
+
+
+def moe_linear_forward(cfg: moe_linear_config, x, W, bias, residual, pre, y, workspace, stream=None):
+    """y = act(x W^T + bias) + residual; bias, residual and pre (z, for the backward pass) may
+    be None.  Rows of x, W, residual and y may be strided as the configuration says."""
+    T, i, o, od = cfg.T, cfg.in_features, cfg.out_features, cfg.out_dtype
+    _check("moe_linear_forward", _lib.moe_linear_forward(
+        ctypes.byref(cfg), _mat("x", x, T, i, cfg.ldx, cfg.dtype), _mat("W", W, o, i, cfg.ldw, cfg.dtype),
+        _vec("bias", bias, o), _mat("residual", residual, T, o, cfg.ldr, od),
+        _mat("pre", pre, T, o, 0, od), _mat("y", y, T, o, cfg.ldy, od), _ptr(workspace),
+        workspace.numel(), _stream(stream)))
+
+
+def moe_linear_backward(cfg: moe_linear_config, x, W, pre, dy, dx, dW, dbias, workspace, stream=None):
+    """dx, dW, dbias (each may be None) for the gradient dy of y; pre is the forward call's."""
+    T, i, o, od = cfg.T, cfg.in_features, cfg.out_features, cfg.out_dtype
+    _check("moe_linear_backward", _lib.moe_linear_backward(
+        ctypes.byref(cfg), _mat("x", x, T, i, cfg.ldx, cfg.dtype), _mat("W", W, o, i, cfg.ldw, cfg.dtype),
+        _mat("pre", pre, T, o, 0, od), _mat("dy", dy, T, o, cfg.ldy, od),
+        _mat("dx", dx, T, i, 0, cfg.dx_dtype), _mat("dW", dW, o, i, 0, cfg.dw_dtype),
+        _vec("dbias", dbias, o), _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def _rows_of(name, t, shape=None):
+    """(rows, cols, row stride) of a contiguous tensor or a row-strided matrix."""
+    _on_device(name, t)
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dim() == 0:
+        raise ValueError(f"{name}: a tensor with at least one dimension is expected")
+    cols = t.shape[-1]
+    if t.is_contiguous():
+        return (t.numel() // cols if cols else 0), cols, cols
+    if t.dim() == 2 and (t.stride(1) == 1 or cols == 1):
+        return t.shape[0], cols, (t.stride(0) if t.shape[0] > 1 else cols)
+    raise ValueError(f"{name}: contiguous tensors, or matrices of contiguous rows, are expected")
+
+
+def _dropout_config(x, y, residual, p):
+    c = moe_dropout_config()
+    c.rows, c.cols, c.ldx = _rows_of("x", x)
+    _, _, c.ldy = _rows_of("y", y, x.shape)
+    c.x_dtype, c.y_dtype = _dtype_of(x), _dtype_of(y)
+    c.p = float(p)
+    if residual is not None:
+        _, _, c.ldr = _rows_of("residual", residual, x.shape)
+        c.residual_dtype = _dtype_of(residual)
+    return c
+
+
+def moe_dropout_add(x, residual, p, rng_state, y, stream=None):
+    """y = residual + keep * x / (1 - p); residual may be None.  rng_state: int64 [2] device
+    tensor (seed, offset).  The mask depends on them and the element's number alone."""
+    c = _dropout_config(x, y, residual, p)
+    _check("moe_dropout_add", _lib.moe_dropout_add(
+        ctypes.byref(c), c_void_p(x.data_ptr()),
+        None if residual is None else c_void_p(residual.data_ptr()),
+        _vec("rng_state", rng_state, 2, "torch.int64"), c_void_p(y.data_ptr()), _stream(stream)))
+
+
+def moe_dropout_backward(dy, p, rng_state, dx, stream=None):
+    """dx = keep * dy / (1 - p) with the mask of moe_dropout_add for the same p and rng_state."""
+    c = _dropout_config(dx, dy, None, p)
+    _check("moe_dropout_backward", _lib.moe_dropout_backward(
+        ctypes.byref(c), c_void_p(dy.data_ptr()), _vec("rng_state", rng_state, 2, "torch.int64"),
+        c_void_p(dx.data_ptr()), _stream(stream)))
+
+
+def moe_balance_loss_workspace_size(cfg: moe_config, seq_len: int = 0) -> int:
+    n = c_size_t(0)
+    _check("moe_balance_loss_workspace_size", _lib.moe_balance_loss_workspace_size(
+        ctypes.byref(cfg), int(seq_len), ctypes.byref(n)))
+    return int(n.value)
+
+
+def alloc_balance_loss_workspace(cfg: moe_config, seq_len: int = 0, device="cuda", stream=None):
+    """A zero-status workspace (uint8 tensor) for moe_balance_loss."""
+    import torch
+    ws = torch.empty(moe_balance_loss_workspace_size(cfg, seq_len), dtype=torch.uint8, device=device)
+    moe_workspace_init(ws, stream)
+    return ws
+
+
+def moe_balance_loss(cfg: moe_config, logits, topk_idx, token_mask, seq_len, coef_balance, coef_z,
+                     grad_scale, counts, P, loss, dlogits, workspace, stream=None):
+    """Balance loss and z-loss of a routed batch: loss [3] (total, balance, z), counts and P
+    [sequences][N], dlogits [T][N]; each output, token_mask (uint8 or bool [T]) and
+    grad_scale (fp32 [1]) may be None.  seq_len 0 takes the batch as one sequence."""
+    T, N, K = cfg.T, cfg.N, cfg.K
+    S = -(-T // min(int(seq_len) or T, T)) if T else 0
+    mask = "torch.bool" if token_mask is not None and str(token_mask.dtype) == "torch.bool" else "torch.uint8"
+    _check("moe_balance_loss", _lib.moe_balance_loss(
+        ctypes.byref(cfg), _vec("logits", logits, T * N), _vec("topk_idx", topk_idx, T * K, "torch.int32"),
+        _vec("token_mask", token_mask, T, mask), int(seq_len), float(coef_balance), float(coef_z),
+        _vec("grad_scale", grad_scale, 1), _vec("counts", counts, S * N, "torch.int32"),
+        _vec("P", P, S * N), _vec("loss", loss, 3), _vec("dlogits", dlogits, T * N), _ptr(workspace),
+        workspace.numel(), _stream(stream)))

@@ -669,8 +669,8 @@ moe_status bwd_family(const moe_config& c, bool routed, const int32_t* seg_pad, 
 }
 
 moe_status layer_backward(const moe_config* cfg, const moe_weights* w, const void* x,
-                          const moe_outputs* fwd, const float* dy, const moe_grads* g,
-                          void* ws, size_t ws_bytes, cudaStream_t st) {
+                          const moe_outputs* fwd, const float* dy, const float* dlogits,
+                          const moe_grads* g, void* ws, size_t ws_bytes, cudaStream_t st) {
   moe_status s = check_bwd_cfg(cfg);
   if (s != MOE_OK) return s;
   const moe_config& c = *cfg;
@@ -688,6 +688,7 @@ moe_status layer_backward(const moe_config* cfg, const moe_weights* w, const voi
   const bool router = g->dW_router != nullptr;
   const bool gate = router && shared && c.shared_mode == MOE_SHARED_SIGMOID_GATE;
   if (router && (!fwd->logits || !w->W_router)) return MOE_ERR_INVALID_ARG;
+  if (dlogits && !router) return MOE_ERR_INVALID_ARG;
   if (gate && (!g->dshared_gate_w || !w->shared_gate_w)) return MOE_ERR_INVALID_ARG;
   if (c.T > 0 && (!x || !dy)) return MOE_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_MISALIGNED;
@@ -763,6 +764,7 @@ moe_status layer_backward(const moe_config* cfg, const moe_weights* w, const voi
     zp.n128 = L.n128;
     du = gate ? at<float>(ws, L.du) : nullptr;
     zp.du = du;
+    zp.dlogits = dlogits;
     zp.status = status;
     if (!ok(launch_router_bwd(zp, st))) return MOE_ERR_CUDA;
     CUtensorMap mZk, mZm, mWr, mX;
@@ -904,7 +906,14 @@ moe_status moe_backward_workspace_size(const moe_config* cfg, size_t* bytes) {
 moe_status moe_layer_backward(const moe_config* cfg, const moe_weights* w, const void* x,
                               const moe_outputs* fwd, const float* dy, const moe_grads* grads,
                               void* workspace, size_t workspace_bytes, cudaStream_t stream) {
-  return layer_backward(cfg, w, x, fwd, dy, grads, workspace, workspace_bytes, stream);
+  return layer_backward(cfg, w, x, fwd, dy, nullptr, grads, workspace, workspace_bytes, stream);
+}
+
+moe_status moe_layer_backward_aux(const moe_config* cfg, const moe_weights* w, const void* x,
+                                  const moe_outputs* fwd, const float* dy, const float* dlogits,
+                                  const moe_grads* grads, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream) {
+  return layer_backward(cfg, w, x, fwd, dy, dlogits, grads, workspace, workspace_bytes, stream);
 }
 
 moe_status moe_workspace_init(void* workspace, size_t workspace_bytes, cudaStream_t stream) {

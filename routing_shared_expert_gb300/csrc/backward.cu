@@ -303,6 +303,7 @@ __global__ void __launch_bounds__(256) router_bwd_kernel(RouterBwdParams p) {
       for (int k = 0; k < kMaxTopK; ++k)
         if (k < p.K && si[k] == j) v += dzS[k];
       if (soft && p.norm != MOE_NORM_SOFTMAX_SELECTED) v -= expf(z[j] - m) / sum * c;
+      if (p.dlogits != nullptr) v += p.dlogits[t * p.N + j];
     }
     out[j] = __float2bfloat16(v);
   }

@@ -277,6 +277,7 @@ struct RouterBwdParams {
   __nv_bfloat16* dz;          // [T][n128]
   int32_t n128;
   float* du;                  // [T] or nullptr
+  const float* dlogits;       // [T][N] further gradient of the logits, or nullptr
   int32_t* status;
 };
 constexpr int kDwsChunks = 64;

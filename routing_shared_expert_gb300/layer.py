@@ -135,11 +135,14 @@ class MoELayer:
         return o["y"]
 
     def backward(self, x: torch.Tensor, dy: torch.Tensor, stream=None,
-                 router_grad: bool = False) -> Dict[str, torch.Tensor]:
+                 router_grad: bool = False,
+                 dlogits: Optional[torch.Tensor] = None) -> Dict[str, torch.Tensor]:
         """Gradients for upstream gradient dy [T][d] fp32, using the routing of the last
         forward call (which must have written the logits when ``router_grad``); returns dx
         and the weight gradients (fp32).  ``router_grad`` adds the gradient through the
-        router coefficients (dW_router, and dshared_gate_w for a learned shared gate)."""
+        router coefficients (dW_router, and dshared_gate_w for a learned shared gate);
+        ``dlogits`` (fp32 [T][N], with ``router_grad``) is a further gradient of the logits,
+        as ``moe_balance_loss`` writes it."""
         if not hasattr(self, "cfg_bwd"):
             # the backward reads the bf16 down projections: a configuration that says so
             self.cfg_bwd = nat.copy_config(self.cfg, h_format=nat.H_FORMATS["bf16"])
@@ -167,7 +170,8 @@ class MoELayer:
                 if c.shared_mode == nat.SHARED_MODES["gate"]:
                     self.grads["dshared_gate_w"] = torch.empty((d,), **f32)
             self.grads_c = nat.make_grads(**self.grads)
-        nat.moe_layer_backward(c, self.w_bwd, x, self.outputs, dy, self.grads_c, self.bwd_ws, stream)
+        nat.moe_layer_backward_aux(c, self.w_bwd, x, self.outputs, dy, dlogits, self.grads_c,
+                                   self.bwd_ws, stream)
         return self.grads
 
     def backward_status(self) -> int:

@@ -177,6 +177,20 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t smem_addr) {
   return d;
 }
 
+// The same of an MN-major operand tile (M or N contiguous): 64-wide boxes of 64 K-rows, kMnLbo
+// bytes between the two boxes of a 128-wide tile, kMnSbo between groups of 8 K-rows.
+constexpr uint32_t kMnLbo = 8192;
+constexpr uint32_t kMnSbo = 1024;
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>((kMnLbo >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>((kMnSbo >> 4) & 0x3FFFu) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
 // Instruction descriptor of tcgen05.mma kind::f16: bf16 A and B, fp32 accumulator,
 // both operands K-major, tile M x N.
 //   bits 4-5 D format (1 = f32), 7-9 A format (1 = bf16), 10-12 B format (1 = bf16),
@@ -319,6 +333,11 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 // the shared-memory sources of every committed store have been read
 __device__ __forceinline__ void bulk_wait_read_all() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+// the sources of every committed store but the newest N have been read
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 // every committed store has completed
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }

@@ -56,19 +56,6 @@ constexpr int THREADS = 192;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainLimitNs = 100000000ull;
-constexpr uint32_t kMnLbo = 8192;   // bytes between the two 64-wide MN halves of a CTA's tile
-constexpr uint32_t kMnSbo = 1024;   // bytes between groups of 8 K-rows
-
-// SMEM descriptor of an MN-major, 128-byte-swizzled operand tile.
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t addr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>((kMnLbo >> 4) & 0x3FFFu) << 16;
-  d |= static_cast<uint64_t>((kMnSbo >> 4) & 0x3FFFu) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
-}
 
 struct BwdTile {
   int g, m, n;

@@ -1,0 +1,294 @@
+// The dense projection for few tokens: y = act(x W^T + b) + r bound by reading W once.
+//
+// The MMA's rows are 128 output features and its columns NT tokens (tcgen05, M = 128, N = NT,
+// one CTA), so a tile streams 128 weight rows and a token costs no more tensor work than it
+// needs.  out / 128 tiles are too few to keep 152 SMs reading, so the CTAs of a cluster split
+// the depth: each accumulates its range of K in its own TMEM, writes the partial sums to its
+// shared memory, and after a cluster barrier each CTA adds the partials of its share of the
+// tokens in rank order over distributed shared memory (a fixed order, so every call gives the
+// same bits, and no second launch or global scratch).  The epilogue has one thread per
+// feature: its loads and stores run along the rows of y, whatever their alignment.
+//
+// The ring holds one 64-wide K block per stage (16 KB of W, 128 NT bytes of x).  Up to NT = 64
+// it takes about 100 KB, so two CTAs share an SM and one streams while the other starts or ends.
+//
+// Every wait is bounded; a wait that runs out records MOE_ERR_TIMEOUT and the CTA waits for
+// what it issued before it frees its TMEM.
+#include <algorithm>
+
+#include "activation.cuh"
+#include "linear.h"
+
+namespace moe {
+namespace {
+
+constexpr int FM = 128;                    // features per tile
+constexpr int BK = 64;
+constexpr int W_BYTES = FM * BK * 2;
+constexpr int THREADS = 192;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint64_t kDrainLimitNs = 100000000ull;
+
+template <int NT> struct Shape {
+  static constexpr int X_BYTES = NT * BK * 2;
+  static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
+  static constexpr int STAGES = NT <= 16 ? 6 : NT <= 32 ? 5 : NT <= 64 ? 4 : NT <= 128 ? 6 : 4;
+  static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+  static constexpr size_t SMEM = 1024 + RING_BYTES + 8 * (2 * STAGES + 2) + 32;
+  static constexpr int PER_SM = SMEM <= 113 * 1024 ? 2 : 1;
+  static constexpr uint32_t TMEM_COLS = NT < 32 ? 32 : NT;
+  static_assert(NT * FM * 4 <= RING_BYTES, "the partial sums take the ring's place");
+};
+
+struct Args {
+  int32_t T, N, K;         // tokens, features, depth
+  int32_t t_tiles;
+  int32_t split;           // CTAs per cluster
+  int32_t act;
+  const float* bias;
+  const void* residual;
+  void* pre;
+  void* C;
+  int64_t ldr, ldc;
+  int32_t* status;
+};
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <typename OUT>
+__device__ __forceinline__ void finish(const Args& a, int64_t t, int f, float acc, float bias) {
+  const float z = acc + bias;
+  if (a.pre) static_cast<OUT*>(a.pre)[t * a.N + f] = from_f32<OUT>(z);
+  float y = act_value(z, a.act);
+  if (a.residual) y += to_f32(static_cast<const OUT*>(a.residual)[t * a.ldr + f]);
+  static_cast<OUT*>(a.C)[t * a.ldc + f] = from_f32<OUT>(y);
+}
+
+template <int NT, typename OUT>
+__global__ void __launch_bounds__(THREADS, Shape<NT>::PER_SM)
+    linear_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                      const Args args) {
+  using S = Shape<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::RING_BYTES);
+  uint64_t* empty = full + S::STAGES;
+  uint64_t* tfull = empty + S::STAGES;
+  uint64_t* drain = tfull + 1;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  int* never = const_cast<int*>(abort_flag) + 1;
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int split = args.split;
+  const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const uint32_t smem_base = smem_u32(smem);
+  const int tile = static_cast<int>(blockIdx.x) / split;
+  const int f0 = tile / args.t_tiles * FM;            // the token tiles of one weight tile together
+  const int t0 = tile % args.t_tiles * NT;
+  const int k_blocks = (args.K + BK - 1) / BK;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(k_blocks) * rank / split);
+  const int kbs = static_cast<int>(static_cast<int64_t>(k_blocks) * (rank + 1) / split) - kb0;
+
+  auto load = [&](int i) {                            // K block kb0 + i into its stage
+    const int s = i % S::STAGES;
+    const uint32_t at = smem_base + s * S::STAGE_BYTES;
+    mbar_arrive_expect_tx(smem_u32(&full[s]), S::STAGE_BYTES);
+    tma_load_2d(at, &tmW, (kb0 + i) * BK, f0, smem_u32(&full[s]));
+    tma_load_2d(at + W_BYTES, &tmX, (kb0 + i) * BK, t0, smem_u32(&full[s]));
+  };
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::STAGES; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    mbar_init(smem_u32(tfull), 1);
+    mbar_init(smem_u32(drain), 1);
+    *abort_flag = 0;
+    *never = 0;
+    mbar_fence_init();
+    fence_proxy_async_smem();
+    for (int i = 0; i < S::STAGES && i < kbs; ++i) load(i);   // before the other warps are ready
+  }
+  if (warp == 1) tmem_alloc(smem_u32(tmem_holder), S::TMEM_COLS);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  bool ok = true;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------- producer
+    if (lane == 0) {
+      int i = S::STAGES;
+      for (; i < kbs; ++i) {
+        const int use = i / S::STAGES;
+        if (!mbar_wait_bounded(smem_u32(&empty[i % S::STAGES]), (use & 1) ^ 1, abort_flag, args.status,
+                               kWaitLimitNs)) {
+          ok = false;
+          break;
+        }
+        load(i);
+      }
+      if (!ok)   // the blocks issued last, one per stage
+        for (int j = max(0, i - S::STAGES); j < i; ++j)
+          mbar_wait_bounded(smem_u32(&full[j % S::STAGES]), (j / S::STAGES) & 1, never, nullptr,
+                            kDrainLimitNs);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(FM, NT);
+      for (int i = 0; i < kbs; ++i) {
+        const int s = i % S::STAGES;
+        if (!mbar_wait_bounded(smem_u32(&full[s]), (i / S::STAGES) & 1, abort_flag, args.status,
+                               kWaitLimitNs)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t at = smem_base + s * S::STAGE_BYTES;
+#pragma unroll
+        for (int j = 0; j < BK / 16; ++j)
+          tc_mma_bf16(tmem_base, sw128_kmajor_desc(at) + 2 * j, sw128_kmajor_desc(at + W_BYTES) + 2 * j,
+                      idesc, (i > 0 || j > 0) ? 1u : 0u);
+        tc_commit(smem_u32(&empty[s]));
+      }
+      if (ok) {
+        tc_commit(smem_u32(tfull));
+      } else {
+        tc_commit(smem_u32(drain));
+        mbar_wait_bounded(smem_u32(drain), 0, never, nullptr, kDrainLimitNs);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------- epilogue
+    ok = mbar_wait_bounded(smem_u32(tfull), 0, abort_flag, args.status, kWaitLimitNs);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) {
+      tc_fence_after();
+      const int q = warp & 3;
+      const int f = f0 + q * 32 + lane;
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+      const float bias = (split == 1 && args.bias && f < args.N) ? __ldg(args.bias + f) : 0.f;
+      float* part = reinterpret_cast<float*>(smem);   // [NT][FM]: the ring is idle
+#pragma unroll 1
+      for (int c = 0; c < NT; c += 32) {
+        if (t0 + c >= args.T) break;
+        uint32_t v[32];
+        tmem_ld32(taddr + c, v);
+#pragma unroll
+        for (int j = 0; j < (NT < 32 ? NT : 32); ++j) {
+          const int64_t t = t0 + c + j;
+          if (split > 1)
+            part[(c + j) * FM + q * 32 + lane] = kbs > 0 ? __uint_as_float(v[j]) : 0.f;
+          else if (t < args.T && f < args.N)
+            finish<OUT>(args, t, f, __uint_as_float(v[j]), bias);
+        }
+      }
+      tc_fence_before();
+    }
+  }
+  __syncwarp();
+  if (split > 1) {
+    cluster_sync_all();   // every CTA's partial sums are in its shared memory
+    if (warp >= 2 && ok) {
+      const int i = threadIdx.x - 64;
+      const int f = f0 + i;
+      const float bias = (args.bias && f < args.N) ? __ldg(args.bias + f) : 0.f;
+      const int tokens = min(NT, args.T - t0);
+      if (f < args.N) {
+#pragma unroll 1
+        for (int j = rank; j < tokens; j += split) {
+          const uint32_t at = smem_base + static_cast<uint32_t>(j * FM + i) * 4u;
+          float p[8];
+#pragma unroll
+          for (int r = 0; r < 8; ++r) p[r] = r < split ? ld_cluster_f32(mapa_shared(at, r)) : 0.f;
+          float sum = p[0];
+#pragma unroll
+          for (int r = 1; r < 8; ++r) sum += p[r];
+          finish<OUT>(args, t0 + j, f, sum, bias);
+        }
+      }
+    }
+    cluster_sync_all();   // no CTA leaves while another reads its partial sums
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, S::TMEM_COLS);
+  }
+}
+
+template <int NT, typename OUT>
+cudaError_t launch_typed(const LinearGemm& g, int split, cudaStream_t s) {
+  using S = Shape<NT>;
+  Args a{};
+  a.T = static_cast<int32_t>(g.M);
+  a.N = g.N;
+  a.K = g.K;
+  a.t_tiles = (a.T + NT - 1) / NT;
+  a.split = split;
+  a.act = g.act;
+  a.bias = g.bias;
+  a.residual = g.residual;
+  a.pre = g.pre;
+  a.C = g.C;
+  a.ldr = g.ldr;
+  a.ldc = g.ldc;
+  a.status = g.status;
+  CUtensorMap mW, mX;
+  if (!make_strided_map(&mW, MOE_BF16, g.B, g.K, g.N, g.ldb, BK, FM) ||
+      !make_strided_map(&mX, MOE_BF16, g.A, g.K, static_cast<uint64_t>(g.M), g.lda, BK, NT))
+    return cudaErrorInvalidValue;
+  auto kern = linear_few_kernel<NT, OUT>;
+  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), S::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((a.N + FM - 1) / FM * a.t_tiles * split));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = S::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, mW, mX, a);
+}
+
+template <typename OUT>
+cudaError_t launch_out(const LinearGemm& g, cudaStream_t s) {
+  const int T = static_cast<int>(g.M);
+  const int NT = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
+  // CTAs per cluster: enough for every SM to read, at least two K blocks each
+  const int64_t tiles = static_cast<int64_t>((g.N + FM - 1) / FM) * ((T + NT - 1) / NT);
+  const int k_blocks = (g.K + BK - 1) / BK;
+  const int64_t want = static_cast<int64_t>(device_sm_count()) * (NT <= 64 ? 2 : 1);
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= want && k_blocks >= 4 * split) split *= 2;
+  switch (NT) {
+    case 16: return launch_typed<16, OUT>(g, split, s);
+    case 32: return launch_typed<32, OUT>(g, split, s);
+    case 64: return launch_typed<64, OUT>(g, split, s);
+    case 128: return launch_typed<128, OUT>(g, split, s);
+    default: return launch_typed<256, OUT>(g, split, s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_linear_few(const LinearGemm& g, cudaStream_t s) {
+  return g.out_dtype == MOE_F32 ? launch_out<float>(g, s) : launch_out<__nv_bfloat16>(g, s);
+}
+
+}  // namespace moe

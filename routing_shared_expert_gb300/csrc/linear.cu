@@ -3,108 +3,133 @@
 //   z = x W^T + b,  y = act(z) + r
 //   dz = dy act'(z),  dx = dz W,  dW = dz^T x,  db = sum_t dz
 //
-// The three products are one kernel over operand strides: C[m][n] = sum_k A(m, k) B(n, k), a
-// 64 x 64 tile per CTA staged through shared memory in steps of 16, fp32 accumulation.
+// The products run on the tensor cores (gemm_linear.cu; gemm_linear_few.cu for few tokens).
+// Here: the argument checks, the pass that forms dz (rounded to bf16, which the products need,
+// while db sums the unrounded values) and the copy that gives unaligned operands 16-byte rows.
+#include "linear.h"
+
 #include <algorithm>
 
 #include "activation.cuh"
-#include "internal.h"
 
 namespace moe {
 namespace {
 
-constexpr int TILE = 64;
-constexpr int KSTEP = 16;
-constexpr int kDbRows = 256;   // rows per partial sum of db
+constexpr int kDzRows = 64;     // rows per block of the dz pass, and per partial sum of db
+constexpr int kDzCols = 256;    // columns per block: 8 per lane
+constexpr int kFewTokens = 256; // at most this many take the few-token kernel
 
-struct ProductArgs {
-  const __nv_bfloat16* A;
-  const __nv_bfloat16* B;
-  int64_t sam, sak, sbn, sbk;   // element strides
-  int64_t M, N, K;
-  const float* bias;            // [N]
-  const void* residual;         // [M][ldr]
-  void* pre;                    // [M][N]
-  void* C;                      // [M][ldc]
-  int64_t ldr, ldc;
-  int32_t act;
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+struct DzArgs {
+  const void* dy;
+  const void* pre;              // nullptr: the identity
+  int64_t ldy, T, col_blocks, ld_dz;
+  int32_t n, act;
+  __nv_bfloat16* dz;            // [T][ld_dz] or nullptr
+  float* part;                  // [row blocks][n] or nullptr
 };
 
-template <typename OUT>
-__global__ void __launch_bounds__(256) product_kernel(ProductArgs a) {
-  __shared__ float sA[KSTEP][TILE + 1], sB[KSTEP][TILE + 1];
-  const int64_t tiles_n = (a.N + TILE - 1) / TILE;
-  const int64_t m0 = blockIdx.x / tiles_n * TILE, n0 = blockIdx.x % tiles_n * TILE;
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < a.K; k0 += KSTEP) {
-    for (int i = threadIdx.x; i < TILE * KSTEP; i += 256) {
-      const int r = i / KSTEP, k = i % KSTEP;
-      const bool kin = k0 + k < a.K;
-      sA[k][r] = kin && m0 + r < a.M ? to_f32(a.A[(m0 + r) * a.sam + (k0 + k) * a.sak]) : 0.f;
-      sB[k][r] = kin && n0 + r < a.N ? to_f32(a.B[(n0 + r) * a.sbn + (k0 + k) * a.sbk]) : 0.f;
+// dz = dy act'(pre) and, per block of kDzRows rows, its column sums (each warp its rows in
+// order, then the warps in order).  VEC: 16-byte loads of whole groups of eight columns.
+template <typename OUT, bool VEC>
+__global__ void __launch_bounds__(256) dz_kernel(DzArgs a) {
+  __shared__ float s_sum[8][kDzCols];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int64_t rb = blockIdx.x / a.col_blocks;
+  const int c0 = static_cast<int>(blockIdx.x % a.col_blocks) * kDzCols + lane * 8;
+  const int64_t t1 = min(a.T, (rb + 1) * kDzRows);
+  float sum[8] = {};
+  if (c0 < a.n) {
+    for (int64_t t = rb * kDzRows + warp; t < t1; t += 8) {
+      const OUT* dy = static_cast<const OUT*>(a.dy) + t * a.ldy + c0;
+      const OUT* pre = static_cast<const OUT*>(a.pre) + t * a.n + c0;
+      float g[8], z[8];
+      if (VEC) {
+        load8(dy, g);
+        if (a.pre) load8(pre, z);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          g[e] = c0 + e < a.n ? to_f32(dy[e]) : 0.f;
+          z[e] = a.pre && c0 + e < a.n ? to_f32(pre[e]) : 0.f;
+        }
+      }
+      if (a.pre) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] *= act_slope(z[e], a.act);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += g[e];
+      if (a.dz)   // ld_dz is a multiple of 8: whole groups, the last one padded
+        *reinterpret_cast<uint4*>(a.dz + t * a.ld_dz + c0) =
+            make_uint4(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]), pack_bf16x2(g[4], g[5]),
+                       pack_bf16x2(g[6], g[7]));
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < KSTEP; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] += sA[k][ty * 4 + i] * sB[k][tx + 16 * j];
-    __syncthreads();
   }
+  if (!a.part) return;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int e = 0; e < 8; ++e) s_sum[warp][lane * 8 + e] = sum[e];
+  __syncthreads();
+  const int col = static_cast<int>(blockIdx.x % a.col_blocks) * kDzCols + threadIdx.x;
+  if (col < a.n) {
+    float v = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty * 4 + i, n = n0 + tx + 16 * j;
-      if (m >= a.M || n >= a.N) continue;
-      const float z = acc[i][j] + (a.bias ? a.bias[n] : 0.f);
-      if (a.pre) static_cast<OUT*>(a.pre)[m * a.N + n] = from_f32<OUT>(z);
-      float y = act_value(z, a.act);
-      if (a.residual) y += to_f32(static_cast<const OUT*>(a.residual)[m * a.ldr + n]);
-      static_cast<OUT*>(a.C)[m * a.ldc + n] = from_f32<OUT>(y);
+    for (int w = 0; w < 8; ++w) v += s_sum[w][threadIdx.x];
+    a.part[rb * a.n + col] = v;
+  }
+}
+
+// db: 32 columns per CTA, 32 warps that each add every 32nd block, then the warps in order.
+__global__ void __launch_bounds__(1024) db_kernel(const float* part, int64_t blocks, int n, float* db) {
+  __shared__ float s_sum[32][33];
+  const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int col = blockIdx.x * 32 + lane;
+  float sum = 0.f;
+  if (col < n)
+    for (int64_t b = w; b < blocks; b += 32) sum += part[b * n + col];
+  s_sum[w][lane] = sum;
+  __syncthreads();
+  if (w == 0 && col < n) {
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v += s_sum[i][lane];
+    db[col] = v;
+  }
+}
+
+// Rows of cols bf16 values, ld apart, to rows ldd (a multiple of 8) apart: a warp per row.
+__global__ void __launch_bounds__(256) align_rows_kernel(const __nv_bfloat16* src, int64_t rows, int cols,
+                                                         int64_t ld, __nv_bfloat16* dst, int64_t ldd) {
+  const int lane = threadIdx.x % 32;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32; r < rows; r += step) {
+    const unsigned short* s = reinterpret_cast<const unsigned short*>(src + r * ld);
+    unsigned short* d = reinterpret_cast<unsigned short*>(dst + r * ldd);
+    for (int c = lane * 2; c < cols; c += 64) {
+      const unsigned lo = s[c], hi = c + 1 < cols ? s[c + 1] : 0u;
+      *reinterpret_cast<unsigned*>(d + c) = lo | hi << 16;
     }
-}
-
-// dz rows (bf16) and, per block of kDbRows rows, their column sums.
-template <typename OUT>
-__global__ void __launch_bounds__(256) dz_kernel(const void* dy, int64_t ldy, const void* pre, int act,
-                                                 int64_t T, int64_t n, __nv_bfloat16* dz, float* part) {
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (col >= n) return;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.y) * kDbRows;
-  const int64_t t1 = min(T, t0 + kDbRows);
-  float sum = 0.f;
-  for (int64_t t = t0; t < t1; ++t) {
-    float v = to_f32(static_cast<const OUT*>(dy)[t * ldy + col]);
-    if (act != MOE_ACT_NONE) v *= act_slope(to_f32(static_cast<const OUT*>(pre)[t * n + col]), act);
-    sum += v;
-    dz[t * n + col] = from_f32<__nv_bfloat16>(v);
   }
-  part[blockIdx.y * n + col] = sum;
 }
 
-__global__ void __launch_bounds__(256) db_kernel(const float* part, int64_t blocks, int64_t n, float* db) {
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (col >= n) return;
-  float sum = 0.f;
-  for (int64_t b = 0; b < blocks; ++b) sum += part[b * n + col];
-  db[col] = sum;
-}
-
-cudaError_t launch_product(const ProductArgs& a, int32_t out_dtype, cudaStream_t s) {
-  const int64_t tiles = ((a.M + TILE - 1) / TILE) * ((a.N + TILE - 1) / TILE);
-  if (tiles == 0) return cudaSuccess;
-  if (out_dtype == MOE_F32)
-    product_kernel<float><<<static_cast<unsigned>(tiles), 256, 0, s>>>(a);
-  else
-    product_kernel<__nv_bfloat16><<<static_cast<unsigned>(tiles), 256, 0, s>>>(a);
-  return cudaGetLastError();
-}
+int64_t up8(int64_t v) { return (v + 7) & ~int64_t{7}; }
 
 struct LinearLayout {
-  size_t dz, db_part, total;
+  size_t dz, db_part, x, w, total;
 };
 
 size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
@@ -113,11 +138,33 @@ LinearLayout linear_layout(const moe_linear_config& c) {
   LinearLayout L{};
   size_t o = 256;
   L.dz = o;
-  o = up256(o + static_cast<size_t>(c.T) * c.out_features * 2);
+  o = up256(o + static_cast<size_t>(c.T) * up8(c.out_features) * 2);
   L.db_part = o;
-  o = up256(o + static_cast<size_t>((c.T + kDbRows - 1) / kDbRows) * c.out_features * 4);
+  o = up256(o + static_cast<size_t>((c.T + kDzRows - 1) / kDzRows) * c.out_features * 4);
+  L.x = o;      // aligned copies of x and W
+  o = up256(o + static_cast<size_t>(c.T) * up8(c.in_features) * 2);
+  L.w = o;
+  o = up256(o + static_cast<size_t>(c.out_features) * up8(c.in_features) * 2);
   L.total = o;
   return L;
+}
+
+// The operand itself where its rows start on 16-byte boundaries, else an aligned copy.
+struct Operand {
+  const void* p;
+  int64_t ld;
+};
+cudaError_t aligned_operand(const void* p, int64_t rows, int32_t cols, int64_t ld, void* copy, Operand* o,
+                            cudaStream_t s) {
+  if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld % 8 == 0 || rows == 1)) {
+    *o = {p, up8(ld)};
+    return cudaSuccess;
+  }
+  *o = {copy, up8(cols)};
+  const int64_t blocks = std::min<int64_t>((rows + 7) / 8, static_cast<int64_t>(device_sm_count()) * 16);
+  align_rows_kernel<<<static_cast<unsigned>(blocks), 256, 0, s>>>(
+      static_cast<const __nv_bfloat16*>(p), rows, cols, ld, static_cast<__nv_bfloat16*>(copy), o->ld);
+  return cudaGetLastError();
 }
 
 bool dtype_ok(int32_t t) { return t == MOE_F32 || t == MOE_BF16; }
@@ -179,23 +226,31 @@ moe_status moe_linear_forward(const moe_linear_config* cfg, const void* x, const
       !elem_aligned(residual, c.out_dtype) || !elem_aligned(pre, c.out_dtype) ||
       !elem_aligned(y, c.out_dtype))
     return MOE_ERR_MISALIGNED;
-  ProductArgs a{};
-  a.A = static_cast<const __nv_bfloat16*>(x);
-  a.B = static_cast<const __nv_bfloat16*>(W);
-  a.sam = c.ldx ? c.ldx : c.in_features;
-  a.sbn = c.ldw ? c.ldw : c.in_features;
-  a.sak = a.sbk = 1;
-  a.M = c.T;
-  a.N = c.out_features;
-  a.K = c.in_features;
-  a.bias = bias;
-  a.residual = residual;
-  a.pre = pre;
-  a.C = y;
-  a.ldr = c.ldr ? c.ldr : c.out_features;
-  a.ldc = c.ldy ? c.ldy : c.out_features;
-  a.act = c.act;
-  return launch_product(a, c.out_dtype, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  const LinearLayout L = linear_layout(c);
+  char* ws = static_cast<char*>(workspace);
+  Operand ox, ow;
+  if (aligned_operand(x, c.T, c.in_features, c.ldx ? c.ldx : c.in_features, ws + L.x, &ox, stream) != cudaSuccess ||
+      aligned_operand(W, c.out_features, c.in_features, c.ldw ? c.ldw : c.in_features, ws + L.w, &ow, stream) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  LinearGemm g{};
+  g.A = ox.p;
+  g.lda = ox.ld;
+  g.B = ow.p;
+  g.ldb = ow.ld;
+  g.M = c.T;
+  g.N = c.out_features;
+  g.K = c.in_features;
+  g.out_dtype = c.out_dtype;
+  g.act = c.act;
+  g.bias = bias;
+  g.residual = residual;
+  g.pre = pre;
+  g.C = y;
+  g.ldr = c.ldr ? c.ldr : c.out_features;
+  g.ldc = c.ldy ? c.ldy : c.out_features;
+  g.status = static_cast<int32_t*>(workspace);
+  const cudaError_t e = c.T <= kFewTokens ? launch_linear_few(g, stream) : launch_linear_pair(g, stream);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status moe_linear_backward(const moe_linear_config* cfg, const void* x, const void* W,
@@ -220,48 +275,75 @@ moe_status moe_linear_backward(const moe_linear_config* cfg, const void* x, cons
   if (!dy || (c.act != MOE_ACT_NONE && !pre) || (dW && !x) || (dx && !W)) return MOE_ERR_INVALID_ARG;
   const LinearLayout L = linear_layout(c);
   char* ws = static_cast<char*>(workspace);
-  __nv_bfloat16* dz = reinterpret_cast<__nv_bfloat16*>(ws + L.dz);
-  float* part = reinterpret_cast<float*>(ws + L.db_part);
-  const int64_t ldy = c.ldy ? c.ldy : c.out_features, blocks = (c.T + kDbRows - 1) / kDbRows;
-  const dim3 grid(static_cast<unsigned>((c.out_features + 255) / 256), static_cast<unsigned>(blocks));
-  if (c.out_dtype == MOE_F32)
-    dz_kernel<float><<<grid, 256, 0, stream>>>(dy, ldy, pre, c.act, c.T, c.out_features, dz, part);
-  else
-    dz_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(dy, ldy, pre, c.act, c.T, c.out_features, dz, part);
-  if (dbias)
-    db_kernel<<<grid.x, 256, 0, stream>>>(part, blocks, c.out_features, dbias);
-  cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && dx) {
-    ProductArgs a{};
-    a.A = dz;
-    a.sam = c.out_features;
-    a.sak = 1;
-    a.B = static_cast<const __nv_bfloat16*>(W);
-    a.sbn = 1;
-    a.sbk = c.ldw ? c.ldw : c.in_features;
-    a.M = c.T;
-    a.N = c.in_features;
-    a.K = c.out_features;
-    a.C = dx;
-    a.ldc = c.in_features;
-    e = launch_product(a, c.dx_dtype, stream);
+  const int64_t ldy = c.ldy ? c.ldy : c.out_features;
+  const int32_t n = c.out_features;
+  const int64_t blocks = (c.T + kDzRows - 1) / kDzRows;
+  const bool identity = c.act == MOE_ACT_NONE;
+  Operand oz{dy, ldy};
+  // dy is dz where nothing has to be multiplied or rounded and its rows are aligned
+  const bool as_is = identity && c.out_dtype == MOE_BF16 && (reinterpret_cast<uintptr_t>(dy) & 15u) == 0 && ldy % 8 == 0;
+  if (dbias || ((dx || dW) && !as_is)) {
+    DzArgs a{};
+    a.dy = dy;
+    a.pre = identity ? nullptr : pre;
+    a.ldy = ldy;
+    a.T = c.T;
+    a.col_blocks = (n + kDzCols - 1) / kDzCols;
+    a.ld_dz = up8(n);
+    a.n = n;
+    a.act = c.act;
+    if ((dx || dW) && !as_is) {
+      a.dz = reinterpret_cast<__nv_bfloat16*>(ws + L.dz);
+      oz = {a.dz, a.ld_dz};
+    }
+    a.part = dbias ? reinterpret_cast<float*>(ws + L.db_part) : nullptr;
+    const bool vec = n % 8 == 0 && ldy % 8 == 0 && (reinterpret_cast<uintptr_t>(dy) & 15u) == 0 &&
+                     (reinterpret_cast<uintptr_t>(a.pre) & 15u) == 0;
+    const unsigned grid = static_cast<unsigned>(blocks * a.col_blocks);
+    if (c.out_dtype == MOE_F32) {
+      if (vec) dz_kernel<float, true><<<grid, 256, 0, stream>>>(a);
+      else dz_kernel<float, false><<<grid, 256, 0, stream>>>(a);
+    } else {
+      if (vec) dz_kernel<__nv_bfloat16, true><<<grid, 256, 0, stream>>>(a);
+      else dz_kernel<__nv_bfloat16, false><<<grid, 256, 0, stream>>>(a);
+    }
+    if (dbias) db_kernel<<<static_cast<unsigned>((n + 31) / 32), 1024, 0, stream>>>(a.part, blocks, n, dbias);
+    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
   }
-  if (e == cudaSuccess && dW) {
-    ProductArgs a{};
-    a.A = dz;
-    a.sam = 1;
-    a.sak = c.out_features;
-    a.B = static_cast<const __nv_bfloat16*>(x);
-    a.sbn = 1;
-    a.sbk = c.ldx ? c.ldx : c.in_features;
-    a.M = c.out_features;
-    a.N = c.in_features;
-    a.K = c.T;
-    a.C = dW;
-    a.ldc = c.in_features;
-    e = launch_product(a, c.dw_dtype, stream);
+  LinearGemm g{};
+  g.A = oz.p;
+  g.lda = oz.ld;
+  g.b_mn = true;
+  g.N = c.in_features;
+  g.ldc = c.in_features;
+  g.act = MOE_ACT_NONE;
+  g.status = static_cast<int32_t*>(workspace);
+  if (dx) {
+    Operand o;
+    if (aligned_operand(W, n, c.in_features, c.ldw ? c.ldw : c.in_features, ws + L.w, &o, stream) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    g.B = o.p;
+    g.ldb = o.ld;
+    g.M = c.T;
+    g.K = n;
+    g.out_dtype = c.dx_dtype;
+    g.C = dx;
+    if (launch_linear_pair(g, stream) != cudaSuccess) return MOE_ERR_CUDA;
   }
-  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  if (dW) {
+    Operand o;
+    if (aligned_operand(x, c.T, c.in_features, c.ldx ? c.ldx : c.in_features, ws + L.x, &o, stream) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    g.B = o.p;
+    g.ldb = o.ld;
+    g.a_mn = true;
+    g.M = n;
+    g.K = static_cast<int32_t>(c.T);
+    g.out_dtype = c.dw_dtype;
+    g.C = dW;
+    if (launch_linear_pair(g, stream) != cudaSuccess) return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
 }
 
 }  // extern "C"

@@ -1,0 +1,33 @@
+// Internal declarations of the dense projection's matrix products.
+#pragma once
+
+#include "internal.h"
+
+namespace moe {
+
+// C[m][n] = epilogue(sum_k A(m, k) B(n, k)): A and B bf16 with 16-byte aligned rows, either
+// K-major (a row per m or n, K contiguous) or MN-major (a row per k, M or N contiguous).
+//   z = sum + bias[n];  pre[m][n] = z;  C[m][n] = act(z) + residual[m][n]
+struct LinearGemm {
+  const void* A;
+  const void* B;
+  int64_t lda, ldb;        // elements between rows
+  bool a_mn, b_mn;
+  int64_t M;
+  int32_t N, K;
+  int32_t out_dtype;       // of C, pre and residual
+  int32_t act;
+  const float* bias;       // [N] or nullptr
+  const void* residual;    // [M][ldr] or nullptr
+  void* pre;               // [M][N] or nullptr
+  void* C;                 // [M][ldc]
+  int64_t ldr, ldc;
+  int32_t* status;
+};
+
+// CTA pairs, 256 x 256 tiles (gemm_linear.cu).
+cudaError_t launch_linear_pair(const LinearGemm& g, cudaStream_t s);
+// Few rows of A (both operands K-major), depth split over a cluster (gemm_linear_few.cu).
+cudaError_t launch_linear_few(const LinearGemm& g, cudaStream_t s);
+
+}  // namespace moe

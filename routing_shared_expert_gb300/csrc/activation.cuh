@@ -1,42 +1,72 @@
-// Activations of the dense projections (moe_act) and their derivatives, in fp32.
+// Activations of the dense projections (moe_act) and their derivatives, in fp32 on the fast
+// exponential and reciprocal (each good to a few 2^-23 here, far below the bf16 rounding of the
+// operands).
 #pragma once
 
 #include "common.cuh"
 
 namespace moe {
 
-constexpr float kSqrtHalf = 0.70710678118654752f;
-constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTwoSqrt2OverPi = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float kGeluCubic = 0.044715f;
 
-// The tanh form uses (1 + tanh u) / 2 = sigmoid(2 u).
-__device__ __forceinline__ float act_value(float z, int act) {
-  switch (act) {
-    case MOE_ACT_RELU: return z > 0.f ? z : 0.f;
-    case MOE_ACT_GELU: return 0.5f * z * (1.f + erff(z * kSqrtHalf));
-    case MOE_ACT_GELU_TANH:
-      return z / (1.f + __expf(-kTwoSqrt2OverPi * (z + kGeluCubic * z * z * z)));
-    case MOE_ACT_SILU: return z / (1.f + __expf(-z));
-    default: return z;
-  }
+__device__ __forceinline__ float fast_sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+// The normal distribution function Phi(z) and e = exp(-z^2 / 2), by the rational
+// approximation 7.1.26 of Abramowitz and Stegun: erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2)
+// with t = 1 / (1 + 0.3275911 x), absolute error at most 1.5e-7.  The negative side takes the
+// tail itself, so nothing cancels there.
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  const float t = __fdividef(1.f, 1.f + 0.3275911f * x);
+  e = __expf(-x * x);
+  const float half_erfc =
+      0.5f * e * t *
+      (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+  return z < 0.f ? half_erfc : 1.f - half_erfc;
 }
 
-__device__ __forceinline__ float act_slope(float z, int act) {
-  switch (act) {
-    case MOE_ACT_RELU: return z > 0.f ? 1.f : 0.f;
-    case MOE_ACT_GELU:
-      return 0.5f * (1.f + erff(z * kSqrtHalf)) + z * __expf(-0.5f * z * z) * kInvSqrt2Pi;
-    case MOE_ACT_GELU_TANH: {
-      const float g = 1.f / (1.f + __expf(-kTwoSqrt2OverPi * (z + kGeluCubic * z * z * z)));
-      return g + z * g * (1.f - g) * kTwoSqrt2OverPi * (1.f + 3.f * kGeluCubic * z * z);
-    }
-    case MOE_ACT_SILU: {
-      const float g = 1.f / (1.f + __expf(-z));
-      return g + z * g * (1.f - g);
-    }
-    default: return 1.f;
+// The tanh form of GELU uses (1 + tanh u) / 2 = sigmoid(2 u).
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+  if (ACT == MOE_ACT_RELU) return z > 0.f ? z : 0.f;
+  if (ACT == MOE_ACT_GELU) {
+    float e;
+    return z * normal_cdf(z, e);
   }
+  if (ACT == MOE_ACT_GELU_TANH)
+    return __fdividef(z, 1.f + __expf(-kTwoSqrt2OverPi * z * (1.f + kGeluCubic * z * z)));
+  if (ACT == MOE_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
+  return z;
 }
+
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+  if (ACT == MOE_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+  if (ACT == MOE_ACT_GELU) {
+    float e;
+    const float p = normal_cdf(z, e);
+    return p + z * e * 0.39894228040143268f;   // z times the density
+  }
+  if (ACT == MOE_ACT_GELU_TANH) {
+    const float g = fast_sigmoid(kTwoSqrt2OverPi * z * (1.f + kGeluCubic * z * z));
+    return g + z * g * (1.f - g) * kTwoSqrt2OverPi * (1.f + 3.f * kGeluCubic * z * z);
+  }
+  if (ACT == MOE_ACT_SILU) {
+    const float g = fast_sigmoid(z);
+    return g + z * g * (1.f - g);
+  }
+  return 1.f;
+}
+
+// f<ACT>() for the run-time activation.
+#define MOE_DISPATCH_ACT(act, CALL)                  \
+  switch (act) {                                     \
+    case MOE_ACT_RELU: return CALL(MOE_ACT_RELU);    \
+    case MOE_ACT_GELU: return CALL(MOE_ACT_GELU);    \
+    case MOE_ACT_GELU_TANH: return CALL(MOE_ACT_GELU_TANH); \
+    case MOE_ACT_SILU: return CALL(MOE_ACT_SILU);    \
+    default: return CALL(MOE_ACT_NONE);              \
+  }
 
 }  // namespace moe

@@ -12,11 +12,24 @@
 // of one tile runs beside the products of the next.  Ragged edges need no masks: TMA fills
 // what lies past an operand with zeros, and clips what lies past the output.
 //
-// Epilogue (four warps per CTA, a lane per row): 128 bytes of each of 32 rows at a time go
-// through a swizzled staging block: the residual's block arrives there by TMA while the
-// previous one is worked on, is replaced in place by act(z) + r, and leaves by a TMA store.
-// An output, residual or pre whose rows do not start on 16-byte boundaries is moved by the
-// lanes instead, coalesced along the rows.
+// Tiles rarely fill whole rounds of 76 pairs.  Where the last, partial round would leave enough
+// of them idle, its tiles are cut along the depth into equal parts for as many pairs: each leaves
+// its partial sums (fp32) in scratch memory, and the CTA that finds itself the last of a tile
+// adds the parts in their order along K, whoever came last, so the result does not depend on
+// it.  The cut tiles come first: the joining runs beside the products of the whole tiles.
+//
+// Epilogue: eight warps per CTA (two per TMEM lane quarter, 128 columns each), a lane per row.
+// It works in steps of 64 bytes of each of 32 rows.  Results go from the registers to memory as
+// whole 32-byte sectors (256-bit stores).  The residual's blocks come by TMA into two buffers per
+// warp, the first two while the tile's products still run and each next one as soon as its
+// buffer has been read: read by the lanes themselves, too little of it would be on its way to
+// cover the latency of memory.  A matrix whose rows are not aligned to 16 bytes goes through a
+// staging block with the lanes' element accesses along the rows.
+//
+// The tensor core drops the bits of an addition that do not fit fp32 instead of rounding, an
+// error that grows with the length of the sum and has one sign (measured 2.7e-6 of the result
+// at a depth of 2560).  bf16 outputs do not see it.  For fp32 outputs a sum is taken in segments
+// of at most 896: each ends in its own TMEM buffer and the epilogue adds them in registers, rounded.
 //
 // Every wait is bounded; a wait that runs out records MOE_ERR_TIMEOUT and the CTA waits for
 // what it issued before it frees its TMEM.
@@ -34,10 +47,19 @@ constexpr int BK = 64;
 constexpr int STAGES = 3;
 constexpr int BLOCK_BYTES = HALF * BK * 2; // one operand, one K block, one CTA
 constexpr int STAGE_BYTES = 4 * BLOCK_BYTES;   // two K blocks of A and B
-constexpr int STAGING_BYTES = 4096;        // 32 rows of 128 bytes
-constexpr int EPI_WARPS = 4;
+constexpr int STAGING_BYTES = 2048;        // 32 rows of 64 bytes
+constexpr int EPI_WARPS = 8;
+constexpr int WARP_COLS = BN / 2;          // columns of one epilogue warp
+constexpr int F32_SEGMENT = 14;            // most K blocks of one fp32 partial sum
 constexpr int EPI_BYTES = EPI_WARPS * 2 * STAGING_BYTES;
-constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr int EPI_WARP0 = 4;               // warps 0, 1: producer, issuer; a warpgroup of their own
+constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
+// Registers of the epilogue's threads and of the others, within the 384 x 168 of the launch; the
+// epilogue of fp32 outputs holds 128 sums.
+template <bool F32> struct Regs {
+  static constexpr int EPI = F32 ? 224 : 208, OTHER = F32 ? 56 : 80;
+  static_assert(32 * (EPI_WARPS * EPI + EPI_WARP0 * OTHER) <= THREADS * 168, "register split");
+};
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainLimitNs = 100000000ull;
@@ -46,69 +68,182 @@ constexpr int GROUP_M = 8;                 // row tiles that share the column ti
 struct Args {
   int32_t M, N, K;
   int32_t m_tiles, n_tiles;
-  int32_t act;
+  int32_t cut_tiles;        // tiles 0 .. cut_tiles - 1 are cut along K
+  int32_t parts;            // into this many parts; pair r parts + k holds part k of tile r
   const float* bias;
   const void* residual;
   void* pre;
   void* C;
   int64_t ldr, ldc;
-  bool tma_r, tma_pre, tma_c;
+  bool bias16;              // the bias is 16-byte aligned
+  int32_t al_r, al_pre, al_c;   // bytes the rows are aligned to: 32, 16, or 0 (less)
   int32_t* status;
+  float* scratch;
+  unsigned* tickets;
 };
 
-// Tile t: groups of GROUP_M row tiles; within one, the row tiles of a column tile together, so
-// the tiles in flight are about as many rows as columns wide and their operands stay in L2.
-__device__ __forceinline__ void tile_at(const Args& a, int64_t t, int& m, int& n) {
+// One piece of a pair's work: K blocks [kb0, kb1) of tile (m, n).
+struct Item {
+  int m, n, kb0, kb1;
+  int parts;                // parts of this tile; 1: the whole tile
+  int cut;                  // index of the cut tile
+};
+
+// Item i of a pair; false past the last.  A pair's part of a cut tile comes first.
+// Tiles are numbered in groups of GROUP_M row tiles, within one the row tiles of a column tile
+// together, so that the tiles in flight are about as many rows as columns wide and their
+// operands stay in L2.
+__device__ __forceinline__ bool item_at(const Args& a, int pair, int n_pairs, int i, Item& o) {
+  const int k_blocks = (a.K + BK - 1) / BK;
+  int64_t t;
+  if (pair < a.cut_tiles * a.parts && i == 0) {
+    // parts of whole ring stages (two K blocks)
+    const int stages = (k_blocks + 1) / 2, k = pair % a.parts;
+    o.parts = a.parts;
+    o.cut = pair / a.parts;
+    o.kb0 = static_cast<int>(static_cast<int64_t>(stages) * k / a.parts) * 2;
+    o.kb1 = min(static_cast<int>(static_cast<int64_t>(stages) * (k + 1) / a.parts) * 2, k_blocks);
+    t = o.cut;
+  } else {
+    o.parts = 1;
+    o.kb0 = 0;
+    o.kb1 = k_blocks;
+    t = a.cut_tiles + pair + static_cast<int64_t>(pair < a.cut_tiles * a.parts ? i - 1 : i) * n_pairs;
+  }
+  if (t >= static_cast<int64_t>(a.m_tiles) * a.n_tiles) return false;
   const int64_t per = static_cast<int64_t>(GROUP_M) * a.n_tiles;
   const int first = static_cast<int>(t / per) * GROUP_M;
   const int rows = min(GROUP_M, a.m_tiles - first);
   const int in = static_cast<int>(t - (t / per) * per);
-  m = first + in % rows;
-  n = in / rows;
+  o.m = first + in % rows;
+  o.n = in / rows;
+  return true;
 }
 
-template <typename OUT> struct Piece;      // 16 bytes of an output row
-template <> struct Piece<float> {
-  static constexpr int N = 4;
-  __device__ static void add(float (&y)[4], uint4 r) {
-    y[0] += __uint_as_float(r.x);
-    y[1] += __uint_as_float(r.y);
-    y[2] += __uint_as_float(r.z);
-    y[3] += __uint_as_float(r.w);
+// K blocks of one accumulation: all, or for fp32 outputs equal segments of at most F32_SEGMENT.
+template <bool SEGMENTED>
+__device__ __forceinline__ int segment_blocks(const Item& it) {
+  const int blocks = it.kb1 - it.kb0;
+  if (!SEGMENTED) return blocks;
+  const int n = (blocks + F32_SEGMENT - 1) / F32_SEGMENT;
+  return (blocks + 2 * n - 1) / (2 * n) * 2;   // whole ring stages
+}
+
+// Barrier of the epilogue warps that tells whether `ok` holds in all of them.
+__device__ __forceinline__ bool epilogue_all(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(ok ? 1u : 0u), "n"(32 * EPI_WARPS)
+      : "memory");
+  return all != 0;
+}
+
+// 64 bytes of a row, 16 words, to global memory.
+__device__ __forceinline__ void store64(void* p, int align, const uint32_t (&w)[16]) {
+  if (align == 32) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<char*>(p) + 32 * h),
+                   "r"(w[8 * h]), "r"(w[8 * h + 1]), "r"(w[8 * h + 2]), "r"(w[8 * h + 3]), "r"(w[8 * h + 4]),
+                   "r"(w[8 * h + 5]), "r"(w[8 * h + 6]), "r"(w[8 * h + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+      static_cast<uint4*>(p)[h] = make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
   }
-  __device__ static uint4 pack(const float (&y)[4]) {
-    return make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]),
-                      __float_as_uint(y[3]));
+}
+
+template <typename OUT> struct Row64;      // CW values as 16 words
+template <> struct Row64<float> {
+  static constexpr int CW = 16;
+  __device__ __forceinline__ static void add(float (&z)[16], const uint32_t (&w)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] += __uint_as_float(w[i]);
+  }
+  __device__ __forceinline__ static void pack(const float (&z)[16], uint32_t (&w)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(z[i]);
   }
 };
-template <> struct Piece<__nv_bfloat16> {
-  static constexpr int N = 8;
-  __device__ static void add(float (&y)[8], uint4 r) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+template <> struct Row64<__nv_bfloat16> {
+  static constexpr int CW = 32;
+  __device__ __forceinline__ static void add(float (&z)[32], const uint32_t (&w)[16]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      y[2 * i] += __uint_as_float(w[i] << 16);
-      y[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < 16; ++i) {
+      z[2 * i] += __uint_as_float(w[i] << 16);
+      z[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
     }
   }
-  __device__ static uint4 pack(const float (&y)[8]) {
-    return make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                      pack_bf16x2(y[6], y[7]));
+  __device__ __forceinline__ static void pack(const float (&z)[32], uint32_t (&w)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(z[2 * i], z[2 * i + 1]);
   }
 };
 
-// Element e of row r in a swizzled staging block.
+// The 16-byte piece j of row r of a staging block (32 rows of 64 bytes), swizzled so that the
+// lanes' row accesses do not collide.
+__device__ __forceinline__ uint4* staged_piece(uint8_t* blk, int r, int j) {
+  return reinterpret_cast<uint4*>(blk + r * 64 + ((j ^ ((r >> 1) & 3)) * 16));
+}
 template <typename OUT>
 __device__ __forceinline__ OUT* staged(uint8_t* blk, int r, int e) {
-  constexpr int N = Piece<OUT>::N;
-  return reinterpret_cast<OUT*>(blk + r * 128 + (((e / N) ^ (r & 7)) * 16)) + e % N;
+  constexpr int N = 16 / static_cast<int>(sizeof(OUT));
+  return reinterpret_cast<OUT*>(staged_piece(blk, r, e / N)) + e % N;
 }
 
-template <bool A_MN, bool B_MN, typename OUT>
+// A warp's 32 rows of one step: lane l holds row l in w; rows x cols of them exist, ld elements
+// apart from p on.  Called by the whole warp.  Element by element through the staging block, the
+// lanes along the rows; whole aligned steps are stored straight from the registers.
+template <typename OUT>
+__device__ __forceinline__ void load_rows(const OUT* p, int64_t ld, int rows, int cols, int lane, uint8_t* blk,
+                                          uint32_t (&w)[16]) {
+  constexpr int CW = Row64<OUT>::CW;
+  __syncwarp();
+  for (int i = lane; i < rows * CW; i += 32) {
+    const int r = i / CW, e = i % CW;
+    if (e < cols) *staged<OUT>(blk, r, e) = p[r * ld + e];
+  }
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint4 u = *staged_piece(blk, lane, j);
+    w[4 * j] = u.x;
+    w[4 * j + 1] = u.y;
+    w[4 * j + 2] = u.z;
+    w[4 * j + 3] = u.w;
+  }
+}
+template <typename OUT>
+__device__ __forceinline__ void store_rows(OUT* p, int64_t ld, int align, int rows, int cols, int lane,
+                                           uint8_t* blk, const uint32_t (&w)[16]) {
+  constexpr int CW = Row64<OUT>::CW;
+  if (align != 0 && cols == CW) {
+    if (lane < rows) store64(p + lane * ld, align, w);
+    return;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *staged_piece(blk, lane, j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  __syncwarp();
+  for (int i = lane; i < rows * CW; i += 32) {
+    const int r = i / CW, e = i % CW;
+    if (e < cols) p[r * ld + e] = *staged<OUT>(blk, r, e);
+  }
+  fence_proxy_async_smem();   // the block may take a TMA load next
+  __syncwarp();
+}
+
+template <bool A_MN, bool B_MN, typename OUT, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                       const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmR,
-                       const __grid_constant__ CUtensorMap tmP, const Args args) {
+                       const __grid_constant__ CUtensorMap tmR, const Args args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -122,14 +257,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* never = const_cast<int*>(abort_flag) + 1;
+  int* last_part = never + 1;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const uint32_t smem_base = smem_u32(smem);
-  const int64_t pair_id = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
-  const int64_t tiles = static_cast<int64_t>(args.m_tiles) * args.n_tiles;
-  const int k_blocks = (args.K + BK - 1) / BK;
+  const int pair_id = static_cast<int>(blockIdx.x >> 1), n_pairs = static_cast<int>(gridDim.x >> 1);
+  constexpr bool SEGMENTED = sizeof(OUT) == 4;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -138,7 +273,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&tfull[b]), 1);
-      mbar_init(smem_u32(&tempty[b]), 2 * EPI_WARPS);
+      mbar_init(smem_u32(&tempty[b]), 2 * EPI_WARPS);   // of both CTAs
     }
     for (int i = 0; i < 2 * EPI_WARPS; ++i) mbar_init(smem_u32(&rbar[i]), 1);
     mbar_init(smem_u32(drain), 1);
@@ -157,6 +292,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
 
+  if (warp < EPI_WARP0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<SEGMENTED>::OTHER));
   if (warp == 0) {
     // ---------------------------------------------------------- producer (both CTAs)
     if (lane == 0) {
@@ -166,18 +303,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int s = 0; s < STAGES; ++s) issued_parity[s] = -1;
       bool ok = true;
-      for (int64_t t = pair_id; ok && t < tiles; t += n_pairs) {
-        int m, n;
-        tile_at(args, t, m, n);
-        const int m0 = m * BM + static_cast<int>(rank) * HALF;
-        const int n0 = n * BN + static_cast<int>(rank) * HALF;
-        for (int kb = 0; kb < k_blocks; kb += 2) {
+      Item it;
+      for (int i = 0; ok && item_at(args, pair_id, n_pairs, i, it); ++i) {
+        const int m0 = it.m * BM + static_cast<int>(rank) * HALF;
+        const int n0 = it.n * BN + static_cast<int>(rank) * HALF;
+        for (int kb = it.kb0; kb < it.kb1; kb += 2) {
           if (!mbar_wait_bounded(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, args.status,
                                  kWaitLimitNs)) {
             ok = false;
             break;
           }
-          const int subs = min(2, k_blocks - kb);
+          const int subs = min(2, it.kb1 - kb);
           const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
           if (leader) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * subs * 2 * BLOCK_BYTES);
           for (int u = 0; u < subs; ++u) {
@@ -215,179 +351,302 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      int64_t local = 0;
-      for (int64_t t = pair_id; ok && t < tiles; t += n_pairs, ++local) {
-        const int buf = static_cast<int>(local & 1);
-        const uint32_t use = static_cast<uint32_t>(local >> 1);
-        if (!mbar_wait_bounded(smem_u32(&tempty[buf]), (use & 1u) ^ 1u, abort_flag, args.status,
-                               kWaitLimitNs)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d_acc = tmem_base + static_cast<uint32_t>(buf * BN);
-        for (int kb = 0; kb < k_blocks; kb += 2) {
-          if (!mbar_wait_bounded(smem_u32(&full[stage]), phase, abort_flag, args.status,
-                                 kWaitLimitNs)) {
-            ok = false;
-            break;
-          }
+      uint32_t fill = 0;                     // TMEM buffers filled
+      Item it;
+      for (int i = 0; ok && item_at(args, pair_id, n_pairs, i, it); ++i) {
+        const int seg = segment_blocks<SEGMENTED>(it);
+        for (int s0 = it.kb0; ok && s0 < it.kb1; s0 += seg, ++fill) {
+          const int s1 = min(s0 + seg, it.kb1);
+          const uint32_t d_acc = tmem_base + (fill & 1) * BN;
+          ok = mbar_wait_bounded(smem_u32(&tempty[fill & 1]), ((fill >> 1) & 1u) ^ 1u, abort_flag, args.status,
+                                 kWaitLimitNs);
           tc_fence_after();
-          const int subs = min(2, k_blocks - kb);
-          for (int u = 0; u < subs; ++u) {
-            const uint32_t sA = smem_base + stage * STAGE_BYTES + u * 2 * BLOCK_BYTES;
-            const uint32_t sB = sA + BLOCK_BYTES;
+          for (int kb = s0; ok && kb < s1; kb += 2) {
+            ok = mbar_wait_bounded(smem_u32(&full[stage]), phase, abort_flag, args.status, kWaitLimitNs);
+            if (!ok) break;
+            tc_fence_after();
+            const int subs = min(2, it.kb1 - kb);
+            for (int u = 0; u < subs; ++u) {
+              const uint32_t sA = smem_base + stage * STAGE_BYTES + u * 2 * BLOCK_BYTES;
+              const uint32_t sB = sA + BLOCK_BYTES;
 #pragma unroll
-            for (int j = 0; j < BK / 16; ++j) {
-              const uint64_t ad = A_MN ? sw128_mnmajor_desc(sA + j * 2048) : sw128_kmajor_desc(sA) + 2 * j;
-              const uint64_t bd = B_MN ? sw128_mnmajor_desc(sB + j * 2048) : sw128_kmajor_desc(sB) + 2 * j;
-              tc_mma_bf16_pair(d_acc, ad, bd, idesc, (kb > 0 || u > 0 || j > 0) ? 1u : 0u);
+              for (int j = 0; j < BK / 16; ++j) {
+                const uint64_t ad = A_MN ? sw128_mnmajor_desc(sA + j * 2048) : sw128_kmajor_desc(sA) + 2 * j;
+                const uint64_t bd = B_MN ? sw128_mnmajor_desc(sB + j * 2048) : sw128_kmajor_desc(sB) + 2 * j;
+                tc_mma_bf16_pair(d_acc, ad, bd, idesc, (kb > s0 || u > 0 || j > 0) ? 1u : 0u);
+              }
             }
+            tc_commit_pair(smem_u32(&empty[stage]), 0x3);
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
           }
-          tc_commit_pair(smem_u32(&empty[stage]), 0x3);
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          if (ok) tc_commit_pair(smem_u32(&tfull[fill & 1]), 0x3);
         }
-        if (!ok) break;
-        tc_commit_pair(smem_u32(&tfull[buf]), 0x3);
       }
       if (!ok) {
         tc_commit_pair(smem_u32(drain), 0x1);
         mbar_wait_bounded(smem_u32(drain), 0, never, nullptr, kDrainLimitNs);
       }
     }
+  }
   } else {
     // ---------------------------------------------------------- epilogue (both CTAs)
-    constexpr int CW = 128 / static_cast<int>(sizeof(OUT));   // columns of a staging block
-    constexpr int CHUNKS = BN / CW;
-    constexpr int PN = Piece<OUT>::N;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<SEGMENTED>::EPI));
+    constexpr int CW = Row64<OUT>::CW;       // columns of a step
+    constexpr int STEPS = WARP_COLS / CW;
     const int q = warp & 3;                  // TMEM lanes of this warp
-    uint8_t* blk0 = epi + (warp - 2) * 2 * STAGING_BYTES;
-    uint64_t* bars = rbar + 2 * (warp - 2);
-    const bool res = args.residual != nullptr, pre = args.pre != nullptr;
-    uint32_t rphase = 0, inflight = 0;      // a bit per staging block; residual blocks on their way
-    int64_t local = 0;
+    const int half = (warp - EPI_WARP0) >> 2;        // its columns
+    uint8_t* blk = epi + (warp - EPI_WARP0) * 2 * STAGING_BYTES;
+    uint64_t* bars = rbar + 2 * (warp - EPI_WARP0);
+    uint32_t loads = 0, reads = 0;           // residual blocks asked for and read, over all tiles
+    const bool res = args.residual != nullptr;
+    uint32_t fill = 0;
     bool ok = true;
-    for (int64_t t = pair_id; ok && t < tiles; t += n_pairs, ++local) {
-      int m, n;
-      tile_at(args, t, m, n);
-      const int buf = static_cast<int>(local & 1);
-      const uint32_t use = static_cast<uint32_t>(local >> 1);
-      const int64_t row0 = static_cast<int64_t>(m) * BM + rank * HALF + q * 32;
-      const int rows = static_cast<int>(min(static_cast<int64_t>(32), args.M - row0));   // <= 0: none
-      // Residual block of chunk c into staging block b, once the stores from it have been read.
-      auto load_residual = [&](int c, int b) {
-        inflight |= 1u << b;
+    Item it;
+    // a part of a cut tile is taken up even after a failure: the epilogue warps agree there
+    for (int i = 0; item_at(args, pair_id, n_pairs, i, it) && (ok || it.parts > 1); ++i) {
+      const int64_t row0 = static_cast<int64_t>(it.m) * BM + rank * HALF + q * 32;
+      const int col0 = it.n * BN + half * WARP_COLS;
+      // rows and columns of this warp's block; none where it lies past the output
+      const int rows = col0 < args.N ? static_cast<int>(min(static_cast<int64_t>(32), args.M - row0)) : 0;
+      const OUT* rrow = static_cast<const OUT*>(args.residual) + row0 * args.ldr + col0;
+      const int steps = rows > 0 ? min(STEPS, (args.N - col0 + CW - 1) / CW) : 0;
+      const bool tma_res = res && args.al_r != 0;
+      // the residual block of step c into the buffer of its turn
+      auto load_residual = [&](int c) {
+        if (c >= steps) return;
         if (lane == 0) {
-          bulk_wait_read<0>();
-          mbar_arrive_expect_tx(smem_u32(&bars[b]), STAGING_BYTES);
-          tma_load_2d(smem_u32(blk0 + b * STAGING_BYTES), &tmR, n * BN + c * CW,
-                      static_cast<int32_t>(row0), smem_u32(&bars[b]));
+          const uint32_t bar = smem_u32(&bars[loads & 1]);
+          mbar_arrive_expect_tx(bar, STAGING_BYTES);
+          tma_load_2d(smem_u32(blk + (loads & 1) * STAGING_BYTES), &tmR, col0 + c * CW,
+                      static_cast<int32_t>(row0), bar);
         }
+        ++loads;
       };
-      const bool tma_res = res && args.tma_r && rows > 0;
-      if (tma_res) load_residual(0, 0);
-      bool ready = true;
-      if (lane == 0)
-        ready = mbar_wait_bounded(smem_u32(&tfull[buf]), use & 1u, abort_flag, args.status, kWaitLimitNs);
-      ok = __shfl_sync(0xffffffffu, ready ? 1 : 0, 0) != 0;
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                             static_cast<uint32_t>(buf * BN);
-      if (rows > 0) {
-#pragma unroll 1
-        for (int c = 0; c < CHUNKS; ++c) {
-          const int col = n * BN + c * CW;
-          if (col >= args.N) break;
-          const int cols = min(CW, args.N - col);
-          // y uses the two blocks in turn, or block 0 beside a pre in block 1
-          const int yb = pre ? 0 : c & 1;
-          uint8_t* yblk = blk0 + yb * STAGING_BYTES;
-          uint8_t* pblk = blk0 + STAGING_BYTES;
-          uint32_t va[32], vb[32];
-          if (CW == 64)
-            tmem_ld32x2(taddr + c * CW, taddr + c * CW + 32, va, vb);
-          else
-            tmem_ld32(taddr + c * CW, va);
-          if (tma_res) {
-            if (pre) {
-              if (c > 0) load_residual(c, 0);
-            } else if (c + 1 < CHUNKS && col + CW < args.N) {
-              load_residual(c + 1, (c + 1) & 1);
+      if (tma_res && it.parts == 1) {
+        load_residual(0);
+        load_residual(1);
+      }
+      // Waits for the next TMEM buffer; its columns of this warp start at taddr.
+      uint32_t taddr = 0;
+      auto wait_fill = [&]() {
+        bool ready = true;
+        if (lane == 0)
+          ready = mbar_wait_bounded(smem_u32(&tfull[fill & 1]), (fill >> 1) & 1u, abort_flag, args.status,
+                                    kWaitLimitNs);
+        ready = __shfl_sync(0xffffffffu, ready ? 1 : 0, 0) != 0;
+        tc_fence_after();
+        taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                static_cast<uint32_t>((fill & 1) * BN + half * WARP_COLS);
+        return ready;
+      };
+      auto release_fill = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[fill & 1]), 0));
+        ++fill;
+      };
+      // where this warp's lane of a pair's partial sums starts (32 groups of four columns)
+      auto slot = [&](int pair) {
+        return reinterpret_cast<float4*>(args.scratch) + static_cast<size_t>(pair) * (BM * BN / 4) +
+               (static_cast<size_t>(rank) * EPI_WARPS + (warp - EPI_WARP0)) * (WARP_COLS / 4) * 32 + lane;
+      };
+      float acc[SEGMENTED ? WARP_COLS : 1];
+      // Leaves this part of a cut tile in scratch memory, four columns of a row per access; the
+      // last CTA to come puts the parts' sum in this part's place in TMEM.
+      enum { kFailed, kNotLast, kJoined };
+      auto join = [&]() -> int {
+        float4* mine = slot(pair_id);
+        if (ok) {
+          if (SEGMENTED) {
+#pragma unroll
+            for (int e = 0; e < WARP_COLS; e += 4) {
+              float f[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) f[k] = acc[(e + k) % (SEGMENTED ? WARP_COLS : 1)];
+              __stcg(mine + e / 4 * 32, make_float4(f[0], f[1], f[2], f[3]));
             }
-            const bool here =
-                mbar_wait_bounded(smem_u32(&bars[yb]), (rphase >> yb) & 1u, abort_flag, args.status, kWaitLimitNs);
-            ok = __all_sync(0xffffffffu, here);
-            if (!ok) break;
-            rphase ^= 1u << yb;
-            inflight &= ~(1u << yb);
           } else {
-            // the stores that left from the blocks about to be written have been read
-            if (lane == 0) {
-              if (pre) bulk_wait_read<0>(); else bulk_wait_read<1>();
+#pragma unroll 1
+            for (int c = 0; c < WARP_COLS; c += 32) {
+              uint32_t v[32];
+              tmem_ld32(taddr + c, v);
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                __stcg(mine + (c + e) / 4 * 32, make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]),
+                                                            __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])));
             }
-            __syncwarp();
-            if (res) {
-              const OUT* r = static_cast<const OUT*>(args.residual) + row0 * args.ldr + col;
-              for (int i = lane; i < rows * CW; i += 32) {
-                const int rr = i / CW, e = i % CW;
-                if (e < cols) *staged<OUT>(yblk, rr, e) = r[rr * args.ldr + e];
+          }
+        }
+        __threadfence();
+        if (!epilogue_all(ok)) return kFailed;
+        if (warp == EPI_WARP0 && lane == 0) {
+          // byte 2 cut + rank of the counts: parts that have arrived
+          const int b = 2 * it.cut + static_cast<int>(rank);
+          const unsigned before = (atomicAdd(args.tickets + b / 4, 1u << (8 * (b % 4))) >> (8 * (b % 4))) & 0xffu;
+          const bool last = static_cast<int>(before) == it.parts - 1;
+          if (last) atomicSub(args.tickets + b / 4, static_cast<unsigned>(it.parts) << (8 * (b % 4)));
+          *last_part = last ? 1 : 0;
+          __threadfence();
+        }
+        epilogue_all(true);
+        const bool last = *reinterpret_cast<volatile int*>(last_part) != 0;
+        epilogue_all(true);   // read by all before the next part writes it
+        if (!last) return kNotLast;
+        __threadfence();
+#pragma unroll 1
+        for (int c = 0; c < WARP_COLS; c += 32) {
+          float sum[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) sum[e] = 0.f;
+#pragma unroll 4
+          for (int k = 0; k < it.parts; ++k) {
+            const float4* p = slot(it.cut * it.parts + k) + c / 4 * 32;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 w = __ldcg(p + e * 32);
+              sum[4 * e] += w.x;
+              sum[4 * e + 1] += w.y;
+              sum[4 * e + 2] += w.z;
+              sum[4 * e + 3] += w.w;
+            }
+          }
+          uint32_t v[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(sum[e]);
+          tmem_st32(taddr + c, v);
+        }
+        return kJoined;
+      };
+      int joined = it.parts > 1 ? kNotLast : kJoined;
+      if (SEGMENTED) {
+        // segment after segment, and in the joining CTA of a cut tile the parts' sum once more
+        const int seg = segment_blocks<SEGMENTED>(it);
+        int s0 = it.kb0;
+        bool again = true;
+        while (again) {
+          if (s0 < it.kb1 && ok) ok = wait_fill();
+          if (!ok && it.parts == 1) break;
+          const bool first = s0 == it.kb0 || s0 >= it.kb1;
+          if (ok) {
+#pragma unroll
+            for (int k = 0; k < WARP_COLS; k += 64) {
+              uint32_t v[64];
+              tmem_ld64(taddr + k, v);
+#pragma unroll
+              for (int e = 0; e < 64; ++e) {
+                float& sum = acc[(k + e) % (SEGMENTED ? WARP_COLS : 1)];
+                sum = (first ? 0.f : sum) + __uint_as_float(v[e]);
               }
-              __syncwarp();
             }
           }
-#pragma unroll
-          for (int j = 0; j < CW / PN; ++j) {
-            float z[PN];
-#pragma unroll
-            for (int e = 0; e < PN; ++e) {
-              const int i = j * PN + e;
-              z[e] = __uint_as_float(i < 32 ? va[i & 31] : vb[i & 31]);
-              if (args.bias != nullptr && i < cols) z[e] += __ldg(args.bias + col + i);
-            }
-            const int off = lane * 128 + ((j ^ (lane & 7)) * 16);
-            if (pre) *reinterpret_cast<uint4*>(pblk + off) = Piece<OUT>::pack(z);
-            if (args.act != MOE_ACT_NONE) {
-#pragma unroll
-              for (int e = 0; e < PN; ++e) z[e] = act_value(z[e], args.act);
-            }
-            if (res) Piece<OUT>::add(z, *reinterpret_cast<const uint4*>(yblk + off));
-            *reinterpret_cast<uint4*>(yblk + off) = Piece<OUT>::pack(z);
+          const bool summed = s0 >= it.kb1;
+          s0 += seg;
+          again = ok && !summed && s0 < it.kb1;
+          if (!again && !summed && it.parts > 1) {
+            joined = join();
+            ok = joined != kFailed;
+            again = joined == kJoined;
+            s0 = it.kb1;
+            if (again) continue;   // the buffer still holds the sum to read
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0 && (args.tma_c || (pre && args.tma_pre))) {
-            if (args.tma_c) tma_store_2d(&tmC, col, static_cast<int32_t>(row0), smem_u32(yblk));
-            if (pre && args.tma_pre) tma_store_2d(&tmP, col, static_cast<int32_t>(row0), smem_u32(pblk));
-            bulk_commit();
-          }
-          if (!args.tma_c) {
-            OUT* y = static_cast<OUT*>(args.C) + row0 * args.ldc + col;
-            for (int i = lane; i < rows * CW; i += 32) {
-              const int rr = i / CW, e = i % CW;
-              if (e < cols) y[rr * args.ldc + e] = *staged<OUT>(yblk, rr, e);
-            }
-          }
-          if (pre && !args.tma_pre) {
-            OUT* p = static_cast<OUT*>(args.pre) + row0 * args.N + col;
-            for (int i = lane; i < rows * CW; i += 32) {
-              const int rr = i / CW, e = i % CW;
-              if (e < cols) p[rr * static_cast<int64_t>(args.N) + e] = *staged<OUT>(pblk, rr, e);
-            }
-          }
-          __syncwarp();   // the staging blocks have been read
+          if (ok) release_fill();
+        }
+      } else {
+        if (ok) ok = wait_fill();
+        if (it.parts > 1) {
+          joined = join();
+          ok = joined != kFailed;
+          if (joined == kNotLast) release_fill();
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[buf]), 0));
+      if (!ok) break;
+      if (joined == kNotLast) continue;
+      if (tma_res && it.parts > 1) {
+        load_residual(0);
+        load_residual(1);
+      }
+      // one step of CW columns: z from the accumulators on
+      auto finish = [&](int c, float (&z)[CW]) {
+        const int col = col0 + c * CW, cols = min(CW, args.N - col);
+        uint32_t rw[16];
+        if (tma_res) {
+          const uint32_t b = reads & 1;
+          const bool here = mbar_wait_bounded(smem_u32(&bars[b]), (reads >> 1) & 1u, abort_flag, args.status, kWaitLimitNs);
+          ok = __all_sync(0xffffffffu, here) && ok;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 u = *staged_piece(blk + b * STAGING_BYTES, lane, j);
+            rw[4 * j] = u.x;
+            rw[4 * j + 1] = u.y;
+            rw[4 * j + 2] = u.z;
+            rw[4 * j + 3] = u.w;
+          }
+          // The buffer's next TMA load must not overtake these reads, which can wait behind stores.
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (ok) {
+            ++reads;
+            load_residual(c + 2);
+          }
+        } else if (res) {
+          load_rows<OUT>(rrow + c * CW, args.ldr, rows, cols, lane, blk, rw);
+        }
+        if (args.bias != nullptr) {
+          if (args.bias16 && cols == CW) {
+#pragma unroll
+            for (int e = 0; e < CW; e += 4) {
+              const float4 b4 = __ldg(reinterpret_cast<const float4*>(args.bias + col + e));
+              z[e] += b4.x;
+              z[e + 1] += b4.y;
+              z[e + 2] += b4.z;
+              z[e + 3] += b4.w;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < CW; ++e)
+              if (e < cols) z[e] += __ldg(args.bias + col + e);
+          }
+        }
+        uint32_t w[16];
+        if (args.pre != nullptr) {
+          Row64<OUT>::pack(z, w);
+          store_rows<OUT>(static_cast<OUT*>(args.pre) + row0 * args.N + col, args.N, args.al_pre, rows, cols, lane, blk, w);
+        }
+#pragma unroll
+        for (int e = 0; e < CW; ++e) z[e] = act_value<ACT>(z[e]);
+        if (res) Row64<OUT>::add(z, rw);
+        Row64<OUT>::pack(z, w);
+        store_rows<OUT>(static_cast<OUT*>(args.C) + row0 * args.ldc + col, args.ldc, args.al_c, rows, cols, lane, blk, w);
+      };
+      if (SEGMENTED) {
+#pragma unroll
+        for (int c = 0; c < STEPS; ++c) {
+          if (c < steps && ok) {
+            float z[CW];
+#pragma unroll
+            for (int e = 0; e < CW; ++e) z[e] = acc[(c * CW + e) % (SEGMENTED ? WARP_COLS : 1)];
+            finish(c, z);
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < STEPS; c += 2) {
+          uint32_t v[64];
+          tmem_ld64(taddr + c * 32, v);
+          if (c + 2 == STEPS) release_fill();   // the last read of the buffer
+          float z[CW];
+#pragma unroll
+          for (int e = 0; e < CW; ++e) z[e] = __uint_as_float(v[e % 32]);
+          if (c < steps && ok) finish(c, z);
+#pragma unroll
+          for (int e = 0; e < CW; ++e) z[e] = __uint_as_float(v[32 + e % 32]);
+          if (c + 1 < steps && ok) finish(c + 1, z);
+        }
+      }
     }
-    if (lane == 0) {
-      for (int b = 0; b < 2; ++b)
-        if ((inflight >> b) & 1u)   // only after a wait ran out
-          mbar_wait_bounded(smem_u32(&bars[b]), (rphase >> b) & 1u, never, nullptr, kDrainLimitNs);
-      bulk_wait_all();   // the output blocks are written
-    }
+    if (lane == 0)   // blocks still on their way after a failed wait
+      for (; reads != loads; ++reads)
+        mbar_wait_bounded(smem_u32(&bars[reads & 1]), (reads >> 1) & 1u, never, nullptr, kDrainLimitNs);
   }
 
   __syncwarp();
@@ -401,21 +660,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
 constexpr size_t kSmemBytes = 1024 + STAGES * STAGE_BYTES + EPI_BYTES + 8 * (2 * STAGES + 4 + 2 * EPI_WARPS + 1) + 32;
 
-bool rows16(const void* p, int64_t ld, int32_t dtype) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % (dtype == MOE_F32 ? 4 : 8) == 0;
+// Parts to cut the `rest` tiles of a partial round into, of `stages` ring stages (two K blocks,
+// about half a microsecond) each: 1, or the number that saves most.  Joining s parts costs
+// about as much as kJoin + kJoinPart s stages (they pass through scratch memory).
+constexpr int kJoin = 12, kJoinPart = 4, kMaxParts = 8;
+int cut_parts(int64_t rest, int64_t pairs, int64_t stages) {
+  int best = 1;
+  int64_t gain = 0;
+  for (int s = 2; s <= kMaxParts && rest * s <= pairs && 2 * s <= stages; ++s) {
+    const int64_t g = stages - (stages + s - 1) / s - kJoin - kJoinPart * s;
+    if (g > gain) {
+      gain = g;
+      best = s;
+    }
+  }
+  return best;
 }
 
-template <bool A_MN, bool B_MN, typename OUT>
+// Bytes (32, 16 or 0 for less) that rows ld elements apart are aligned to.
+int32_t row_alignment(const void* p, int64_t ld, size_t elem) {
+  const uintptr_t v = reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * elem);
+  return v % 32 == 0 ? 32 : v % 16 == 0 ? 16 : 0;
+}
+
+template <bool A_MN, bool B_MN, typename OUT, int ACT>
 cudaError_t launch_typed(const LinearGemm& g, cudaStream_t s) {
-  constexpr int32_t dt = sizeof(OUT) == 4 ? MOE_F32 : MOE_BF16;
-  constexpr uint32_t cw = 128 / sizeof(OUT);
   Args a{};
   a.M = static_cast<int32_t>(g.M);
   a.N = g.N;
   a.K = g.K;
   a.m_tiles = static_cast<int32_t>((g.M + BM - 1) / BM);
   a.n_tiles = (g.N + BN - 1) / BN;
-  a.act = g.act;
   a.bias = g.bias;
   a.residual = g.residual;
   a.pre = g.pre;
@@ -423,39 +698,60 @@ cudaError_t launch_typed(const LinearGemm& g, cudaStream_t s) {
   a.ldr = g.ldr;
   a.ldc = g.ldc;
   a.status = g.status;
-  a.tma_c = rows16(g.C, g.ldc, dt);
-  a.tma_r = g.residual && rows16(g.residual, g.ldr, dt);
-  a.tma_pre = g.pre && rows16(g.pre, g.N, dt);
-  CUtensorMap mA, mB, mC, mR, mP;
+  a.al_c = row_alignment(g.C, g.ldc, sizeof(OUT));
+  a.al_r = row_alignment(g.residual, g.ldr, sizeof(OUT));
+  a.al_pre = row_alignment(g.pre, g.N, sizeof(OUT));
+  if (a.al_c == 0 || a.al_pre == 0) a.al_r = 0;   // the staging block is the residual's first buffer
+  a.bias16 = (reinterpret_cast<uintptr_t>(g.bias) & 15u) == 0;
+  CUtensorMap mA, mB;
   const uint64_t M = static_cast<uint64_t>(g.M), N = g.N, K = g.K;
   if (!(A_MN ? make_strided_map(&mA, MOE_BF16, g.A, M, K, g.lda, 64, BK)
              : make_strided_map(&mA, MOE_BF16, g.A, K, M, g.lda, BK, HALF)) ||
       !(B_MN ? make_strided_map(&mB, MOE_BF16, g.B, N, K, g.ldb, 64, BK)
              : make_strided_map(&mB, MOE_BF16, g.B, K, N, g.ldb, BK, HALF)))
     return cudaErrorInvalidValue;
-  mC = mR = mP = mA;
-  if ((a.tma_c && !make_strided_map(&mC, dt, g.C, N, M, g.ldc, cw, 32)) ||
-      (a.tma_r && !make_strided_map(&mR, dt, g.residual, N, M, g.ldr, cw, 32)) ||
-      (a.tma_pre && !make_strided_map(&mP, dt, g.pre, N, M, N, cw, 32)))
+  CUtensorMap mR = mA;
+  if (g.residual && a.al_r != 0 &&
+      !make_strided_map(&mR, sizeof(OUT) == 4 ? MOE_F32 : MOE_BF16, g.residual, N, M, g.ldr, 64 / sizeof(OUT), 32, 64))
     return cudaErrorInvalidValue;
-  auto kern = linear_pair_kernel<A_MN, B_MN, OUT>;
+  auto kern = linear_pair_kernel<A_MN, B_MN, OUT, ACT>;
   const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), kSmemBytes);
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
-  const int64_t pairs = std::min<int64_t>(tiles, std::max(1, device_sm_count() / 2));
-  kern<<<static_cast<unsigned>(2 * pairs), THREADS, kSmemBytes, s>>>(mA, mB, mC, mR, mP, a);
+  const int64_t most = std::min(kMaxPairs, std::max(1, device_sm_count() / 2));
+  int64_t pairs = std::min(tiles, most);
+  a.scratch = g.scratch;
+  a.tickets = g.tickets;
+  const int64_t rest = tiles % most;
+  a.parts = rest > 0 ? cut_parts(rest, most, ((g.K + BK - 1) / BK + 1) / 2) : 1;
+  if (a.parts > 1) {
+    a.cut_tiles = static_cast<int32_t>(rest);
+    pairs = tiles > rest ? most : rest * a.parts;
+  }
+  kern<<<static_cast<unsigned>(2 * pairs), THREADS, kSmemBytes, s>>>(mA, mB, mR, a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
+namespace {
+template <typename OUT>
+cudaError_t launch_forward(const LinearGemm& g, cudaStream_t s) {
+#define MOE_CALL(ACT) launch_typed<false, false, OUT, ACT>(g, s)
+  MOE_DISPATCH_ACT(g.act, MOE_CALL)
+#undef MOE_CALL
+}
+}  // namespace
+
 cudaError_t launch_linear_pair(const LinearGemm& g, cudaStream_t s) {
   const bool f32 = g.out_dtype == MOE_F32;
   if (g.a_mn)
-    return f32 ? launch_typed<true, true, float>(g, s) : launch_typed<true, true, __nv_bfloat16>(g, s);
+    return f32 ? launch_typed<true, true, float, MOE_ACT_NONE>(g, s)
+               : launch_typed<true, true, __nv_bfloat16, MOE_ACT_NONE>(g, s);
   if (g.b_mn)
-    return f32 ? launch_typed<false, true, float>(g, s) : launch_typed<false, true, __nv_bfloat16>(g, s);
-  return f32 ? launch_typed<false, false, float>(g, s) : launch_typed<false, false, __nv_bfloat16>(g, s);
+    return f32 ? launch_typed<false, true, float, MOE_ACT_NONE>(g, s)
+               : launch_typed<false, true, __nv_bfloat16, MOE_ACT_NONE>(g, s);
+  return f32 ? launch_forward<float>(g, s) : launch_forward<__nv_bfloat16>(g, s);
 }
 
 }  // namespace moe

@@ -6,8 +6,13 @@
 // the depth: each accumulates its range of K in its own TMEM, writes the partial sums to its
 // shared memory, and after a cluster barrier each CTA adds the partials of its share of the
 // tokens in rank order over distributed shared memory (a fixed order, so every call gives the
-// same bits, and no second launch or global scratch).  The epilogue has one thread per
-// feature: its loads and stores run along the rows of y, whatever their alignment.
+// same bits, and no second launch or global scratch).  There a warp takes a token and a lane
+// four neighbouring features, several tokens at a time, so that the remote reads, the
+// residual's reads and the stores of one group overlap.
+//
+// For fp32 outputs the sum of a CTA is taken in segments of at most 512 deep (as TMEM allows),
+// each in its own TMEM columns, and added in rounded fp32: the tensor core's additions drop
+// bits, an error that grows with the length of a sum.
 //
 // The ring holds one 64-wide K block per stage (16 KB of W, 128 NT bytes of x).  Up to NT = 64
 // it takes about 100 KB, so two CTAs share an SM and one streams while the other starts or ends.
@@ -15,6 +20,7 @@
 // Every wait is bounded; a wait that runs out records MOE_ERR_TIMEOUT and the CTA waits for
 // what it issued before it frees its TMEM.
 #include <algorithm>
+#include <type_traits>
 
 #include "activation.cuh"
 #include "linear.h"
@@ -36,7 +42,8 @@ template <int NT> struct Shape {
   static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
   static constexpr size_t SMEM = 1024 + RING_BYTES + 8 * (2 * STAGES + 2) + 32;
   static constexpr int PER_SM = SMEM <= 113 * 1024 ? 2 : 1;
-  static constexpr uint32_t TMEM_COLS = NT < 32 ? 32 : NT;
+  // TMEM columns of one CTA: room for fp32 segments, half of the 512 where two CTAs share an SM
+  static constexpr int MAX_SEGMENTS = (PER_SM == 2 ? 256 : 512) / (NT < 32 ? 32 : NT);
   static_assert(NT * FM * 4 <= RING_BYTES, "the partial sums take the ring's place");
 };
 
@@ -44,7 +51,8 @@ struct Args {
   int32_t T, N, K;         // tokens, features, depth
   int32_t t_tiles;
   int32_t split;           // CTAs per cluster
-  int32_t act;
+  int32_t segments;        // TMEM accumulators of a CTA's depth range
+  uint32_t tmem_cols;
   const float* bias;
   const void* residual;
   void* pre;
@@ -53,22 +61,48 @@ struct Args {
   int32_t* status;
 };
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
-template <typename OUT>
-__device__ __forceinline__ void finish(const Args& a, int64_t t, int f, float acc, float bias) {
-  const float z = acc + bias;
-  if (a.pre) static_cast<OUT*>(a.pre)[t * a.N + f] = from_f32<OUT>(z);
-  float y = act_value(z, a.act);
-  if (a.residual) y += to_f32(static_cast<const OUT*>(a.residual)[t * a.ldr + f]);
-  static_cast<OUT*>(a.C)[t * a.ldc + f] = from_f32<OUT>(y);
-}
+// Four neighbouring output values of a lane.
+template <typename OUT> struct alignas(4 * sizeof(OUT)) Four {
+  OUT v[4];
+  __device__ Four() {}
+  __device__ explicit Four(const float (&z)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = from_f32<OUT>(z[e]);
+  }
+  using Word = typename std::conditional<sizeof(OUT) == 4, uint4, uint2>::type;
+  __device__ void load(const OUT* p, bool vec, int n) {
+    if (vec) {
+      *reinterpret_cast<Word*>(v) = *reinterpret_cast<const Word*>(p);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = e < n ? p[e] : from_f32<OUT>(0.f);
+    }
+  }
+  __device__ void store(OUT* p, bool vec, int n) const {
+    if (vec) {
+      *reinterpret_cast<Word*>(p) = *reinterpret_cast<const Word*>(v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < n) p[e] = v[e];
+    }
+  }
+  __device__ void add_to(float (&z)[4]) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z[e] += to_f32(v[e]);
+  }
+};
 
-template <int NT, typename OUT>
+template <int NT, typename OUT, int ACT>
 __global__ void __launch_bounds__(THREADS, Shape<NT>::PER_SM)
     linear_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                       const Args args) {
@@ -115,7 +149,7 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::PER_SM)
     fence_proxy_async_smem();
     for (int i = 0; i < S::STAGES && i < kbs; ++i) load(i);   // before the other warps are ready
   }
-  if (warp == 1) tmem_alloc(smem_u32(tmem_holder), S::TMEM_COLS);
+  if (warp == 1) tmem_alloc(smem_u32(tmem_holder), args.tmem_cols);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -145,7 +179,15 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::PER_SM)
     // ------------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(FM, NT);
+      constexpr int SEG_COLS = NT < 32 ? 32 : NT;
+      int seg = 0, seg_end = kbs / args.segments;   // segment g ends at (g + 1) kbs / segments
+      bool first = true;
       for (int i = 0; i < kbs; ++i) {
+        if (i == seg_end) {
+          ++seg;
+          seg_end = static_cast<int>(static_cast<int64_t>(kbs) * (seg + 1) / args.segments);
+          first = true;
+        }
         const int s = i % S::STAGES;
         if (!mbar_wait_bounded(smem_u32(&full[s]), (i / S::STAGES) & 1, abort_flag, args.status,
                                kWaitLimitNs)) {
@@ -156,8 +198,9 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::PER_SM)
         const uint32_t at = smem_base + s * S::STAGE_BYTES;
 #pragma unroll
         for (int j = 0; j < BK / 16; ++j)
-          tc_mma_bf16(tmem_base, sw128_kmajor_desc(at) + 2 * j, sw128_kmajor_desc(at + W_BYTES) + 2 * j,
-                      idesc, (i > 0 || j > 0) ? 1u : 0u);
+          tc_mma_bf16(tmem_base + static_cast<uint32_t>(seg * SEG_COLS), sw128_kmajor_desc(at) + 2 * j,
+                      sw128_kmajor_desc(at + W_BYTES) + 2 * j, idesc, (!first || j > 0) ? 1u : 0u);
+        first = false;
         tc_commit(smem_u32(&empty[s]));
       }
       if (ok) {
@@ -168,66 +211,96 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::PER_SM)
       }
     }
   } else {
-    // ------------------------------------------------------------------- epilogue
+    // ------------------------------------------- partial sums to shared memory
     ok = mbar_wait_bounded(smem_u32(tfull), 0, abort_flag, args.status, kWaitLimitNs);
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
       tc_fence_after();
+      constexpr int SEG_COLS = NT < 32 ? 32 : NT;
+      constexpr int W = NT < 32 ? NT : 32;
       const int q = warp & 3;
-      const int f = f0 + q * 32 + lane;
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-      const float bias = (split == 1 && args.bias && f < args.N) ? __ldg(args.bias + f) : 0.f;
-      float* part = reinterpret_cast<float*>(smem);   // [NT][FM]: the ring is idle
+      float* part = reinterpret_cast<float*>(smem) + q * 32 + lane;   // [NT][FM]: the ring is idle
 #pragma unroll 1
-      for (int c = 0; c < NT; c += 32) {
-        if (t0 + c >= args.T) break;
+      for (int c = 0; c < NT && t0 + c < args.T; c += 32) {
         uint32_t v[32];
         tmem_ld32(taddr + c, v);
+        for (int g = 1; g < args.segments; ++g) {
+          uint32_t u[32];
+          tmem_ld32(taddr + g * SEG_COLS + c, u);
 #pragma unroll
-        for (int j = 0; j < (NT < 32 ? NT : 32); ++j) {
-          const int64_t t = t0 + c + j;
-          if (split > 1)
-            part[(c + j) * FM + q * 32 + lane] = kbs > 0 ? __uint_as_float(v[j]) : 0.f;
-          else if (t < args.T && f < args.N)
-            finish<OUT>(args, t, f, __uint_as_float(v[j]), bias);
+          for (int j = 0; j < W; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(u[j]));
         }
+#pragma unroll
+        for (int j = 0; j < W; ++j) part[(c + j) * FM] = __uint_as_float(v[j]);
       }
-      tc_fence_before();
     }
   }
   __syncwarp();
-  if (split > 1) {
-    cluster_sync_all();   // every CTA's partial sums are in its shared memory
-    if (warp >= 2 && ok) {
-      const int i = threadIdx.x - 64;
-      const int f = f0 + i;
-      const float bias = (args.bias && f < args.N) ? __ldg(args.bias + f) : 0.f;
-      const int tokens = min(NT, args.T - t0);
-      if (f < args.N) {
-#pragma unroll 1
-        for (int j = rank; j < tokens; j += split) {
-          const uint32_t at = smem_base + static_cast<uint32_t>(j * FM + i) * 4u;
-          float p[8];
+  tc_fence_before();
+  if (split > 1) cluster_sync_all(); else __syncthreads();   // every partial sum is in place
+  {
+    // ------------------------------------------- join, epilogue, output (all warps)
+    const int f = f0 + lane * 4;
+    const int tokens = min(NT, args.T - t0);
+    float b[4];
 #pragma unroll
-          for (int r = 0; r < 8; ++r) p[r] = r < split ? ld_cluster_f32(mapa_shared(at, r)) : 0.f;
-          float sum = p[0];
+    for (int e = 0; e < 4; ++e) b[e] = args.bias && f + e < args.N ? __ldg(args.bias + f + e) : 0.f;
+    constexpr int WARPS = THREADS / 32, UNROLL = 4;
+    constexpr int VEC = 4 * sizeof(OUT);   // bytes of a lane's four values
+    // whole groups of four go as one access where every row's groups are aligned to it
+    const bool whole = f + 4 <= args.N;
+    const bool vec_y = whole && args.ldc % 4 == 0 && (reinterpret_cast<uintptr_t>(args.C) & (VEC - 1)) == 0;
+    const bool vec_r = whole && args.ldr % 4 == 0 && (reinterpret_cast<uintptr_t>(args.residual) & (VEC - 1)) == 0;
+    const bool vec_p = whole && args.N % 4 == 0 && (reinterpret_cast<uintptr_t>(args.pre) & (VEC - 1)) == 0;
+    // this CTA's tokens are rank, rank + split, ...
+    for (int j0 = warp; rank + j0 * split < tokens && f < args.N; j0 += WARPS * UNROLL) {
+      float4 p[UNROLL];
+      Four<OUT> r[UNROLL];
 #pragma unroll
-          for (int r = 1; r < 8; ++r) sum += p[r];
-          finish<OUT>(args, t0 + j, f, sum, bias);
+      for (int u = 0; u < UNROLL; ++u) {
+        const int j = rank + (j0 + u * WARPS) * split;
+        if (j >= tokens) break;
+        if (args.residual)
+          r[u].load(static_cast<const OUT*>(args.residual) + (t0 + j) * args.ldr + f, vec_r, args.N - f);
+        const uint32_t at = smem_base + static_cast<uint32_t>(j * FM + lane * 4) * 4u;
+        if (split == 1) {
+          p[u] = *reinterpret_cast<const float4*>(smem + (j * FM + lane * 4) * 4);
+        } else {
+          p[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int k = 0; k < split; ++k) {
+            const float4 o = ld_cluster_f32x4(mapa_shared(at, k));
+            p[u] = make_float4(p[u].x + o.x, p[u].y + o.y, p[u].z + o.z, p[u].w + o.w);
+          }
         }
       }
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        const int j = rank + (j0 + u * WARPS) * split;
+        if (j >= tokens) break;
+        const int64_t t = t0 + j;
+        float z[4] = {p[u].x + b[0], p[u].y + b[1], p[u].z + b[2], p[u].w + b[3]};
+        if (args.pre) Four<OUT>(z).store(static_cast<OUT*>(args.pre) + t * args.N + f, vec_p, args.N - f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[e] = act_value<ACT>(z[e]);
+        if (args.residual) r[u].add_to(z);
+        Four<OUT>(z).store(static_cast<OUT*>(args.C) + t * args.ldc + f, vec_y, args.N - f);
+      }
     }
+  }
+  if (split > 1) {
+    __syncwarp();
     cluster_sync_all();   // no CTA leaves while another reads its partial sums
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, S::TMEM_COLS);
+    tmem_dealloc(tmem_base, args.tmem_cols);
   }
 }
 
-template <int NT, typename OUT>
+template <int NT, typename OUT, int ACT>
 cudaError_t launch_typed(const LinearGemm& g, int split, cudaStream_t s) {
   using S = Shape<NT>;
   Args a{};
@@ -236,7 +309,12 @@ cudaError_t launch_typed(const LinearGemm& g, int split, cudaStream_t s) {
   a.K = g.K;
   a.t_tiles = (a.T + NT - 1) / NT;
   a.split = split;
-  a.act = g.act;
+  // segments of at most 512 deep for fp32 outputs, one otherwise
+  const int cta_blocks = ((a.K + BK - 1) / BK + split - 1) / split;
+  a.segments = sizeof(OUT) == 4 ? std::min(S::MAX_SEGMENTS, std::max(1, (cta_blocks + 7) / 8)) : 1;
+  a.segments = std::min(a.segments, std::max(1, (a.K + BK - 1) / BK / split));   // none empty
+  a.tmem_cols = 32;
+  while (a.tmem_cols < static_cast<uint32_t>(a.segments * (NT < 32 ? 32 : NT))) a.tmem_cols *= 2;
   a.bias = g.bias;
   a.residual = g.residual;
   a.pre = g.pre;
@@ -248,7 +326,7 @@ cudaError_t launch_typed(const LinearGemm& g, int split, cudaStream_t s) {
   if (!make_strided_map(&mW, MOE_BF16, g.B, g.K, g.N, g.ldb, BK, FM) ||
       !make_strided_map(&mX, MOE_BF16, g.A, g.K, static_cast<uint64_t>(g.M), g.lda, BK, NT))
     return cudaErrorInvalidValue;
-  auto kern = linear_few_kernel<NT, OUT>;
+  auto kern = linear_few_kernel<NT, OUT, ACT>;
   cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), S::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -266,7 +344,7 @@ cudaError_t launch_typed(const LinearGemm& g, int split, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kern, mW, mX, a);
 }
 
-template <typename OUT>
+template <typename OUT, int ACT>
 cudaError_t launch_out(const LinearGemm& g, cudaStream_t s) {
   const int T = static_cast<int>(g.M);
   const int NT = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
@@ -277,18 +355,25 @@ cudaError_t launch_out(const LinearGemm& g, cudaStream_t s) {
   int split = 1;
   while (split < 8 && tiles * split * 2 <= want && k_blocks >= 4 * split) split *= 2;
   switch (NT) {
-    case 16: return launch_typed<16, OUT>(g, split, s);
-    case 32: return launch_typed<32, OUT>(g, split, s);
-    case 64: return launch_typed<64, OUT>(g, split, s);
-    case 128: return launch_typed<128, OUT>(g, split, s);
-    default: return launch_typed<256, OUT>(g, split, s);
+    case 16: return launch_typed<16, OUT, ACT>(g, split, s);
+    case 32: return launch_typed<32, OUT, ACT>(g, split, s);
+    case 64: return launch_typed<64, OUT, ACT>(g, split, s);
+    case 128: return launch_typed<128, OUT, ACT>(g, split, s);
+    default: return launch_typed<256, OUT, ACT>(g, split, s);
   }
+}
+
+template <typename OUT>
+cudaError_t launch_act(const LinearGemm& g, cudaStream_t s) {
+#define MOE_CALL(ACT) launch_out<OUT, ACT>(g, s)
+  MOE_DISPATCH_ACT(g.act, MOE_CALL)
+#undef MOE_CALL
 }
 
 }  // namespace
 
 cudaError_t launch_linear_few(const LinearGemm& g, cudaStream_t s) {
-  return g.out_dtype == MOE_F32 ? launch_out<float>(g, s) : launch_out<__nv_bfloat16>(g, s);
+  return g.out_dtype == MOE_F32 ? launch_act<float>(g, s) : launch_act<__nv_bfloat16>(g, s);
 }
 
 }  // namespace moe

@@ -509,10 +509,10 @@ bool make_map_2d(CUtensorMap* m, CUtensorMapDataType type, uint32_t elem_bytes, 
 
 }  // namespace
 
-// A 2-D tensor of 16-byte aligned rows ld elements apart, box box_inner x box_rows of 128-byte
-// rows, 128-byte swizzle; encoded at every call.
+// A 2-D tensor of 16-byte aligned rows ld elements apart, box box_inner x box_rows of
+// row_bytes-byte rows (128 or 64) with the swizzle of that width; encoded at every call.
 bool make_strided_map(CUtensorMap* m, int32_t dtype, const void* base, uint64_t inner, uint64_t rows,
-                      uint64_t ld, uint32_t box_inner, uint32_t box_rows) {
+                      uint64_t ld, uint32_t box_inner, uint32_t box_rows, uint32_t row_bytes) {
   EncodeFn enc = encode_fn();
   if (!enc) return false;
   const bool f32 = dtype == MOE_F32;
@@ -522,8 +522,8 @@ bool make_strided_map(CUtensorMap* m, int32_t dtype, const void* base, uint64_t 
   cuuint32_t estr[2] = {1, 1};
   return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // bf16 [rows][inner], box 64 x box_rows (128-byte rows of the box), 128-byte swizzle.

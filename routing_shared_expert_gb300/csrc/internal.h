@@ -68,9 +68,9 @@ cudaError_t launch_route_pair(const RouteParams& p, cudaStream_t s);
 // 2-D bf16 tensor map of a dense row-major [rows][inner] tensor: box 64 x box_rows,
 // 128-byte swizzle, zero fill out of bounds.  False if the driver rejects it.
 bool make_bf16_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows);
-// The same for rows ld elements apart of either moe_dtype; the box is 128 bytes wide.
+// The same for rows ld elements apart of either moe_dtype; the box is row_bytes wide.
 bool make_strided_map(CUtensorMap* m, int32_t dtype, const void* base, uint64_t inner, uint64_t rows,
-                      uint64_t ld, uint32_t box_inner, uint32_t box_rows);
+                      uint64_t ld, uint32_t box_inner, uint32_t box_rows, uint32_t row_bytes = 128);
 bool make_f32_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows);
 bool make_bf16_store_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows);
 bool make_f16_store_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows);

@@ -38,14 +38,14 @@ struct DzArgs {
   const void* dy;
   const void* pre;              // nullptr: the identity
   int64_t ldy, T, col_blocks, ld_dz;
-  int32_t n, act;
+  int32_t n;
   __nv_bfloat16* dz;            // [T][ld_dz] or nullptr
   float* part;                  // [row blocks][n] or nullptr
 };
 
 // dz = dy act'(pre) and, per block of kDzRows rows, its column sums (each warp its rows in
 // order, then the warps in order).  VEC: 16-byte loads of whole groups of eight columns.
-template <typename OUT, bool VEC>
+template <typename OUT, bool VEC, int ACT>
 __global__ void __launch_bounds__(256) dz_kernel(DzArgs a) {
   __shared__ float s_sum[8][kDzCols];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -60,17 +60,17 @@ __global__ void __launch_bounds__(256) dz_kernel(DzArgs a) {
       float g[8], z[8];
       if (VEC) {
         load8(dy, g);
-        if (a.pre) load8(pre, z);
+        if (ACT != MOE_ACT_NONE) load8(pre, z);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           g[e] = c0 + e < a.n ? to_f32(dy[e]) : 0.f;
-          z[e] = a.pre && c0 + e < a.n ? to_f32(pre[e]) : 0.f;
+          z[e] = ACT != MOE_ACT_NONE && c0 + e < a.n ? to_f32(pre[e]) : 0.f;
         }
       }
-      if (a.pre) {
+      if (ACT != MOE_ACT_NONE) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] *= act_slope(z[e], a.act);
+        for (int e = 0; e < 8; ++e) g[e] *= act_slope<ACT>(z[e]);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[e] += g[e];
@@ -91,6 +91,20 @@ __global__ void __launch_bounds__(256) dz_kernel(DzArgs a) {
     for (int w = 0; w < 8; ++w) v += s_sum[w][threadIdx.x];
     a.part[rb * a.n + col] = v;
   }
+}
+
+template <typename OUT, int ACT>
+cudaError_t launch_dz_act(const DzArgs& a, bool vec, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>((a.T + kDzRows - 1) / kDzRows * a.col_blocks);
+  if (vec) dz_kernel<OUT, true, ACT><<<grid, 256, 0, s>>>(a);
+  else dz_kernel<OUT, false, ACT><<<grid, 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+template <typename OUT>
+cudaError_t launch_dz(const DzArgs& a, int act, bool vec, cudaStream_t s) {
+#define MOE_CALL(ACT) launch_dz_act<OUT, ACT>(a, vec, s)
+  MOE_DISPATCH_ACT(act, MOE_CALL)
+#undef MOE_CALL
 }
 
 // db: 32 columns per CTA, 32 warps that each add every 32nd block, then the warps in order.
@@ -129,7 +143,7 @@ __global__ void __launch_bounds__(256) align_rows_kernel(const __nv_bfloat16* sr
 int64_t up8(int64_t v) { return (v + 7) & ~int64_t{7}; }
 
 struct LinearLayout {
-  size_t dz, db_part, x, w, total;
+  size_t dz, db_part, x, w, scratch, total;
 };
 
 size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
@@ -145,6 +159,8 @@ LinearLayout linear_layout(const moe_linear_config& c) {
   o = up256(o + static_cast<size_t>(c.T) * up8(c.in_features) * 2);
   L.w = o;
   o = up256(o + static_cast<size_t>(c.out_features) * up8(c.in_features) * 2);
+  L.scratch = o;
+  o = up256(o + kPairScratchFloats * 4);
   L.total = o;
   return L;
 }
@@ -249,6 +265,8 @@ moe_status moe_linear_forward(const moe_linear_config* cfg, const void* x, const
   g.ldr = c.ldr ? c.ldr : c.out_features;
   g.ldc = c.ldy ? c.ldy : c.out_features;
   g.status = static_cast<int32_t*>(workspace);
+  g.scratch = reinterpret_cast<float*>(ws + L.scratch);
+  g.tickets = reinterpret_cast<unsigned*>(ws + kPairTicketOffset);
   const cudaError_t e = c.T <= kFewTokens ? launch_linear_few(g, stream) : launch_linear_pair(g, stream);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -291,7 +309,6 @@ moe_status moe_linear_backward(const moe_linear_config* cfg, const void* x, cons
     a.col_blocks = (n + kDzCols - 1) / kDzCols;
     a.ld_dz = up8(n);
     a.n = n;
-    a.act = c.act;
     if ((dx || dW) && !as_is) {
       a.dz = reinterpret_cast<__nv_bfloat16*>(ws + L.dz);
       oz = {a.dz, a.ld_dz};
@@ -299,14 +316,9 @@ moe_status moe_linear_backward(const moe_linear_config* cfg, const void* x, cons
     a.part = dbias ? reinterpret_cast<float*>(ws + L.db_part) : nullptr;
     const bool vec = n % 8 == 0 && ldy % 8 == 0 && (reinterpret_cast<uintptr_t>(dy) & 15u) == 0 &&
                      (reinterpret_cast<uintptr_t>(a.pre) & 15u) == 0;
-    const unsigned grid = static_cast<unsigned>(blocks * a.col_blocks);
-    if (c.out_dtype == MOE_F32) {
-      if (vec) dz_kernel<float, true><<<grid, 256, 0, stream>>>(a);
-      else dz_kernel<float, false><<<grid, 256, 0, stream>>>(a);
-    } else {
-      if (vec) dz_kernel<__nv_bfloat16, true><<<grid, 256, 0, stream>>>(a);
-      else dz_kernel<__nv_bfloat16, false><<<grid, 256, 0, stream>>>(a);
-    }
+    const cudaError_t e = c.out_dtype == MOE_F32 ? launch_dz<float>(a, c.act, vec, stream)
+                                                 : launch_dz<__nv_bfloat16>(a, c.act, vec, stream);
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
     if (dbias) db_kernel<<<static_cast<unsigned>((n + 31) / 32), 1024, 0, stream>>>(a.part, blocks, n, dbias);
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
   }
@@ -318,6 +330,8 @@ moe_status moe_linear_backward(const moe_linear_config* cfg, const void* x, cons
   g.ldc = c.in_features;
   g.act = MOE_ACT_NONE;
   g.status = static_cast<int32_t*>(workspace);
+  g.scratch = reinterpret_cast<float*>(ws + L.scratch);
+  g.tickets = reinterpret_cast<unsigned*>(ws + kPairTicketOffset);
   if (dx) {
     Operand o;
     if (aligned_operand(W, n, c.in_features, c.ldw ? c.ldw : c.in_features, ws + L.w, &o, stream) != cudaSuccess)

@@ -23,7 +23,17 @@ struct LinearGemm {
   void* C;                 // [M][ldc]
   int64_t ldr, ldc;
   int32_t* status;
+  float* scratch;          // kPairScratchFloats: partial tiles of launch_linear_pair
+  unsigned* tickets;       // kPairTicketBytes, zero between calls
 };
+
+// Most CTA pairs of a launch, and the partial tiles (256 x 256 per pair) and arrival counts (a
+// byte per cut tile and CTA of the pair) its cut tiles need.
+constexpr int kMaxPairs = 76;
+constexpr size_t kPairScratchFloats = static_cast<size_t>(kMaxPairs) * 256 * 256;
+constexpr size_t kPairTicketOffset = 64;   // bytes into the workspace header
+constexpr size_t kPairTicketBytes = 2 * kMaxPairs;
+static_assert(kPairTicketOffset + kPairTicketBytes <= 256, "the counts lie in the header");
 
 // CTA pairs, 256 x 256 tiles (gemm_linear.cu).
 cudaError_t launch_linear_pair(const LinearGemm& g, cudaStream_t s);

@@ -80,7 +80,8 @@ def forward(moe, T, n_in, n_out, act="none", out="bf16", bias=True, residual=Tru
 
 SIZES = [(1, 64, 64), (1, 2048, 2048), (2, 8, 1), (3, 72, 60), (7, 1000, 257), (16, 256, 130), (17, 512, 384),
          (33, 64, 1000), (64, 2048, 512), (127, 128, 128), (128, 320, 256), (129, 192, 264), (256, 1024, 640),
-         (257, 2560, 512), (300, 64, 72), (1000, 200, 1407), (1237, 2048, 768), (2050, 136, 2056)]
+         (257, 2560, 512), (300, 64, 72), (1000, 200, 1407), (1237, 2048, 768), (2050, 136, 2056),
+         (2700, 1024, 2048)]
 
 
 @pytest.mark.parametrize("T,n_in,n_out", SIZES)

@@ -213,7 +213,8 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         import torch
-        return c_void_p(torch.cuda.current_stream().cuda_stream)
+        # the raw handle, without building a Stream object at every call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return c_void_p(stream)
     return c_void_p(stream.cuda_stream)
@@ -442,42 +443,49 @@ def make_linear_config(T, in_features, out_features, act="none", out_dtype="bf16
     return c
 
 
-_TORCH_DTYPES = {"torch.float32": 0, "torch.bfloat16": 1}
+_TORCH_DTYPES = {}     # torch dtype -> moe_dtype
+
+
+def _dtypes():
+    if not _TORCH_DTYPES:
+        import torch
+        _TORCH_DTYPES.update({torch.float32: 0, torch.bfloat16: 1})
+    return _TORCH_DTYPES
 
 
 def _dtype_of(t) -> int:
     try:
-        return _TORCH_DTYPES[str(t.dtype)]
+        return _dtypes()[t.dtype]
     except KeyError:
         raise ValueError(f"fp32 or bf16 tensors are expected, got {t.dtype}") from None
 
 
-def _on_device(name, t):
+def _mat(name, t, rows, cols, ld, dtype):
+    """Address of a row-strided [rows][cols] matrix, checked against what the call assumes."""
+    if t is None:
+        return None
     if not t.is_cuda:
         raise ValueError(f"{name}: a CUDA tensor is expected")
-
-
-def _mat(name, t, rows, cols, ld, dtype):
-    """Pointer of a row-strided [rows][cols] matrix, checked against what the call assumes."""
-    if t is None:
-        return None
-    _on_device(name, t)
-    if tuple(t.shape) != (rows, cols) or _dtype_of(t) != dtype:
+    if t.shape != (rows, cols) or _dtypes().get(t.dtype) != dtype:
         raise ValueError(f"{name}: expected [{rows}][{cols}] of "
                          f"{'fp32' if dtype == 0 else 'bf16'}, got {tuple(t.shape)} {t.dtype}")
-    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) != (ld or cols)):
+    s0, s1 = t.stride()
+    if (s1 != 1 and cols > 1) or (s0 != (ld or cols) and rows > 1):
         raise ValueError(f"{name}: strides {t.stride()} do not match a row stride of {ld or cols}")
-    return c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def _vec(name, t, n, dtype="torch.float32"):
+def _vec(name, t, n, dtype="float32"):
+    """Address of n contiguous values."""
     if t is None:
         return None
-    _on_device(name, t)
-    if t.numel() != n or not t.is_contiguous() or str(t.dtype) != dtype:
+    if not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor is expected")
+    import torch
+    if t.numel() != n or t.dtype is not getattr(torch, dtype) or not t.is_contiguous():
         raise ValueError(f"{name}: expected {n} contiguous values of {dtype}, "
                          f"got {tuple(t.shape)} {t.dtype}")
-    return c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def moe_linear_workspace_size(cfg: moe_linear_config) -> int:
@@ -517,8 +525,9 @@ def moe_linear_backward(cfg: moe_linear_config, x, W, pre, dy, dx, dW, dbias, wo
 
 def _rows_of(name, t, shape=None):
     """(rows, cols, row stride) of a contiguous tensor or a row-strided matrix."""
-    _on_device(name, t)
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor is expected")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dim() == 0:
         raise ValueError(f"{name}: a tensor with at least one dimension is expected")
@@ -531,15 +540,11 @@ def _rows_of(name, t, shape=None):
 
 
 def _dropout_config(x, y, residual, p):
-    c = moe_dropout_config()
-    c.rows, c.cols, c.ldx = _rows_of("x", x)
-    _, _, c.ldy = _rows_of("y", y, x.shape)
-    c.x_dtype, c.y_dtype = _dtype_of(x), _dtype_of(y)
-    c.p = float(p)
-    if residual is not None:
-        _, _, c.ldr = _rows_of("residual", residual, x.shape)
-        c.residual_dtype = _dtype_of(residual)
-    return c
+    rows, cols, ldx = _rows_of("x", x)
+    ldy = _rows_of("y", y, x.shape)[2]
+    ldr = _rows_of("residual", residual, x.shape)[2] if residual is not None else 0
+    return moe_dropout_config(rows, cols, float(p), _dtype_of(x),
+                              _dtype_of(residual) if residual is not None else 0, _dtype_of(y), ldx, ldr, ldy)
 
 
 def moe_dropout_add(x, residual, p, rng_state, y, stream=None):
@@ -547,17 +552,16 @@ def moe_dropout_add(x, residual, p, rng_state, y, stream=None):
     tensor (seed, offset).  The mask depends on them and the element's number alone."""
     c = _dropout_config(x, y, residual, p)
     _check("moe_dropout_add", _lib.moe_dropout_add(
-        ctypes.byref(c), c_void_p(x.data_ptr()),
-        None if residual is None else c_void_p(residual.data_ptr()),
-        _vec("rng_state", rng_state, 2, "torch.int64"), c_void_p(y.data_ptr()), _stream(stream)))
+        ctypes.byref(c), x.data_ptr(), None if residual is None else residual.data_ptr(),
+        _vec("rng_state", rng_state, 2, "int64"), y.data_ptr(), _stream(stream)))
 
 
 def moe_dropout_backward(dy, p, rng_state, dx, stream=None):
     """dx = keep * dy / (1 - p) with the mask of moe_dropout_add for the same p and rng_state."""
     c = _dropout_config(dx, dy, None, p)
     _check("moe_dropout_backward", _lib.moe_dropout_backward(
-        ctypes.byref(c), c_void_p(dy.data_ptr()), _vec("rng_state", rng_state, 2, "torch.int64"),
-        c_void_p(dx.data_ptr()), _stream(stream)))
+        ctypes.byref(c), dy.data_ptr(), _vec("rng_state", rng_state, 2, "int64"), dx.data_ptr(),
+        _stream(stream)))
 
 
 def moe_balance_loss_workspace_size(cfg: moe_config, seq_len: int = 0) -> int:
@@ -582,10 +586,11 @@ def moe_balance_loss(cfg: moe_config, logits, topk_idx, token_mask, seq_len, coe
     grad_scale (fp32 [1]) may be None.  seq_len 0 takes the batch as one sequence."""
     T, N, K = cfg.T, cfg.N, cfg.K
     S = -(-T // min(int(seq_len) or T, T)) if T else 0
-    mask = "torch.bool" if token_mask is not None and str(token_mask.dtype) == "torch.bool" else "torch.uint8"
+    mask = "bool" if token_mask is not None and token_mask.element_size() == 1 and \
+        str(token_mask.dtype) == "torch.bool" else "uint8"
     _check("moe_balance_loss", _lib.moe_balance_loss(
-        ctypes.byref(cfg), _vec("logits", logits, T * N), _vec("topk_idx", topk_idx, T * K, "torch.int32"),
+        ctypes.byref(cfg), _vec("logits", logits, T * N), _vec("topk_idx", topk_idx, T * K, "int32"),
         _vec("token_mask", token_mask, T, mask), int(seq_len), float(coef_balance), float(coef_z),
-        _vec("grad_scale", grad_scale, 1), _vec("counts", counts, S * N, "torch.int32"),
+        _vec("grad_scale", grad_scale, 1), _vec("counts", counts, S * N, "int32"),
         _vec("P", P, S * N), _vec("loss", loss, 3), _vec("dlogits", dlogits, T * N), _ptr(workspace),
         workspace.numel(), _stream(stream)))

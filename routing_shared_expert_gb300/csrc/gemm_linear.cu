@@ -743,6 +743,14 @@ cudaError_t launch_forward(const LinearGemm& g, cudaStream_t s) {
 }
 }  // namespace
 
+int64_t pair_cycles(int64_t M, int64_t N, int64_t K, int sms) {
+  const int64_t tiles = (M + BM - 1) / BM * ((N + BN - 1) / BN), pairs = std::min(kMaxPairs, std::max(1, sms / 2));
+  const int64_t stages = ((K + BK - 1) / BK + 1) / 2, rest = tiles % pairs;
+  const int parts = rest > 0 ? cut_parts(rest, pairs, stages) : 1;
+  const int64_t last = rest == 0 ? 0 : parts == 1 ? stages : (stages + parts - 1) / parts + kJoin + kJoinPart * parts;
+  return 20000 + (tiles / pairs * stages + last) * 2 * (tiles <= pairs ? 640 : 573);
+}
+
 cudaError_t launch_linear_pair(const LinearGemm& g, cudaStream_t s) {
   const bool f32 = g.out_dtype == MOE_F32;
   if (g.a_mn)

@@ -14,8 +14,10 @@
 // each in its own TMEM columns, and added in rounded fp32: the tensor core's additions drop
 // bits, an error that grows with the length of a sum.
 //
-// The ring holds one 64-wide K block per stage (16 KB of W, 128 NT bytes of x).  Up to NT = 64
-// it takes about 100 KB, so two CTAs share an SM and one streams while the other starts or ends.
+// The ring holds one 64-wide K block per stage (16 KB of W, 128 NT bytes of x), about 100 KB, so
+// that two CTAs share an SM and one streams while the other starts or ends.  More than 64 tokens
+// are tiles of 64 (measured ahead of one wider tile, whose CTAs are too few: 256 tokens of 2048 x
+// 2048 in 10.1 us against 10.6 with tiles of 128 and 12.5 with 256).
 //
 // Every wait is bounded; a wait that runs out records MOE_ERR_TIMEOUT and the CTA waits for
 // what it issued before it frees its TMEM.
@@ -38,12 +40,12 @@ constexpr uint64_t kDrainLimitNs = 100000000ull;
 template <int NT> struct Shape {
   static constexpr int X_BYTES = NT * BK * 2;
   static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
-  static constexpr int STAGES = NT <= 16 ? 6 : NT <= 32 ? 5 : NT <= 64 ? 4 : NT <= 128 ? 6 : 4;
+  static constexpr int STAGES = NT <= 16 ? 6 : NT <= 32 ? 5 : 4;
   static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
   static constexpr size_t SMEM = 1024 + RING_BYTES + 8 * (2 * STAGES + 2) + 32;
-  static constexpr int PER_SM = SMEM <= 113 * 1024 ? 2 : 1;
-  // TMEM columns of one CTA: room for fp32 segments, half of the 512 where two CTAs share an SM
-  static constexpr int MAX_SEGMENTS = (PER_SM == 2 ? 256 : 512) / (NT < 32 ? 32 : NT);
+  static_assert(SMEM <= 113 * 1024, "two CTAs share an SM");
+  // fp32 segments in one CTA's half of the 512 TMEM columns
+  static constexpr int MAX_SEGMENTS = 256 / (NT < 32 ? 32 : NT);
   static_assert(NT * FM * 4 <= RING_BYTES, "the partial sums take the ring's place");
 };
 
@@ -103,7 +105,7 @@ template <typename OUT> struct alignas(4 * sizeof(OUT)) Four {
 };
 
 template <int NT, typename OUT, int ACT>
-__global__ void __launch_bounds__(THREADS, Shape<NT>::PER_SM)
+__global__ void __launch_bounds__(THREADS, 2)
     linear_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                       const Args args) {
   using S = Shape<NT>;
@@ -346,20 +348,11 @@ cudaError_t launch_typed(const LinearGemm& g, int split, cudaStream_t s) {
 
 template <typename OUT, int ACT>
 cudaError_t launch_out(const LinearGemm& g, cudaStream_t s) {
-  const int T = static_cast<int>(g.M);
-  const int NT = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
-  // CTAs per cluster: enough for every SM to read, at least two K blocks each
-  const int64_t tiles = static_cast<int64_t>((g.N + FM - 1) / FM) * ((T + NT - 1) / NT);
-  const int k_blocks = (g.K + BK - 1) / BK;
-  const int64_t want = static_cast<int64_t>(device_sm_count()) * (NT <= 64 ? 2 : 1);
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= want && k_blocks >= 4 * split) split *= 2;
-  switch (NT) {
-    case 16: return launch_typed<16, OUT, ACT>(g, split, s);
-    case 32: return launch_typed<32, OUT, ACT>(g, split, s);
-    case 64: return launch_typed<64, OUT, ACT>(g, split, s);
-    case 128: return launch_typed<128, OUT, ACT>(g, split, s);
-    default: return launch_typed<256, OUT, ACT>(g, split, s);
+  const FewShape f = few_shape(g.M, g.N, g.K, device_sm_count());
+  switch (f.tokens) {
+    case 16: return launch_typed<16, OUT, ACT>(g, f.split, s);
+    case 32: return launch_typed<32, OUT, ACT>(g, f.split, s);
+    default: return launch_typed<64, OUT, ACT>(g, f.split, s);
   }
 }
 
@@ -371,6 +364,23 @@ cudaError_t launch_act(const LinearGemm& g, cudaStream_t s) {
 }
 
 }  // namespace
+
+FewShape few_shape(int64_t T, int64_t N, int64_t K, int sms) {
+  FewShape f;
+  f.tokens = T <= 16 ? 16 : T <= 32 ? 32 : 64;
+  const int64_t tiles = (N + FM - 1) / FM * ((T + f.tokens - 1) / f.tokens), k_blocks = (K + BK - 1) / BK;
+  // As many CTAs per cluster as leave one round of two CTAs per SM (one and a half where x is
+  // narrow and a CTA little but reads: there more CTAs only add joins), two K blocks each.
+  const int64_t most = f.tokens <= 32 ? sms * 3 / 2 : sms * 2;
+  f.split = 1;
+  for (int sp : {2, 3, 4, 6, 8})
+    if (tiles * sp <= most && k_blocks >= 2 * sp) f.split = sp;
+  f.one_round = tiles <= 2 * sms;
+  // Cycles: the K blocks an SM loads at 64 bytes a cycle, and what a launch costs besides.
+  const int64_t per_sm = (tiles * f.split + sms - 1) / sms;
+  f.cycles = 9000 + per_sm * ((k_blocks + f.split - 1) / f.split) * (W_BYTES + f.tokens * BK * 2) / 64;
+  return f;
+}
 
 cudaError_t launch_linear_few(const LinearGemm& g, cudaStream_t s) {
   return g.out_dtype == MOE_F32 ? launch_act<float>(g, s) : launch_act<__nv_bfloat16>(g, s);

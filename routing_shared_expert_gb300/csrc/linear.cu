@@ -17,7 +17,23 @@ namespace {
 
 constexpr int kDzRows = 64;     // rows per block of the dz pass, and per partial sum of db
 constexpr int kDzCols = 256;    // columns per block: 8 per lane
-constexpr int kFewTokens = 256; // at most this many take the few-token kernel
+
+// Which kernel takes a forward product.  A warp per weight row (linear_vec.cu) needs no aligned
+// copies and starts soonest, but reads x anew for every row: it wins for one token up to about
+// 2^25 weights (2048 x 2048: 5.0 us against 6.0; 7168 x 7168: 20.3 against 20.0) and for up to
+// four where the whole product is small (512 x 512: 2.7 against 4.3; two tokens of 2048 x 2048:
+// 6.8 against 6.5), and for one or two tokens of unaligned rows (2047 x 2047: 7.6 against 10.8).
+// The few-token kernel wins while its tiles are resident at once and its loads take less than
+// the pair kernel's rounds (384 tokens of 2048 x 5632: 17.1 us against 19.2; 512: 29.7
+// against 19.6).
+enum class Form { kVec, kFew, kPair };
+Form forward_form(int64_t T, int64_t N, int64_t K, bool aligned) {
+  if (T <= kVecTokens && (T * N * K <= (T == 1 ? int64_t{1} << 25 : int64_t{1} << 22) || (!aligned && T <= 2)))
+    return Form::kVec;
+  const int sms = device_sm_count();
+  const FewShape f = few_shape(T, N, K, sms);
+  return f.one_round && f.cycles < pair_cycles(T, N, K, sms) ? Form::kFew : Form::kPair;
+}
 
 __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
   const uint4 u = *reinterpret_cast<const uint4*>(p);
@@ -125,18 +141,20 @@ __global__ void __launch_bounds__(1024) db_kernel(const float* part, int64_t blo
   }
 }
 
-// Rows of cols bf16 values, ld apart, to rows ldd (a multiple of 8) apart: a warp per row.
+// Rows of cols bf16 values, ld apart, to rows ldd (a multiple of 8) apart: eight values per
+// thread and step, zeros past cols.
 __global__ void __launch_bounds__(256) align_rows_kernel(const __nv_bfloat16* src, int64_t rows, int cols,
                                                          int64_t ld, __nv_bfloat16* dst, int64_t ldd) {
-  const int lane = threadIdx.x % 32;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32; r < rows; r += step) {
+  const int64_t per = ldd / 8, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < rows * per; i += step) {
+    const int64_t r = i / per;
+    const int c = static_cast<int>(i - r * per) * 8;
     const unsigned short* s = reinterpret_cast<const unsigned short*>(src + r * ld);
-    unsigned short* d = reinterpret_cast<unsigned short*>(dst + r * ldd);
-    for (int c = lane * 2; c < cols; c += 64) {
-      const unsigned lo = s[c], hi = c + 1 < cols ? s[c + 1] : 0u;
-      *reinterpret_cast<unsigned*>(d + c) = lo | hi << 16;
-    }
+    uint32_t v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? __ldg(s + c + e) : 0u;
+    *reinterpret_cast<uint4*>(dst + r * ldd + c) =
+        make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
   }
 }
 
@@ -177,7 +195,7 @@ cudaError_t aligned_operand(const void* p, int64_t rows, int32_t cols, int64_t l
     return cudaSuccess;
   }
   *o = {copy, up8(cols)};
-  const int64_t blocks = std::min<int64_t>((rows + 7) / 8, static_cast<int64_t>(device_sm_count()) * 16);
+  const int64_t blocks = std::min<int64_t>((rows * (o->ld / 8) + 255) / 256, static_cast<int64_t>(device_sm_count()) * 32);
   align_rows_kernel<<<static_cast<unsigned>(blocks), 256, 0, s>>>(
       static_cast<const __nv_bfloat16*>(p), rows, cols, ld, static_cast<__nv_bfloat16*>(copy), o->ld);
   return cudaGetLastError();
@@ -244,9 +262,13 @@ moe_status moe_linear_forward(const moe_linear_config* cfg, const void* x, const
     return MOE_ERR_MISALIGNED;
   const LinearLayout L = linear_layout(c);
   char* ws = static_cast<char*>(workspace);
-  Operand ox, ow;
-  if (aligned_operand(x, c.T, c.in_features, c.ldx ? c.ldx : c.in_features, ws + L.x, &ox, stream) != cudaSuccess ||
-      aligned_operand(W, c.out_features, c.in_features, c.ldw ? c.ldw : c.in_features, ws + L.w, &ow, stream) != cudaSuccess)
+  const int64_t ldx = c.ldx ? c.ldx : c.in_features, ldw = c.ldw ? c.ldw : c.in_features;
+  const bool aligned = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(W)) & 15u) == 0 &&
+                       (ldx % 8 == 0 || c.T == 1) && ldw % 8 == 0;
+  const Form form = forward_form(c.T, c.out_features, c.in_features, aligned);
+  Operand ox{x, ldx}, ow{W, ldw};
+  if (form != Form::kVec && (aligned_operand(x, c.T, c.in_features, ldx, ws + L.x, &ox, stream) != cudaSuccess ||
+               aligned_operand(W, c.out_features, c.in_features, ldw, ws + L.w, &ow, stream) != cudaSuccess))
     return MOE_ERR_CUDA;
   LinearGemm g{};
   g.A = ox.p;
@@ -267,7 +289,9 @@ moe_status moe_linear_forward(const moe_linear_config* cfg, const void* x, const
   g.status = static_cast<int32_t*>(workspace);
   g.scratch = reinterpret_cast<float*>(ws + L.scratch);
   g.tickets = reinterpret_cast<unsigned*>(ws + kPairTicketOffset);
-  const cudaError_t e = c.T <= kFewTokens ? launch_linear_few(g, stream) : launch_linear_pair(g, stream);
+  const cudaError_t e = form == Form::kVec   ? launch_linear_vec(g, stream)
+                        : form == Form::kFew ? launch_linear_few(g, stream)
+                                             : launch_linear_pair(g, stream);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -64,7 +64,8 @@ def check(moe, rows, cols, p, x="f32", r="bf16", y="bf16", ldx=None, ldr=None, l
 
 
 @pytest.mark.parametrize("rows,cols", [(1, 1), (1, 3), (1, 4), (1, 5), (2, 7), (3, 8), (5, 64), (7, 33), (64, 100),
-                                       (129, 1023), (1000, 256), (77, 4099)])
+                                       (129, 1023), (1000, 256), (77, 4099),
+                                       (1025, 2049), (300, 8192)])
 @pytest.mark.parametrize("p", [0.0, 0.1, 0.5, 1.0])
 def test_sizes(moe, rows, cols, p):
     check(moe, rows, cols, p)

@@ -80,36 +80,46 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
 // Bound by memory for large operands: 8192 x 7168, fp32 + bf16 -> bf16, in 66 us (7.1 TB/s) on one
 // GB300, 16383 x 2047 bf16 -> fp32 in 30.4 us.  With one group per thread the generator's integer
 // products bind instead (75 and 38 us).
-template <typename X, typename R, typename Y, bool RES, int G>
+template <typename X, typename R, typename Y, bool RES, int G, bool DENSE>
 __global__ void __launch_bounds__(256) dropout_vec_kernel(DropoutArgs a) {
   const int64_t i0 = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * (8 * G);
   const int64_t n = a.rows * a.cols;
   if (i0 >= n) return;
-  float v[G][8], q[G][8];
-  Y* y[G];
+  int64_t ox[G], oy[G], orr[G];   // where the groups start
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     const int64_t i = i0 + 8 * g;
-    const int64_t row = a.rows == 1 ? 0 : i / a.cols, col = i - row * a.cols;
-    const X* x = static_cast<const X*>(a.x) + row * a.ldx + col;
-    const R* r = static_cast<const R*>(a.r) + row * a.ldr + col;
-    y[g] = static_cast<Y*>(a.y) + row * a.ldy + col;
-    if (i + 8 <= n) {
-      load8(x, v[g]);
-      if (RES) load8(r, q[g]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[g][j] = i + j < n ? to_f32(x[j]) : 0.f;
-        if (RES) q[g][j] = i + j < n ? to_f32(r[j]) : 0.f;
-      }
+    const int64_t row = DENSE ? 0 : i / a.cols, col = i - row * a.cols;
+    ox[g] = row * a.ldx + col;
+    oy[g] = row * a.ldy + col;
+    orr[g] = row * a.ldr + col;
+  }
+  const X* x = static_cast<const X*>(a.x);
+  const R* r = static_cast<const R*>(a.r);
+  Y* y = static_cast<Y*>(a.y);
+  if (i0 + 8 * G > n) {   // the last thread's rest, one by one and apart: inside, it costs registers
+#pragma unroll 1
+    for (int64_t i = i0; i < n; ++i) {
+      const int64_t row = DENSE ? 0 : i / a.cols, col = i - row * a.cols;
+      uint4 u[1];
+      philox4x32<1>(a.rng, static_cast<uint64_t>(i) / 4, u);
+      const uint32_t w = i % 4 == 0 ? u[0].x : i % 4 == 1 ? u[0].y : i % 4 == 2 ? u[0].z : u[0].w;
+      float z = w >= a.threshold && !a.drop_all ? to_f32(x[row * a.ldx + col]) * a.scale : 0.f;
+      if (RES) z += to_f32(r[row * a.ldr + col]);
+      y[row * a.ldy + col] = from_f32<Y>(z);
     }
+    return;
+  }
+  float v[G][8], q[G][8];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    load8(x + ox[g], v[g]);
+    if (RES) load8(r + orr[g], q[g]);
   }
   uint4 c[2 * G];
   philox4x32<2 * G>(a.rng, static_cast<uint64_t>(i0) / 4, c);
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const int64_t i = i0 + 8 * g;
     const uint32_t w[8] = {c[2 * g].x,     c[2 * g].y,     c[2 * g].z,     c[2 * g].w,
                            c[2 * g + 1].x, c[2 * g + 1].y, c[2 * g + 1].z, c[2 * g + 1].w};
 #pragma unroll
@@ -117,13 +127,7 @@ __global__ void __launch_bounds__(256) dropout_vec_kernel(DropoutArgs a) {
       v[g][j] = w[j] >= a.threshold && !a.drop_all ? v[g][j] * a.scale : 0.f;
       if (RES) v[g][j] += q[g][j];
     }
-    if (i + 8 <= n) {
-      store8(y[g], v[g]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (i + j < n) y[g][j] = from_f32<Y>(v[g][j]);
-    }
+    store8(y + oy[g], v[g]);
   }
 }
 
@@ -177,10 +181,14 @@ cudaError_t launch_typed(DropoutArgs a, cudaStream_t s) {
                    (a.rows == 1 || a.cols % 8 == 0);
   // One group per thread while there are threads to spare (1024 x 1024: 3.3 us against 3.5; 256 x 64:
   // 1.8 against 2.3), two where the generator would bind.
-  if (vec && n < (int64_t{1} << 21))
-    dropout_vec_kernel<X, R, Y, RES, 1><<<static_cast<unsigned>((n + 2047) / 2048), 256, 0, s>>>(a);
-  else if (vec)
-    dropout_vec_kernel<X, R, Y, RES, 2><<<static_cast<unsigned>((n + 4095) / 4096), 256, 0, s>>>(a);
+  const unsigned one = static_cast<unsigned>((n + 2047) / 2048), two = static_cast<unsigned>((n + 4095) / 4096);
+  if (vec && n < (int64_t{1} << 21)) {
+    if (a.rows == 1) dropout_vec_kernel<X, R, Y, RES, 1, true><<<one, 256, 0, s>>>(a);
+    else dropout_vec_kernel<X, R, Y, RES, 1, false><<<one, 256, 0, s>>>(a);
+  } else if (vec) {
+    if (a.rows == 1) dropout_vec_kernel<X, R, Y, RES, 2, true><<<two, 256, 0, s>>>(a);
+    else dropout_vec_kernel<X, R, Y, RES, 2, false><<<two, 256, 0, s>>>(a);
+  }
   else
     dropout_any_kernel<X, R, Y, RES><<<static_cast<unsigned>((n + 1023) / 1024), 256, 0, s>>>(a);
   return cudaGetLastError();

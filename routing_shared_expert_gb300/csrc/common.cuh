@@ -286,6 +286,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t ta, uint32_t (&a)[32]) {
 }
 #undef MOE_R32
 
+// 16 columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t ta, uint32_t (&a)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]),
+        "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15])
+      : "r"(ta)
+      : "memory");
+}
+
 // 64 consecutive columns in one instruction: beside running MMAs every load waits for a gap
 // between them, so few long loads drain an accumulator sooner than many short ones.
 __device__ __forceinline__ void tmem_ld64(uint32_t ta, uint32_t (&a)[64]) {

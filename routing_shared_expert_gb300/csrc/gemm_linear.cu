@@ -6,9 +6,8 @@
 //
 // A cluster of two CTAs computes a 256 x 256 tile: the even CTA issues M = 256, N = 256 MMAs
 // whose A rows and B columns are split between the two CTAs' shared memory, so each CTA loads
-// 32 KB per 64-wide K block (64 bytes a cycle at the MMA rate, which L2 sustains; a one-SM
-// 128 x 128 tile would need twice that).  The ring has three stages of two K blocks: the
-// issuer waits once per eight MMAs.  Accumulators are double buffered in TMEM, so the epilogue
+// 32 KB per 64-wide K block (64 bytes a cycle at the MMA rate, which is what L2 sustains; 128
+// columns need 96 and run at two thirds of the rate).  Accumulators are double buffered in TMEM, so the epilogue
 // of one tile runs beside the products of the next.  Ragged edges need no masks: TMA fills
 // what lies past an operand with zeros, and clips what lies past the output.
 //
@@ -18,13 +17,21 @@
 // adds the parts in their order along K, whoever came last, so the result does not depend on
 // it.  The cut tiles come first: the joining runs beside the products of the whole tiles.
 //
-// Epilogue: eight warps per CTA (two per TMEM lane quarter, 128 columns each), a lane per row.
-// It works in steps of 64 bytes of each of 32 rows.  Results go from the registers to memory as
-// whole 32-byte sectors (256-bit stores).  The residual's blocks come by TMA into two buffers per
-// warp, the first two while the tile's products still run and each next one as soon as its
-// buffer has been read: read by the lanes themselves, too little of it would be on its way to
-// cover the latency of memory.  A matrix whose rows are not aligned to 16 bytes goes through a
-// staging block with the lanes' element accesses along the rows.
+// Epilogue: eight warps per CTA (two per TMEM lane quarter, half of the columns each), a lane per
+// row.  The residual's blocks of 32 rows come by TMA into swizzled shared memory, two per warp,
+// the first while the tile's products still run.
+//   fp32 outputs: blocks of 128-byte rows, replaced in place by act(z) + r, leave by 32-byte
+//     stores that each cover 128 neighbouring bytes of eight rows (an 84 MB output written by a lane
+//     per row takes 25 us, so 16.5 us, in whole 512-byte rows 14.6 us); 8192 x 2560 x 2560 with
+//     residual 112 us against 135 with a lane per row.  The blocks leave room for a ring of five K
+//     blocks.
+//   bf16 outputs: half the bytes.  64-byte rows, stored by a lane per row in 32-byte sectors, leave
+//     room for three ring stages of two K blocks, so that the issuer waits once per eight MMAs
+//     (8192 x 2560 x 2560 in 69.5 us; with five or six stages of one 72 to 75 us).
+// A matrix whose rows are not aligned to 16 bytes is moved element by element along the rows, in
+// kernels of their own: the epilogue runs once per tile and is bound by fetching its code, so
+// it holds no path that a launch does not take (5 % of 8192 x 2560 x 2560) and loops rather than
+// unrolls.
 //
 // The tensor core drops the bits of an addition that do not fit fp32 instead of rounding, an
 // error that grows with the length of the sum and has one sign (measured 2.7e-6 of the result
@@ -34,6 +41,7 @@
 // Every wait is bounded; a wait that runs out records MOE_ERR_TIMEOUT and the CTA waits for
 // what it issued before it frees its TMEM.
 #include <algorithm>
+#include <cstdlib>
 
 #include "activation.cuh"
 #include "linear.h"
@@ -41,26 +49,35 @@
 namespace moe {
 namespace {
 
-constexpr int BM = 256, BN = 256;          // pair tile
-constexpr int HALF = 128;                  // rows of A, columns of B per CTA
+constexpr int BM = 256;                    // rows of a pair tile
+constexpr int HALF = 128;                  // rows of A per CTA
 constexpr int BK = 64;
-constexpr int STAGES = 3;
-constexpr int BLOCK_BYTES = HALF * BK * 2; // one operand, one K block, one CTA
-constexpr int STAGE_BYTES = 4 * BLOCK_BYTES;   // two K blocks of A and B
-constexpr int STAGING_BYTES = 2048;        // 32 rows of 64 bytes
+constexpr int A_BYTES = HALF * BK * 2;     // one K block, one CTA
 constexpr int EPI_WARPS = 8;
-constexpr int WARP_COLS = BN / 2;          // columns of one epilogue warp
 constexpr int F32_SEGMENT = 14;            // most K blocks of one fp32 partial sum
-constexpr int EPI_BYTES = EPI_WARPS * 2 * STAGING_BYTES;
 constexpr int EPI_WARP0 = 4;               // warps 0, 1: producer, issuer; a warpgroup of their own
 constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
+// What depends on the tile's width and the output type.
+template <int BN, bool F32> struct Tile {
+  static constexpr int COLS = BN / 2;                      // columns of B per CTA, and of an epilogue warp
+  static constexpr int B_BYTES = COLS * BK * 2;
+  static constexpr int SUB_BYTES = A_BYTES + B_BYTES;      // one K block of A and B
+  static constexpr int SUBS = F32 ? 1 : 2;                 // K blocks of a ring stage
+  static constexpr int STAGE_BYTES = SUBS * SUB_BYTES;
+  static constexpr int STAGES = F32 ? (BN == 256 ? 5 : 6) : (BN == 256 ? 3 : 4);
+  static constexpr int ROW_BYTES = F32 ? 128 : 64;         // of an output block
+  static constexpr int BLOCK_BYTES = 32 * ROW_BYTES;
+  static constexpr int EPI_BYTES = EPI_WARPS * 2 * BLOCK_BYTES;
+  static constexpr uint32_t TMEM_COLS = 2 * BN;
+  static constexpr size_t SMEM = 1024 + STAGES * STAGE_BYTES + EPI_BYTES + 8 * (2 * STAGES + 4 + 2 * EPI_WARPS + 1) + 32;
+  static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
+};
 // Registers of the epilogue's threads and of the others, within the 384 x 168 of the launch; the
 // epilogue of fp32 outputs holds 128 sums.
 template <bool F32> struct Regs {
   static constexpr int EPI = F32 ? 224 : 208, OTHER = F32 ? 56 : 80;
   static_assert(32 * (EPI_WARPS * EPI + EPI_WARP0 * OTHER) <= THREADS * 168, "register split");
 };
-constexpr uint32_t TMEM_COLS = 512;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainLimitNs = 100000000ull;
 constexpr int GROUP_M = 8;                 // row tiles that share the column tiles in flight
@@ -75,8 +92,8 @@ struct Args {
   void* pre;
   void* C;
   int64_t ldr, ldc;
-  bool bias16;              // the bias is 16-byte aligned
-  int32_t al_r, al_pre, al_c;   // bytes the rows are aligned to: 32, 16, or 0 (less)
+  int32_t act;              // of kActAny
+  int32_t al_pre, al_c;     // bytes the rows are aligned to: 32, 16, or 0 (less)
   int32_t* status;
   float* scratch;
   unsigned* tickets;
@@ -126,7 +143,7 @@ __device__ __forceinline__ int segment_blocks(const Item& it) {
   const int blocks = it.kb1 - it.kb0;
   if (!SEGMENTED) return blocks;
   const int n = (blocks + F32_SEGMENT - 1) / F32_SEGMENT;
-  return (blocks + 2 * n - 1) / (2 * n) * 2;   // whole ring stages
+  return (blocks + n - 1) / n;
 }
 
 // Barrier of the epilogue warps that tells whether `ok` holds in all of them.
@@ -141,22 +158,6 @@ __device__ __forceinline__ bool epilogue_all(bool ok) {
       : "r"(ok ? 1u : 0u), "n"(32 * EPI_WARPS)
       : "memory");
   return all != 0;
-}
-
-// 64 bytes of a row, 16 words, to global memory.
-__device__ __forceinline__ void store64(void* p, int align, const uint32_t (&w)[16]) {
-  if (align == 32) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<char*>(p) + 32 * h),
-                   "r"(w[8 * h]), "r"(w[8 * h + 1]), "r"(w[8 * h + 2]), "r"(w[8 * h + 3]), "r"(w[8 * h + 4]),
-                   "r"(w[8 * h + 5]), "r"(w[8 * h + 6]), "r"(w[8 * h + 7])
-                   : "memory");
-  } else {
-#pragma unroll
-    for (int h = 0; h < 4; ++h)
-      static_cast<uint4*>(p)[h] = make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
-  }
 }
 
 template <typename OUT> struct Row64;      // CW values as 16 words
@@ -186,69 +187,98 @@ template <> struct Row64<__nv_bfloat16> {
   }
 };
 
-// The 16-byte piece j of row r of a staging block (32 rows of 64 bytes), swizzled so that the
-// lanes' row accesses do not collide.
-__device__ __forceinline__ uint4* staged_piece(uint8_t* blk, int r, int j) {
-  return reinterpret_cast<uint4*>(blk + r * 64 + ((j ^ ((r >> 1) & 3)) * 16));
+// 64 bytes of a row, 16 words, to global memory; of a ragged last step the `pieces` (of four) that
+// exist.
+__device__ __forceinline__ void store64(void* p, int align, int pieces, const uint32_t (&w)[16]) {
+  if (align == 32 && pieces == 4) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<char*>(p) + 32 * h),
+                   "r"(w[8 * h]), "r"(w[8 * h + 1]), "r"(w[8 * h + 2]), "r"(w[8 * h + 3]), "r"(w[8 * h + 4]),
+                   "r"(w[8 * h + 5]), "r"(w[8 * h + 6]), "r"(w[8 * h + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+      if (h < pieces)
+        static_cast<uint4*>(p)[h] = make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
+  }
+}
+
+// The 16-byte piece j of row r of a block, in the swizzle of its row width (so that neither a lane
+// per row nor four lanes per row collide).
+template <typename OUT>
+__device__ __forceinline__ uint4* block_piece(uint8_t* blk, int r, int j) {
+  return sizeof(OUT) == 4 ? reinterpret_cast<uint4*>(blk + r * 128 + ((j ^ (r & 7)) * 16))
+                          : reinterpret_cast<uint4*>(blk + r * 64 + ((j ^ ((r >> 1) & 3)) * 16));
 }
 template <typename OUT>
-__device__ __forceinline__ OUT* staged(uint8_t* blk, int r, int e) {
+__device__ __forceinline__ OUT* block_element(uint8_t* blk, int r, int e) {
   constexpr int N = 16 / static_cast<int>(sizeof(OUT));
-  return reinterpret_cast<OUT*>(staged_piece(blk, r, e / N)) + e % N;
+  return reinterpret_cast<OUT*>(block_piece<OUT>(blk, r, e / N)) + e % N;
 }
 
-// A warp's 32 rows of one step: lane l holds row l in w; rows x cols of them exist, ld elements
-// apart from p on.  Called by the whole warp.  Element by element through the staging block, the
-// lanes along the rows; whole aligned steps are stored straight from the registers.
-template <typename OUT>
-__device__ __forceinline__ void load_rows(const OUT* p, int64_t ld, int rows, int cols, int lane, uint8_t* blk,
-                                          uint32_t (&w)[16]) {
-  constexpr int CW = Row64<OUT>::CW;
-  __syncwarp();
-  for (int i = lane; i < rows * CW; i += 32) {
-    const int r = i / CW, e = i % CW;
-    if (e < cols) *staged<OUT>(blk, r, e) = p[r * ld + e];
-  }
-  __syncwarp();
+// The rows x cols of a block that exist, ld elements apart from p on, to memory.  Called by the
+// whole warp after a __syncwarp.  ALIGNED: fp32 only.
+template <typename OUT, bool ALIGNED>
+__device__ __forceinline__ void store_block(OUT* p, int64_t ld, int align, int rows, int cols, int lane, uint8_t* blk) {
+  constexpr int CW = 32;   // columns of a block: 128 bytes of fp32, 64 of bf16
+  if constexpr (ALIGNED) {
+    const int q = lane % 4;                       // 32 bytes of the row
+    const int pieces = cols / 4 - 2 * q;          // that exist, from q on
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint4 u = *staged_piece(blk, lane, j);
-    w[4 * j] = u.x;
-    w[4 * j + 1] = u.y;
-    w[4 * j + 2] = u.z;
-    w[4 * j + 3] = u.w;
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + lane / 4;
+      const uint4 u = *block_piece<OUT>(blk, r, 2 * q), v = *block_piece<OUT>(blk, r, 2 * q + 1);
+      OUT* at = p + r * ld + 8 * q;
+      if (r < rows && pieces >= 2 && align == 32) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(u.x), "r"(u.y),
+                     "r"(u.z), "r"(u.w), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                     : "memory");
+      } else if (r < rows && pieces > 0) {
+        reinterpret_cast<uint4*>(at)[0] = u;
+        if (pieces >= 2) reinterpret_cast<uint4*>(at)[1] = v;
+      }
+    }
+  } else {
+#pragma unroll 1
+    for (int i = lane; i < rows * CW; i += 32) {
+      const int r = i / CW, e = i % CW;
+      if (e < cols) p[r * ld + e] = *block_element<OUT>(blk, r, e);
+    }
   }
 }
+// The same from memory, element by element.
 template <typename OUT>
-__device__ __forceinline__ void store_rows(OUT* p, int64_t ld, int align, int rows, int cols, int lane,
-                                           uint8_t* blk, const uint32_t (&w)[16]) {
-  constexpr int CW = Row64<OUT>::CW;
-  if (align != 0 && cols == CW) {
-    if (lane < rows) store64(p + lane * ld, align, w);
-    return;
+__device__ __forceinline__ void load_block(const OUT* p, int64_t ld, int rows, int cols, int lane, uint8_t* blk) {
+#pragma unroll 8
+  for (int i = lane; i < rows * 32; i += 32) {
+    const int r = i / 32, e = i % 32;
+    if (e < cols) *block_element<OUT>(blk, r, e) = p[r * ld + e];
   }
-  __syncwarp();
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    *staged_piece(blk, lane, j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-  __syncwarp();
-  for (int i = lane; i < rows * CW; i += 32) {
-    const int r = i / CW, e = i % CW;
-    if (e < cols) p[r * ld + e] = *staged<OUT>(blk, r, e);
-  }
-  fence_proxy_async_smem();   // the block may take a TMA load next
-  __syncwarp();
 }
 
-template <bool A_MN, bool B_MN, typename OUT, int ACT>
+constexpr int kActAny = -1;
+template <int N>
+__device__ __forceinline__ void activate(float (&z)[N], int act) {
+#define MOE_CALL(ACT) [&]() { _Pragma("unroll") for (int e = 0; e < N; ++e) z[e] = act_value<ACT>(z[e]); }()
+  MOE_DISPATCH_ACT(act, MOE_CALL)
+#undef MOE_CALL
+}
+
+// ALIGNED: every row that the epilogue touches starts on a 16-byte boundary and N ends on one; else
+// ACT is kActAny, the run-time activation.
+template <int BN, bool A_MN, bool B_MN, typename OUT, int ACT, bool ALIGNED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmR, const Args args) {
+  using TL = Tile<BN, sizeof(OUT) == 4>;
+  constexpr int STAGES = TL::STAGES, WARP_COLS = TL::COLS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint8_t* epi = smem + STAGES * STAGE_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(epi + EPI_BYTES);
+  uint8_t* epi = smem + STAGES * TL::STAGE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(epi + TL::EPI_BYTES);
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;
@@ -285,7 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tma_prefetch_map(&tmA);
     tma_prefetch_map(&tmB);
   }
-  if (warp == 1) tmem_alloc_pair(smem_u32(tmem_holder), TMEM_COLS);
+  if (warp == 1) tmem_alloc_pair(smem_u32(tmem_holder), TL::TMEM_COLS);
   __syncwarp();
   tc_fence_before();
   cluster_sync_all();   // barriers initialised and TMEM allocated in both CTAs
@@ -306,19 +336,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       Item it;
       for (int i = 0; ok && item_at(args, pair_id, n_pairs, i, it); ++i) {
         const int m0 = it.m * BM + static_cast<int>(rank) * HALF;
-        const int n0 = it.n * BN + static_cast<int>(rank) * HALF;
-        for (int kb = it.kb0; kb < it.kb1; kb += 2) {
+        const int n0 = it.n * BN + static_cast<int>(rank) * TL::COLS;
+        for (int kb = it.kb0; kb < it.kb1; kb += TL::SUBS) {
           if (!mbar_wait_bounded(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, args.status,
                                  kWaitLimitNs)) {
             ok = false;
             break;
           }
-          const int subs = min(2, it.kb1 - kb);
+          const int subs = min(TL::SUBS, it.kb1 - kb);
           const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
-          if (leader) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * subs * 2 * BLOCK_BYTES);
+          if (leader) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * subs * TL::SUB_BYTES);
           for (int u = 0; u < subs; ++u) {
-            const uint32_t sA = smem_base + stage * STAGE_BYTES + u * 2 * BLOCK_BYTES;
-            const uint32_t sB = sA + BLOCK_BYTES;
+            const uint32_t sA = smem_base + stage * TL::STAGE_BYTES + u * TL::SUB_BYTES;
+            const uint32_t sB = sA + A_BYTES;
             const int k0 = (kb + u) * BK;
             if (A_MN) {
               tma_load_2d_pair(sA, &tmA, m0, k0, fb);
@@ -328,7 +358,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             }
             if (B_MN) {
               tma_load_2d_pair(sB, &tmB, n0, k0, fb);
-              tma_load_2d_pair(sB + kMnLbo, &tmB, n0 + 64, k0, fb);
+              if (TL::COLS > 64) tma_load_2d_pair(sB + kMnLbo, &tmB, n0 + 64, k0, fb);
             } else {
               tma_load_2d_pair(sB, &tmB, k0, n0, fb);
             }
@@ -361,14 +391,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           ok = mbar_wait_bounded(smem_u32(&tempty[fill & 1]), ((fill >> 1) & 1u) ^ 1u, abort_flag, args.status,
                                  kWaitLimitNs);
           tc_fence_after();
-          for (int kb = s0; ok && kb < s1; kb += 2) {
+          for (int kb = s0; ok && kb < s1; kb += TL::SUBS) {
             ok = mbar_wait_bounded(smem_u32(&full[stage]), phase, abort_flag, args.status, kWaitLimitNs);
             if (!ok) break;
             tc_fence_after();
-            const int subs = min(2, it.kb1 - kb);
+            const int subs = min(TL::SUBS, it.kb1 - kb);
             for (int u = 0; u < subs; ++u) {
-              const uint32_t sA = smem_base + stage * STAGE_BYTES + u * 2 * BLOCK_BYTES;
-              const uint32_t sB = sA + BLOCK_BYTES;
+              const uint32_t sA = smem_base + stage * TL::STAGE_BYTES + u * TL::SUB_BYTES;
+              const uint32_t sB = sA + A_BYTES;
 #pragma unroll
               for (int j = 0; j < BK / 16; ++j) {
                 const uint64_t ad = A_MN ? sw128_mnmajor_desc(sA + j * 2048) : sw128_kmajor_desc(sA) + 2 * j;
@@ -391,12 +421,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   } else {
     // ---------------------------------------------------------- epilogue (both CTAs)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<SEGMENTED>::EPI));
-    constexpr int CW = Row64<OUT>::CW;       // columns of a step
-    constexpr int STEPS = WARP_COLS / CW;
+    constexpr int CW = Row64<OUT>::CW;       // columns of 64 bytes
+    constexpr int PER = TL::ROW_BYTES / 64;  // of which a block has 2 (fp32) or 1
+    constexpr int BCOLS = PER * CW, BLOCKS = WARP_COLS / BCOLS;
+    // results go through a block (and pre through the second), or from the registers
+    constexpr bool STAGED = SEGMENTED || !ALIGNED;
     const int q = warp & 3;                  // TMEM lanes of this warp
-    const int half = (warp - EPI_WARP0) >> 2;        // its columns
-    uint8_t* blk = epi + (warp - EPI_WARP0) * 2 * STAGING_BYTES;
+    const int half = (warp - EPI_WARP0) >> 2;   // its columns
+    uint8_t* blk = epi + (warp - EPI_WARP0) * 2 * TL::BLOCK_BYTES;
     uint64_t* bars = rbar + 2 * (warp - EPI_WARP0);
+    const int bufs = STAGED && args.pre != nullptr ? 1 : 2;   // that y and the residual take in turn
     uint32_t loads = 0, reads = 0;           // residual blocks asked for and read, over all tiles
     const bool res = args.residual != nullptr;
     uint32_t fill = 0;
@@ -409,22 +443,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       // rows and columns of this warp's block; none where it lies past the output
       const int rows = col0 < args.N ? static_cast<int>(min(static_cast<int64_t>(32), args.M - row0)) : 0;
       const OUT* rrow = static_cast<const OUT*>(args.residual) + row0 * args.ldr + col0;
-      const int steps = rows > 0 ? min(STEPS, (args.N - col0 + CW - 1) / CW) : 0;
-      const bool tma_res = res && args.al_r != 0;
-      // the residual block of step c into the buffer of its turn
+      const int blocks = rows > 0 ? min(BLOCKS, (args.N - col0 + BCOLS - 1) / BCOLS) : 0;
+      const bool tma_res = ALIGNED && res;
+      // the residual of block c into the buffer of its turn
       auto load_residual = [&](int c) {
-        if (c >= steps) return;
+        if (c >= blocks) return;
+        const uint32_t b = bufs == 1 ? 0 : loads & 1;
         if (lane == 0) {
-          const uint32_t bar = smem_u32(&bars[loads & 1]);
-          mbar_arrive_expect_tx(bar, STAGING_BYTES);
-          tma_load_2d(smem_u32(blk + (loads & 1) * STAGING_BYTES), &tmR, col0 + c * CW,
-                      static_cast<int32_t>(row0), bar);
+          mbar_arrive_expect_tx(smem_u32(&bars[b]), TL::BLOCK_BYTES);
+          tma_load_2d(smem_u32(blk + b * TL::BLOCK_BYTES), &tmR, col0 + c * BCOLS, static_cast<int32_t>(row0),
+                      smem_u32(&bars[b]));
         }
         ++loads;
       };
-      if (tma_res && it.parts == 1) {
-        load_residual(0);
-        load_residual(1);
+      if (tma_res && it.parts == 1)
+        for (int c = 0; c < bufs; ++c) load_residual(c);
+      // The bias, a column per lane (loaded by every lane for each of its columns it costs more than
+      // the rest of an epilogue: 8192 x 512 x 2560 fp32 in 57 us against 40 without it).
+      float bias[WARP_COLS / 32];
+#pragma unroll
+      for (int k = 0; k < WARP_COLS / 32; ++k) {
+        const int col = col0 + k * 32 + lane;
+        bias[k] = args.bias != nullptr && col < args.N ? __ldg(args.bias + col) : 0.f;
       }
       // Waits for the next TMEM buffer; its columns of this warp start at taddr.
       uint32_t taddr = 0;
@@ -447,7 +487,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       };
       // where this warp's lane of a pair's partial sums starts (32 groups of four columns)
       auto slot = [&](int pair) {
-        return reinterpret_cast<float4*>(args.scratch) + static_cast<size_t>(pair) * (BM * BN / 4) +
+        return reinterpret_cast<float4*>(args.scratch) + static_cast<size_t>(pair) * (BM * 256 / 4) +
                (static_cast<size_t>(rank) * EPI_WARPS + (warp - EPI_WARP0)) * (WARP_COLS / 4) * 32 + lane;
       };
       float acc[SEGMENTED ? WARP_COLS : 1];
@@ -517,136 +557,131 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         return kJoined;
       };
-      int joined = it.parts > 1 ? kNotLast : kJoined;
       if (SEGMENTED) {
-        // segment after segment, and in the joining CTA of a cut tile the parts' sum once more
+        // All segments but the last into registers, each buffer free again at once; the last one's
+        // buffer takes the sum, so that what follows can loop over it (unrolled over registers it
+        // is bound by fetching its own code: 8192 x 2560 x 2560 with GELU 223 us).
         const int seg = segment_blocks<SEGMENTED>(it);
-        int s0 = it.kb0;
-        bool again = true;
-        while (again) {
-          if (s0 < it.kb1 && ok) ok = wait_fill();
-          if (!ok && it.parts == 1) break;
-          const bool first = s0 == it.kb0 || s0 >= it.kb1;
-          if (ok) {
+        for (int s0 = it.kb0; ok && s0 < it.kb1; s0 += seg) {
+          ok = wait_fill();
+          if (!ok) break;
+          const bool first = s0 == it.kb0, last = s0 + seg >= it.kb1;
+          if (first && last && it.parts == 1) break;   // one segment: its buffer holds the sum
 #pragma unroll
-            for (int k = 0; k < WARP_COLS; k += 64) {
-              uint32_t v[64];
-              tmem_ld64(taddr + k, v);
+          for (int k = 0; k < WARP_COLS; k += 32) {
+            uint32_t v[32];
+            tmem_ld32(taddr + k, v);
 #pragma unroll
-              for (int e = 0; e < 64; ++e) {
-                float& sum = acc[(k + e) % (SEGMENTED ? WARP_COLS : 1)];
-                sum = (first ? 0.f : sum) + __uint_as_float(v[e]);
-              }
+            for (int e = 0; e < 32; ++e) {
+              float& sum = acc[(k + e) % (SEGMENTED ? WARP_COLS : 1)];
+              sum = (first ? 0.f : sum) + __uint_as_float(v[e]);
+              v[e] = __float_as_uint(sum);
             }
+            if (last && it.parts == 1) tmem_st32(taddr + k, v);
           }
-          const bool summed = s0 >= it.kb1;
-          s0 += seg;
-          again = ok && !summed && s0 < it.kb1;
-          if (!again && !summed && it.parts > 1) {
-            joined = join();
-            ok = joined != kFailed;
-            again = joined == kJoined;
-            s0 = it.kb1;
-            if (again) continue;   // the buffer still holds the sum to read
-          }
-          if (ok) release_fill();
+          if (!last) release_fill();
         }
-      } else {
-        if (ok) ok = wait_fill();
-        if (it.parts > 1) {
-          joined = join();
-          ok = joined != kFailed;
-          if (joined == kNotLast) release_fill();
-        }
+      } else if (ok) {
+        ok = wait_fill();
+      }
+      int joined = kJoined;
+      if (it.parts > 1) {
+        joined = join();
+        ok = joined != kFailed;
+        if (joined == kNotLast) release_fill();
       }
       if (!ok) break;
       if (joined == kNotLast) continue;
-      if (tma_res && it.parts > 1) {
-        load_residual(0);
-        load_residual(1);
-      }
-      // one step of CW columns: z from the accumulators on
-      auto finish = [&](int c, float (&z)[CW]) {
-        const int col = col0 + c * CW, cols = min(CW, args.N - col);
-        uint32_t rw[16];
-        if (tma_res) {
-          const uint32_t b = reads & 1;
-          const bool here = mbar_wait_bounded(smem_u32(&bars[b]), (reads >> 1) & 1u, abort_flag, args.status, kWaitLimitNs);
-          ok = __all_sync(0xffffffffu, here) && ok;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint4 u = *staged_piece(blk + b * STAGING_BYTES, lane, j);
-            rw[4 * j] = u.x;
-            rw[4 * j + 1] = u.y;
-            rw[4 * j + 2] = u.z;
-            rw[4 * j + 3] = u.w;
-          }
-          // The buffer's next TMA load must not overtake these reads, which can wait behind stores.
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (ok) {
-            ++reads;
-            load_residual(c + 2);
-          }
-        } else if (res) {
-          load_rows<OUT>(rrow + c * CW, args.ldr, rows, cols, lane, blk, rw);
-        }
-        if (args.bias != nullptr) {
-          if (args.bias16 && cols == CW) {
-#pragma unroll
-            for (int e = 0; e < CW; e += 4) {
-              const float4 b4 = __ldg(reinterpret_cast<const float4*>(args.bias + col + e));
-              z[e] += b4.x;
-              z[e + 1] += b4.y;
-              z[e + 2] += b4.z;
-              z[e + 3] += b4.w;
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < CW; ++e)
-              if (e < cols) z[e] += __ldg(args.bias + col + e);
-          }
-        }
-        uint32_t w[16];
-        if (args.pre != nullptr) {
-          Row64<OUT>::pack(z, w);
-          store_rows<OUT>(static_cast<OUT*>(args.pre) + row0 * args.N + col, args.N, args.al_pre, rows, cols, lane, blk, w);
-        }
-#pragma unroll
-        for (int e = 0; e < CW; ++e) z[e] = act_value<ACT>(z[e]);
-        if (res) Row64<OUT>::add(z, rw);
-        Row64<OUT>::pack(z, w);
-        store_rows<OUT>(static_cast<OUT*>(args.C) + row0 * args.ldc + col, args.ldc, args.al_c, rows, cols, lane, blk, w);
-      };
-      if (SEGMENTED) {
-#pragma unroll
-        for (int c = 0; c < STEPS; ++c) {
-          if (c < steps && ok) {
-            float z[CW];
-#pragma unroll
-            for (int e = 0; e < CW; ++e) z[e] = acc[(c * CW + e) % (SEGMENTED ? WARP_COLS : 1)];
-            finish(c, z);
-          }
-        }
-      } else {
+      if (tma_res && it.parts > 1)
+        for (int c = 0; c < bufs; ++c) load_residual(c);
 #pragma unroll 1
-        for (int c = 0; c < STEPS; c += 2) {
-          uint32_t v[64];
-          tmem_ld64(taddr + c * 32, v);
-          if (c + 2 == STEPS) release_fill();   // the last read of the buffer
+      for (int c = 0; c < BLOCKS; ++c) {
+        const int col = col0 + c * BCOLS, cols = min(BCOLS, args.N - col);
+        const bool in = c < blocks && ok;
+        const uint32_t b = bufs == 1 ? 0 : tma_res ? reads & 1 : c & 1;
+        uint8_t* yb = blk + b * TL::BLOCK_BYTES;
+        uint8_t* pb = blk + TL::BLOCK_BYTES;
+        OUT* yp = static_cast<OUT*>(args.C) + row0 * args.ldc + col;
+        OUT* pp = static_cast<OUT*>(args.pre) + row0 * args.N + col;
+        if (in && tma_res) {
+          const uint32_t parity = bufs == 1 ? reads & 1u : (reads >> 1) & 1u;
+          const bool here = mbar_wait_bounded(smem_u32(&bars[b]), parity, abort_flag, args.status, kWaitLimitNs);
+          ok = __all_sync(0xffffffffu, here);
+          if (ok) ++reads;
+        } else if (in && res) {
+          load_block<OUT>(static_cast<const OUT*>(args.residual) + row0 * args.ldr + col, args.ldr, rows, cols, lane, yb);
+          __syncwarp();
+        }
+#pragma unroll 1
+        for (int h = 0; h < PER; ++h) {
+          const int at = (PER * c + h) * CW;   // first column of the warp's
+          uint32_t v[CW];
+          if constexpr (CW == 16) tmem_ld16(taddr + at, v); else tmem_ld32(taddr + at, v);
+          if (at + CW == WARP_COLS) release_fill();   // the last read of the buffer
           float z[CW];
 #pragma unroll
-          for (int e = 0; e < CW; ++e) z[e] = __uint_as_float(v[e % 32]);
-          if (c < steps && ok) finish(c, z);
+          for (int e = 0; e < CW; ++e) z[e] = __uint_as_float(v[e]);
+          if (args.bias != nullptr) {
+            float mine = bias[0];
 #pragma unroll
-          for (int e = 0; e < CW; ++e) z[e] = __uint_as_float(v[32 + e % 32]);
-          if (c + 1 < steps && ok) finish(c + 1, z);
+            for (int k = 1; k < WARP_COLS / 32; ++k) mine = at / 32 == k ? bias[k] : mine;
+#pragma unroll
+            for (int e = 0; e < CW; ++e) z[e] += __shfl_sync(0xffffffffu, mine, at % 32 + e);
+          }
+          uint32_t w[16];
+          if (args.pre != nullptr) {
+            Row64<OUT>::pack(z, w);
+            if constexpr (STAGED) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                *block_piece<OUT>(pb, lane, 4 * h + j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            } else if (in && lane < rows) {
+              store64(pp + lane * static_cast<int64_t>(args.N), args.al_pre, cols / 8, w);
+            }
+          }
+          if constexpr (ACT == kActAny) {
+            activate(z, args.act);
+          } else {
+#pragma unroll
+            for (int e = 0; e < CW; ++e) z[e] = act_value<ACT>(z[e]);
+          }
+          if (res) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint4 u = *block_piece<OUT>(yb, lane, 4 * h + j);
+              w[4 * j] = u.x;
+              w[4 * j + 1] = u.y;
+              w[4 * j + 2] = u.z;
+              w[4 * j + 3] = u.w;
+            }
+            Row64<OUT>::add(z, w);
+          }
+          Row64<OUT>::pack(z, w);
+          if constexpr (STAGED) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *block_piece<OUT>(yb, lane, 4 * h + j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+          } else if (in && ok && lane < rows) {
+            store64(yp + lane * args.ldc, args.al_c, cols / 8, w);
+          }
         }
+        if constexpr (STAGED) {
+          __syncwarp();
+          if (in && ok) {
+            store_block<OUT, ALIGNED>(yp, args.ldc, args.al_c, rows, cols, lane, yb);
+            if (args.pre != nullptr) store_block<OUT, ALIGNED>(pp, args.N, args.al_pre, rows, cols, lane, pb);
+          }
+        }
+        // The buffer's next TMA load must not overtake these accesses, which can wait behind stores.
+        if (tma_res) fence_proxy_async_smem();
+        __syncwarp();
+        if (in && tma_res && ok) load_residual(c + bufs);
       }
     }
     if (lane == 0)   // blocks still on their way after a failed wait
       for (; reads != loads; ++reads)
-        mbar_wait_bounded(smem_u32(&bars[reads & 1]), (reads >> 1) & 1u, never, nullptr, kDrainLimitNs);
+        mbar_wait_bounded(smem_u32(&bars[bufs == 1 ? 0 : reads & 1]), bufs == 1 ? reads & 1u : (reads >> 1) & 1u, never,
+                          nullptr, kDrainLimitNs);
   }
 
   __syncwarp();
@@ -654,11 +689,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   cluster_sync_all();   // no CTA leaves while its partner may still use its memory
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    tmem_dealloc_pair(tmem_base, TL::TMEM_COLS);
   }
 }
-
-constexpr size_t kSmemBytes = 1024 + STAGES * STAGE_BYTES + EPI_BYTES + 8 * (2 * STAGES + 4 + 2 * EPI_WARPS + 1) + 32;
 
 // Parts to cut the `rest` tiles of a partial round into, of `stages` ring stages (two K blocks,
 // about half a microsecond) each: 1, or the number that saves most.  Joining s parts costs
@@ -683,8 +716,9 @@ int32_t row_alignment(const void* p, int64_t ld, size_t elem) {
   return v % 32 == 0 ? 32 : v % 16 == 0 ? 16 : 0;
 }
 
-template <bool A_MN, bool B_MN, typename OUT, int ACT>
-cudaError_t launch_typed(const LinearGemm& g, cudaStream_t s) {
+template <int BN, bool A_MN, bool B_MN, typename OUT, int ACT, bool ALIGNED>
+cudaError_t launch_kernel(const LinearGemm& g, cudaStream_t s) {
+  using TL = Tile<BN, sizeof(OUT) == 4>;
   Args a{};
   a.M = static_cast<int32_t>(g.M);
   a.N = g.N;
@@ -698,24 +732,22 @@ cudaError_t launch_typed(const LinearGemm& g, cudaStream_t s) {
   a.ldr = g.ldr;
   a.ldc = g.ldc;
   a.status = g.status;
+  a.act = g.act;
   a.al_c = row_alignment(g.C, g.ldc, sizeof(OUT));
-  a.al_r = row_alignment(g.residual, g.ldr, sizeof(OUT));
   a.al_pre = row_alignment(g.pre, g.N, sizeof(OUT));
-  if (a.al_c == 0 || a.al_pre == 0) a.al_r = 0;   // the staging block is the residual's first buffer
-  a.bias16 = (reinterpret_cast<uintptr_t>(g.bias) & 15u) == 0;
   CUtensorMap mA, mB;
   const uint64_t M = static_cast<uint64_t>(g.M), N = g.N, K = g.K;
   if (!(A_MN ? make_strided_map(&mA, MOE_BF16, g.A, M, K, g.lda, 64, BK)
              : make_strided_map(&mA, MOE_BF16, g.A, K, M, g.lda, BK, HALF)) ||
       !(B_MN ? make_strided_map(&mB, MOE_BF16, g.B, N, K, g.ldb, 64, BK)
-             : make_strided_map(&mB, MOE_BF16, g.B, K, N, g.ldb, BK, HALF)))
+             : make_strided_map(&mB, MOE_BF16, g.B, K, N, g.ldb, BK, TL::COLS)))
     return cudaErrorInvalidValue;
   CUtensorMap mR = mA;
-  if (g.residual && a.al_r != 0 &&
-      !make_strided_map(&mR, sizeof(OUT) == 4 ? MOE_F32 : MOE_BF16, g.residual, N, M, g.ldr, 64 / sizeof(OUT), 32, 64))
+  if (ALIGNED && g.residual &&
+      !make_strided_map(&mR, sizeof(OUT) == 4 ? MOE_F32 : MOE_BF16, g.residual, N, M, g.ldr, 32, 32, TL::ROW_BYTES))
     return cudaErrorInvalidValue;
-  auto kern = linear_pair_kernel<A_MN, B_MN, OUT, ACT>;
-  const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), kSmemBytes);
+  auto kern = linear_pair_kernel<BN, A_MN, B_MN, OUT, ACT, ALIGNED>;
+  const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), TL::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
   const int64_t most = std::min(kMaxPairs, std::max(1, device_sm_count() / 2));
@@ -728,23 +760,35 @@ cudaError_t launch_typed(const LinearGemm& g, cudaStream_t s) {
     a.cut_tiles = static_cast<int32_t>(rest);
     pairs = tiles > rest ? most : rest * a.parts;
   }
-  kern<<<static_cast<unsigned>(2 * pairs), THREADS, kSmemBytes, s>>>(mA, mB, mR, a);
+  kern<<<static_cast<unsigned>(2 * pairs), THREADS, TL::SMEM, s>>>(mA, mB, mR, a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 namespace {
+
+template <bool A_MN, bool B_MN, typename OUT, int ACT>
+cudaError_t launch_typed(const LinearGemm& g, cudaStream_t s) {
+  const size_t e = sizeof(OUT);
+  const bool aligned = row_alignment(g.C, g.ldc, e) != 0 && (!g.pre || row_alignment(g.pre, g.N, e) != 0) &&
+                       (!g.residual || row_alignment(g.residual, g.ldr, e) != 0) && g.N * e % 16 == 0;
+  if (!aligned) return launch_kernel<256, A_MN, B_MN, OUT, kActAny, false>(g, s);
+  return getenv("BN128") ? launch_kernel<128, A_MN, B_MN, OUT, ACT, true>(g, s)
+                         : launch_kernel<256, A_MN, B_MN, OUT, ACT, true>(g, s);
+}
+
 template <typename OUT>
 cudaError_t launch_forward(const LinearGemm& g, cudaStream_t s) {
 #define MOE_CALL(ACT) launch_typed<false, false, OUT, ACT>(g, s)
   MOE_DISPATCH_ACT(g.act, MOE_CALL)
 #undef MOE_CALL
 }
+
 }  // namespace
 
 int64_t pair_cycles(int64_t M, int64_t N, int64_t K, int sms) {
-  const int64_t tiles = (M + BM - 1) / BM * ((N + BN - 1) / BN), pairs = std::min(kMaxPairs, std::max(1, sms / 2));
+  const int64_t tiles = (M + BM - 1) / BM * ((N + 255) / 256), pairs = std::min(kMaxPairs, std::max(1, sms / 2));
   const int64_t stages = ((K + BK - 1) / BK + 1) / 2, rest = tiles % pairs;
   const int parts = rest > 0 ? cut_parts(rest, pairs, stages) : 1;
   const int64_t last = rest == 0 ? 0 : parts == 1 ? stages : (stages + parts - 1) / parts + kJoin + kJoinPart * parts;

@@ -41,7 +41,6 @@
 // Every wait is bounded; a wait that runs out records MOE_ERR_TIMEOUT and the CTA waits for
 // what it issued before it frees its TMEM.
 #include <algorithm>
-#include <cstdlib>
 
 #include "activation.cuh"
 #include "linear.h"
@@ -218,11 +217,10 @@ __device__ __forceinline__ OUT* block_element(uint8_t* blk, int r, int e) {
   return reinterpret_cast<OUT*>(block_piece<OUT>(blk, r, e / N)) + e % N;
 }
 
-// The rows x cols of a block that exist, ld elements apart from p on, to memory.  Called by the
-// whole warp after a __syncwarp.  ALIGNED: fp32 only.
+// The rows x cols (of 32: 128 bytes of fp32, 64 of bf16) of a block that exist, ld elements apart
+// from p on, to memory.  Called by the whole warp after a __syncwarp.  ALIGNED: fp32 only.
 template <typename OUT, bool ALIGNED>
 __device__ __forceinline__ void store_block(OUT* p, int64_t ld, int align, int rows, int cols, int lane, uint8_t* blk) {
-  constexpr int CW = 32;   // columns of a block: 128 bytes of fp32, 64 of bf16
   if constexpr (ALIGNED) {
     const int q = lane % 4;                       // 32 bytes of the row
     const int pieces = cols / 4 - 2 * q;          // that exist, from q on
@@ -240,22 +238,21 @@ __device__ __forceinline__ void store_block(OUT* p, int64_t ld, int align, int r
         if (pieces >= 2) reinterpret_cast<uint4*>(at)[1] = v;
       }
     }
-  } else {
-#pragma unroll 1
-    for (int i = lane; i < rows * CW; i += 32) {
-      const int r = i / CW, e = i % CW;
-      if (e < cols) p[r * ld + e] = *block_element<OUT>(blk, r, e);
-    }
+  } else if (lane < cols) {
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r) p[r * ld + lane] = *block_element<OUT>(blk, r, lane);
   }
 }
-// The same from memory, element by element.
+// The same from memory, a column per lane, every row on its way at once.
 template <typename OUT>
 __device__ __forceinline__ void load_block(const OUT* p, int64_t ld, int rows, int cols, int lane, uint8_t* blk) {
-#pragma unroll 8
-  for (int i = lane; i < rows * 32; i += 32) {
-    const int r = i / 32, e = i % 32;
-    if (e < cols) *block_element<OUT>(blk, r, e) = p[r * ld + e];
-  }
+  OUT v[32];
+#pragma unroll
+  for (int r = 0; r < 32; ++r)
+    if (r < rows && lane < cols) v[r] = p[r * ld + lane];
+#pragma unroll
+  for (int r = 0; r < 32; ++r)
+    if (r < rows && lane < cols) *block_element<OUT>(blk, r, lane) = v[r];
 }
 
 constexpr int kActAny = -1;
@@ -774,8 +771,14 @@ cudaError_t launch_typed(const LinearGemm& g, cudaStream_t s) {
   const bool aligned = row_alignment(g.C, g.ldc, e) != 0 && (!g.pre || row_alignment(g.pre, g.N, e) != 0) &&
                        (!g.residual || row_alignment(g.residual, g.ldr, e) != 0) && g.N * e % 16 == 0;
   if (!aligned) return launch_kernel<256, A_MN, B_MN, OUT, kActAny, false>(g, s);
-  return getenv("BN128") ? launch_kernel<128, A_MN, B_MN, OUT, ACT, true>(g, s)
-                         : launch_kernel<256, A_MN, B_MN, OUT, ACT, true>(g, s);
+  // Gradients whose narrow tiles fit one round take those: half the columns are half the epilogue
+  // and half the products of a pair, and with few pairs L2 keeps up (300 x 1024 x 1024: dx 11.9 -> 10.3
+  // us; beyond one round 4096 x 2560 x 1280: 26 -> 34 us).
+  if constexpr (B_MN) {
+    const int64_t narrow = (g.M + BM - 1) / BM * ((g.N + 127) / 128);
+    if (narrow <= std::min(kMaxPairs, device_sm_count() / 2)) return launch_kernel<128, A_MN, B_MN, OUT, ACT, true>(g, s);
+  }
+  return launch_kernel<256, A_MN, B_MN, OUT, ACT, true>(g, s);
 }
 
 template <typename OUT>

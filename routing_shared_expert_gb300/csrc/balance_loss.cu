@@ -76,7 +76,7 @@ struct BalanceArgs {
 
 __global__ void __launch_bounds__(kCountThreads) balance_count_kernel(BalanceArgs a) {
   __shared__ int s_hist[kMaxExperts + 1];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  launch_dependents();
   const int ctas = a.count_ctas;
   const int rank = ctas > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int64_t cluster = blockIdx.x / ctas;
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(32 * kWarps, SIG ? 3 : 4) balance_rows_kernel(
   };
   int64_t t = t0 + warp * G + lane / W;
   fetch(t);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_previous();
 
   // a count of this sequence: requests of expert i, or (i = N) valid tokens
   auto count = [&](int i) {

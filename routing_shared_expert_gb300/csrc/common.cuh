@@ -52,6 +52,12 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
   return t;
 }
 
+// Programmatic dependent launch: lets the next launch of the stream begin its set-up, and waits
+// for everything that the previous one wrote (or reads).  Without the launch attribute both do
+// nothing.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ------------------------------------------------------------------ mbarrier --
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

@@ -318,6 +318,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   cluster_sync_all();   // barriers initialised and TMEM allocated in both CTAs
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
+  launch_dependents();
+  wait_for_previous();
 
   if (warp < EPI_WARP0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<SEGMENTED>::OTHER));
@@ -757,8 +759,7 @@ cudaError_t launch_kernel(const LinearGemm& g, cudaStream_t s) {
     a.cut_tiles = static_cast<int32_t>(rest);
     pairs = tiles > rest ? most : rest * a.parts;
   }
-  kern<<<static_cast<unsigned>(2 * pairs), THREADS, TL::SMEM, s>>>(mA, mB, mR, a);
-  return cudaGetLastError();
+  return launch_overlapped(kern, 2 * pairs, THREADS, TL::SMEM, s, 0, mA, mB, mR, a);
 }
 
 }  // namespace

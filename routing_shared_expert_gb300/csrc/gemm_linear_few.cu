@@ -149,6 +149,8 @@ __global__ void __launch_bounds__(THREADS, 2)
     *never = 0;
     mbar_fence_init();
     fence_proxy_async_smem();
+    launch_dependents();
+    wait_for_previous();
     for (int i = 0; i < S::STAGES && i < kbs; ++i) load(i);   // before the other warps are ready
   }
   if (warp == 1) tmem_alloc(smem_u32(tmem_holder), args.tmem_cols);
@@ -157,6 +159,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
+  wait_for_previous();
   bool ok = true;
 
   if (warp == 0) {
@@ -331,19 +334,8 @@ cudaError_t launch_typed(const LinearGemm& g, int split, cudaStream_t s) {
   auto kern = linear_few_kernel<NT, OUT, ACT>;
   cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), S::SMEM);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.N + FM - 1) / FM * a.t_tiles * split));
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = S::SMEM;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, mW, mX, a);
+  return launch_overlapped(kern, static_cast<int64_t>((a.N + FM - 1) / FM) * a.t_tiles * split, THREADS, S::SMEM, s, split,
+                           mW, mX, a);
 }
 
 template <typename OUT, int ACT>

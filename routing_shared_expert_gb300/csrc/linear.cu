@@ -64,6 +64,8 @@ struct DzArgs {
 template <typename OUT, bool VEC, int ACT>
 __global__ void __launch_bounds__(256) dz_kernel(DzArgs a) {
   __shared__ float s_sum[8][kDzCols];
+  launch_dependents();
+  wait_for_previous();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int64_t rb = blockIdx.x / a.col_blocks;
   const int c0 = static_cast<int>(blockIdx.x % a.col_blocks) * kDzCols + lane * 8;
@@ -111,10 +113,9 @@ __global__ void __launch_bounds__(256) dz_kernel(DzArgs a) {
 
 template <typename OUT, int ACT>
 cudaError_t launch_dz_act(const DzArgs& a, bool vec, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>((a.T + kDzRows - 1) / kDzRows * a.col_blocks);
-  if (vec) dz_kernel<OUT, true, ACT><<<grid, 256, 0, s>>>(a);
-  else dz_kernel<OUT, false, ACT><<<grid, 256, 0, s>>>(a);
-  return cudaGetLastError();
+  const int64_t grid = (a.T + kDzRows - 1) / kDzRows * a.col_blocks;
+  return vec ? launch_overlapped(dz_kernel<OUT, true, ACT>, grid, 256, 0, s, 0, a)
+             : launch_overlapped(dz_kernel<OUT, false, ACT>, grid, 256, 0, s, 0, a);
 }
 template <typename OUT>
 cudaError_t launch_dz(const DzArgs& a, int act, bool vec, cudaStream_t s) {
@@ -126,6 +127,8 @@ cudaError_t launch_dz(const DzArgs& a, int act, bool vec, cudaStream_t s) {
 // db: 32 columns per CTA, 32 warps that each add every 32nd block, then the warps in order.
 __global__ void __launch_bounds__(1024) db_kernel(const float* part, int64_t blocks, int n, float* db) {
   __shared__ float s_sum[32][33];
+  launch_dependents();
+  wait_for_previous();
   const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int col = blockIdx.x * 32 + lane;
   float sum = 0.f;
@@ -145,6 +148,8 @@ __global__ void __launch_bounds__(1024) db_kernel(const float* part, int64_t blo
 // thread and step, zeros past cols.
 __global__ void __launch_bounds__(256) align_rows_kernel(const __nv_bfloat16* src, int64_t rows, int cols,
                                                          int64_t ld, __nv_bfloat16* dst, int64_t ldd) {
+  launch_dependents();
+  wait_for_previous();
   const int64_t per = ldd / 8, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < rows * per; i += step) {
     const int64_t r = i / per;
@@ -196,9 +201,8 @@ cudaError_t aligned_operand(const void* p, int64_t rows, int32_t cols, int64_t l
   }
   *o = {copy, up8(cols)};
   const int64_t blocks = std::min<int64_t>((rows * (o->ld / 8) + 255) / 256, static_cast<int64_t>(device_sm_count()) * 32);
-  align_rows_kernel<<<static_cast<unsigned>(blocks), 256, 0, s>>>(
-      static_cast<const __nv_bfloat16*>(p), rows, cols, ld, static_cast<__nv_bfloat16*>(copy), o->ld);
-  return cudaGetLastError();
+  return launch_overlapped(align_rows_kernel, blocks, 256, 0, s, 0, static_cast<const __nv_bfloat16*>(p), rows, cols, ld,
+                           static_cast<__nv_bfloat16*>(copy), o->ld);
 }
 
 bool dtype_ok(int32_t t) { return t == MOE_F32 || t == MOE_BF16; }
@@ -343,8 +347,9 @@ moe_status moe_linear_backward(const moe_linear_config* cfg, const void* x, cons
     const cudaError_t e = c.out_dtype == MOE_F32 ? launch_dz<float>(a, c.act, vec, stream)
                                                  : launch_dz<__nv_bfloat16>(a, c.act, vec, stream);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
-    if (dbias) db_kernel<<<static_cast<unsigned>((n + 31) / 32), 1024, 0, stream>>>(a.part, blocks, n, dbias);
-    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    if (dbias && launch_overlapped(db_kernel, (n + 31) / 32, 1024, 0, stream, 0, static_cast<const float*>(a.part), blocks,
+                                   n, dbias) != cudaSuccess)
+      return MOE_ERR_CUDA;
   }
   LinearGemm g{};
   g.A = oz.p;

@@ -5,6 +5,29 @@
 
 namespace moe {
 
+// Launches a kernel that may begin its set-up under the previous one of the stream: it calls
+// wait_for_previous() before it touches global memory.  cluster: CTAs per cluster where the kernel
+// does not fix them itself.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), int64_t grid, int block, size_t smem, cudaStream_t s, int cluster,
+                              const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(block));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // C[m][n] = epilogue(sum_k A(m, k) B(n, k)): A and B bf16 with 16-byte aligned rows, either
 // K-major (a row per m or n, K contiguous) or MN-major (a row per k, M or N contiguous).
 //   z = sum + bias[n];  pre[m][n] = z;  C[m][n] = act(z) + residual[m][n]

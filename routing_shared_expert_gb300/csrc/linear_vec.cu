@@ -60,6 +60,8 @@ __device__ __forceinline__ float act_any(float z, int act) {
 template <int T, bool VEC, typename OUT>
 __global__ void __launch_bounds__(32 * WARPS) linear_vec_kernel(const Args a) {
   __shared__ float s_part[WARPS][T];
+  launch_dependents();
+  wait_for_previous();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rows = WARPS / a.split;               // of this CTA
   const int part = warp % a.split;
@@ -133,10 +135,9 @@ cudaError_t launch_typed(const LinearGemm& g, cudaStream_t s) {
   const bool vec = ((reinterpret_cast<uintptr_t>(g.A) | reinterpret_cast<uintptr_t>(g.B)) & 15u) == 0 &&
                    g.K % 8 == 0 && g.ldb % 8 == 0 && (T == 1 || g.lda % 8 == 0);
   const int rows = WARPS / a.split;
-  const unsigned grid = static_cast<unsigned>((g.N + rows - 1) / rows);
-  if (vec) linear_vec_kernel<T, true, OUT><<<grid, 32 * WARPS, 0, s>>>(a);
-  else linear_vec_kernel<T, false, OUT><<<grid, 32 * WARPS, 0, s>>>(a);
-  return cudaGetLastError();
+  const int64_t grid = (static_cast<int64_t>(g.N) + rows - 1) / rows;
+  return vec ? launch_overlapped(linear_vec_kernel<T, true, OUT>, grid, 32 * WARPS, 0, s, 0, a)
+             : launch_overlapped(linear_vec_kernel<T, false, OUT>, grid, 32 * WARPS, 0, s, 0, a);
 }
 
 template <int T>

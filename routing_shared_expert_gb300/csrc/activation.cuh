@@ -1,6 +1,5 @@
 // Activations of the dense projections (moe_act) and their derivatives, in fp32 on the fast
-// exponential and reciprocal (each good to a few 2^-23 here, far below the bf16 rounding of the
-// operands).
+// exponential and reciprocal (each good to a few 2^-23, far below the bf16 rounding of the operands).
 #pragma once
 
 #include "common.cuh"
@@ -10,7 +9,7 @@ namespace moe {
 constexpr float kTwoSqrt2OverPi = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float kGeluCubic = 0.044715f;
 
-__device__ __forceinline__ float fast_sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+__device__ __forceinline__ float fast_sigmoid(float x) { return rcp_ftz(1.f + exp_ftz(-x)); }
 
 // The normal distribution function Phi(z) and e = exp(-z^2 / 2), by the rational
 // approximation 7.1.26 of Abramowitz and Stegun: erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2)
@@ -18,8 +17,8 @@ __device__ __forceinline__ float fast_sigmoid(float x) { return __fdividef(1.f, 
 // tail itself, so nothing cancels there.
 __device__ __forceinline__ float normal_cdf(float z, float& e) {
   const float x = fabsf(z) * 0.70710678118654752f;
-  const float t = __fdividef(1.f, 1.f + 0.3275911f * x);
-  e = __expf(-x * x);
+  const float t = rcp_ftz(1.f + 0.3275911f * x);
+  e = exp_ftz(-x * x);
   const float half_erfc =
       0.5f * e * t *
       (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
@@ -35,8 +34,8 @@ __device__ __forceinline__ float act_value(float z) {
     return z * normal_cdf(z, e);
   }
   if (ACT == MOE_ACT_GELU_TANH)
-    return __fdividef(z, 1.f + __expf(-kTwoSqrt2OverPi * z * (1.f + kGeluCubic * z * z)));
-  if (ACT == MOE_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
+    return z * fast_sigmoid(kTwoSqrt2OverPi * z * (1.f + kGeluCubic * z * z));
+  if (ACT == MOE_ACT_SILU) return z * fast_sigmoid(z);
   return z;
 }
 

@@ -344,10 +344,10 @@ __global__ void __launch_bounds__(32 * kWarps, SIG ? 3 : 4) balance_rows_kernel(
       float se = 0.f, sp = 0.f, sd = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        E[e] = __expf(x[e]);
+        E[e] = exp_ftz(x[e]);
         se += E[e];
         if (SIG) {
-          slope[e] = __fdividef(1.f, 1.f + E[e]);
+          slope[e] = rcp_ftz(1.f + E[e]);
           p[e] = E[e] * slope[e];
           sp += p[e];
         } else {
@@ -361,9 +361,9 @@ __global__ void __launch_bounds__(32 * kWarps, SIG ? 3 : 4) balance_rows_kernel(
         sd += __shfl_xor_sync(0xffffffffu, sd, o);
         if (SIG) sp += __shfl_xor_sync(0xffffffffu, sp, o);
       }
-      inv_e = 1.f / se;
+      inv_e = rcp_ftz(se);
       lse = logf(se);
-      inv_p = SIG ? 1.f / sp : inv_e;
+      inv_p = SIG ? rcp_ftz(sp) : inv_e;
       dp = sd * inv_p;
     } else {
       float m = -INFINITY;

@@ -243,16 +243,29 @@ __device__ __forceinline__ void store_block(OUT* p, int64_t ld, int align, int r
     for (int r = 0; r < rows; ++r) p[r * ld + lane] = *block_element<OUT>(blk, r, lane);
   }
 }
-// The same from memory, a column per lane, every row on its way at once.
+// The same from memory, a column per lane, every row on its way at once: fp32 by asynchronous
+// copies (through registers the epilogue's sums leave too few), bf16 through registers.
 template <typename OUT>
 __device__ __forceinline__ void load_block(const OUT* p, int64_t ld, int rows, int cols, int lane, uint8_t* blk) {
-  OUT v[32];
+  if constexpr (sizeof(OUT) == 4) {
+    if (lane < cols) {
+#pragma unroll 4
+      for (int r = 0; r < rows; ++r)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(block_element<OUT>(blk, r, lane))),
+                     "l"(p + r * ld + lane)
+                     : "memory");
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+  } else {
+    OUT v[32];
 #pragma unroll
-  for (int r = 0; r < 32; ++r)
-    if (r < rows && lane < cols) v[r] = p[r * ld + lane];
+    for (int r = 0; r < 32; ++r)
+      if (r < rows && lane < cols) v[r] = p[r * ld + lane];
 #pragma unroll
-  for (int r = 0; r < 32; ++r)
-    if (r < rows && lane < cols) *block_element<OUT>(blk, r, lane) = v[r];
+    for (int r = 0; r < 32; ++r)
+      if (r < rows && lane < cols) *block_element<OUT>(blk, r, lane) = v[r];
+  }
 }
 
 constexpr int kActAny = -1;

@@ -16,6 +16,12 @@
 // its partial sums (fp32) in scratch memory, and the CTA that finds itself the last of a tile
 // adds the parts in their order along K, whoever came last, so the result does not depend on
 // it.  The cut tiles come first: the joining runs beside the products of the whole tiles.
+// Otherwise, where the partial round of a bf16 output has at most half as many tiles as there are
+// pairs, each is shared by two pairs as tiles of 128 columns: half the epilogue, and the products
+// in about three quarters of the time (a narrow tile needs 96 bytes a cycle, more than an SM
+// gets).  1237 x 2048 x 5632: 26.4 -> 24.7 us, with GELU 29.8 -> 27.7 us; 8192 x 2560 x 2560:
+// 67.4 -> 65.8 us.  Kernels without narrow tiles are built apart: the width is a constant there
+// (1 to 2 % of 16384 x 2048 x 5632).
 //
 // Epilogue: eight warps per CTA (two per TMEM lane quarter, half of the columns each), a lane per
 // row.  The residual's blocks of 32 rows come by TMA into swizzled shared memory, two per warp,
@@ -86,6 +92,7 @@ struct Args {
   int32_t m_tiles, n_tiles;
   int32_t cut_tiles;        // tiles 0 .. cut_tiles - 1 are cut along K
   int32_t parts;            // into this many parts; pair r parts + k holds part k of tile r
+  int64_t whole;            // NARROW: tiles past this one are two narrow ones each
   const float* bias;
   const void* residual;
   void* pre;
@@ -101,14 +108,17 @@ struct Args {
 // One piece of a pair's work: K blocks [kb0, kb1) of tile (m, n).
 struct Item {
   int m, n, kb0, kb1;
+  int first, cols;          // NARROW: of the tile's columns: 0, 256, or one half of them
   int parts;                // parts of this tile; 1: the whole tile
   int cut;                  // index of the cut tile
 };
 
-// Item i of a pair; false past the last.  A pair's part of a cut tile comes first.
+// Item i of a pair; false past the last.  A pair's part of a cut tile comes first, a narrow tile
+// last.
 // Tiles are numbered in groups of GROUP_M row tiles, within one the row tiles of a column tile
 // together, so that the tiles in flight are about as many rows as columns wide and their
 // operands stay in L2.
+template <bool NARROW>
 __device__ __forceinline__ bool item_at(const Args& a, int pair, int n_pairs, int i, Item& o) {
   const int k_blocks = (a.K + BK - 1) / BK;
   int64_t t;
@@ -125,6 +135,14 @@ __device__ __forceinline__ bool item_at(const Args& a, int pair, int n_pairs, in
     o.kb0 = 0;
     o.kb1 = k_blocks;
     t = a.cut_tiles + pair + static_cast<int64_t>(pair < a.cut_tiles * a.parts ? i - 1 : i) * n_pairs;
+  }
+  o.first = 0;
+  o.cols = 256;
+  if (NARROW && t >= a.whole) {   // narrow tiles t - whole: the halves of whole, whole + 1, ...
+    const int64_t h = t - a.whole;
+    t = a.whole + h / 2;
+    o.first = static_cast<int>(h % 2) * 128;
+    o.cols = 128;
   }
   if (t >= static_cast<int64_t>(a.m_tiles) * a.n_tiles) return false;
   const int64_t per = static_cast<int64_t>(GROUP_M) * a.n_tiles;
@@ -278,10 +296,12 @@ __device__ __forceinline__ void activate(float (&z)[N], int act) {
 
 // ALIGNED: every row that the epilogue touches starts on a 16-byte boundary and N ends on one; else
 // ACT is kActAny, the run-time activation.
-template <int BN, bool A_MN, bool B_MN, typename OUT, int ACT, bool ALIGNED>
+template <int BN, bool A_MN, bool B_MN, typename OUT, int ACT, bool ALIGNED, bool NARROW>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                       const __grid_constant__ CUtensorMap tmR, const Args args) {
+                       const __grid_constant__ CUtensorMap tmBn, const __grid_constant__ CUtensorMap tmR,
+                       const Args args) {
+  static_assert(!NARROW || (BN == 256 && !A_MN && !B_MN && sizeof(OUT) == 2), "narrow tiles");
   using TL = Tile<BN, sizeof(OUT) == 4>;
   constexpr int STAGES = TL::STAGES, WARP_COLS = TL::COLS;
   extern __shared__ uint8_t smem_raw[];
@@ -336,106 +356,108 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
   if (warp < EPI_WARP0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<SEGMENTED>::OTHER));
-  if (warp == 0) {
-    // ---------------------------------------------------------- producer (both CTAs)
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int issued_parity[STAGES];
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer (both CTAs)
+      if (lane == 0) {
+        int stage = 0;
+        uint32_t phase = 0;
+        int issued_parity[STAGES];
 #pragma unroll
-      for (int s = 0; s < STAGES; ++s) issued_parity[s] = -1;
-      bool ok = true;
-      Item it;
-      for (int i = 0; ok && item_at(args, pair_id, n_pairs, i, it); ++i) {
-        const int m0 = it.m * BM + static_cast<int>(rank) * HALF;
-        const int n0 = it.n * BN + static_cast<int>(rank) * TL::COLS;
-        for (int kb = it.kb0; kb < it.kb1; kb += TL::SUBS) {
-          if (!mbar_wait_bounded(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, args.status,
-                                 kWaitLimitNs)) {
-            ok = false;
-            break;
-          }
-          const int subs = min(TL::SUBS, it.kb1 - kb);
-          const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
-          if (leader) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * subs * TL::SUB_BYTES);
-          for (int u = 0; u < subs; ++u) {
-            const uint32_t sA = smem_base + stage * TL::STAGE_BYTES + u * TL::SUB_BYTES;
-            const uint32_t sB = sA + A_BYTES;
-            const int k0 = (kb + u) * BK;
-            if (A_MN) {
-              tma_load_2d_pair(sA, &tmA, m0, k0, fb);
-              tma_load_2d_pair(sA + kMnLbo, &tmA, m0 + 64, k0, fb);
-            } else {
-              tma_load_2d_pair(sA, &tmA, k0, m0, fb);
+        for (int s = 0; s < STAGES; ++s) issued_parity[s] = -1;
+        bool ok = true;
+        Item it;
+        for (int i = 0; ok && item_at<NARROW>(args, pair_id, n_pairs, i, it); ++i) {
+          const int m0 = it.m * BM + static_cast<int>(rank) * HALF;
+          const int cols = NARROW ? it.cols / 2 : TL::COLS;   // of this CTA
+          const int n0 = it.n * BN + it.first + static_cast<int>(rank) * cols;
+          const uint32_t sub_bytes = A_BYTES + cols * BK * 2;
+          for (int kb = it.kb0; kb < it.kb1; kb += TL::SUBS) {
+            if (!mbar_wait_bounded(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, args.status,
+                                   kWaitLimitNs)) {
+              ok = false;
+              break;
             }
-            if (B_MN) {
-              tma_load_2d_pair(sB, &tmB, n0, k0, fb);
-              if (TL::COLS > 64) tma_load_2d_pair(sB + kMnLbo, &tmB, n0 + 64, k0, fb);
-            } else {
-              tma_load_2d_pair(sB, &tmB, k0, n0, fb);
-            }
-          }
-          issued_parity[stage] = static_cast<int>(phase);
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-        }
-      }
-      if (!ok && leader)
-        for (int s = 0; s < STAGES; ++s)
-          if (issued_parity[s] >= 0)
-            mbar_wait_bounded(smem_u32(&full[s]), static_cast<uint32_t>(issued_parity[s]), never,
-                              nullptr, kDrainLimitNs);
-    }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------- MMA issuer (even CTA)
-    if (leader && lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(BM, BN) | (A_MN ? (1u << 15) : 0u) |
-                                 (B_MN ? (1u << 16) : 0u);
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      uint32_t fill = 0;                     // TMEM buffers filled
-      Item it;
-      for (int i = 0; ok && item_at(args, pair_id, n_pairs, i, it); ++i) {
-        const int seg = segment_blocks<SEGMENTED>(it);
-        for (int s0 = it.kb0; ok && s0 < it.kb1; s0 += seg, ++fill) {
-          const int s1 = min(s0 + seg, it.kb1);
-          const uint32_t d_acc = tmem_base + (fill & 1) * BN;
-          ok = mbar_wait_bounded(smem_u32(&tempty[fill & 1]), ((fill >> 1) & 1u) ^ 1u, abort_flag, args.status,
-                                 kWaitLimitNs);
-          tc_fence_after();
-          for (int kb = s0; ok && kb < s1; kb += TL::SUBS) {
-            ok = mbar_wait_bounded(smem_u32(&full[stage]), phase, abort_flag, args.status, kWaitLimitNs);
-            if (!ok) break;
-            tc_fence_after();
             const int subs = min(TL::SUBS, it.kb1 - kb);
+            const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
+            if (leader) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * subs * sub_bytes);
             for (int u = 0; u < subs; ++u) {
               const uint32_t sA = smem_base + stage * TL::STAGE_BYTES + u * TL::SUB_BYTES;
               const uint32_t sB = sA + A_BYTES;
-#pragma unroll
-              for (int j = 0; j < BK / 16; ++j) {
-                const uint64_t ad = A_MN ? sw128_mnmajor_desc(sA + j * 2048) : sw128_kmajor_desc(sA) + 2 * j;
-                const uint64_t bd = B_MN ? sw128_mnmajor_desc(sB + j * 2048) : sw128_kmajor_desc(sB) + 2 * j;
-                tc_mma_bf16_pair(d_acc, ad, bd, idesc, (kb > s0 || u > 0 || j > 0) ? 1u : 0u);
+              const int k0 = (kb + u) * BK;
+              if (A_MN) {
+                tma_load_2d_pair(sA, &tmA, m0, k0, fb);
+                tma_load_2d_pair(sA + kMnLbo, &tmA, m0 + 64, k0, fb);
+              } else {
+                tma_load_2d_pair(sA, &tmA, k0, m0, fb);
+              }
+              if (B_MN) {
+                tma_load_2d_pair(sB, &tmB, n0, k0, fb);
+                if (TL::COLS > 64) tma_load_2d_pair(sB + kMnLbo, &tmB, n0 + 64, k0, fb);
+              } else {
+                tma_load_2d_pair(sB, NARROW && it.cols != BN ? &tmBn : &tmB, k0, n0, fb);
               }
             }
-            tc_commit_pair(smem_u32(&empty[stage]), 0x3);
+            issued_parity[stage] = static_cast<int>(phase);
             if (++stage == STAGES) { stage = 0; phase ^= 1u; }
           }
-          if (ok) tc_commit_pair(smem_u32(&tfull[fill & 1]), 0x3);
+        }
+        if (!ok && leader)
+          for (int s = 0; s < STAGES; ++s)
+            if (issued_parity[s] >= 0)
+              mbar_wait_bounded(smem_u32(&full[s]), static_cast<uint32_t>(issued_parity[s]), never,
+                                nullptr, kDrainLimitNs);
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer (even CTA)
+      if (leader && lane == 0) {
+        constexpr uint32_t major = (A_MN ? (1u << 15) : 0u) | (B_MN ? (1u << 16) : 0u);
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        uint32_t fill = 0;                     // TMEM buffers filled
+        Item it;
+        for (int i = 0; ok && item_at<NARROW>(args, pair_id, n_pairs, i, it); ++i) {
+          const int seg = segment_blocks<SEGMENTED>(it);
+          const uint32_t idesc = (NARROW && it.cols != BN ? idesc_bf16_f32(BM, BN / 2) : idesc_bf16_f32(BM, BN)) | major;
+          for (int s0 = it.kb0; ok && s0 < it.kb1; s0 += seg, ++fill) {
+            const int s1 = min(s0 + seg, it.kb1);
+            const uint32_t d_acc = tmem_base + (fill & 1) * BN;
+            ok = mbar_wait_bounded(smem_u32(&tempty[fill & 1]), ((fill >> 1) & 1u) ^ 1u, abort_flag, args.status,
+                                   kWaitLimitNs);
+            tc_fence_after();
+            for (int kb = s0; ok && kb < s1; kb += TL::SUBS) {
+              ok = mbar_wait_bounded(smem_u32(&full[stage]), phase, abort_flag, args.status, kWaitLimitNs);
+              if (!ok) break;
+              tc_fence_after();
+              const int subs = min(TL::SUBS, it.kb1 - kb);
+              for (int u = 0; u < subs; ++u) {
+                const uint32_t sA = smem_base + stage * TL::STAGE_BYTES + u * TL::SUB_BYTES;
+                const uint32_t sB = sA + A_BYTES;
+#pragma unroll
+                for (int j = 0; j < BK / 16; ++j) {
+                  const uint64_t ad = A_MN ? sw128_mnmajor_desc(sA + j * 2048) : sw128_kmajor_desc(sA) + 2 * j;
+                  const uint64_t bd = B_MN ? sw128_mnmajor_desc(sB + j * 2048) : sw128_kmajor_desc(sB) + 2 * j;
+                  tc_mma_bf16_pair(d_acc, ad, bd, idesc, (kb > s0 || u > 0 || j > 0) ? 1u : 0u);
+                }
+              }
+              tc_commit_pair(smem_u32(&empty[stage]), 0x3);
+              if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+            }
+            if (ok) tc_commit_pair(smem_u32(&tfull[fill & 1]), 0x3);
+          }
+        }
+        if (!ok) {
+          tc_commit_pair(smem_u32(drain), 0x1);
+          mbar_wait_bounded(smem_u32(drain), 0, never, nullptr, kDrainLimitNs);
         }
       }
-      if (!ok) {
-        tc_commit_pair(smem_u32(drain), 0x1);
-        mbar_wait_bounded(smem_u32(drain), 0, never, nullptr, kDrainLimitNs);
-      }
     }
-  }
   } else {
     // ---------------------------------------------------------- epilogue (both CTAs)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<SEGMENTED>::EPI));
     constexpr int CW = Row64<OUT>::CW;       // columns of 64 bytes
     constexpr int PER = TL::ROW_BYTES / 64;  // of which a block has 2 (fp32) or 1
-    constexpr int BCOLS = PER * CW, BLOCKS = WARP_COLS / BCOLS;
+    constexpr int BCOLS = PER * CW;
     // results go through a block (and pre through the second), or from the registers
     constexpr bool STAGED = SEGMENTED || !ALIGNED;
     const int q = warp & 3;                  // TMEM lanes of this warp
@@ -449,13 +471,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     bool ok = true;
     Item it;
     // a part of a cut tile is taken up even after a failure: the epilogue warps agree there
-    for (int i = 0; item_at(args, pair_id, n_pairs, i, it) && (ok || it.parts > 1); ++i) {
+    for (int i = 0; item_at<NARROW>(args, pair_id, n_pairs, i, it) && (ok || it.parts > 1); ++i) {
       const int64_t row0 = static_cast<int64_t>(it.m) * BM + rank * HALF + q * 32;
-      const int col0 = it.n * BN + half * WARP_COLS;
+      const int warp_cols = NARROW ? it.cols / 2 : WARP_COLS;   // of this warp
+      const int col0 = it.n * BN + it.first + half * warp_cols;
       // rows and columns of this warp's block; none where it lies past the output
       const int rows = col0 < args.N ? static_cast<int>(min(static_cast<int64_t>(32), args.M - row0)) : 0;
       const OUT* rrow = static_cast<const OUT*>(args.residual) + row0 * args.ldr + col0;
-      const int blocks = rows > 0 ? min(BLOCKS, (args.N - col0 + BCOLS - 1) / BCOLS) : 0;
+      const int blocks = rows > 0 ? min(warp_cols / BCOLS, (args.N - col0 + BCOLS - 1) / BCOLS) : 0;
       const bool tma_res = ALIGNED && res;
       // the residual of block c into the buffer of its turn
       auto load_residual = [&](int c) {
@@ -476,7 +499,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int k = 0; k < WARP_COLS / 32; ++k) {
         const int col = col0 + k * 32 + lane;
-        bias[k] = args.bias != nullptr && col < args.N ? __ldg(args.bias + col) : 0.f;
+        bias[k] = args.bias != nullptr && k * 32 < warp_cols && col < args.N ? __ldg(args.bias + col) : 0.f;
       }
       // Waits for the next TMEM buffer; its columns of this warp start at taddr.
       uint32_t taddr = 0;
@@ -488,7 +511,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         ready = __shfl_sync(0xffffffffu, ready ? 1 : 0, 0) != 0;
         tc_fence_after();
         taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                static_cast<uint32_t>((fill & 1) * BN + half * WARP_COLS);
+                static_cast<uint32_t>((fill & 1) * BN + half * warp_cols);
         return ready;
       };
       auto release_fill = [&]() {
@@ -607,7 +630,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (tma_res && it.parts > 1)
         for (int c = 0; c < bufs; ++c) load_residual(c);
 #pragma unroll 1
-      for (int c = 0; c < BLOCKS; ++c) {
+      for (int c = 0; c < warp_cols / BCOLS; ++c) {
         const int col = col0 + c * BCOLS, cols = min(BCOLS, args.N - col);
         const bool in = c < blocks && ok;
         const uint32_t b = bufs == 1 ? 0 : tma_res ? reads & 1 : c & 1;
@@ -629,7 +652,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           const int at = (PER * c + h) * CW;   // first column of the warp's
           uint32_t v[CW];
           if constexpr (CW == 16) tmem_ld16(taddr + at, v); else tmem_ld32(taddr + at, v);
-          if (at + CW == WARP_COLS) release_fill();   // the last read of the buffer
+          if (at + CW == warp_cols) release_fill();   // the last read of the buffer
           float z[CW];
 #pragma unroll
           for (int e = 0; e < CW; ++e) z[e] = __uint_as_float(v[e]);
@@ -705,22 +728,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
 }
 
-// Parts to cut the `rest` tiles of a partial round into, of `stages` ring stages (two K blocks,
-// about half a microsecond) each: 1, or the number that saves most.  Joining s parts costs
-// about as much as kJoin + kJoinPart s stages (they pass through scratch memory).
+// What becomes of the `rest` tiles of a partial round, of `stages` pairs of K blocks (about half a
+// microsecond) each: cut into `parts` along K, or narrow where that is allowed, or neither; and
+// about the stages that the round then takes.  Joining s parts costs about as much as
+// kJoin + kJoinPart s stages (they pass through scratch memory).
 constexpr int kJoin = 12, kJoinPart = 4, kMaxParts = 8;
-int cut_parts(int64_t rest, int64_t pairs, int64_t stages) {
-  int best = 1;
-  int64_t gain = 0;
+struct Rest {
+  int parts;
+  bool narrow;
+  int64_t stages;
+};
+Rest plan_rest(int64_t rest, int64_t pairs, int64_t stages, bool narrow) {
+  Rest best{1, false, rest > 0 ? stages : 0};
+  if (rest == 0) return best;
+  if (narrow && 2 * rest <= pairs) best = Rest{1, true, (3 * stages + 3) / 4};
   for (int s = 2; s <= kMaxParts && rest * s <= pairs && 2 * s <= stages; ++s) {
-    const int64_t g = stages - (stages + s - 1) / s - kJoin - kJoinPart * s;
-    if (g > gain) {
-      gain = g;
-      best = s;
-    }
+    const int64_t cost = (stages + s - 1) / s + kJoin + kJoinPart * s;
+    if (cost < best.stages) best = Rest{s, false, cost};
   }
   return best;
 }
+// Of an M x N output in tiles of 256 x BN, in rounds of `pairs`.
+template <int BN>
+Rest plan_output(int64_t M, int64_t N, int64_t K, int64_t pairs, bool narrow) {
+  const int64_t tiles = (M + BM - 1) / BM * ((N + BN - 1) / BN);
+  return plan_rest(tiles % pairs, pairs, ((K + BK - 1) / BK + 1) / 2, narrow);
+}
+int64_t most_pairs(int sms) { return std::min(kMaxPairs, std::max(1, sms / 2)); }
 
 // Bytes (32, 16 or 0 for less) that rows ld elements apart are aligned to.
 int32_t row_alignment(const void* p, int64_t ld, size_t elem) {
@@ -728,8 +762,8 @@ int32_t row_alignment(const void* p, int64_t ld, size_t elem) {
   return v % 32 == 0 ? 32 : v % 16 == 0 ? 16 : 0;
 }
 
-template <int BN, bool A_MN, bool B_MN, typename OUT, int ACT, bool ALIGNED>
-cudaError_t launch_kernel(const LinearGemm& g, cudaStream_t s) {
+template <int BN, bool A_MN, bool B_MN, typename OUT, int ACT, bool ALIGNED, bool NARROW = false>
+cudaError_t launch_kernel(const LinearGemm& g, const Rest& plan, cudaStream_t s) {
   using TL = Tile<BN, sizeof(OUT) == 4>;
   Args a{};
   a.M = static_cast<int32_t>(g.M);
@@ -754,25 +788,29 @@ cudaError_t launch_kernel(const LinearGemm& g, cudaStream_t s) {
       !(B_MN ? make_strided_map(&mB, MOE_BF16, g.B, N, K, g.ldb, 64, BK)
              : make_strided_map(&mB, MOE_BF16, g.B, K, N, g.ldb, BK, TL::COLS)))
     return cudaErrorInvalidValue;
-  CUtensorMap mR = mA;
+  CUtensorMap mR = mA, mBn = mB;
+  if (NARROW && !make_strided_map(&mBn, MOE_BF16, g.B, K, N, g.ldb, BK, TL::COLS / 2)) return cudaErrorInvalidValue;
   if (ALIGNED && g.residual &&
       !make_strided_map(&mR, sizeof(OUT) == 4 ? MOE_F32 : MOE_BF16, g.residual, N, M, g.ldr, 32, 32, TL::ROW_BYTES))
     return cudaErrorInvalidValue;
-  auto kern = linear_pair_kernel<BN, A_MN, B_MN, OUT, ACT, ALIGNED>;
+  auto kern = linear_pair_kernel<BN, A_MN, B_MN, OUT, ACT, ALIGNED, NARROW>;
   const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), TL::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
-  const int64_t most = std::min(kMaxPairs, std::max(1, device_sm_count() / 2));
+  const int64_t most = most_pairs(device_sm_count()), rest = tiles % most;
   int64_t pairs = std::min(tiles, most);
   a.scratch = g.scratch;
   a.tickets = g.tickets;
-  const int64_t rest = tiles % most;
-  a.parts = rest > 0 ? cut_parts(rest, most, ((g.K + BK - 1) / BK + 1) / 2) : 1;
-  if (a.parts > 1) {
+  a.parts = plan.parts;
+  a.whole = tiles;
+  if (plan.parts > 1) {
     a.cut_tiles = static_cast<int32_t>(rest);
-    pairs = tiles > rest ? most : rest * a.parts;
+    pairs = tiles > rest ? most : rest * plan.parts;
+  } else if (NARROW) {
+    a.whole = tiles - rest;
+    pairs = tiles > rest ? most : 2 * rest;
   }
-  return launch_overlapped(kern, 2 * pairs, THREADS, TL::SMEM, s, 0, mA, mB, mR, a);
+  return launch_overlapped(kern, 2 * pairs, THREADS, TL::SMEM, s, 0, mA, mB, mBn, mR, a);
 }
 
 }  // namespace
@@ -784,15 +822,23 @@ cudaError_t launch_typed(const LinearGemm& g, cudaStream_t s) {
   const size_t e = sizeof(OUT);
   const bool aligned = row_alignment(g.C, g.ldc, e) != 0 && (!g.pre || row_alignment(g.pre, g.N, e) != 0) &&
                        (!g.residual || row_alignment(g.residual, g.ldr, e) != 0) && g.N * e % 16 == 0;
-  if (!aligned) return launch_kernel<256, A_MN, B_MN, OUT, kActAny, false>(g, s);
+  constexpr bool NARROWABLE = !B_MN && sizeof(OUT) == 2;
+  const int64_t pairs = most_pairs(device_sm_count());
   // Gradients whose narrow tiles fit one round take those: half the columns are half the epilogue
   // and half the products of a pair, and with few pairs L2 keeps up (300 x 1024 x 1024: dx 11.9 -> 10.3
   // us; beyond one round 4096 x 2560 x 1280: 26 -> 34 us).
   if constexpr (B_MN) {
-    const int64_t narrow = (g.M + BM - 1) / BM * ((g.N + 127) / 128);
-    if (narrow <= std::min(kMaxPairs, device_sm_count() / 2)) return launch_kernel<128, A_MN, B_MN, OUT, ACT, true>(g, s);
+    if (aligned && (g.M + BM - 1) / BM * ((g.N + 127) / 128) <= pairs)
+      return launch_kernel<128, A_MN, B_MN, OUT, ACT, true>(g, plan_output<128>(g.M, g.N, g.K, pairs, false), s);
   }
-  return launch_kernel<256, A_MN, B_MN, OUT, ACT, true>(g, s);
+  const Rest plan = plan_output<256>(g.M, g.N, g.K, pairs, NARROWABLE);
+  if constexpr (NARROWABLE) {
+    if (plan.narrow)
+      return aligned ? launch_kernel<256, A_MN, B_MN, OUT, ACT, true, true>(g, plan, s)
+                     : launch_kernel<256, A_MN, B_MN, OUT, kActAny, false, true>(g, plan, s);
+  }
+  return aligned ? launch_kernel<256, A_MN, B_MN, OUT, ACT, true>(g, plan, s)
+                 : launch_kernel<256, A_MN, B_MN, OUT, kActAny, false>(g, plan, s);
 }
 
 template <typename OUT>
@@ -804,11 +850,9 @@ cudaError_t launch_forward(const LinearGemm& g, cudaStream_t s) {
 
 }  // namespace
 
-int64_t pair_cycles(int64_t M, int64_t N, int64_t K, int sms) {
-  const int64_t tiles = (M + BM - 1) / BM * ((N + 255) / 256), pairs = std::min(kMaxPairs, std::max(1, sms / 2));
-  const int64_t stages = ((K + BK - 1) / BK + 1) / 2, rest = tiles % pairs;
-  const int parts = rest > 0 ? cut_parts(rest, pairs, stages) : 1;
-  const int64_t last = rest == 0 ? 0 : parts == 1 ? stages : (stages + parts - 1) / parts + kJoin + kJoinPart * parts;
+int64_t pair_cycles(int64_t M, int64_t N, int64_t K, bool f32, int sms) {
+  const int64_t tiles = (M + BM - 1) / BM * ((N + 255) / 256), pairs = most_pairs(sms);
+  const int64_t stages = ((K + BK - 1) / BK + 1) / 2, last = plan_output<256>(M, N, K, pairs, !f32).stages;
   return 20000 + (tiles / pairs * stages + last) * 2 * (tiles <= pairs ? 640 : 573);
 }
 

@@ -27,12 +27,12 @@ constexpr int kDzCols = 256;    // columns per block: 8 per lane
 // the pair kernel's rounds (384 tokens of 2048 x 5632: 17.1 us against 19.2; 512: 29.7
 // against 19.6).
 enum class Form { kVec, kFew, kPair };
-Form forward_form(int64_t T, int64_t N, int64_t K, bool aligned) {
+Form forward_form(int64_t T, int64_t N, int64_t K, bool f32, bool aligned) {
   if (T <= kVecTokens && (T * N * K <= (T == 1 ? int64_t{1} << 25 : int64_t{1} << 22) || (!aligned && T <= 2)))
     return Form::kVec;
   const int sms = device_sm_count();
   const FewShape f = few_shape(T, N, K, sms);
-  return f.one_round && f.cycles < pair_cycles(T, N, K, sms) ? Form::kFew : Form::kPair;
+  return f.one_round && f.cycles < pair_cycles(T, N, K, f32, sms) ? Form::kFew : Form::kPair;
 }
 
 __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
@@ -269,7 +269,7 @@ moe_status moe_linear_forward(const moe_linear_config* cfg, const void* x, const
   const int64_t ldx = c.ldx ? c.ldx : c.in_features, ldw = c.ldw ? c.ldw : c.in_features;
   const bool aligned = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(W)) & 15u) == 0 &&
                        (ldx % 8 == 0 || c.T == 1) && ldw % 8 == 0;
-  const Form form = forward_form(c.T, c.out_features, c.in_features, aligned);
+  const Form form = forward_form(c.T, c.out_features, c.in_features, c.out_dtype == MOE_F32, aligned);
   Operand ox{x, ldx}, ow{W, ldw};
   if (form != Form::kVec && (aligned_operand(x, c.T, c.in_features, ldx, ws + L.x, &ox, stream) != cudaSuccess ||
                aligned_operand(W, c.out_features, c.in_features, ldw, ws + L.w, &ow, stream) != cudaSuccess))

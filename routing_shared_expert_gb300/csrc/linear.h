@@ -61,8 +61,9 @@ static_assert(kPairTicketOffset + kPairTicketBytes <= 256, "the counts lie in th
 // CTA pairs, 256 x 256 tiles (gemm_linear.cu).
 cudaError_t launch_linear_pair(const LinearGemm& g, cudaStream_t s);
 // About the cycles of a launch_linear_pair: its rounds of tiles (a K block takes 573 cycles once
-// the operands are in L2, 640 in a single round), or of their parts, and what a launch costs.
-int64_t pair_cycles(int64_t M, int64_t N, int64_t K, int sms);
+// the operands are in L2, 640 in a single round), or of their parts, and what a launch costs.  f32:
+// the output's type.
+int64_t pair_cycles(int64_t M, int64_t N, int64_t K, bool f32, int sms);
 // One to kVecTokens rows of A (both operands K-major, any alignment), a warp per row of B
 // (linear_vec.cu).
 constexpr int kVecTokens = 4;

@@ -107,6 +107,15 @@ def test_forward_odd_features(moe, T, n_in, n_out):
         forward(moe, T, n_in, n_out, act="gelu", out=out)
 
 
+@pytest.mark.parametrize("T,n_in,n_out", [(5200, 72, 1280), (5200, 72, 1100), (5200, 72, 1275), (20000, 64, 256)])
+def test_forward_whole_and_narrow_tiles(moe, T, n_in, n_out):
+    """A full round of tiles, then a partial one: 29 or 3 tiles on 76 pairs; 1100 and 1275 end inside
+    the first and the second half of a tile."""
+    for out in ("bf16", "f32"):
+        forward(moe, T, n_in, n_out, act="gelu", out=out)
+        forward(moe, T, n_in, n_out, out=out, bias=False, residual=False, pre=False)
+
+
 @pytest.mark.parametrize("T", [1, 19, 130, 700])
 def test_forward_strides_and_offsets(moe, T):
     forward(moe, T, 256, 192, act="silu", ldx=264, ldw=512, ldr=200, ldy=1024)      # aligned strides

@@ -826,10 +826,14 @@ cudaError_t launch_typed(const LinearGemm& g, cudaStream_t s) {
   const int64_t pairs = most_pairs(device_sm_count());
   // Gradients whose narrow tiles fit one round take those: half the columns are half the epilogue
   // and half the products of a pair, and with few pairs L2 keeps up (300 x 1024 x 1024: dx 11.9 -> 10.3
-  // us; beyond one round 4096 x 2560 x 1280: 26 -> 34 us).
+  // us; 300 x 1001 x 1000, unaligned: both gradients 35 -> 31 us; beyond one round 4096 x 2560 x 1280: 26 ->
+  // 34 us).
   if constexpr (B_MN) {
-    if (aligned && (g.M + BM - 1) / BM * ((g.N + 127) / 128) <= pairs)
-      return launch_kernel<128, A_MN, B_MN, OUT, ACT, true>(g, plan_output<128>(g.M, g.N, g.K, pairs, false), s);
+    if ((g.M + BM - 1) / BM * ((g.N + 127) / 128) <= pairs) {
+      const Rest plan = plan_output<128>(g.M, g.N, g.K, pairs, false);
+      return aligned ? launch_kernel<128, A_MN, B_MN, OUT, ACT, true>(g, plan, s)
+                     : launch_kernel<128, A_MN, B_MN, OUT, kActAny, false>(g, plan, s);
+    }
   }
   const Rest plan = plan_output<256>(g.M, g.N, g.K, pairs, NARROWABLE);
   if constexpr (NARROWABLE) {

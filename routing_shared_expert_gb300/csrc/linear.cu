@@ -7,6 +7,7 @@
 // Here: the argument checks, the pass that forms dz (rounded to bf16, which the products need,
 // while db sums the unrounded values) and the copy that gives unaligned operands 16-byte rows.
 #include "linear.h"
+#include "load_any.cuh"
 
 #include <algorithm>
 
@@ -22,14 +23,15 @@ constexpr int kDzCols = 256;    // columns per block: 8 per lane
 // copies and starts soonest, but reads x anew for every row: it wins for one token up to about
 // 2^25 weights (2048 x 2048: 5.0 us against 6.0; 7168 x 7168: 20.3 against 20.0) and for up to
 // four where the whole product is small (512 x 512: 2.7 against 4.3; two tokens of 2048 x 2048:
-// 6.8 against 6.5), and for one or two tokens of unaligned rows (2047 x 2047: 7.6 against 10.8).
+// 6.8 against 6.5).  Unaligned rows spare it the copies: one token of 4095 x 14336 46.8 against
+// 63.7, two of 2047 x 2047 9.4 against 10.3, of 2810 x 2816 17.1 against 13.7.
 // The few-token kernel wins while its tiles are resident at once and its loads take less than
 // the pair kernel's rounds (384 tokens of 2048 x 5632: 17.1 us against 19.2; 512: 29.7
 // against 19.6).
 enum class Form { kVec, kFew, kPair };
 Form forward_form(int64_t T, int64_t N, int64_t K, bool f32, bool aligned) {
-  if (T <= kVecTokens && (T * N * K <= (T == 1 ? int64_t{1} << 25 : int64_t{1} << 22) || (!aligned && T <= 2)))
-    return Form::kVec;
+  const int64_t most = T == 1 ? int64_t{1} << 25 : T == 2 && !aligned ? int64_t{1} << 23 : int64_t{1} << 22;
+  if (T <= kVecTokens && (T * N * K <= most || (T == 1 && !aligned))) return Form::kVec;
   const int sms = device_sm_count();
   const FewShape f = few_shape(T, N, K, sms);
   return f.one_round && f.cycles < pair_cycles(T, N, K, f32, sms) ? Form::kFew : Form::kPair;
@@ -72,6 +74,7 @@ __global__ void __launch_bounds__(256) dz_kernel(DzArgs a) {
   const int64_t t1 = min(a.T, (rb + 1) * kDzRows);
   float sum[8] = {};
   if (c0 < a.n) {
+    const Span sy = span_of(a.dy, a.T, a.ldy, a.n, sizeof(OUT)), sp = span_of(a.pre, a.T, a.n, a.n, sizeof(OUT));
     for (int64_t t = rb * kDzRows + warp; t < t1; t += 8) {
       const OUT* dy = static_cast<const OUT*>(a.dy) + t * a.ldy + c0;
       const OUT* pre = static_cast<const OUT*>(a.pre) + t * a.n + c0;
@@ -80,11 +83,11 @@ __global__ void __launch_bounds__(256) dz_kernel(DzArgs a) {
         load8(dy, g);
         if (ACT != MOE_ACT_NONE) load8(pre, z);
       } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          g[e] = c0 + e < a.n ? to_f32(dy[e]) : 0.f;
-          z[e] = ACT != MOE_ACT_NONE && c0 + e < a.n ? to_f32(pre[e]) : 0.f;
-        }
+        const Raw8 rg = load8_raw(dy, sy);
+        Raw8 rz;
+        if (ACT != MOE_ACT_NONE) rz = load8_raw(pre, sp);
+        take8(rg, dy, a.n - c0, g);
+        if (ACT != MOE_ACT_NONE) take8(rz, pre, a.n - c0, z);
       }
       if (ACT != MOE_ACT_NONE) {
 #pragma unroll

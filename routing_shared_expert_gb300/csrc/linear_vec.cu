@@ -1,4 +1,4 @@
-// The dense projection of one or two tokens: y = act(x W^T + b) + r, bound by reading W once.
+// The dense projection of one to four tokens: y = act(x W^T + b) + r, bound by reading W once.
 //
 // A warp takes a weight row (or a part of its depth, where the rows alone are too few warps), its
 // lanes neighbouring 16-byte pieces, several on their way at a time; the products accumulate in
@@ -8,6 +8,7 @@
 
 #include "activation.cuh"
 #include "linear.h"
+#include "load_any.cuh"
 
 namespace moe {
 namespace {
@@ -37,19 +38,23 @@ __device__ __forceinline__ void unpack8(uint4 u, float (&v)[8]) {
 }
 
 // Eight values from column k on; zeros past K.  VEC: 16-byte aligned rows of a multiple of 8.
-template <bool VEC>
-__device__ __forceinline__ uint4 piece(const __nv_bfloat16* row, int k, int K) {
-  if (VEC) return k < K ? __ldg(reinterpret_cast<const uint4*>(row + k)) : make_uint4(0u, 0u, 0u, 0u);
-  const unsigned short* s = reinterpret_cast<const unsigned short*>(row);
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = k + 2 * i < K ? __ldg(s + k + 2 * i) : 0u;
-    const uint32_t hi = k + 2 * i + 1 < K ? __ldg(s + k + 2 * i + 1) : 0u;
-    w[i] = lo | hi << 16;
+template <bool VEC> struct Piece;
+template <> struct Piece<true> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* row, int k, int K, const Span&) {
+    u = k < K ? __ldg(reinterpret_cast<const uint4*>(row + k)) : make_uint4(0u, 0u, 0u, 0u);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
+  __device__ __forceinline__ void take(const __nv_bfloat16*, int, int, float (&v)[8]) const { unpack8(u, v); }
+};
+template <> struct Piece<false> {
+  Raw8 r;
+  __device__ __forceinline__ void load(const __nv_bfloat16* row, int k, int K, const Span& span) {
+    r = load8_raw(row + k, k < K ? span : Span{1, 0});
+  }
+  __device__ __forceinline__ void take(const __nv_bfloat16* row, int k, int K, float (&v)[8]) const {
+    take8(r, row + k, K - k, v);
+  }
+};
 
 __device__ __forceinline__ float act_any(float z, int act) {
 #define MOE_CALL(ACT) act_value<ACT>(z)
@@ -71,19 +76,25 @@ __global__ void __launch_bounds__(32 * WARPS) linear_vec_kernel(const Args a) {
   for (int t = 0; t < T; ++t) acc[t] = 0.f;
   if (f < a.N) {
     const __nv_bfloat16* wr = a.W + f * a.ldw;
+    const Span sw = span_of(a.W, a.N, a.ldw, a.K, 2), sx = span_of(a.x, T, a.ldx, a.K, 2);
     // pieces of 256 columns a warp step, the parts of a row in turn
     for (int k0 = part * 256 + lane * 8; k0 < a.K; k0 += a.split * 256 * DEEP) {
-      uint4 w[DEEP];
+      Piece<VEC> w[DEEP];
 #pragma unroll
-      for (int d = 0; d < DEEP; ++d) w[d] = piece<VEC>(wr, k0 + d * a.split * 256, a.K);
+      for (int d = 0; d < DEEP; ++d) w[d].load(wr, k0 + d * a.split * 256, a.K, sw);
 #pragma unroll
       for (int d = 0; d < DEEP; ++d) {
+        const int k = k0 + d * a.split * 256;
+        if (!VEC && k - lane * 8 >= a.K) break;
+        Piece<VEC> x[T];
+#pragma unroll
+        for (int t = 0; t < T; ++t) x[t].load(a.x + t * a.ldx, k, a.K, sx);
         float wv[8];
-        unpack8(w[d], wv);
+        w[d].take(wr, k, a.K, wv);
 #pragma unroll
         for (int t = 0; t < T; ++t) {
           float xv[8];
-          unpack8(piece<VEC>(a.x + t * a.ldx, k0 + d * a.split * 256, a.K), xv);
+          x[t].take(a.x + t * a.ldx, k, a.K, xv);
 #pragma unroll
           for (int e = 0; e < 8; ++e) acc[t] += wv[e] * xv[e];
         }

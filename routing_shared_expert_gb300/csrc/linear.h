@@ -48,6 +48,12 @@ struct LinearGemm {
   int32_t* status;
   float* scratch;          // kPairScratchFloats: partial tiles of launch_linear_pair
   unsigned* tickets;       // kPairTicketBytes, zero between calls
+  // Gradients: db[c] = sum of part[b][c] over b < parts, for c < part_cols, beside the products (db
+  // nullptr: none).
+  const float* part;
+  int64_t parts;
+  int32_t part_cols;
+  float* db;
 };
 
 // Most CTA pairs of a launch, and the partial tiles (256 x 256 per pair) and arrival counts (a
@@ -64,6 +70,8 @@ cudaError_t launch_linear_pair(const LinearGemm& g, cudaStream_t s);
 // the operands are in L2, 640 in a single round), or of their parts, and what a launch costs.  f32:
 // the output's type.
 int64_t pair_cycles(int64_t M, int64_t N, int64_t K, bool f32, int sms);
+// Whether such a launch hides those sums: each of its lanes adds few enough of them.
+bool pair_hides_sums(const LinearGemm& g, int sms);
 // One to kVecTokens rows of A (both operands K-major, any alignment), a warp per row of B
 // (linear_vec.cu).
 constexpr int kVecTokens = 4;

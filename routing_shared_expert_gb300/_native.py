@@ -535,7 +535,11 @@ def _rows_of(name, t, shape=None):
     if t.is_contiguous():
         return (t.numel() // cols if cols else 0), cols, cols
     if t.dim() == 2 and (t.stride(1) == 1 or cols == 1):
-        return t.shape[0], cols, (t.stride(0) if t.shape[0] > 1 else cols)
+        ld = t.stride(0) if t.shape[0] > 1 else cols
+        if ld < cols:   # expanded rows (a stride of 0 would mean dense ones) or overlapping ones
+            raise ValueError(f"{name}: rows {ld} elements apart share memory, rows of {cols} elements of their "
+                             "own are expected (an expanded tensor needs .contiguous())")
+        return t.shape[0], cols, ld
     raise ValueError(f"{name}: contiguous tensors, or matrices of contiguous rows, are expected")
 
 

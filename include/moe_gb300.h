@@ -504,7 +504,8 @@ moe_status moe_layer_backward(const moe_config* cfg, const moe_weights* w, const
 /* moe_layer_backward with a further gradient of the router logits: dlogits [T][N] fp32
  * (device; moe_balance_loss writes it), or NULL.  It is added to dz, the gradient through the
  * coefficients, before dz is rounded to bf16 for dW_r = dz^T x and dx += dz W_r.  A dlogits
- * without grads->dW_router returns MOE_ERR_INVALID_ARG. */
+ * without grads->dW_router returns MOE_ERR_INVALID_ARG, one that is not aligned to 4 bytes
+ * MOE_ERR_MISALIGNED. */
 moe_status moe_layer_backward_aux(const moe_config* cfg, const moe_weights* w, const void* x,
                                   const moe_outputs* fwd, const float* dy, const float* dlogits,
                                   const moe_grads* grads, void* workspace, size_t workspace_bytes,

@@ -423,10 +423,10 @@ def moe_layer_backward(cfg, weights: moe_weights, x, fwd_outputs: moe_outputs, d
 
 def moe_layer_backward_aux(cfg, weights: moe_weights, x, fwd_outputs: moe_outputs, dy, dlogits,
                            grads: moe_grads, workspace, stream=None):
-    """moe_layer_backward with a further gradient of the router logits (fp32 [T][N])."""
+    """moe_layer_backward with a further gradient of the router logits (fp32 [T][N], or None)."""
     _check("moe_layer_backward_aux", _lib.moe_layer_backward_aux(
         ctypes.byref(cfg), ctypes.byref(weights), _ptr(x), ctypes.byref(fwd_outputs), _ptr(dy),
-        _ptr(dlogits), ctypes.byref(grads), _ptr(workspace), workspace.numel(), _stream(stream)))
+        _mat("dlogits", dlogits, cfg.T, cfg.N, 0, DTYPES["f32"]), ctypes.byref(grads), _ptr(workspace), workspace.numel(), _stream(stream)))
 
 
 # ---- the block around the layer ------------------------------------------------------

@@ -695,6 +695,7 @@ moe_status layer_backward(const moe_config* cfg, const moe_weights* w, const voi
   const BwdLayout L = make_bwd_layout(c);
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned16(x) || !aligned16(dy) || !aligned16(g->dx)) return MOE_ERR_MISALIGNED;
+  if ((reinterpret_cast<uintptr_t>(dlogits) & 3u) != 0) return MOE_ERR_MISALIGNED;
   int32_t* status = at<int32_t>(ws, L.status);
   int32_t* seg_pad = at<int32_t>(ws, L.seg_pad);
   auto ok = [](cudaError_t e) { return e == cudaSuccess; };

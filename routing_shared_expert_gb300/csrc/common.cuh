@@ -67,7 +67,8 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 
 // Programmatic dependent launch: lets the next launch of the stream begin its set-up, and waits
 // for everything that the previous one wrote (or reads).  Without the launch attribute both do
-// nothing.
+// nothing.  What follows the wait takes plain loads: a read-only one (ld.global.nc) is defined only
+// for data that nothing writes during the kernel's life, and the previous launch writes during it.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -531,7 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int k = 0; k < WARP_COLS / 32; ++k) {
         const int col = col0 + k * 32 + lane;
-        bias[k] = args.bias != nullptr && k * 32 < warp_cols && col < args.N ? __ldg(args.bias + col) : 0.f;
+        bias[k] = args.bias != nullptr && k * 32 < warp_cols && col < args.N ? args.bias[col] : 0.f;
       }
       // Waits for the next TMEM buffer; its columns of this warp start at taddr.
       uint32_t taddr = 0;

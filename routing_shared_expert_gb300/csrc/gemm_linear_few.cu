@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     const int tokens = min(NT, args.T - t0);
     float b[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) b[e] = args.bias && f + e < args.N ? __ldg(args.bias + f + e) : 0.f;
+    for (int e = 0; e < 4; ++e) b[e] = args.bias && f + e < args.N ? args.bias[f + e] : 0.f;
     constexpr int WARPS = THREADS / 32, UNROLL = 4;
     constexpr int VEC = 4 * sizeof(OUT);   // bytes of a lane's four values
     // whole groups of four go as one access where every row's groups are aligned to it

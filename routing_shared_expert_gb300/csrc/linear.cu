@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(256) align_rows_kernel(const __nv_bfloat16* sr
     const unsigned short* s = reinterpret_cast<const unsigned short*>(src + r * ld);
     uint32_t v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? __ldg(s + c + e) : 0u;
+    for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? s[c + e] : 0u;
     *reinterpret_cast<uint4*>(dst + r * ldd + c) =
         make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
   }

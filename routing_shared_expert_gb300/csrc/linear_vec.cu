@@ -42,7 +42,7 @@ template <bool VEC> struct Piece;
 template <> struct Piece<true> {
   uint4 u;
   __device__ __forceinline__ void load(const __nv_bfloat16* row, int k, int K, const Span&) {
-    u = k < K ? __ldg(reinterpret_cast<const uint4*>(row + k)) : make_uint4(0u, 0u, 0u, 0u);
+    u = k < K ? *reinterpret_cast<const uint4*>(row + k) : make_uint4(0u, 0u, 0u, 0u);
   }
   __device__ __forceinline__ void take(const __nv_bfloat16*, int, int, float (&v)[8]) const { unpack8(u, v); }
 };
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(32 * WARPS) linear_vec_kernel(const Args a) {
   if (t >= T || g >= a.N) return;
   float z = 0.f;
   for (int p = 0; p < a.split; ++p) z += s_part[r * a.split + p][t];
-  if (a.bias) z += __ldg(a.bias + g);
+  if (a.bias) z += a.bias[g];
   if (a.pre) static_cast<OUT*>(a.pre)[static_cast<int64_t>(t) * a.N + g] = from_f32<OUT>(z);
   float y = act_any(z, a.act);
   if (a.residual) y += to_f32(static_cast<const OUT*>(a.residual)[t * a.ldr + g]);

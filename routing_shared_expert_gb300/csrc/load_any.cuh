@@ -41,7 +41,7 @@ __device__ __forceinline__ Raw8 load8_raw(const T* p, const Span& s) {
 #pragma unroll
   for (int i = 0; i < N + 1; ++i) {
     r.piece[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (r.whole && (i < N || off)) r.piece[i] = __ldg(q + i);
+    if (r.whole && (i < N || off)) r.piece[i] = q[i];
   }
   return r;
 }
@@ -62,8 +62,8 @@ __device__ __forceinline__ uint4 take8(const Raw8& r, const __nv_bfloat16* p, in
     const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = 2 * i < valid ? __ldg(h + 2 * i) : 0u;
-      const uint32_t hi = 2 * i + 1 < valid ? __ldg(h + 2 * i + 1) : 0u;
+      const uint32_t lo = 2 * i < valid ? h[2 * i] : 0u;
+      const uint32_t hi = 2 * i + 1 < valid ? h[2 * i + 1] : 0u;
       o[i] = lo | hi << 16;
     }
   } else if (valid < 8) {
@@ -92,7 +92,7 @@ __device__ __forceinline__ void take8(const Raw8& r, const float* p, int valid, 
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(off & 4 ? x[i + 1] : x[i]);
   if (!r.whole) {   // at the tensor's ends
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < valid ? __ldg(p + i) : 0.f;
+    for (int i = 0; i < 8; ++i) v[i] = i < valid ? p[i] : 0.f;
   } else if (valid < 8) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = i < valid ? v[i] : 0.f;

@@ -615,7 +615,8 @@ moe_status moe_dropout_backward(const moe_dropout_config* cfg, const void* dy,
  * p the softmax, or sigmoid scores divided by their sum (cfg->score).  With f held fixed,
  *   dlogits_ti = g [coef_balance N / (S' V_s) p_ti (f_si - sum_j f_sj p_tj) (1 - sigma_ti if sigmoid)
  *                   + coef_z (2 / V) lse_t softmax_ti],   g = *grad_scale (NULL = 1).
- * A valid token whose logits are all -infinity has p = 0 and no z-loss.  V = 0: everything is 0.
+ * A valid token whose logits are all -infinity has p = 0 and no z-loss; one with a NaN logit makes
+ * its gradient, its sequence's P and the losses NaN.  V = 0: everything is 0.
  *   logits [T][N] fp32 and topk_idx [T][K] as moe_route wrote them (an index outside [0, N)
  *   counts for no expert and leaves MOE_ERR_DEVICE_BOUNDS in the status word; -1 is an empty
  *   slot and leaves nothing); grad_scale device fp32 or NULL.

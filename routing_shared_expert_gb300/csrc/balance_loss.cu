@@ -185,6 +185,13 @@ __device__ __forceinline__ void store_row8(float* p, int i, int N, int align, co
   }
 }
 
+// The larger value, or NaN where either is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
 // Sums and maxima over the W lanes of a row.
 template <int W> __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
@@ -193,7 +200,7 @@ template <int W> __device__ __forceinline__ float row_sum(float v) {
 }
 template <int W> __device__ __forceinline__ float row_max(float v) {
 #pragma unroll
-  for (int o = W / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = W / 2; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 
@@ -339,7 +346,7 @@ __global__ void __launch_bounds__(32 * kWarps, SIG ? 3 : 4) balance_rows_kernel(
       for (int e = 0; e < 8; ++e)
         if (i0 + e < N) reach = fmaxf(reach, fabsf(x[e]));
     }
-    // fmaxf drops a NaN: it stays in the sums, and so in the row, either way
+    // fmaxf drops a NaN: where the rest of the warp's logits are small it stays in its row's sums
     if (__all_sync(0xffffffffu, reach < kPlain)) {
       float se = 0.f, sp = 0.f, sd = 0.f;
 #pragma unroll
@@ -368,9 +375,9 @@ __global__ void __launch_bounds__(32 * kWarps, SIG ? 3 : 4) balance_rows_kernel(
     } else {
       float m = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m = fmaxf(m, i0 + e < N ? x[e] : -INFINITY);
+      for (int e = 0; e < 8; ++e) m = max_nan(m, i0 + e < N ? x[e] : -INFINITY);
       m = row_max<W>(m);
-      const bool any = m > -INFINITY;         // some logit is not -infinity
+      const bool any = !(m == -INFINITY);     // some logit is not -infinity (m is NaN if one is)
       float se = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {

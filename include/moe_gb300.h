@@ -516,8 +516,9 @@ moe_status moe_layer_backward_aux(const moe_config* cfg, const moe_weights* w, c
  * their epilogue, the router's balance loss with its gradient, and residual dropout.  The pages
  * stop at the layer (Eq. 80) and the loss value (Eq. 30); what each computes is given here. */
 
-/* Activation of a dense projection: identity, max(z, 0), z Phi(z) with the normal distribution
- * function Phi, its tanh form z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))), z sigmoid(z). */
+/* Activation of a dense projection: identity, max(z, 0) (NaN where z is, with slope 1), z Phi(z)
+ * with the normal distribution function Phi, its tanh form
+ * z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))), z sigmoid(z). */
 typedef enum {
   MOE_ACT_NONE = 0,
   MOE_ACT_RELU = 1,

@@ -20,7 +20,7 @@ def half_step(dtype):
 
 def act(z, kind):
     if kind == "relu":
-        return torch.where(z > 0, z, torch.zeros_like(z))
+        return torch.where(z <= 0, torch.zeros_like(z), z)      # NaN stays
     if kind == "gelu":
         return z * 0.5 * torch.special.erfc(-z / math.sqrt(2))
     if kind == "gelu_tanh":
@@ -32,7 +32,7 @@ def act(z, kind):
 
 def act_slope(z, kind):
     if kind == "relu":
-        return (z > 0).to(z.dtype)
+        return 1 - (z <= 0).to(z.dtype)
     if kind == "gelu":
         return 0.5 * torch.special.erfc(-z / math.sqrt(2)) + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
     if kind == "gelu_tanh":

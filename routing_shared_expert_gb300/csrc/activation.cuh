@@ -28,7 +28,7 @@ __device__ __forceinline__ float normal_cdf(float z, float& e) {
 // The tanh form of GELU uses (1 + tanh u) / 2 = sigmoid(2 u).
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
-  if (ACT == MOE_ACT_RELU) return z > 0.f ? z : 0.f;
+  if (ACT == MOE_ACT_RELU) return z <= 0.f ? 0.f : z;   // NaN stays
   if (ACT == MOE_ACT_GELU) {
     float e;
     return z * normal_cdf(z, e);
@@ -41,7 +41,7 @@ __device__ __forceinline__ float act_value(float z) {
 
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
-  if (ACT == MOE_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+  if (ACT == MOE_ACT_RELU) return z <= 0.f ? 0.f : 1.f;
   if (ACT == MOE_ACT_GELU) {
     float e;
     const float p = normal_cdf(z, e);

@@ -47,3 +47,41 @@ def test_balance_loss(moe, score, N, kind, seq):
     rest = torch.ones(T, dtype=torch.bool, device="cuda")
     rest[bad] = False
     assert torch.isfinite(out["dlogits"][rest]).all()
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("T,n", [(2, 64), (24, 257), (300, 256), (300, 255), (2000, 264)])
+def test_projection_forward(moe, act, out, T, n):
+    """A NaN pre-activation stays one through every activation, and no other value is touched."""
+    dt = torch.bfloat16 if out == "bf16" else torch.float32
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn((T, 64), generator=g, device="cuda").bfloat16()
+    W = torch.randn((n, 64), generator=g, device="cuda").bfloat16()
+    b = torch.zeros(n, device="cuda")
+    x[1, 3] = NAN
+    b[5] = NAN
+    cfg = moe.make_linear_config(T, 64, n, act=act, out_dtype=out)
+    ws, y = moe.alloc_linear_workspace(cfg), torch.zeros((T, n), dtype=dt, device="cuda")
+    moe.moe_linear_forward(cfg, x, W, b, None, None, y, ws)
+    want = torch.zeros((T, n), dtype=torch.bool, device="cuda")
+    want[1] = True
+    want[:, 5] = True
+    assert torch.equal(torch.isnan(y), want)
+    assert torch.isfinite(y[~want]).all()
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [64, 63])
+def test_projection_backward_through_relu(moe, out, n):
+    """The gradient passes where the pre-activation is NaN, as it does in max(z, 0) by torch, and stops
+    at negative values and zero."""
+    dt = torch.bfloat16 if out == "bf16" else torch.float32
+    T = 70
+    pre = torch.tensor([1.0, -1.0, 0.0, -0.0, NAN, INF, -INF], device="cuda").repeat(T * n // 7)[:T * n].view(T, n).to(dt)
+    dy = (torch.arange(T * n, device="cuda") % 31 + 1.0).view(T, n).to(dt)
+    cfg = moe.make_linear_config(T, 64, n, act="relu", out_dtype=out)
+    ws, db = moe.alloc_linear_workspace(cfg), torch.zeros(n, device="cuda")
+    moe.moe_linear_backward(cfg, None, None, pre, dy, None, None, db, ws)
+    zero = torch.zeros((), dtype=dt, device="cuda")
+    assert torch.equal(db, torch.where(pre <= 0, zero, dy).float().sum(0))

@@ -30,6 +30,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "smem_table.h"
 
 namespace moe {
 namespace {
@@ -561,29 +562,17 @@ bool make_bf16_store_map(CUtensorMap* m, const void* base, uint64_t inner, uint6
 }
 
 cudaError_t set_smem_once(const void* func, size_t bytes) {
-  struct Entry {
-    const void* func;
-    int dev;
-    size_t bytes;
-  };
   static std::mutex mu;
-  static Entry seen[64];
-  static int n = 0;
+  static SmemTable table;
   int dev = 0;
   cudaGetDevice(&dev);
   std::lock_guard<std::mutex> lock(mu);
-  for (int i = 0; i < n; ++i)
-    if (seen[i].func == func && seen[i].dev == dev && seen[i].bytes >= bytes) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(bytes));
-  if (e != cudaSuccess) return e;
-  for (int i = 0; i < n; ++i)
-    if (seen[i].func == func && seen[i].dev == dev) {
-      seen[i].bytes = bytes;
-      return cudaSuccess;
-    }
-  if (n < 64) seen[n++] = Entry{func, dev, bytes};
-  return cudaSuccess;
+  SmemTable::Entry* e = table.find(func, dev);
+  if (e && e->bytes >= bytes) return cudaSuccess;
+  const cudaError_t err = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(bytes));
+  if (err == cudaSuccess && e) e->bytes = bytes;
+  return err;
 }
 
 int device_sm_count() {

@@ -168,6 +168,9 @@ __global__ void __launch_bounds__(256) align_rows_kernel(const __nv_bfloat16* sr
 
 int64_t up8(int64_t v) { return (v + 7) & ~int64_t{7}; }
 
+// Elements between rows: dense ones for 0, and for a single row, whose stride may be anything.
+int64_t row_stride(int64_t ld, int64_t rows, int32_t cols) { return ld == 0 || rows == 1 ? cols : ld; }
+
 struct LinearLayout {
   size_t dz, db_part, x, w, scratch, total;
 };
@@ -269,7 +272,7 @@ moe_status moe_linear_forward(const moe_linear_config* cfg, const void* x, const
     return MOE_ERR_MISALIGNED;
   const LinearLayout L = linear_layout(c);
   char* ws = static_cast<char*>(workspace);
-  const int64_t ldx = c.ldx ? c.ldx : c.in_features, ldw = c.ldw ? c.ldw : c.in_features;
+  const int64_t ldx = row_stride(c.ldx, c.T, c.in_features), ldw = row_stride(c.ldw, c.out_features, c.in_features);
   const bool aligned = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(W)) & 15u) == 0 &&
                        (ldx % 8 == 0 || c.T == 1) && ldw % 8 == 0;
   const Form form = forward_form(c.T, c.out_features, c.in_features, c.out_dtype == MOE_F32, aligned);
@@ -291,8 +294,8 @@ moe_status moe_linear_forward(const moe_linear_config* cfg, const void* x, const
   g.residual = residual;
   g.pre = pre;
   g.C = y;
-  g.ldr = c.ldr ? c.ldr : c.out_features;
-  g.ldc = c.ldy ? c.ldy : c.out_features;
+  g.ldr = row_stride(c.ldr, c.T, c.out_features);
+  g.ldc = row_stride(c.ldy, c.T, c.out_features);
   g.status = static_cast<int32_t*>(workspace);
   g.scratch = reinterpret_cast<float*>(ws + L.scratch);
   g.tickets = reinterpret_cast<unsigned*>(ws + kPairTicketOffset);
@@ -324,7 +327,7 @@ moe_status moe_linear_backward(const moe_linear_config* cfg, const void* x, cons
   if (!dy || (c.act != MOE_ACT_NONE && !pre) || (dW && !x) || (dx && !W)) return MOE_ERR_INVALID_ARG;
   const LinearLayout L = linear_layout(c);
   char* ws = static_cast<char*>(workspace);
-  const int64_t ldy = c.ldy ? c.ldy : c.out_features;
+  const int64_t ldy = row_stride(c.ldy, c.T, c.out_features);
   const int32_t n = c.out_features;
   const int64_t blocks = (c.T + kDzRows - 1) / kDzRows;
   const bool identity = c.act == MOE_ACT_NONE;
@@ -377,7 +380,7 @@ moe_status moe_linear_backward(const moe_linear_config* cfg, const void* x, cons
   }
   if (dx) {
     Operand o;
-    if (aligned_operand(W, n, c.in_features, c.ldw ? c.ldw : c.in_features, ws + L.w, &o, stream) != cudaSuccess)
+    if (aligned_operand(W, n, c.in_features, row_stride(c.ldw, n, c.in_features), ws + L.w, &o, stream) != cudaSuccess)
       return MOE_ERR_CUDA;
     g.B = o.p;
     g.ldb = o.ld;
@@ -390,7 +393,7 @@ moe_status moe_linear_backward(const moe_linear_config* cfg, const void* x, cons
   }
   if (dW) {
     Operand o;
-    if (aligned_operand(x, c.T, c.in_features, c.ldx ? c.ldx : c.in_features, ws + L.x, &o, stream) != cudaSuccess)
+    if (aligned_operand(x, c.T, c.in_features, row_stride(c.ldx, c.T, c.in_features), ws + L.x, &o, stream) != cudaSuccess)
       return MOE_ERR_CUDA;
     g.B = o.p;
     g.ldb = o.ld;

@@ -105,3 +105,69 @@ def test_forward_and_backward_in_turn(moe, T, n):
     for x, dx in seen:
         gate = (x.roll(5, 1) > 0).to(dy.dtype)
         assert torch.equal(dx, (dy * gate).roll(-5, 1))
+
+
+@pytest.mark.parametrize("T,n", [(1, 512), (24, 512), (300, 512), (300, 511)])
+def test_captured_beside_copies_and_another_stream(moe, T, n):
+    """Captured: operands written by a copy node and by a call on a second stream that joins."""
+    cfg, add = moe.make_linear_config(T, n, n), moe.make_linear_config(T, n, n)
+    ws, ws2, W = moe.alloc_linear_workspace(cfg), moe.alloc_linear_workspace(cfg), shift(n, 5)
+    src = numbers(T, n, torch.bfloat16) % 16
+    x, a, b, y, z = (torch.zeros_like(src) for _ in range(5))
+    side = torch.cuda.Stream()
+
+    def work():
+        main = torch.cuda.current_stream()
+        x.copy_(src)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            for _ in range(6):          # longer than what it joins
+                moe.moe_linear_forward(cfg, x, W, None, None, None, a, ws2)
+                moe.moe_linear_forward(cfg, a, W, None, None, None, b, ws2)
+        moe.moe_linear_forward(cfg, x, W, None, None, None, y, ws)
+        main.wait_stream(side)
+        moe.moe_linear_forward(add, y, W, None, b, None, z, ws)     # reads both streams' outputs
+        y.zero_()                                                   # and its operand is cleared behind it
+
+    warm = torch.cuda.Stream()
+    warm.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(warm):
+        work()
+    torch.cuda.current_stream().wait_stream(warm)
+    assert torch.equal(z, 2 * src.roll(10, 1))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work()
+    for i in range(5):
+        src.copy_(src.roll(1, 1))
+        for t in (x, a, b, z):
+            t.zero_()
+        graph.replay()
+        assert torch.equal(z, 2 * src.roll(10, 1)), i
+        assert (y == 0).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,N,seq", [(20000, 64, 0), (20000, 256, 2048), (600, 8, 100)])
+def test_balance_loss_of_logits_rewritten_in_place(moe, score, T, N, seq):
+    """The second launch of the loss begins under its first with logits that the call before it read
+    as other values."""
+    cfg = moe.make_config(T=T, d_model=64, N=N, K=2, d_expert=64, d_shared=0, shared_mode="none", score=score)
+    ws = moe.alloc_balance_loss_workspace(cfg, seq)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    base = torch.randn((T, N), generator=g, device="cuda")
+    z, idx = torch.empty_like(base), torch.topk(base, 2, dim=1).indices.to(torch.int32)
+    outs = [(torch.empty(3, device="cuda"), torch.empty_like(base)) for _ in range(12)]
+
+    def turn(i, loss, dz):
+        torch.mul(base, 1.0 - 0.125 * i, out=z)
+        moe.moe_balance_loss(cfg, z, idx, None, seq, 0.3, 0.01, None, None, None, loss, dz, ws)
+
+    for i, o in enumerate(outs):
+        turn(i, *o)
+    torch.cuda.synchronize()
+    again = (torch.empty(3, device="cuda"), torch.empty_like(base))
+    for i, o in enumerate(outs):
+        turn(i, *again)
+        torch.cuda.synchronize()
+        assert torch.equal(o[0], again[0]) and torch.equal(o[1], again[1]), i

@@ -568,7 +568,8 @@ moe_status moe_linear_forward(const moe_linear_config* cfg, const void* x, const
  *   dx = dz W [T][in] (dx_dtype),  dW = dz^T x [out][in] (dw_dtype),  dbias = sum_t dz (fp32).
  * The gradient of the residual is dy itself.  dx, dW and dbias may each be NULL (not computed);
  * each is overwritten.  The matrix products take dz rounded to bf16 once (dy as it is, when
- * act is none and dy is bf16) and accumulate in fp32; dbias sums the unrounded dz in a fixed
+ * act is none and dy is bf16), fp32 dy, dx and dW included: those types keep the sums, not dz, and
+ * leave a relative error of about 2e-3.  They accumulate in fp32; dbias sums the unrounded dz in a fixed
  * order.  T = 0 writes dW = 0 and dbias = 0.  x is needed for dW only and W for dx only.
  * Errors as above. */
 moe_status moe_linear_backward(const moe_linear_config* cfg, const void* x, const void* W,

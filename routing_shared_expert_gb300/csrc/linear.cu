@@ -63,6 +63,12 @@ struct DzArgs {
 
 // dz = dy act'(pre) and, per block of kDzRows rows, its column sums (each warp its rows in
 // order, then the warps in order).  VEC: 16-byte loads of whole groups of eight columns.
+//
+// dz is rounded to bf16 whatever the types of dy, dx and dW: a product on the tensor cores takes both
+// operands in one 16-bit type, and the others, x and W, are bf16.  With bf16 results the error of dx and
+// dW is 2.35e-3 (rms, relative) against 1.66e-3 if only they were rounded; with fp32 ones it is 1.7e-3.
+// The rest dz - bf16(dz) as a second operand would bring that to a few 10^-6 and take dx and dW twice
+// as long.
 template <typename OUT, bool VEC, int ACT>
 __global__ void __launch_bounds__(256) dz_kernel(DzArgs a) {
   __shared__ float s_sum[8][kDzCols];

@@ -77,8 +77,8 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
 // G groups of eight elements per thread, each one access of each operand, the generator between
 // the loads and the stores.  Dense operands are one row of n elements, whatever their shape;
 // strided ones have rows of a multiple of eight.
-// Bound by memory for large operands: 8192 x 7168, fp32 + bf16 -> bf16, in 66 us (7.1 TB/s) on one
-// GB300, 16383 x 2047 bf16 -> fp32 in 30.4 us.  With one group per thread the generator's integer
+// Bound by memory for large operands: 8192 x 7168, fp32 + bf16 -> bf16, in 66 to 69 us (7.1 to 6.8
+// TB/s, by the GB300), 16383 x 2047 bf16 -> fp32 in 30.4 to 32.8 us.  With one group per thread the generator's integer
 // products bind instead (75 and 38 us).
 template <typename X, typename R, typename Y, bool RES, int G, bool DENSE>
 __global__ void __launch_bounds__(256) dropout_vec_kernel(DropoutArgs a) {

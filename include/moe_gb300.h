@@ -634,6 +634,118 @@ moe_status moe_balance_loss(const moe_config* cfg, const float* logits, const in
                             float* loss, float* dlogits, void* workspace, size_t workspace_bytes,
                             cudaStream_t stream);
 
+/* ---- Around the block: what a training step puts in front of it, under it and behind it ---- */
+
+/* Normalisation of rows: LAYER centres each row, RMS does not. */
+typedef enum { MOE_LAYERNORM_LAYER = 0, MOE_LAYERNORM_RMS = 1 } moe_layernorm_kind;
+
+/* One normalisation over T rows of d values.  Each call's configuration describes its own
+ * operands; the forward and the backward call of one layer usually differ in x_dtype and ldx.
+ * Rows may be strided (elements between rows; 0 = d, a single row's is not looked at), elements
+ * within a row are contiguous, pointers are aligned to their element type. */
+typedef struct moe_layernorm_config {
+  int64_t T;             /* rows, 0..2^30 */
+  int32_t d;             /* values of a row, 1..2^20 */
+  int32_t kind;          /* moe_layernorm_kind */
+  float eps;             /* >= 0, finite */
+  int32_t x_dtype;       /* moe_dtype of x; of h in the backward pass */
+  int32_t stream_dtype;  /* moe_dtype of the residual and sum; of dsum and dx */
+  int32_t y_dtype;       /* moe_dtype of y and dy */
+  int32_t w_dtype;       /* moe_dtype of weight and bias */
+  int64_t ldx, ldr, lds, ldy;  /* rows of x (h), residual (dsum), sum (dx), y (dy) */
+} moe_layernorm_config;
+
+/* y = (h - mean) rstd w + b with h = x + r, mean = sum_c h / d (0 for RMS) and
+ * rstd = (sum_c (h - mean)^2 / d + eps)^(-1/2).
+ * residual [T][d] stream_dtype or NULL (h = x); sum [T][d] stream_dtype or NULL: x + r, rounded to
+ * that type before the row is normalised, so that a backward pass on sum sees the same h.  A sum
+ * without a residual is MOE_ERR_INVALID_ARG.  weight [d] (NULL: 1) and bias [d] (NULL: 0) w_dtype;
+ * mean, rstd fp32 [T] or NULL (mean with RMS: MOE_ERR_INVALID_ARG).  Statistics and products in
+ * fp32, the mean before the deviations, one rounding of y.  A row that holds an infinity or a NaN gives
+ * what the formula gives; no other row is touched by it.
+ * sum may be x or the residual itself and y may be x or the residual (when sum is not), each where
+ * type and stride agree; no other buffers may overlap.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (rows past 2^40 elements), MOE_ERR_MISALIGNED,
+ * MOE_ERR_CUDA. */
+moe_status moe_layernorm_forward(const moe_layernorm_config* cfg, const void* x,
+                                 const void* residual, const void* weight, const void* bias,
+                                 void* sum, void* y, float* mean, float* rstd, cudaStream_t stream);
+
+/* Gradients for dy [T][d] of y and, where the stream has one of its own, dsum [T][d] of sum
+ * (NULL: 0), with xhat = (h - mean) rstd, g = dy w:
+ *   dx = rstd (g - sum_c g / d [LAYER only] - xhat sum_c g xhat / d) + dsum   (of x and residual)
+ *   dweight = sum_t dy xhat,   dbias = sum_t dy   (fp32 [d], each may be NULL; overwritten).
+ * h [T][d] is what was normalised: sum, or x where there was no residual; mean (ignored for RMS) and
+ * rstd as the forward call wrote them.  Sums in fp32 in a fixed order.  dx may be dsum, dy or h
+ * itself where type and stride agree, or NULL.  T = 0 writes zeros to dweight and dbias.
+ * workspace: moe_layernorm_workspace_size bytes, prepared by moe_workspace_init (its status word
+ * stays MOE_OK).  Errors: those of the forward call, MOE_ERR_WORKSPACE_TOO_SMALL. */
+moe_status moe_layernorm_workspace_size(int64_t T, int32_t d, size_t* bytes);
+moe_status moe_layernorm_backward(const moe_layernorm_config* cfg, const void* h,
+                                  const void* weight, const float* mean, const float* rstd,
+                                  const void* dy, const void* dsum, void* dx, float* dweight,
+                                  float* dbias, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream);
+
+/* Token embedding: T token numbers into a table of V rows of d values.  Rows of the table (and of
+ * its gradient) and of out (and its gradient) may be strided as above. */
+typedef struct moe_embedding_config {
+  int64_t T;            /* tokens, 0..2^26 */
+  int64_t V;            /* rows of the table, 1..2^30 */
+  int32_t d;            /* values of a row, 1..2^20 */
+  int32_t ids_int64;    /* 1: ids are int64, 0: int32 */
+  int32_t table_dtype;  /* moe_dtype of the table and of its gradient */
+  int32_t out_dtype;    /* moe_dtype of out and of its gradient */
+  float scale;          /* finite */
+  int64_t ldt, ldo;
+} moe_embedding_config;
+
+/* out_t = scale table[ids_t], the product in fp32, rounded once.  ids -1: no token, a row of zeros.  Any
+ * other number outside [0, V) gives a row of zeros and leaves MOE_ERR_DEVICE_BOUNDS in the status word.
+ * workspace: moe_embedding_workspace_size bytes, prepared by moe_workspace_init; the forward call
+ * uses its first 256 bytes.  Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (more than 2^40
+ * elements), MOE_ERR_MISALIGNED, MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_CUDA. */
+moe_status moe_embedding_workspace_size(int64_t T, int64_t V, int32_t d, size_t* bytes);
+moe_status moe_embedding_forward(const moe_embedding_config* cfg, const void* ids, const void* table,
+                                 void* out, void* workspace, size_t workspace_bytes,
+                                 cudaStream_t stream);
+
+/* dtable_v = scale sum_{t: ids_t = v} dout_t over the tokens in ascending blocks, in fp32 and in a
+ * fixed order, rounded once.  accumulate 0: every row of dtable is written, zeros where no token
+ * is; 1: the sum is added to what dtable holds (in fp32, rounded once) and rows without a token stay
+ * as they are.  Numbers outside [0, V) as above add nothing.  dout's rows at such tokens are not
+ * looked at.  Errors as above. */
+moe_status moe_embedding_backward(const moe_embedding_config* cfg, const void* ids, const void* dout,
+                                  void* dtable, int32_t accumulate, void* workspace,
+                                  size_t workspace_bytes, cudaStream_t stream);
+
+/* One tensor of a list: rows x cols elements, rows ld elements apart (dense: rows = 1, ld = 0). */
+typedef struct moe_tensor {
+  void* data;           /* device, aligned to its element type; may be NULL when it is empty */
+  int64_t rows, cols, ld;
+  int32_t dtype;        /* moe_dtype */
+} moe_tensor;
+
+/* norm[0] = (sum over the tensors' elements of g^2)^(1/2), norm[1] = 1 where max_norm is infinite,
+ * else min(1, max_norm / (norm + 1e-6)) (device fp32 [2]).  grads: HOST [count], count 0..2^20,
+ * read before the call returns.  Squares and sums in fp32 in a fixed order, joined in fp64: an element
+ * above 1.8e19 makes the norm infinite, squares below 1.2e-38 lose bits.  An infinity or a NaN in any
+ * element shows in both numbers as the formula has it.  max_norm >= 0; a NaN is refused.
+ * workspace: moe_grad_norm_workspace_size bytes, prepared by moe_workspace_init.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (a tensor or the list past 2^40 elements),
+ * MOE_ERR_MISALIGNED, MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_CUDA. */
+moe_status moe_grad_norm_workspace_size(size_t* bytes);
+moe_status moe_grad_norm(const moe_tensor* grads, int32_t count, float max_norm, float* norm,
+                         void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* moe_grad_norm, then out_i = norm[1] g_i in fp32, rounded once.  out: HOST [count], shapes and types
+ * of grads, or NULL: the gradients themselves are scaled, and stay untouched when norm[1] is 1.
+ * No two tensors that the call writes, and none that it writes and another that it reads, may
+ * share memory, out_i = grads_i (same address and stride) apart: MOE_ERR_INVALID_ARG.  Errors as above. */
+moe_status moe_clip_grad_norm(const moe_tensor* grads, const moe_tensor* out, int32_t count,
+                              float max_norm, float* norm, void* workspace, size_t workspace_bytes,
+                              cudaStream_t stream);
+
 /* Prepare a fresh workspace: zero its device status word (the first 256 bytes).  Call once
  * after allocating a workspace, before its first use.  Asynchronous on the stream. */
 moe_status moe_workspace_init(void* workspace, size_t workspace_bytes, cudaStream_t stream);

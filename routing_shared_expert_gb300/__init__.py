@@ -5,6 +5,9 @@ The compute path is the CUDA library ``libmoe_gb300.so`` (C ABI in
 requires the built library: there is no CPU fallback.
 """
 from ._native import (  # noqa: F401
+    alloc_embedding_workspace, alloc_grad_norm_workspace, alloc_layernorm_workspace, moe_clip_grad_norm,
+    moe_embedding_backward, moe_embedding_forward, moe_embedding_workspace_size, moe_grad_norm,
+    moe_layernorm_backward, moe_layernorm_forward, moe_layernorm_workspace_size,
     ACTS, STATS, MoEError, alloc_balance_loss_workspace, alloc_linear_workspace, alloc_workspace,
     copy_config, library, make_config, make_linear_config, make_outputs, make_weights,
     moe_balance_loss, moe_balance_loss_workspace_size, moe_dropout_add, moe_dropout_backward,

@@ -26,6 +26,7 @@ SHARED_MODES = {"none": 0, "const": 1, "gate": 2}
 CAP_POLICIES = {"none": 0, "per_expert": 1, "rank_wide": 2}
 H_FORMATS = {"bf16": 0, "f16": 1}
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+LAYERNORM_KINDS = {"layer": 0, "rms": 1}
 
 
 class MoEError(RuntimeError):
@@ -59,6 +60,22 @@ class moe_dropout_config(ctypes.Structure):
     _fields_ = [("rows", c_int64), ("cols", c_int64), ("p", c_double), ("x_dtype", c_int32),
                 ("residual_dtype", c_int32), ("y_dtype", c_int32), ("ldx", c_int64), ("ldr", c_int64),
                 ("ldy", c_int64)]
+
+
+class moe_layernorm_config(ctypes.Structure):
+    _fields_ = [("T", c_int64), ("d", c_int32), ("kind", c_int32), ("eps", c_float), ("x_dtype", c_int32),
+                ("stream_dtype", c_int32), ("y_dtype", c_int32), ("w_dtype", c_int32), ("ldx", c_int64),
+                ("ldr", c_int64), ("lds", c_int64), ("ldy", c_int64)]
+
+
+class moe_embedding_config(ctypes.Structure):
+    _fields_ = [("T", c_int64), ("V", c_int64), ("d", c_int32), ("ids_int64", c_int32),
+                ("table_dtype", c_int32), ("out_dtype", c_int32), ("scale", c_float), ("ldt", c_int64),
+                ("ldo", c_int64)]
+
+
+class moe_tensor(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("rows", c_int64), ("cols", c_int64), ("ld", c_int64), ("dtype", c_int32)]
 
 
 GRAD_FIELDS = ("dx", "dW_gate", "dW_up", "dW_down", "dWs_gate", "dWs_up", "dWs_down", "dW_router",
@@ -135,6 +152,16 @@ def _load():
                                 c_int32),
         "moe_dropout_add": ([POINTER(moe_dropout_config), P, P, P, P, P], c_int32),
         "moe_dropout_backward": ([POINTER(moe_dropout_config), P, P, P, P], c_int32),
+        "moe_layernorm_forward": ([POINTER(moe_layernorm_config), P, P, P, P, P, P, P, P, P], c_int32),
+        "moe_layernorm_workspace_size": ([c_int64, c_int32, POINTER(c_size_t)], c_int32),
+        "moe_layernorm_backward": ([POINTER(moe_layernorm_config), P, P, P, P, P, P, P, P, P, P, c_size_t, P],
+                                   c_int32),
+        "moe_embedding_workspace_size": ([c_int64, c_int64, c_int32, POINTER(c_size_t)], c_int32),
+        "moe_embedding_forward": ([POINTER(moe_embedding_config), P, P, P, P, c_size_t, P], c_int32),
+        "moe_embedding_backward": ([POINTER(moe_embedding_config), P, P, P, c_int32, P, c_size_t, P], c_int32),
+        "moe_grad_norm_workspace_size": ([POINTER(c_size_t)], c_int32),
+        "moe_grad_norm": ([P, c_int32, c_float, P, P, c_size_t, P], c_int32),
+        "moe_clip_grad_norm": ([P, P, c_int32, c_float, P, P, c_size_t, P], c_int32),
         "moe_balance_loss_workspace_size": ([C, c_int64, POINTER(c_size_t)], c_int32),
         "moe_balance_loss": ([C, P, P, P, c_int64, c_float, c_float, P, P, P, P, P, P, c_size_t, P],
                              c_int32),
@@ -598,3 +625,242 @@ def moe_balance_loss(cfg: moe_config, logits, topk_idx, token_mask, seq_len, coe
         _vec("grad_scale", grad_scale, 1), _vec("counts", counts, S * N, "int32"),
         _vec("P", P, S * N), _vec("loss", loss, 3), _vec("dlogits", dlogits, T * N), _ptr(workspace),
         workspace.numel(), _stream(stream)))
+
+
+# ---- around the block ------------------------------------------------------------------
+
+def _device_of(name, t) -> int:
+    """Device number of the first tensor of a call, which has to be the current device's."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: a CUDA tensor is expected")
+    import torch
+    if torch._C._cuda_getDevice() != dev:
+        raise ValueError(f"{name}: on device {dev}, which is not the current one")
+    return dev
+
+
+def _rows(name, t, dev, rows, cols):
+    """(address, moe_dtype, row stride) of a [rows][cols] matrix with contiguous rows; a row stride of 0
+    stands for dense rows."""
+    dtype = _TORCH_DTYPES.get(t.dtype)
+    if dtype is None:
+        raise ValueError(f"{name}: fp32 or bf16 is expected, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: a tensor on device {dev} is expected, got {t.device}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name}: expected [{rows}][{cols}], got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), dtype, 0
+    s0, s1 = t.stride()
+    if (s1 != 1 and cols > 1) or s0 < cols:
+        raise ValueError(f"{name}: strides {t.stride()} are not those of contiguous rows of {cols} elements with "
+                         "memory of their own (an expanded or transposed tensor needs .contiguous())")
+    return t.data_ptr(), dtype, s0
+
+
+def _flat(name, t, dev, n, dtype):
+    """Address of n contiguous values of one moe_dtype."""
+    if t is None:
+        return None
+    if t.get_device() != dev or t.shape != (n,) or _TORCH_DTYPES.get(t.dtype) != dtype or \
+            (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name}: expected {n} contiguous values of {'fp32' if dtype == 0 else 'bf16'} on device "
+                         f"{dev}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def _raw_stream(stream, dev):
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _workspace(ws, dev):
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"workspace: a contiguous tensor on device {dev} is expected")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def moe_layernorm_workspace_size(T: int, d: int) -> int:
+    n = c_size_t(0)
+    _check("moe_layernorm_workspace_size", _lib.moe_layernorm_workspace_size(int(T), int(d), ctypes.byref(n)))
+    return int(n.value)
+
+
+def alloc_layernorm_workspace(T: int, d: int, device="cuda", stream=None):
+    """A zero-status workspace (uint8 tensor) for moe_layernorm_backward."""
+    import torch
+    ws = torch.empty(moe_layernorm_workspace_size(T, d), dtype=torch.uint8, device=device)
+    moe_workspace_init(ws, stream)
+    return ws
+
+
+def _norm_param(weight, bias):
+    """moe_dtype of the parameters, which share one."""
+    p = weight if weight is not None else bias
+    return 0 if p is None else _dtype_of(p)
+
+
+def moe_layernorm_forward(x, residual, weight, bias, eps, sum, y, mean, rstd, kind="layer", stream=None):
+    """y = (h - mean) rstd weight + bias of rows h = x + residual, which goes to ``sum`` (then h is the sum as
+    stored), or of x alone.  x, residual, sum, y: matrices [T][d], rows may be strided; residual and sum have
+    one type.  weight, bias [d]; mean, rstd fp32 [T].  residual, weight, bias, sum, mean and rstd may be None;
+    kind "rms" has no mean."""
+    _dtypes()
+    dev = _device_of("x", x)
+    if x.dim() != 2:
+        raise ValueError(f"x: a matrix is expected, got {tuple(x.shape)}")
+    T, d = x.shape
+    px, xt, ldx = _rows("x", x, dev, T, d)
+    pr, st, ldr = (None, 0, 0) if residual is None else _rows("residual", residual, dev, T, d)
+    ps, s2, lds = (None, st, 0) if sum is None else _rows("sum", sum, dev, T, d)
+    if s2 != st and residual is not None:
+        raise ValueError("sum: the type of the residual is expected")
+    py, yt, ldy = _rows("y", y, dev, T, d)
+    wt = _norm_param(weight, bias)
+    c = moe_layernorm_config(T, d, _enum(LAYERNORM_KINDS, kind), eps, xt, st, yt, wt, ldx, ldr, lds, ldy)
+    _check("moe_layernorm_forward", _lib.moe_layernorm_forward(
+        ctypes.byref(c), px, pr, _flat("weight", weight, dev, d, wt), _flat("bias", bias, dev, d, wt), ps, py,
+        _flat("mean", mean, dev, T, 0), _flat("rstd", rstd, dev, T, 0), _raw_stream(stream, dev)))
+
+
+def moe_layernorm_backward(h, weight, mean, rstd, dy, dsum, dx, dweight, dbias, workspace, kind="layer",
+                           stream=None):
+    """dx (of x and of the residual), dweight and dbias (fp32) for the gradient dy of y and dsum of ``sum``; each
+    result, weight and dsum may be None.  h is the forward call's ``sum``, or its x where it had no residual;
+    dsum and dx have one type.  dx may be dsum, dy or h itself."""
+    _dtypes()
+    dev = _device_of("h", h)
+    if h.dim() != 2:
+        raise ValueError(f"h: a matrix is expected, got {tuple(h.shape)}")
+    T, d = h.shape
+    ph, ht, ldh = _rows("h", h, dev, T, d)
+    py, yt, ldy = _rows("dy", dy, dev, T, d)
+    pr, st, ldr = (None, 0, 0) if dsum is None else _rows("dsum", dsum, dev, T, d)
+    px, s2, lds = (None, st, 0) if dx is None else _rows("dx", dx, dev, T, d)
+    if dsum is None:
+        st = s2
+    elif s2 != st:
+        raise ValueError("dx: the type of dsum is expected")
+    wt = _norm_param(weight, None)
+    c = moe_layernorm_config(T, d, _enum(LAYERNORM_KINDS, kind), 0.0, ht, st, yt, wt, ldh, ldr, lds, ldy)
+    pw, nw = _workspace(workspace, dev)
+    _check("moe_layernorm_backward", _lib.moe_layernorm_backward(
+        ctypes.byref(c), ph, _flat("weight", weight, dev, d, wt), _flat("mean", mean, dev, T, 0),
+        _flat("rstd", rstd, dev, T, 0), py, pr, px, _flat("dweight", dweight, dev, d, 0),
+        _flat("dbias", dbias, dev, d, 0), pw, nw, _raw_stream(stream, dev)))
+
+
+def moe_embedding_workspace_size(T: int, V: int, d: int) -> int:
+    n = c_size_t(0)
+    _check("moe_embedding_workspace_size",
+           _lib.moe_embedding_workspace_size(int(T), int(V), int(d), ctypes.byref(n)))
+    return int(n.value)
+
+
+def alloc_embedding_workspace(T: int, V: int, d: int, device="cuda", stream=None):
+    """A zero-status workspace (uint8 tensor) for moe_embedding_forward and moe_embedding_backward of up to T
+    tokens."""
+    import torch
+    ws = torch.empty(moe_embedding_workspace_size(T, V, d), dtype=torch.uint8, device=device)
+    moe_workspace_init(ws, stream)
+    return ws
+
+
+def _embedding(ids, table, out, out_name, table_name, scale):
+    """(configuration, addresses of ids, table and out, device)"""
+    _dtypes()
+    import torch
+    dev = _device_of("ids", ids)
+    if table.dim() != 2 or (ids.dtype is not torch.int64 and ids.dtype is not torch.int32) or \
+            not ids.is_contiguous():
+        raise ValueError("contiguous int64 or int32 token numbers and a matrix are expected, got "
+                         f"{ids.dtype} of strides {ids.stride()} and {tuple(table.shape)}")
+    T, (V, d) = ids.numel(), table.shape
+    pt, tt, ldt = _rows(table_name, table, dev, V, d)
+    if out.dim() > 2 and out.is_contiguous():      # token numbers of any shape
+        if out.shape[:-1] != ids.shape:
+            raise ValueError(f"{out_name}: expected {tuple(ids.shape)} rows of {d}, got {tuple(out.shape)}")
+        out = out.view(-1, out.shape[-1])
+    po, ot, ldo = _rows(out_name, out, dev, T, d)
+    return moe_embedding_config(T, V, d, ids.dtype is torch.int64, tt, ot, scale, ldt, ldo), ids.data_ptr(), pt, po, dev
+
+
+def moe_embedding_forward(ids, table, scale, out, workspace, stream=None):
+    """out[t] = scale table[ids[t]], zeros where ids[t] is -1.  ids: int64 or int32, any shape; table [V][d];
+    out [tokens][d], or the ids' shape and d.  Another number outside the table leaves a row of zeros and
+    MOE_ERR_DEVICE_BOUNDS for moe_read_status."""
+    c, pi, pt, po, dev = _embedding(ids, table, out, "out", "table", scale)
+    pw, nw = _workspace(workspace, dev)
+    _check("moe_embedding_forward", _lib.moe_embedding_forward(ctypes.byref(c), pi, pt, po, pw, nw,
+                                                               _raw_stream(stream, dev)))
+
+
+def moe_embedding_backward(ids, dout, scale, dtable, workspace, accumulate=False, stream=None):
+    """dtable[v] = scale * sum of dout[t] over the tokens with ids[t] = v, zeros for the others; with
+    ``accumulate`` the sums are added to what dtable holds."""
+    c, pi, pt, po, dev = _embedding(ids, dtable, dout, "dout", "dtable", scale)
+    pw, nw = _workspace(workspace, dev)
+    _check("moe_embedding_backward", _lib.moe_embedding_backward(
+        ctypes.byref(c), pi, po, pt, int(bool(accumulate)), pw, nw, _raw_stream(stream, dev)))
+
+
+def alloc_grad_norm_workspace(device="cuda", stream=None):
+    """A zero-status workspace (uint8 tensor) for moe_grad_norm and moe_clip_grad_norm of any list."""
+    import torch
+    n = c_size_t(0)
+    _check("moe_grad_norm_workspace_size", _lib.moe_grad_norm_workspace_size(ctypes.byref(n)))
+    ws = torch.empty(int(n.value), dtype=torch.uint8, device=device)
+    moe_workspace_init(ws, stream)
+    return ws
+
+
+def _tensor_list(name, tensors, dev):
+    """The tensors as an array of moe_tensor, five 64-bit words each."""
+    words = []
+    for t in tensors:
+        dtype = _TORCH_DTYPES.get(t.dtype)
+        if dtype is None or t.get_device() != dev:
+            raise ValueError(f"{name}: fp32 or bf16 tensors on device {dev} are expected, got {t.dtype} on {t.device}")
+        if t.dim() == 2 and t.shape[0] > 1 and t.shape[1] > 0:
+            rows, cols = t.shape
+            s0, s1 = t.stride()
+            if (s1 != 1 and cols > 1) or s0 < cols:
+                raise ValueError(f"{name}: contiguous rows with memory of their own are expected, got strides "
+                                 f"{t.stride()} of {tuple(t.shape)}")
+            words += (t.data_ptr(), rows, cols, s0, dtype)
+        elif t.is_contiguous():
+            words += (t.data_ptr(), 1, t.numel(), 0, dtype)
+        else:
+            raise ValueError(f"{name}: contiguous tensors, or matrices of contiguous rows, are expected, got "
+                             f"strides {t.stride()} of {tuple(t.shape)}")
+    return (c_int64 * len(words))(*words)
+
+
+def _norm_operands(norm, workspace):
+    _dtypes()
+    dev = _device_of("norm", norm)
+    return dev, _flat("norm", norm, dev, 2, 0), *_workspace(workspace, dev)
+
+
+def moe_grad_norm(grads, norm, workspace, max_norm=float("inf"), stream=None):
+    """norm (fp32 [2]) = the 2-norm over all elements of the tensors of ``grads``, and
+    min(1, max_norm / (norm + 1e-6)), the factor that clips it to ``max_norm``."""
+    dev, pn, pw, nw = _norm_operands(norm, workspace)
+    _check("moe_grad_norm", _lib.moe_grad_norm(_tensor_list("grads", grads, dev), len(grads), max_norm, pn, pw, nw,
+                                               _raw_stream(stream, dev)))
+
+
+def moe_clip_grad_norm(grads, max_norm, out, norm, workspace, stream=None):
+    """moe_grad_norm, then every gradient times norm[1]: into the tensors of ``out``, or in place where it is
+    None."""
+    dev, pn, pw, nw = _norm_operands(norm, workspace)
+    po = None
+    if out is not None:
+        if [(t.shape, t.dtype) for t in out] != [(t.shape, t.dtype) for t in grads]:
+            raise ValueError("out: the shapes and types of grads are expected")
+        po = _tensor_list("out", out, dev)
+    _check("moe_clip_grad_norm", _lib.moe_clip_grad_norm(_tensor_list("grads", grads, dev), po, len(grads), max_norm,
+                                                         pn, pw, nw, _raw_stream(stream, dev)))

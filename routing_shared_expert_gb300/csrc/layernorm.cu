@@ -1,41 +1,8 @@
-// Normalisation of rows, LAYER or RMS, with the residual add in front of it, and its gradients.
-//
-//   h = x + r,  mean = sum h / d,  rstd = (sum (h - mean)^2 / d + eps)^(-1/2),  y = (h - mean) rstd w + b
-//   xhat = (h - mean) rstd,  g = dy w,
-//   dx = rstd (g - sum g / d - xhat sum (g xhat) / d) + dsum,  dw = sum_t dy xhat,  db = sum_t dy
-// (RMS: mean = 0, no sum g).  The variance is taken from deviations, never as E h^2 - mean^2.
-#include <algorithm>
-#include <cmath>
-
-#include "common.cuh"
-#include "internal.h"
-#include "row_reduce.cuh"
+// Normalisation of rows, forward; the checks and entry points of both passes.
+#include "layernorm.cuh"
 
 namespace moe {
 namespace {
-
-struct NormArgs {
-  const void* x;        // h in the backward pass
-  const void* r;        // residual, or dsum
-  const void* w;
-  const void* b;
-  void* s;              // sum, or dx
-  void* y;              // dy in the backward pass (read only)
-  float* mean;
-  float* rstd;
-  float* partial;       // [slots][2][d]
-  float* dw;
-  float* db;
-  int64_t T, ldx, ldr, lds, ldy;
-  int32_t d, slots;
-  float eps;
-  int32_t rms, w_dtype;
-};
-
-__device__ __forceinline__ float load_param(const void* p, int32_t dtype, int32_t c, float none) {
-  if (!p) return none;
-  return dtype == MOE_F32 ? static_cast<const float*>(p)[c] : to_f32(static_cast<const __nv_bfloat16*>(p)[c]);
-}
 
 // ------------------------------------------------------------------ any layout --
 // Any strides, alignment and length: a CTA per row, its threads on neighbouring values, each pass
@@ -81,115 +48,152 @@ __global__ void __launch_bounds__(256) norm_any_kernel(NormArgs a) {
   }
 }
 
-template <typename H, typename DY, typename S>
-__global__ void __launch_bounds__(256) norm_dx_any_kernel(NormArgs a) {
-  __shared__ float part[64];
-  const int64_t t = blockIdx.x;
-  const H* h = static_cast<const H*>(a.x) + t * a.ldx;
-  const DY* dy = static_cast<const DY*>(a.y) + t * a.ldy;
-  const S* ds = a.r ? static_cast<const S*>(a.r) + t * a.ldr : nullptr;
-  S* dx = static_cast<S*>(a.s) + t * a.lds;
-  const float mean = a.rms ? 0.f : a.mean[t], rstd = a.rstd[t];
-  float v[2] = {0.f, 0.f};
-  for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
-    const float g = to_f32(dy[c]) * load_param(a.w, a.w_dtype, c, 1.f);
-    v[0] += g;
-    v[1] += g * ((to_f32(h[c]) - mean) * rstd);
-  }
-  block_sum<2>(v, part);
-  const float c1 = a.rms ? 0.f : v[0] / a.d, c2 = v[1] / a.d;
-  for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
-    const float g = to_f32(dy[c]) * load_param(a.w, a.w_dtype, c, 1.f);
-    const float z = rstd * (g - c1 - (to_f32(h[c]) - mean) * rstd * c2);
-    dx[c] = from_f32<S>(ds ? z + to_f32(ds[c]) : z);
-  }
-}
-
-// Column sums of a slot's rows (blockIdx.y): 32 columns by 8 rows at a time, joined in order.
-template <typename H, typename DY>
-__global__ void __launch_bounds__(256) norm_columns_any_kernel(NormArgs a) {
-  __shared__ float part[8][2][32];
-  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  float w = 0.f, b = 0.f;
-  if (c < a.d) {
-    const int64_t per = (a.T + a.slots - 1) / a.slots;
-    const int64_t t0 = blockIdx.y * per, t1 = min(a.T, t0 + per);
-    for (int64_t t = t0 + g; t < t1; t += 8) {
-      const float dy = to_f32(static_cast<const DY*>(a.y)[t * a.ldy + c]);
-      const float u = to_f32(static_cast<const H*>(a.x)[t * a.ldx + c]) - (a.rms ? 0.f : a.mean[t]);
-      w += dy * (u * a.rstd[t]);
-      b += dy;
+template <typename X, typename S, typename Y, int P, bool SPLIT>
+__global__ void __launch_bounds__(SPLIT ? 256 : 512) norm_vec_kernel(NormArgs a) {
+  extern __shared__ float4 smem[];
+  __shared__ float part[2][32];
+  const int lanes = SPLIT ? a.lanes : blockDim.x, lane = SPLIT ? threadIdx.x & (lanes - 1) : threadIdx.x;
+  const int groups = lanes * P, d = a.d;
+  int64_t row = SPLIT ? blockIdx.x + static_cast<int64_t>(threadIdx.x / lanes) * gridDim.x : blockIdx.x;
+  const int64_t step = SPLIT ? static_cast<int64_t>(256 / lanes) * gridDim.x : gridDim.x;
+  const int turns = static_cast<int>((a.T - blockIdx.x + step - 1) / step);   // the same in the whole CTA
+  const int phase = phase_of(static_cast<const X*>(a.x) + blockIdx.x * a.ldx);
+  const bool add = a.r != nullptr;
+  float* w = reinterpret_cast<float*>(smem);
+  float* b = w + (a.w ? 8 * groups : 0);
+  // the ring: pieces of 16 bytes, a thread's own ones blockDim.x pieces apart
+  const uint32_t stride = blockDim.x * 16, stage_bytes = stride * P * (kPieces<X> + (add ? kPieces<S> : 0));
+  char* ring = reinterpret_cast<char*>(b + (a.b ? 8 * groups : 0)) + threadIdx.x * 16;
+  const Extent ex = extent_of(a.x, a.T, a.ldx, d, sizeof(X)), er = extent_of(a.r, a.T, a.ldr, d, sizeof(S));
+  auto fetch = [&](int64_t t, char* to) {
+    if (t < a.T) {
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        const int e0 = 8 * (k * lanes + lane) - phase;
+        copy_group(to + k * kPieces<X> * stride, stride, static_cast<const X*>(a.x) + t * a.ldx, e0, d, ex);
+        if (add)
+          copy_group(to + (P * kPieces<X> + k * kPieces<S>) * stride, stride, static_cast<const S*>(a.r) + t * a.ldr,
+                     e0, d, er);
+      }
     }
-  }
-  part[g][0][lane] = w;
-  part[g][1][lane] = b;
+    cp_async_commit();
+  };
+  for (int i = 0; i < a.stages; ++i) fetch(row + i * step, ring + i * stage_bytes);
+  if (a.w) stage_param(w, a.w, a.w_dtype, groups, phase, d);
+  if (a.b) stage_param(b, a.b, a.w_dtype, groups, phase, d);
   __syncthreads();
-  if (g < 2 && c < a.d) {
-    float v = 0.f;
+  const float inv_d = 1.f / d;
+  int turn = 0, at = 0;
+  for (int it = 0; it < turns; ++it, row += step) {
+    const bool live = !SPLIT || row < a.T;
+    wait_stage(a.stages);
+    char* from = ring + at * stage_bytes;
+    at = at + 1 == a.stages ? 0 : at + 1;
+    float h[P][8];
+    S* s = a.s && live ? static_cast<S*>(a.s) + row * a.lds : nullptr;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v += part[i][g][lane];
-    a.partial[(static_cast<int64_t>(blockIdx.y) * 2 + g) * a.d + c] = v;
-  }
-}
-
-// The slots' partial sums of dw (blockIdx.y 0) and db (1), in order: each of 8 groups takes a run
-// of slots for 32 columns.
-__global__ void __launch_bounds__(256) norm_join_kernel(NormArgs a) {
-  __shared__ float part[8][32];
-  float* out = blockIdx.y == 0 ? a.dw : a.db;
-  if (!out) return;
-  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  float v = 0.f;
-  if (c < a.d) {
-    const int per = (a.slots + 7) / 8;
-    const int s1 = min(a.slots, (g + 1) * per);
-    for (int s = g * per; s < s1; ++s) v += a.partial[(static_cast<int64_t>(s) * 2 + blockIdx.y) * a.d + c];
-  }
-  part[g][lane] = v;
-  __syncthreads();
-  if (g == 0 && c < a.d) {
-    float t = 0.f;
+    for (int k = 0; k < P; ++k) {
+      const int e0 = 8 * (k * lanes + lane) - phase;
+      read_group(from + k * kPieces<X> * stride, stride, static_cast<const X*>(nullptr), h[k]);
+      if (add) {
+        float v[8];
+        read_group(from + (P * kPieces<X> + k * kPieces<S>) * stride, stride, static_cast<const S*>(nullptr), v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t += part[i][lane];
-    out[c] = t;
+        for (int j = 0; j < 8; ++j) {
+          h[k][j] += v[j];
+          if (a.s) h[k][j] = to_f32(from_f32<S>(h[k][j]));   // normalised is the sum as stored
+        }
+      }
+      if (s) store_group(s, e0, d, h[k]);
+      if (!whole_group(e0, d)) clear_outside(h[k], e0, d);
+    }
+    fetch(row + a.stages * step, from);
+    float v[1] = {0.f};
+    float mean = 0.f;
+    if (!a.rms) {
+#pragma unroll
+      for (int k = 0; k < P; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[0] += h[k][j];
+      row_sum<SPLIT, 1>(v, part, turn, lanes);
+      mean = v[0] * inv_d;
+      v[0] = 0.f;
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        const int e0 = 8 * (k * lanes + lane) - phase;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[k][j] -= mean;
+        if (!whole_group(e0, d)) clear_outside(h[k], e0, d);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < P; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[0] += h[k][j] * h[k][j];
+    row_sum<SPLIT, 1>(v, part, turn, lanes);
+    const float rstd = 1.f / sqrtf(v[0] * inv_d + a.eps);
+    if (!live) continue;
+    if (lane == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    Y* y = static_cast<Y*>(a.y) + row * a.ldy;
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      const int q = k * lanes + lane;
+      float u[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[k][j] *= rstd;
+      if (a.w) {
+        param8(w, groups, q, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[k][j] *= u[j];
+      }
+      if (a.b) {
+        param8(b, groups, q, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[k][j] += u[j];
+      }
+      store_group(y, 8 * q - phase, d, h[k]);
+    }
   }
 }
 
 // ---------------------------------------------------------------------- launch --
 
+template <typename X, typename S, typename Y, int P, bool SPLIT>
+cudaError_t launch_vec(const NormArgs& a, const Plan& p, cudaStream_t s) {
+  const auto f = norm_vec_kernel<X, S, Y, P, SPLIT>;
+  const cudaError_t e = allow_smem(f, p.smem);
+  if (e != cudaSuccess) return e;
+  f<<<p.grid, p.threads, p.smem, s>>>(a);
+  return cudaGetLastError();
+}
+
 template <typename X, typename S, typename Y>
-cudaError_t launch_forward(const NormArgs& a, cudaStream_t s) {
+cudaError_t launch_forward(NormArgs a, cudaStream_t s) {
+  const Plan p = make_plan<X, S, Y>(a, kPieces<X> + (a.r ? kPieces<S> : 0), (a.w != nullptr) + (a.b != nullptr),
+                                    int64_t{1} << 30, 1024);
+  a.lanes = p.lanes;
+  a.stages = p.stages;
+  if (p.groups_per_thread == 1) return launch_vec<X, S, Y, 1, true>(a, p, s);
+  if (p.groups_per_thread == 2) return p.split ? launch_vec<X, S, Y, 2, true>(a, p, s) : launch_vec<X, S, Y, 2, false>(a, p, s);
+  if (p.groups_per_thread == 4) return launch_vec<X, S, Y, 4, false>(a, p, s);
   norm_any_kernel<X, S, Y><<<static_cast<unsigned>(a.T), 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 
-template <typename X, typename S, typename Y>
-cudaError_t launch_backward(const NormArgs& a, cudaStream_t s) {
-  // the column sums first: dx may overwrite h or dy
-  const unsigned cols = static_cast<unsigned>((a.d + 31) / 32);
-  if (a.dw || a.db) {
-    norm_columns_any_kernel<X, Y><<<dim3(cols, static_cast<unsigned>(a.slots)), 256, 0, s>>>(a);
-    norm_join_kernel<<<dim3(cols, 2), 256, 0, s>>>(a);
-  }
-  if (a.s) norm_dx_any_kernel<X, Y, S><<<static_cast<unsigned>(a.T), 256, 0, s>>>(a);
-  return cudaGetLastError();
-}
-
-template <bool BWD, typename X, typename S>
+template <typename X, typename S>
 cudaError_t launch_y(const NormArgs& a, int32_t y, cudaStream_t s) {
-  if (BWD) return y == MOE_F32 ? launch_backward<X, S, float>(a, s) : launch_backward<X, S, __nv_bfloat16>(a, s);
   return y == MOE_F32 ? launch_forward<X, S, float>(a, s) : launch_forward<X, S, __nv_bfloat16>(a, s);
 }
-template <bool BWD, typename X>
+template <typename X>
 cudaError_t launch_s(const NormArgs& a, int32_t st, int32_t y, cudaStream_t s) {
-  return st == MOE_F32 ? launch_y<BWD, X, float>(a, y, s) : launch_y<BWD, X, __nv_bfloat16>(a, y, s);
+  return st == MOE_F32 ? launch_y<X, float>(a, y, s) : launch_y<X, __nv_bfloat16>(a, y, s);
 }
-template <bool BWD>
-cudaError_t launch_norm(const NormArgs& a, const moe_layernorm_config& c, cudaStream_t s) {
-  return c.x_dtype == MOE_F32 ? launch_s<BWD, float>(a, c.stream_dtype, c.y_dtype, s)
-                              : launch_s<BWD, __nv_bfloat16>(a, c.stream_dtype, c.y_dtype, s);
+cudaError_t launch_forward_any_type(const NormArgs& a, const moe_layernorm_config& c, cudaStream_t s) {
+  return c.x_dtype == MOE_F32 ? launch_s<float>(a, c.stream_dtype, c.y_dtype, s)
+                              : launch_s<__nv_bfloat16>(a, c.stream_dtype, c.y_dtype, s);
 }
 
 // ---------------------------------------------------------------------- checks --
@@ -204,10 +208,11 @@ bool elem_aligned(const void* p, int32_t t) {
 }
 
 // Rows of partial column sums: one per CTA of a launch that fills the GPU, fewer where rows are so
-// long that the partial sums would be more than the operands.
+// long that the partial sums would be more than the operands, never fewer than the eight CTAs that
+// rows of every phase take.
 int32_t norm_slots(int64_t T, int32_t d) {
   const int64_t most = std::min<int64_t>(608, std::max<int64_t>(16, (int64_t{1} << 24) / d));
-  return static_cast<int32_t>(std::max<int64_t>(1, std::min(T, most)));
+  return static_cast<int32_t>(std::max<int64_t>(8, std::min(T, most)));
 }
 size_t norm_workspace(int64_t T, int32_t d) {
   return 256 + static_cast<size_t>(norm_slots(T, d)) * 2 * static_cast<size_t>(d) * 4;
@@ -264,7 +269,7 @@ moe_status moe_layernorm_forward(const moe_layernorm_config* cfg, const void* x,
   a.y = y;
   a.mean = mean;
   a.rstd = rstd;
-  return launch_norm<false>(a, *cfg, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launch_forward_any_type(a, *cfg, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status moe_layernorm_workspace_size(int64_t T, int32_t d, size_t* bytes) {
@@ -309,7 +314,7 @@ moe_status moe_layernorm_backward(const moe_layernorm_config* cfg, const void* h
   a.db = dbias;
   a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + 256);
   a.slots = norm_slots(a.T, a.d);
-  return launch_norm<true>(a, *cfg, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launch_layernorm_backward(a, *cfg, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // extern "C"

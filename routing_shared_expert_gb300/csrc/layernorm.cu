@@ -48,122 +48,128 @@ __global__ void __launch_bounds__(256) norm_any_kernel(NormArgs a) {
   }
 }
 
-template <typename X, typename S, typename Y, int P, bool SPLIT>
-__global__ void __launch_bounds__(SPLIT ? 256 : 512) norm_vec_kernel(NormArgs a) {
+template <typename X, typename S, typename Y, int E, bool SPLIT>
+__global__ void __launch_bounds__(E == 32 ? 512 : 1024) norm_vec_kernel(NormArgs a) {
+  constexpr int G = kGroup<X, S, Y>, P = E / G, N = G / 2;
   extern __shared__ float4 smem[];
-  __shared__ float part[2][32];
-  const int lanes = SPLIT ? a.lanes : blockDim.x, lane = SPLIT ? threadIdx.x & (lanes - 1) : threadIdx.x;
-  const int groups = lanes * P, d = a.d;
-  int64_t row = SPLIT ? blockIdx.x + static_cast<int64_t>(threadIdx.x / lanes) * gridDim.x : blockIdx.x;
-  const int64_t step = SPLIT ? static_cast<int64_t>(256 / lanes) * gridDim.x : gridDim.x;
-  const int turns = static_cast<int>((a.T - blockIdx.x + step - 1) / step);   // the same in the whole CTA
-  const int phase = phase_of(static_cast<const X*>(a.x) + blockIdx.x * a.ldx);
+  __shared__ float part[SPLIT ? 1 : kMaxTeams * 2 * 32];
+  const Seat<G, P, SPLIT> at(a, phase_of<G>(static_cast<const X*>(a.x) + blockIdx.x * a.ldx));
+  const int d = a.d;
   const bool add = a.r != nullptr;
   float* w = reinterpret_cast<float*>(smem);
-  float* b = w + (a.w ? 8 * groups : 0);
-  // the ring: pieces of 16 bytes, a thread's own ones blockDim.x pieces apart
-  const uint32_t stride = blockDim.x * 16, stage_bytes = stride * P * (kPieces<X> + (add ? kPieces<S> : 0));
-  char* ring = reinterpret_cast<char*>(b + (a.b ? 8 * groups : 0)) + threadIdx.x * 16;
-  const Extent ex = extent_of(a.x, a.T, a.ldx, d, sizeof(X)), er = extent_of(a.r, a.T, a.ldr, d, sizeof(S));
-  auto fetch = [&](int64_t t, char* to) {
-    if (t < a.T) {
-#pragma unroll
-      for (int k = 0; k < P; ++k) {
-        const int e0 = 8 * (k * lanes + lane) - phase;
-        copy_group(to + k * kPieces<X> * stride, stride, static_cast<const X*>(a.x) + t * a.ldx, e0, d, ex);
-        if (add)
-          copy_group(to + (P * kPieces<X> + k * kPieces<S>) * stride, stride, static_cast<const S*>(a.r) + t * a.ldr,
-                     e0, d, er);
-      }
+  float* b = w + (a.w ? G * at.groups : 0);
+  Feed<X, G, P, SPLIT> x(a.x, a.ldx, at);
+  Feed<S, G, P, SPLIT> r(a.r, a.ldr, at);
+  // the ring: each thread's groups of x, then those of r
+  char* const base = reinterpret_cast<char*>(b + (a.b ? G * at.groups : 0));
+  char* const ring = base + threadIdx.x * static_cast<uint32_t>(G * sizeof(X));
+  const uint32_t at_r = P * x.stride + threadIdx.x * static_cast<uint32_t>(G * sizeof(S)) - threadIdx.x * static_cast<uint32_t>(G * sizeof(X));
+  const uint32_t stage_bytes = P * x.stride + (add ? P * r.stride : 0);
+  char* const ring_end = ring + a.stages * stage_bytes;
+  int64_t ahead = at.row;
+  auto fetch = [&](char* to) {
+    if (ahead < a.T) {
+      x.copy(to, at, a, a.x, a.ldx);
+      if (add) r.copy(to + at_r, at, a, a.r, a.ldr);
     }
+    ahead += at.step;
     cp_async_commit();
   };
-  for (int i = 0; i < a.stages; ++i) fetch(row + i * step, ring + i * stage_bytes);
-  if (a.w) stage_param(w, a.w, a.w_dtype, groups, phase, d);
-  if (a.b) stage_param(b, a.b, a.w_dtype, groups, phase, d);
+  for (char* to = ring; to != ring_end; to += stage_bytes) fetch(to);
+  if (a.w) stage_param<G>(w, a.w, a.w_dtype, at.groups, at.phase, d);
+  if (a.b) stage_param<G>(b, a.b, a.w_dtype, at.groups, at.phase, d);
   __syncthreads();
   const float inv_d = 1.f / d;
-  int turn = 0, at = 0;
-  for (int it = 0; it < turns; ++it, row += step) {
+  int turn = 0;
+  int64_t row = at.row;
+  char* from = ring;
+  for (int it = 0; it < at.turns; ++it, row += at.step) {
     const bool live = !SPLIT || row < a.T;
     wait_stage(a.stages);
-    char* from = ring + at * stage_bytes;
-    at = at + 1 == a.stages ? 0 : at + 1;
-    float h[P][8];
-    S* s = a.s && live ? static_cast<S*>(a.s) + row * a.lds : nullptr;
+    if (!at.all || !live) {
+      x.clear(from, at, live ? d : 0);
+      if (add) r.clear(from + at_r, at, live ? d : 0);
+    }
+    float2 h[P][N];
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-      const int e0 = 8 * (k * lanes + lane) - phase;
-      read_group(from + k * kPieces<X> * stride, stride, static_cast<const X*>(nullptr), h[k]);
+      x.read(from, k, h[k]);
       if (add) {
-        float v[8];
-        read_group(from + (P * kPieces<X> + k * kPieces<S>) * stride, stride, static_cast<const S*>(nullptr), v);
+        float2 v[N];
+        r.read(from + at_r, k, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          h[k][j] += v[j];
-          if (a.s) h[k][j] = to_f32(from_f32<S>(h[k][j]));   // normalised is the sum as stored
+        for (int j = 0; j < N; ++j) h[k][j] = add2(h[k][j], v[j]);
+        if (a.s) {
+          if (live) store_group(static_cast<S*>(a.s) + row * a.lds + at.e0[k], at.e0[k], d, at.whole[k], h[k]);
+          round_to<S>(h[k]);     // normalised is the sum as stored
         }
       }
-      if (s) store_group(s, e0, d, h[k]);
-      if (!whole_group(e0, d)) clear_outside(h[k], e0, d);
     }
-    fetch(row + a.stages * step, from);
-    float v[1] = {0.f};
+    fetch(from);
+    from += stage_bytes;
+    if (from == ring_end) from = ring;
+    float v[1];
     float mean = 0.f;
     if (!a.rms) {
+      float2 sum = both(0.f);
 #pragma unroll
       for (int k = 0; k < P; ++k)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[0] += h[k][j];
-      row_sum<SPLIT, 1>(v, part, turn, lanes);
+        for (int j = 0; j < N; ++j) sum = add2(sum, h[k][j]);
+      v[0] = sum.x + sum.y;
+      row_sum<SPLIT, 1>(v, part, turn, at.lanes, at.lane, at.team);
       mean = v[0] * inv_d;
-      v[0] = 0.f;
 #pragma unroll
       for (int k = 0; k < P; ++k) {
-        const int e0 = 8 * (k * lanes + lane) - phase;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[k][j] -= mean;
-        if (!whole_group(e0, d)) clear_outside(h[k], e0, d);
+        for (int j = 0; j < N; ++j) h[k][j] = add2(h[k][j], both(-mean));
+        if (!at.whole[k]) {
+          asm volatile("");      // a branch that few threads take, not selections in all of them
+#pragma unroll
+          for (int j = 0; j < G; ++j)
+            if (at.e0[k] + j < 0 || at.e0[k] + j >= d) (j & 1 ? h[k][j / 2].y : h[k][j / 2].x) = 0.f;
+        }
       }
     }
+    float2 sq = both(0.f);
 #pragma unroll
     for (int k = 0; k < P; ++k)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[0] += h[k][j] * h[k][j];
-    row_sum<SPLIT, 1>(v, part, turn, lanes);
-    const float rstd = 1.f / sqrtf(v[0] * inv_d + a.eps);
+      for (int j = 0; j < N; ++j) sq = fma2(h[k][j], h[k][j], sq);
+    v[0] = sq.x + sq.y;
+    row_sum<SPLIT, 1>(v, part, turn, at.lanes, at.lane, at.team);
+    const float rstd = rsqrtf(v[0] * inv_d + a.eps);
     if (!live) continue;
-    if (lane == 0) {
+    if (at.lane == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
     }
     Y* y = static_cast<Y*>(a.y) + row * a.ldy;
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-      const int q = k * lanes + lane;
-      float u[8];
+      float2 u[N];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) h[k][j] *= rstd;
+      for (int j = 0; j < N; ++j) h[k][j] = mul2(h[k][j], both(rstd));
       if (a.w) {
-        param8(w, groups, q, u);
+        param_group(w, at.groups, k * at.lanes + at.lane, u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[k][j] *= u[j];
+        for (int j = 0; j < N; ++j) h[k][j] = mul2(h[k][j], u[j]);
       }
       if (a.b) {
-        param8(b, groups, q, u);
+        param_group(b, at.groups, k * at.lanes + at.lane, u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[k][j] += u[j];
+        for (int j = 0; j < N; ++j) h[k][j] = add2(h[k][j], u[j]);
       }
-      store_group(y, 8 * q - phase, d, h[k]);
+      store_group(y + at.e0[k], at.e0[k], d, at.whole[k], h[k]);
     }
   }
 }
 
 // ---------------------------------------------------------------------- launch --
 
-template <typename X, typename S, typename Y, int P, bool SPLIT>
+template <typename X, typename S, typename Y, int E, bool SPLIT>
 cudaError_t launch_vec(const NormArgs& a, const Plan& p, cudaStream_t s) {
-  const auto f = norm_vec_kernel<X, S, Y, P, SPLIT>;
+  const auto f = norm_vec_kernel<X, S, Y, E, SPLIT>;
   const cudaError_t e = allow_smem(f, p.smem);
   if (e != cudaSuccess) return e;
   f<<<p.grid, p.threads, p.smem, s>>>(a);
@@ -172,13 +178,13 @@ cudaError_t launch_vec(const NormArgs& a, const Plan& p, cudaStream_t s) {
 
 template <typename X, typename S, typename Y>
 cudaError_t launch_forward(NormArgs a, cudaStream_t s) {
-  const Plan p = make_plan<X, S, Y>(a, kPieces<X> + (a.r ? kPieces<S> : 0), (a.w != nullptr) + (a.b != nullptr),
+  const Plan p = make_plan<X, S, Y>(a, sizeof(X) + (a.r ? sizeof(S) : 0), (a.w != nullptr) + (a.b != nullptr),
                                     int64_t{1} << 30, 1024);
   a.lanes = p.lanes;
   a.stages = p.stages;
-  if (p.groups_per_thread == 1) return launch_vec<X, S, Y, 1, true>(a, p, s);
-  if (p.groups_per_thread == 2) return p.split ? launch_vec<X, S, Y, 2, true>(a, p, s) : launch_vec<X, S, Y, 2, false>(a, p, s);
-  if (p.groups_per_thread == 4) return launch_vec<X, S, Y, 4, false>(a, p, s);
+  if (p.elements == 8) return launch_vec<X, S, Y, 8, true>(a, p, s);
+  if (p.elements == 16) return p.split ? launch_vec<X, S, Y, 16, true>(a, p, s) : launch_vec<X, S, Y, 16, false>(a, p, s);
+  if (p.elements == 32) return launch_vec<X, S, Y, 32, false>(a, p, s);
   norm_any_kernel<X, S, Y><<<static_cast<unsigned>(a.T), 256, 0, s>>>(a);
   return cudaGetLastError();
 }
@@ -192,8 +198,9 @@ cudaError_t launch_s(const NormArgs& a, int32_t st, int32_t y, cudaStream_t s) {
   return st == MOE_F32 ? launch_y<X, float>(a, y, s) : launch_y<X, __nv_bfloat16>(a, y, s);
 }
 cudaError_t launch_forward_any_type(const NormArgs& a, const moe_layernorm_config& c, cudaStream_t s) {
-  return c.x_dtype == MOE_F32 ? launch_s<float>(a, c.stream_dtype, c.y_dtype, s)
-                              : launch_s<__nv_bfloat16>(a, c.stream_dtype, c.y_dtype, s);
+  const int32_t stream = a.r ? c.stream_dtype : c.x_dtype;    // without a residual: the form of x alone
+  return c.x_dtype == MOE_F32 ? launch_s<float>(a, stream, c.y_dtype, s)
+                              : launch_s<__nv_bfloat16>(a, stream, c.y_dtype, s);
 }
 
 // ---------------------------------------------------------------------- checks --

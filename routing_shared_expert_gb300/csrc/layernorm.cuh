@@ -32,7 +32,7 @@ struct NormArgs {
   int32_t d, slots;
   float eps;
   int32_t rms, w_dtype;
-  int32_t lanes;        // of a row (SPLIT)
+  int32_t lanes;        // threads of a team, which takes a row at a time
   int32_t stages;       // rows on their way, 2 to 4
 };
 
@@ -45,33 +45,43 @@ __device__ __forceinline__ float load_param(const void* p, int32_t dtype, int32_
 cudaError_t launch_layernorm_backward(const NormArgs& a, const moe_layernorm_config& c, cudaStream_t s);
 
 // --------------------------------------------------------------- rows in groups --
-// Rows whose operands all start at the same place within a group of eight elements (aligned
-// tensors with one width or stride, odd ones included): a thread takes P groups of eight.  A row
-// that starts `phase` elements into a group has two end groups that are not whole.  The rows of a
-// CTA are gridDim.x apart, a multiple of eight unless the stride is one, so that the phase is the same
-// for all of them; the parameters lie in shared memory at that phase.  SPLIT: `lanes` lanes of a warp
-// (a power of two) take a row and the CTA 256 / lanes rows at once, with no barrier; else the whole CTA
-// takes one.
+// Rows whose operands all start at the same place within a group of G elements (aligned tensors
+// with one width or stride, odd ones included): a thread takes P groups, E = P G elements.  A row
+// that starts `phase` elements into a group has two end groups that are not whole.  A CTA is several
+// teams of `lanes` threads, each with rows of its own, and one copy of the parameters in shared memory.
+// Its rows are gridDim.x apart, a multiple of eight unless the stride is one, so that the phase is the
+// same for all of them and the parameters can lie at that phase.  SPLIT: a team is a power of two of a
+// warp's lanes; else it is whole warps with a barrier of their own.
 //
 // Each thread copies its own groups of the next rows asynchronously into its own slots of a ring in
 // shared memory, a.stages rows ahead: the bytes on their way do not depend on registers, and the
 // ring needs no barrier.
 
-// Values 8 q .. 8 q + 7 of a parameter in shared memory: the lower and the upper half of all groups
-// apart, so that neighbouring lanes' 16-byte reads are neighbours.
-__device__ __forceinline__ void param8(const float* p, int groups, int q, float (&v)[8]) {
-  const float4 lo = reinterpret_cast<const float4*>(p)[q], hi = reinterpret_cast<const float4*>(p)[groups + q];
-  v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w, v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+constexpr int kMaxTeams = 8;     // of whole warps: barriers 1 to 8
+
+template <typename X, typename S, typename Y>
+constexpr int kGroup = sizeof(X) + sizeof(S) + sizeof(Y) == 6 ? 8 : 4;
+
+// Group q of a parameter in shared memory.  G = 8: the lower and the upper half of all groups lie apart, so
+// that neighbouring lanes' 16-byte reads are neighbours.
+__device__ __forceinline__ void param_group(const float* p, int groups, int q, float2 (&v)[2]) {
+  read_group(reinterpret_cast<const char*>(p + 4 * q), static_cast<const float*>(nullptr), v);
 }
+__device__ __forceinline__ void param_group(const float* p, int groups, int q, float2 (&v)[4]) {
+  const float4 lo = reinterpret_cast<const float4*>(p)[q], hi = reinterpret_cast<const float4*>(p)[groups + q];
+  v[0] = make_float2(lo.x, lo.y), v[1] = make_float2(lo.z, lo.w);
+  v[2] = make_float2(hi.x, hi.y), v[3] = make_float2(hi.z, hi.w);
+}
+template <int G>
 __device__ __forceinline__ void stage_param(float* dst, const void* src, int32_t dtype, int groups, int phase, int d) {
-  for (int i = threadIdx.x; i < 8 * groups; i += blockDim.x) {
-    const int c = i - phase, q = i >> 3, j = i & 7;
-    dst[(j >> 2) * 4 * groups + 4 * q + (j & 3)] = c >= 0 && c < d ? load_param(src, dtype, c, 0.f) : 0.f;
+  for (int i = threadIdx.x; i < G * groups; i += blockDim.x) {
+    const int c = i - phase, q = i / G, j = i % G;
+    dst[j / 4 * 4 * groups + 4 * q + j % 4] = c >= 0 && c < d ? load_param(src, dtype, c, 0.f) : 0.f;
   }
 }
-template <typename T>
+template <int G, typename T>
 __device__ __forceinline__ int phase_of(const T* row) {
-  return static_cast<int>(reinterpret_cast<uintptr_t>(row) / sizeof(T)) & 7;
+  return static_cast<int>(reinterpret_cast<uintptr_t>(row) / sizeof(T)) & (G - 1);
 }
 __device__ __forceinline__ void wait_stage(int stages) {   // the oldest of `stages` copies has landed
   if (stages == 2) cp_async_wait<1>();
@@ -79,26 +89,80 @@ __device__ __forceinline__ void wait_stage(int stages) {   // the oldest of `sta
   else cp_async_wait<3>();
 }
 
+// Where a thread stands.
+template <int G, int P, bool SPLIT>
+struct Seat {
+  int lanes, lane, team, groups, phase;
+  int64_t row, step;
+  int turns;          // of its warp, the last of which may be past the last row for some teams (SPLIT)
+  int e0[P];          // first element of each group, within the row
+  bool whole[P], all; // whether each lies in the row, and all do
+  __device__ __forceinline__ Seat(const NormArgs& a, int first_phase) {
+    lanes = a.lanes;
+    team = threadIdx.x / lanes;
+    lane = threadIdx.x - team * lanes;
+    groups = lanes * P;
+    phase = first_phase;
+    row = blockIdx.x + static_cast<int64_t>(team) * gridDim.x;
+    step = static_cast<int64_t>(blockDim.x / lanes) * gridDim.x;
+    const int64_t first = SPLIT ? blockIdx.x + static_cast<int64_t>((threadIdx.x & ~31) / lanes) * gridDim.x : row;
+    turns = first < a.T ? static_cast<int>((a.T - first + step - 1) / step) : 0;
+    all = true;
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      e0[k] = G * (k * lanes + lane) - phase;
+      whole[k] = e0[k] >= 0 && e0[k] + G <= a.d;
+      all = all && whole[k];
+    }
+  }
+};
+
+// The rows of one operand on their way into a thread's slots of the ring, `stride` bytes apart.
+template <typename T, int G, int P, bool SPLIT>
+struct Feed {
+  const T* next;      // element 0 of the row to be copied next
+  int64_t step;       // elements to the team's row after it
+  uint32_t stride;
+  __device__ __forceinline__ Feed(const void* base, int64_t ld, const Seat<G, P, SPLIT>& s)
+      : next(static_cast<const T*>(base) + s.row * ld), step(s.step * ld),
+        stride(blockDim.x * static_cast<uint32_t>(G * sizeof(T))) {}
+  __device__ __forceinline__ void copy(char* to, const Seat<G, P, SPLIT>& s, const NormArgs& a, const void* base, int64_t ld) {
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      if (s.whole[k]) copy_whole<G>(to + k * stride, next + s.e0[k]);
+      else copy_end<G>(to + k * stride, next + s.e0[k], s.e0[k], a.d, extent_of(base, a.T, ld, a.d, sizeof(T)));
+    }
+    next += step;
+  }
+  __device__ __forceinline__ void clear(char* at, const Seat<G, P, SPLIT>& s, int d) {
+#pragma unroll
+    for (int k = 0; k < P; ++k) clear_end<G, T>(at + k * stride, s.e0[k], d);
+  }
+  __device__ __forceinline__ void read(const char* at, int k, float2 (&v)[G / 2]) const {
+    read_group(at + k * stride, static_cast<const T*>(nullptr), v);
+  }
+};
+
 template <bool SPLIT, int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], float (&part)[2][N * 32], int& turn, int lanes) {
+__device__ __forceinline__ void row_sum(float (&v)[N], float* part, int& turn, int lanes, int lane, int team) {
   if (SPLIT) {
     for (int o = lanes / 2; o > 0; o >>= 1)
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
   } else {
-    block_sum<N>(v, part[turn]);
+    team_sum<N>(v, part + (2 * team + turn) * N * 32, lane >> 5, lanes >> 5, 1 + team);
     turn ^= 1;
   }
 }
 
 // ------------------------------------------------------------------ launch plan --
 
-constexpr int kMaxGroups = 2048;                  // of a row: 512 threads of four
+constexpr int kMaxLanes = 512;
 constexpr size_t kSharedPerSm = 227 * 1024;
 
 // How rows are taken in groups of eight, if they can be.
 struct Plan {
-  int groups_per_thread = 0;   // 0: any layout
+  int elements = 0;            // of a thread; 0: any layout
   int lanes = 0, threads = 0, stages = 0;
   bool split = false;
   unsigned grid = 0;
@@ -106,48 +170,55 @@ struct Plan {
 };
 
 template <typename T>
-bool same_phase(const void* p, int64_t ld, int64_t rows, int64_t phase, int64_t ld8) {
+bool same_phase(const void* p, int64_t ld, int64_t rows, int G, int64_t phase, int64_t shift) {
   if (!p) return true;
-  return static_cast<int64_t>(reinterpret_cast<uintptr_t>(p) / sizeof(T) & 7) == phase && (rows == 1 || ld % 8 == ld8);
+  return static_cast<int64_t>(reinterpret_cast<uintptr_t>(p) / sizeof(T) % G) == phase && (rows == 1 || ld % G == shift);
 }
 
-// pieces: of 16 bytes, that a group of all operands which are read takes; params: fp32 rows of
-// parameters in shared memory; most: CTAs at most; resident: threads of an SM that the kernels'
-// registers leave room for, with two groups per thread.
+// bytes: of one element of all operands that are read; params: fp32 rows of parameters in shared memory;
+// most: CTAs at most; resident: threads of a CTA and of an SM that the kernels' registers leave room for.
 template <typename X, typename S, typename Y>
-Plan make_plan(const NormArgs& a, int pieces, int params, int64_t most, int resident) {
+Plan make_plan(const NormArgs& a, size_t bytes, int params, int64_t most, int resident) {
   Plan p;
-  const int64_t phase = reinterpret_cast<uintptr_t>(a.x) / sizeof(X) & 7, ld8 = a.ldx % 8;
-  const bool ok = same_phase<S>(a.r, a.ldr, a.T, phase, ld8) && same_phase<S>(a.s, a.lds, a.T, phase, ld8) &&
-                  same_phase<Y>(a.y, a.ldy, a.T, phase, ld8);
-  const bool shifts = ld8 != 0 && a.T > 1;              // the phase differs from row to row
-  const int groups = static_cast<int>((a.d + (shifts ? 7 : phase) + 7) / 8);
-  if (!ok || groups > kMaxGroups) return p;
-  p.split = groups <= 64;
-  int per;
+  constexpr int G = kGroup<X, S, Y>;
+  const int64_t phase = reinterpret_cast<uintptr_t>(a.x) / sizeof(X) % G, shift = a.T > 1 ? a.ldx % G : 0;
+  if (!same_phase<S>(a.r, a.ldr, a.T, G, phase, shift) || !same_phase<S>(a.s, a.lds, a.T, G, phase, shift) ||
+      !same_phase<Y>(a.y, a.ldy, a.T, G, phase, shift))
+    return p;
+  const int groups = static_cast<int>((a.d + (shift ? G - 1 : phase) + G - 1) / G);   // of any row
+  const int64_t sms = device_sm_count();
+  auto lanes_of = [&](int elements) { return (groups + elements / G - 1) / (elements / G); };
+  p.split = lanes_of(16) <= 32;
+  int E, teams;
   if (p.split) {
-    per = groups <= 32 ? 1 : 2;
+    E = lanes_of(8) <= 32 ? 8 : 16;
     p.lanes = 32;
-    while (p.lanes / 2 >= groups) p.lanes /= 2;
-    p.threads = 256;
+    while (p.lanes / 2 >= lanes_of(E)) p.lanes /= 2;
+    teams = 256 / p.lanes;
   } else {
-    per = groups <= 1024 ? 2 : 4;
-    p.threads = ((groups + per - 1) / per + 31) / 32 * 32;
-    p.lanes = p.threads;
+    E = lanes_of(16) <= kMaxLanes ? 16 : 32;
+    p.lanes = (lanes_of(E) + 31) / 32 * 32;
+    if (p.lanes > kMaxLanes) return p;
+    if (E == 32) resident = 512;
+    // rows for every SM before several for one
+    teams = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kMaxTeams, resident / p.lanes, (a.T + sms - 1) / sms})));
   }
-  // as many CTAs to an SM as their registers let in, fewer where their rings would be too short
-  const size_t fixed = static_cast<size_t>(p.lanes) * per * 32 * params, stage = static_cast<size_t>(p.threads) * per * 16 * pieces;
-  int per_sm = std::max(1, (per == 4 ? 512 : resident) / p.threads);
-  for (;; --per_sm) {
-    for (p.stages = 4; p.stages > 2 && per_sm * (fixed + p.stages * stage + 2048) > kSharedPerSm;) --p.stages;
-    if (per_sm <= 1 || per_sm * (fixed + p.stages * stage + 2048) <= kSharedPerSm) break;
+  // as many CTAs to an SM as their registers let in, fewer teams or CTAs where the rings would be too short
+  int per_sm = std::max(1, resident / (teams * p.lanes));
+  const size_t fixed = static_cast<size_t>(p.lanes) * E * 4 * params, stage = static_cast<size_t>(p.lanes) * E * bytes;
+  auto need = [&] { return per_sm * (fixed + static_cast<size_t>(teams) * p.stages * stage + 6 * 1024); };
+  for (;;) {
+    for (p.stages = 4; p.stages > 2 && need() > kSharedPerSm;) --p.stages;
+    if (need() <= kSharedPerSm) break;
+    if (per_sm > 1) --per_sm;
+    else if (teams > 1 && !p.split) --teams;
+    else return p;
   }
-  p.smem = fixed + p.stages * stage;
-  if (p.smem + 2048 > kSharedPerSm) return p;
-  p.groups_per_thread = per;
-  const int64_t at_once = p.split ? 256 / p.lanes : 1;
-  int64_t ctas = std::min({(a.T + at_once - 1) / at_once, most, static_cast<int64_t>(per_sm) * device_sm_count()});
-  if (shifts && (p.split || ctas < a.T)) ctas = std::max<int64_t>(8, ctas / 8 * 8);
+  p.threads = teams * p.lanes;
+  p.smem = fixed + static_cast<size_t>(teams) * p.stages * stage;
+  p.elements = E;
+  int64_t ctas = std::min({(a.T + teams - 1) / teams, most, per_sm * sms});
+  if (shift) ctas = std::max<int64_t>(8, ctas / 8 * 8);
   p.grid = static_cast<unsigned>(ctas);
   return p;
 }

@@ -85,155 +85,153 @@ __global__ void __launch_bounds__(256) norm_join_kernel(NormArgs a) {
 
 // The backward pass in one reading of the rows; the columns' sums stay in registers over the CTA's rows
 // (B: those of db too) and go out once.  Between the two uses of a row its values stay in the ring.
-template <typename H, typename S, typename DY, int P, bool SPLIT, bool B>
-__global__ void __launch_bounds__(SPLIT ? 256 : 512) norm_grad_kernel(NormArgs a) {
+// With c = h - mean: dw sums (dy rstd) c, and dx = rstd (g - c1) - c (rstd^2 c2), c2 = rstd sum (g c) / d.
+template <typename H, typename S, typename DY, int E, bool SPLIT, bool B>
+__global__ void __launch_bounds__(512) norm_grad_kernel(NormArgs a) {
+  constexpr int G = kGroup<H, S, DY>, P = E / G, N = G / 2;
   extern __shared__ float4 smem[];
-  __shared__ float part[2][64];
-  const int lanes = SPLIT ? a.lanes : blockDim.x, lane = SPLIT ? threadIdx.x & (lanes - 1) : threadIdx.x;
-  const int groups = lanes * P, d = a.d;
-  int64_t row = SPLIT ? blockIdx.x + static_cast<int64_t>(threadIdx.x / lanes) * gridDim.x : blockIdx.x;
-  const int64_t step = SPLIT ? static_cast<int64_t>(256 / lanes) * gridDim.x : gridDim.x;
-  const int turns = static_cast<int>((a.T - blockIdx.x + step - 1) / step);
-  const int phase = phase_of(static_cast<const H*>(a.x) + blockIdx.x * a.ldx);
+  __shared__ float part[SPLIT ? 1 : kMaxTeams * 2 * 64];
+  const Seat<G, P, SPLIT> at(a, phase_of<G>(static_cast<const H*>(a.x) + blockIdx.x * a.ldx));
+  const int d = a.d;
   const bool add = a.r && a.s;
   float* w = reinterpret_cast<float*>(smem);
-  const uint32_t stride = blockDim.x * 16;
-  const uint32_t at_y = P * kPieces<H> * stride, at_s = at_y + P * kPieces<DY> * stride;
-  const uint32_t stage_bytes = at_s + (add ? P * kPieces<S> * stride : 0);
-  char* ring = reinterpret_cast<char*>(w + 8 * groups) + threadIdx.x * 16;
-  const Extent eh = extent_of(a.x, a.T, a.ldx, d, sizeof(H)), ey = extent_of(a.y, a.T, a.ldy, d, sizeof(DY)),
-               es = extent_of(a.r, a.T, a.ldr, d, sizeof(S));
-  auto fetch = [&](int64_t t, char* to) {
-    if (t < a.T) {
-#pragma unroll
-      for (int k = 0; k < P; ++k) {
-        const int e0 = 8 * (k * lanes + lane) - phase;
-        copy_group(to + k * kPieces<H> * stride, stride, static_cast<const H*>(a.x) + t * a.ldx, e0, d, eh);
-        copy_group(to + at_y + k * kPieces<DY> * stride, stride, static_cast<const DY*>(a.y) + t * a.ldy, e0, d, ey);
-        if (add)
-          copy_group(to + at_s + k * kPieces<S> * stride, stride, static_cast<const S*>(a.r) + t * a.ldr, e0, d, es);
-      }
+  Feed<H, G, P, SPLIT> fh(a.x, a.ldx, at);
+  Feed<DY, G, P, SPLIT> fy(a.y, a.ldy, at);
+  Feed<S, G, P, SPLIT> fs(a.r, a.ldr, at);
+  // the ring: each thread's groups of h, then those of dy, then those of dsum
+  constexpr uint32_t kH = G * sizeof(H), kY = G * sizeof(DY), kS = G * sizeof(S);
+  char* const ring = reinterpret_cast<char*>(w + G * at.groups) + threadIdx.x * kH;
+  const uint32_t at_y = P * fh.stride + threadIdx.x * kY - threadIdx.x * kH;
+  const uint32_t at_s = P * (fh.stride + fy.stride) + threadIdx.x * kS - threadIdx.x * kH;
+  const uint32_t stage_bytes = P * (fh.stride + fy.stride + (add ? fs.stride : 0));
+  char* const ring_end = ring + a.stages * stage_bytes;
+  int64_t ahead = at.row;
+  auto fetch = [&](char* to) {
+    if (ahead < a.T) {
+      fh.copy(to, at, a, a.x, a.ldx);
+      fy.copy(to + at_y, at, a, a.y, a.ldy);
+      if (add) fs.copy(to + at_s, at, a, a.r, a.ldr);
     }
+    ahead += at.step;
     cp_async_commit();
   };
-  for (int i = 0; i < a.stages; ++i) fetch(row + i * step, ring + i * stage_bytes);
-  if (a.w) stage_param(w, a.w, a.w_dtype, groups, phase, d);
+  for (char* to = ring; to != ring_end; to += stage_bytes) fetch(to);
+  if (a.w) stage_param<G>(w, a.w, a.w_dtype, at.groups, at.phase, d);
   __syncthreads();
   const float inv_d = 1.f / d;
-  int turn = 0, at = 0;
-  float acc_w[P][8], acc_b[P][8];
+  int turn = 0;
+  float2 acc_w[P][N], acc_b[P][N];
 #pragma unroll
   for (int k = 0; k < P; ++k)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc_w[k][j] = acc_b[k][j] = 0.f;
+    for (int j = 0; j < N; ++j) acc_w[k][j] = acc_b[k][j] = both(0.f);
+  int64_t row = at.row;
   float mean = 0.f, r = 0.f;
   if (row < a.T) {
     r = a.rstd[row];
     if (!a.rms) mean = a.mean[row];
   }
-  for (int it = 0; it < turns; ++it, row += step) {
+  char* from = ring;
+  for (int it = 0; it < at.turns; ++it, row += at.step) {
     const bool live = !SPLIT || row < a.T;
     float next_mean = 0.f, next_r = 0.f;
-    if (row + step < a.T) {
-      next_r = a.rstd[row + step];
-      if (!a.rms) next_mean = a.mean[row + step];
+    if (row + at.step < a.T) {
+      next_r = a.rstd[row + at.step];
+      if (!a.rms) next_mean = a.mean[row + at.step];
     }
     wait_stage(a.stages);
-    char* from = ring + at * stage_bytes;
-    at = at + 1 == a.stages ? 0 : at + 1;
-    // xhat and g of group k
-    auto values = [&](int k, float (&xh)[8], float (&dy)[8], float (&g)[8]) {
-      const int q = k * lanes + lane, e0 = 8 * q - phase;
-      read_group(from + k * kPieces<H> * stride, stride, static_cast<const H*>(nullptr), xh);
-      read_group(from + at_y + k * kPieces<DY> * stride, stride, static_cast<const DY*>(nullptr), dy);
-      if (!live || !whole_group(e0, d)) {
-        clear_outside(xh, e0, live ? d : 0);
-        clear_outside(dy, e0, live ? d : 0);
-      }
+    if (!at.all || !live) {     // with dy = 0 outside the row nothing there counts
+      fh.clear(from, at, live ? d : 0);
+      fy.clear(from + at_y, at, live ? d : 0);
+    }
+    // c and dy of group k
+    auto values = [&](int k, float2 (&c)[N], float2 (&dy)[N]) {
+      fh.read(from, k, c);
+      fy.read(from + at_y, k, dy);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        xh[j] = (xh[j] - mean) * r;
-        g[j] = dy[j];
-      }
-      if (a.w) {
-        float u[8];
-        param8(w, groups, q, u);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] *= u[j];
-      }
+      for (int j = 0; j < N; ++j) c[j] = add2(c[j], both(-mean));
     };
-    float v[2] = {0.f, 0.f};
+    float2 sg = both(0.f), sgc = both(0.f);
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-      float xh[8], dy[8], g[8];
-      values(k, xh, dy, g);
+      float2 c[N], g[N];
+      values(k, c, g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        acc_w[k][j] += dy[j] * xh[j];
-        if (B) acc_b[k][j] += dy[j];
-        v[0] += g[j];
-        v[1] += g[j] * xh[j];
+      for (int j = 0; j < N; ++j) {
+        acc_w[k][j] = fma2(mul2(g[j], both(r)), c[j], acc_w[k][j]);
+        if (B) acc_b[k][j] = add2(acc_b[k][j], g[j]);
+      }
+      if (a.w) {
+        float2 u[N];
+        param_group(w, at.groups, k * at.lanes + at.lane, u);
+#pragma unroll
+        for (int j = 0; j < N; ++j) g[j] = mul2(g[j], u[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        sg = add2(sg, g[j]);
+        sgc = fma2(g[j], c[j], sgc);
       }
     }
     if (a.s) {
-      row_sum<SPLIT, 2>(v, part, turn, lanes);
-      const float c1 = a.rms ? 0.f : v[0] * inv_d, c2 = v[1] * inv_d;
+      float v[2] = {sg.x + sg.y, sgc.x + sgc.y};
+      row_sum<SPLIT, 2>(v, part, turn, at.lanes, at.lane, at.team);
       if (live) {
+        const float2 c1 = both(a.rms ? 0.f : -(v[0] * inv_d) * r), c2 = both(-(v[1] * r * inv_d) * r * r), rr = both(r);
         S* dx = static_cast<S*>(a.s) + row * a.lds;
 #pragma unroll
         for (int k = 0; k < P; ++k) {
-          float xh[8], dy[8], g[8];
-          values(k, xh, dy, g);
+          float2 c[N], g[N], u[N];
+          values(k, c, g);
+          if (a.w) {
+            param_group(w, at.groups, k * at.lanes + at.lane, u);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) g[j] = r * (g[j] - c1 - xh[j] * c2);
-          if (add) {
-            float u[8];
-            read_group(from + at_s + k * kPieces<S> * stride, stride, static_cast<const S*>(nullptr), u);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) g[j] += u[j];
+            for (int j = 0; j < N; ++j) g[j] = mul2(g[j], u[j]);
           }
-          store_group(dx, 8 * (k * lanes + lane) - phase, d, g);
+#pragma unroll
+          for (int j = 0; j < N; ++j) g[j] = fma2(c[j], c2, fma2(g[j], rr, c1));
+          if (add) {
+            fs.read(from + at_s, k, u);
+#pragma unroll
+            for (int j = 0; j < N; ++j) g[j] = add2(g[j], u[j]);
+          }
+          store_group(dx + at.e0[k], at.e0[k], d, at.whole[k], g);
         }
       }
     }
-    fetch(row + a.stages * step, from);
+    fetch(from);
+    from += stage_bytes;
+    if (from == ring_end) from = ring;
     mean = next_mean;
     r = next_r;
   }
   if (!a.dw && !a.db) return;
   float* out = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * d;
-  if (!SPLIT) {
-#pragma unroll
-    for (int k = 0; k < P; ++k) {
-      const int e0 = 8 * (k * lanes + lane) - phase;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (e0 + j >= 0 && e0 + j < d) {
-          out[e0 + j] = acc_w[k][j];
-          if (B) out[d + e0 + j] = acc_b[k][j];
-        }
-    }
-    return;
-  }
-  // a warp's rows by its lanes, then the warps in order
+  // the teams in order; of a warp's own rows (SPLIT) first its lanes
+  const int mine = SPLIT ? threadIdx.x >> 5 : at.team, seats = SPLIT ? blockDim.x >> 5 : blockDim.x / at.lanes;
   float* join = w;
   for (int half = 0; half < (B ? 2 : 1); ++half) {
 #pragma unroll
     for (int k = 0; k < P; ++k)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < N; ++j) {
         if (half) acc_w[k][j] = acc_b[k][j];
-        for (int o = lanes; o < 32; o <<= 1) acc_w[k][j] += __shfl_xor_sync(0xffffffffu, acc_w[k][j], o);
+        if (SPLIT)
+          for (int o = at.lanes; o < 32; o <<= 1) {
+            acc_w[k][j].x += __shfl_xor_sync(0xffffffffu, acc_w[k][j].x, o);
+            acc_w[k][j].y += __shfl_xor_sync(0xffffffffu, acc_w[k][j].y, o);
+          }
       }
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < seats; ++i) {
       __syncthreads();
-      if ((threadIdx.x >> 5) == i && (threadIdx.x & 31) < lanes)
+      if (mine == i && (!SPLIT || (threadIdx.x & 31) < at.lanes))
 #pragma unroll
         for (int k = 0; k < P; ++k)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int c = 8 * (k * lanes + lane) - phase + j;
-            if (c >= 0 && c < d) join[c] = i == 0 ? acc_w[k][j] : join[c] + acc_w[k][j];
+          for (int j = 0; j < G; ++j) {
+            const int c = at.e0[k] + j;
+            const float z = j & 1 ? acc_w[k][j / 2].y : acc_w[k][j / 2].x;
+            if (c >= 0 && c < d) join[c] = i == 0 ? z : join[c] + z;
           }
     }
     __syncthreads();
@@ -243,9 +241,9 @@ __global__ void __launch_bounds__(SPLIT ? 256 : 512) norm_grad_kernel(NormArgs a
 
 // ---------------------------------------------------------------------- launch --
 
-template <typename X, typename S, typename Y, int P, bool SPLIT>
+template <typename X, typename S, typename Y, int E, bool SPLIT>
 cudaError_t launch_grad(const NormArgs& a, const Plan& p, cudaStream_t s) {
-  const auto f = a.db ? norm_grad_kernel<X, S, Y, P, SPLIT, true> : norm_grad_kernel<X, S, Y, P, SPLIT, false>;
+  const auto f = a.db ? norm_grad_kernel<X, S, Y, E, SPLIT, true> : norm_grad_kernel<X, S, Y, E, SPLIT, false>;
   const cudaError_t e = allow_smem(f, p.smem);
   if (e != cudaSuccess) return e;
   f<<<p.grid, p.threads, p.smem, s>>>(a);
@@ -255,14 +253,14 @@ cudaError_t launch_grad(const NormArgs& a, const Plan& p, cudaStream_t s) {
 template <typename X, typename S, typename Y>
 cudaError_t launch_backward(NormArgs a, cudaStream_t s) {
   const unsigned cols = static_cast<unsigned>((a.d + 31) / 32);
-  const Plan p = make_plan<X, S, Y>(a, kPieces<X> + kPieces<Y> + (a.r && a.s ? kPieces<S> : 0), 1, a.slots, 512);
+  const Plan p = make_plan<X, S, Y>(a, sizeof(X) + sizeof(Y) + (a.r && a.s ? sizeof(S) : 0), 1, a.slots, 512);
   a.lanes = p.lanes;
   a.stages = p.stages;
   cudaError_t e = cudaSuccess;
-  if (p.groups_per_thread) {
-    if (p.groups_per_thread == 1) e = launch_grad<X, S, Y, 1, true>(a, p, s);
-    else if (p.groups_per_thread == 2) e = p.split ? launch_grad<X, S, Y, 2, true>(a, p, s) : launch_grad<X, S, Y, 2, false>(a, p, s);
-    else e = launch_grad<X, S, Y, 4, false>(a, p, s);
+  if (p.elements) {
+    if (p.elements == 8) e = launch_grad<X, S, Y, 8, true>(a, p, s);
+    else if (p.elements == 16) e = p.split ? launch_grad<X, S, Y, 16, true>(a, p, s) : launch_grad<X, S, Y, 16, false>(a, p, s);
+    else e = launch_grad<X, S, Y, 32, false>(a, p, s);
     if (e != cudaSuccess) return e;
     a.slots = static_cast<int32_t>(p.grid);
     if (a.dw || a.db) norm_join_kernel<<<dim3(cols, 2), 256, 0, s>>>(a);
@@ -289,8 +287,9 @@ cudaError_t launch_s(const NormArgs& a, int32_t st, int32_t y, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_layernorm_backward(const NormArgs& a, const moe_layernorm_config& c, cudaStream_t s) {
-  return c.x_dtype == MOE_F32 ? launch_s<float>(a, c.stream_dtype, c.y_dtype, s)
-                              : launch_s<__nv_bfloat16>(a, c.stream_dtype, c.y_dtype, s);
+  const int32_t stream = a.s ? c.stream_dtype : c.x_dtype;    // without dx: the form of h and dy alone
+  return c.x_dtype == MOE_F32 ? launch_s<float>(a, stream, c.y_dtype, s)
+                              : launch_s<__nv_bfloat16>(a, stream, c.y_dtype, s);
 }
 
 }  // namespace moe

@@ -1,4 +1,4 @@
-// Sums over the threads of a CTA that share a row.
+// Sums over the threads that share a row.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -11,20 +11,35 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sums of N values over the whole CTA, the same in every thread.  `part` holds N * 32 floats; the
-// callers alternate between two such buffers, so that one barrier per sum is enough.
+// A barrier of the `threads` threads (whole warps) that name it; 0 is __syncthreads' own.
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Sums of N values over the warps of a team, the same in every thread.  `part` holds N * 32 floats of the
+// team's own; its calls alternate between two of them, so that one barrier per sum is enough.
 template <int N>
-__device__ __forceinline__ void block_sum(float (&v)[N], float* part) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+__device__ __forceinline__ void team_sum(float (&v)[N], float* part, int warp, int warps, int barrier) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-  if (warps == 1) return;
   if (lane == 0)
 #pragma unroll
     for (int i = 0; i < N; ++i) part[i * 32 + warp] = v[i];
-  __syncthreads();
+  named_barrier(barrier, warps * 32);
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < warps ? part[i * 32 + lane] : 0.f);
+  for (int i = 0; i < N; ++i) v[i] = lane < warps ? part[i * 32 + lane] : 0.f;
+  for (int o = warps > 16 ? 16 : warps > 8 ? 8 : warps > 4 ? 4 : 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, v[i], 0);
+}
+
+// The same over the whole CTA.
+template <int N>
+__device__ __forceinline__ void block_sum(float (&v)[N], float* part) {
+  team_sum<N>(v, part, threadIdx.x >> 5, blockDim.x >> 5, 0);
 }
 
 }  // namespace moe

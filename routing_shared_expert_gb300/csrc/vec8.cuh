@@ -1,31 +1,42 @@
-// Groups of eight consecutive values: asynchronous copies to shared memory (16-byte pieces: one for
-// bf16, two for fp32), and one 16- or 32-byte store.
+// Groups of G = 4 or 8 consecutive values as pairs: asynchronous copies to shared memory, one of 8 or 16
+// bytes each, arithmetic on pairs (one instruction for two values), and one store each.
+//
+// G is 8 where every operand is bf16 and 4 where one is fp32: a lane's copy is then at most 16 bytes and a
+// warp's copies are one run of memory.  (Eight fp32 in two copies of 16 bytes ask L2 for every 32-byte
+// sector twice.)
 #pragma once
 
 #include "common.cuh"
 
 namespace moe {
 
-template <typename T>
-constexpr int kPieces = static_cast<int>(sizeof(T)) / 2;   // 16-byte pieces of a group
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
 
-__device__ __forceinline__ void unpack_bf16x8(const uint4 u, float (&v)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void store_whole(__nv_bfloat16* p, const float2 (&v)[4]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                                            pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+}
+__device__ __forceinline__ void store_whole(__nv_bfloat16* p, const float2 (&v)[2]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y));
+}
+__device__ __forceinline__ void store_whole(float* p, const float2 (&v)[2]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+}
+// Never called: fp32 operands come in groups of four.
+__device__ __forceinline__ void store_whole(float* p, const float2 (&v)[4]) {}
+
+// The pairs rounded to T and back.
+template <typename T, int N>
+__device__ __forceinline__ void round_to(float2 (&v)[N]) {
+  if (sizeof(T) == 2)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                            pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-}
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]),
-               "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-               : "memory");
+    for (int i = 0; i < N; ++i) v[i] = unpack2(pack_bf16x2(v[i].x, v[i].y));
 }
 
 // The bytes of a tensor with rows ld elements apart: what may be read.
@@ -37,47 +48,62 @@ __device__ __forceinline__ Extent extent_of(const void* p, int64_t rows, int64_t
   return {a, a + static_cast<uintptr_t>(((rows - 1) * ld + cols) * elem)};
 }
 
-// Begins the copy of elements [e0, e0 + 8) of a row of d to a thread's own pieces in shared memory,
-// `stride` bytes apart.  The group is aligned to its size; one that reaches over an end of the row is
-// copied whole, the neighbouring rows' values with it, and element by element only at the
-// tensor's own ends.  Values outside the row are for the reader to leave out.
-template <typename T>
-__device__ __forceinline__ void copy_group(char* dst, uint32_t stride, const T* row, int e0, int d, const Extent& t) {
-  if (e0 + 8 <= 0 || e0 >= d) return;
-  const char* src = reinterpret_cast<const char*>(row + e0);
+// Begins the copy of a group that lies in its row.
+template <int G, typename T>
+__device__ __forceinline__ void copy_whole(char* dst, const T* src) {
+  static_assert(G * sizeof(T) == 16 || G * sizeof(T) == 8, "a group is one copy");
+  if (G * sizeof(T) == 16) cp_async16(smem_u32(dst), src, 16);
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// The same of elements [e0, e0 + G) of a row of d that reach over one of its ends (src: element e0).  The
+// group is aligned to its size and copied whole, the neighbouring row's values with it, and element by
+// element only at the tensor's own ends.
+template <int G, typename T>
+__device__ __noinline__ void copy_end(char* dst, const T* src, int e0, int d, Extent t) {
+  if (e0 + G <= 0 || e0 >= d) return;
   const uintptr_t a = reinterpret_cast<uintptr_t>(src);
-  if (a >= t.lo && a + 8 * sizeof(T) <= t.hi) {
-#pragma unroll
-    for (int i = 0; i < kPieces<T>; ++i) cp_async16(smem_u32(dst) + i * stride, src + 16 * i, 16);
+  if (a >= t.lo && a + G * sizeof(T) <= t.hi) {
+    copy_whole<G>(dst, src);
     return;
   }
 #pragma unroll 1
-  for (int j = max(0, -e0); j < min(8, d - e0); ++j) {
-    constexpr int per = 16 / static_cast<int>(sizeof(T));
-    *reinterpret_cast<T*>(dst + j / per * stride + j % per * sizeof(T)) = row[e0 + j];
-  }
+  for (int j = max(0, -e0); j < min(G, d - e0); ++j) reinterpret_cast<T*>(dst)[j] = src[j];
 }
-__device__ __forceinline__ void read_group(const char* src, uint32_t, const __nv_bfloat16*, float (&v)[8]) {
-  unpack_bf16x8(*reinterpret_cast<const uint4*>(src), v);
+// Zeros in the places of a copied group that lie outside the row.
+template <int G, typename T>
+__device__ __noinline__ void clear_end(char* at, int e0, int d) {
+#pragma unroll 1
+  for (int j = 0; j < G; ++j)
+    if (e0 + j < 0 || e0 + j >= d) reinterpret_cast<T*>(at)[j] = from_f32<T>(0.f);
 }
-__device__ __forceinline__ void read_group(const char* src, uint32_t stride, const float*, float (&v)[8]) {
-  const float4 lo = *reinterpret_cast<const float4*>(src), hi = *reinterpret_cast<const float4*>(src + stride);
-  v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w, v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+__device__ __forceinline__ void read_group(const char* src, const __nv_bfloat16*, float2 (&v)[4]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(src);
+  v[0] = unpack2(u.x), v[1] = unpack2(u.y), v[2] = unpack2(u.z), v[3] = unpack2(u.w);
 }
-__device__ __forceinline__ bool whole_group(int e0, int d) { return e0 >= 0 && e0 + 8 <= d; }
-__device__ __forceinline__ void clear_outside(float (&v)[8], int e0, int d) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (e0 + j < 0 || e0 + j >= d) v[j] = 0.f;
+__device__ __forceinline__ void read_group(const char* src, const __nv_bfloat16*, float2 (&v)[2]) {
+  const uint2 u = *reinterpret_cast<const uint2*>(src);
+  v[0] = unpack2(u.x), v[1] = unpack2(u.y);
 }
+__device__ __forceinline__ void read_group(const char* src, const float*, float2 (&v)[2]) {
+  const float4 u = *reinterpret_cast<const float4*>(src);
+  v[0] = make_float2(u.x, u.y), v[1] = make_float2(u.z, u.w);
+}
+__device__ __forceinline__ void read_group(const char* src, const float*, float2 (&v)[4]) {}   // never called
+// Stores the part of a group that lies in the row (dst: element e0).
 template <typename T>
-__device__ __forceinline__ void store_group(T* row, int e0, int d, const float (&v)[8]) {
-  if (whole_group(e0, d)) {
-    store8(row + e0, v);
-  } else {
+__device__ __noinline__ void store_end(T* dst, int e0, int d, float2 a, float2 b) {
+  const float v[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (e0 + j >= 0 && e0 + j < d) row[e0 + j] = from_f32<T>(v[j]);
+  for (int j = 0; j < 4; ++j)
+    if (e0 + j >= 0 && e0 + j < d) dst[j] = from_f32<T>(v[j]);
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_group(T* dst, int e0, int d, bool whole, const float2 (&v)[N]) {
+  if (whole) {
+    store_whole(dst, v);
+  } else {
+    store_end(dst, e0, d, v[0], v[1]);
+    if (N == 4) store_end(dst + 4, e0 + 4, d, v[N - 2], v[N - 1]);
   }
 }
 

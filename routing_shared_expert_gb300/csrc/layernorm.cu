@@ -48,45 +48,54 @@ __global__ void __launch_bounds__(256) norm_any_kernel(NormArgs a) {
   }
 }
 
-template <typename X, typename S, typename Y, int E, bool SPLIT>
+template <typename X, typename S, typename Y, int E, bool SPLIT, bool ENDS>
 __global__ void __launch_bounds__(E == 32 ? 512 : 1024) norm_vec_kernel(NormArgs a) {
   constexpr int G = kGroup<X, S, Y>, P = E / G, N = G / 2;
   extern __shared__ float4 smem[];
-  __shared__ float part[SPLIT ? 1 : kMaxTeams * 2 * 32];
+  __shared__ float part[SPLIT ? 1 : kMaxTeams * 2 * 16];
   const Seat<G, P, SPLIT> at(a, phase_of<G>(static_cast<const X*>(a.x) + blockIdx.x * a.ldx));
   const int d = a.d;
   const bool add = a.r != nullptr;
   float* w = reinterpret_cast<float*>(smem);
   float* b = w + (a.w ? G * at.groups : 0);
-  Feed<X, G, P, SPLIT> x(a.x, a.ldx, at);
-  Feed<S, G, P, SPLIT> r(a.r, a.ldr, at);
+  Feed<X, G, P, SPLIT, ENDS> x(a.x, a.ldx, at);
+  Feed<S, G, P, SPLIT, ENDS> r(a.r, a.ldr, at);
+  Sink<S, G, P, SPLIT, ENDS> sum(a.s, a.lds, at);
+  Sink<Y, G, P, SPLIT, ENDS> y(a.y, a.ldy, at);
   // the ring: each thread's groups of x, then those of r
   char* const base = reinterpret_cast<char*>(b + (a.b ? G * at.groups : 0));
   char* const ring = base + threadIdx.x * static_cast<uint32_t>(G * sizeof(X));
   const uint32_t at_r = P * x.stride + threadIdx.x * static_cast<uint32_t>(G * sizeof(S)) - threadIdx.x * static_cast<uint32_t>(G * sizeof(X));
   const uint32_t stage_bytes = P * x.stride + (add ? P * r.stride : 0);
   char* const ring_end = ring + a.stages * stage_bytes;
-  int64_t ahead = at.row;
+  const int T = static_cast<int>(a.T);
+  int ahead = at.row;
   auto fetch = [&](char* to) {
-    if (ahead < a.T) {
+    if (ahead < T) {
       x.copy(to, at, a, a.x, a.ldx);
       if (add) r.copy(to + at_r, at, a, a.r, a.ldr);
     }
     ahead += at.step;
     cp_async_commit();
   };
-  for (char* to = ring; to != ring_end; to += stage_bytes) fetch(to);
+  for (char* to = ring; to != ring_end; to += stage_bytes) {
+    if (!ENDS && !at.all) {      // groups past the row are never copied
+      x.clear(to, at, d);
+      if (add) r.clear(to + at_r, at, d);
+    }
+    fetch(to);
+  }
   if (a.w) stage_param<G>(w, a.w, a.w_dtype, at.groups, at.phase, d);
   if (a.b) stage_param<G>(b, a.b, a.w_dtype, at.groups, at.phase, d);
   __syncthreads();
   const float inv_d = 1.f / d;
   int turn = 0;
-  int64_t row = at.row;
+  int row = at.row;
   char* from = ring;
   for (int it = 0; it < at.turns; ++it, row += at.step) {
-    const bool live = !SPLIT || row < a.T;
+    const bool live = !SPLIT || row < T;
     wait_stage(a.stages);
-    if (!at.all || !live) {
+    if ((ENDS && !at.all) || !live) {
       x.clear(from, at, live ? d : 0);
       if (add) r.clear(from + at_r, at, live ? d : 0);
     }
@@ -100,7 +109,7 @@ __global__ void __launch_bounds__(E == 32 ? 512 : 1024) norm_vec_kernel(NormArgs
 #pragma unroll
         for (int j = 0; j < N; ++j) h[k][j] = add2(h[k][j], v[j]);
         if (a.s) {
-          if (live) store_group(static_cast<S*>(a.s) + row * a.lds + at.e0[k], at.e0[k], d, at.whole[k], h[k]);
+          if (live) sum.store(k, at, d, h[k]);
           round_to<S>(h[k]);     // normalised is the sum as stored
         }
       }
@@ -108,22 +117,23 @@ __global__ void __launch_bounds__(E == 32 ? 512 : 1024) norm_vec_kernel(NormArgs
     fetch(from);
     from += stage_bytes;
     if (from == ring_end) from = ring;
+    sum.row += sum.step;
     float v[1];
     float mean = 0.f;
     if (!a.rms) {
-      float2 sum = both(0.f);
+      float2 total = both(0.f);
 #pragma unroll
       for (int k = 0; k < P; ++k)
 #pragma unroll
-        for (int j = 0; j < N; ++j) sum = add2(sum, h[k][j]);
-      v[0] = sum.x + sum.y;
+        for (int j = 0; j < N; ++j) total = add2(total, h[k][j]);
+      v[0] = total.x + total.y;
       row_sum<SPLIT, 1>(v, part, turn, at.lanes, at.lane, at.team);
       mean = v[0] * inv_d;
 #pragma unroll
       for (int k = 0; k < P; ++k) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) h[k][j] = add2(h[k][j], both(-mean));
-        if (!at.whole[k]) {
+        for (int j = 0; j < N; ++j) h[k][j] = add2(h[k][j], both(ENDS || at.whole[k] ? -mean : 0.f));
+        if (ENDS && !at.whole[k]) {
           asm volatile("");      // a branch that few threads take, not selections in all of them
 #pragma unroll
           for (int j = 0; j < G; ++j)
@@ -139,12 +149,11 @@ __global__ void __launch_bounds__(E == 32 ? 512 : 1024) norm_vec_kernel(NormArgs
     v[0] = sq.x + sq.y;
     row_sum<SPLIT, 1>(v, part, turn, at.lanes, at.lane, at.team);
     const float rstd = rsqrtf(v[0] * inv_d + a.eps);
-    if (!live) continue;
+    if (!live) continue;      // its last turn
     if (at.lane == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
     }
-    Y* y = static_cast<Y*>(a.y) + row * a.ldy;
 #pragma unroll
     for (int k = 0; k < P; ++k) {
       float2 u[N];
@@ -160,8 +169,9 @@ __global__ void __launch_bounds__(E == 32 ? 512 : 1024) norm_vec_kernel(NormArgs
 #pragma unroll
         for (int j = 0; j < N; ++j) h[k][j] = add2(h[k][j], u[j]);
       }
-      store_group(y + at.e0[k], at.e0[k], d, at.whole[k], h[k]);
+      y.store(k, at, d, h[k]);
     }
+    y.row += y.step;
   }
 }
 
@@ -169,7 +179,7 @@ __global__ void __launch_bounds__(E == 32 ? 512 : 1024) norm_vec_kernel(NormArgs
 
 template <typename X, typename S, typename Y, int E, bool SPLIT>
 cudaError_t launch_vec(const NormArgs& a, const Plan& p, cudaStream_t s) {
-  const auto f = norm_vec_kernel<X, S, Y, E, SPLIT>;
+  const auto f = p.ends ? norm_vec_kernel<X, S, Y, E, SPLIT, true> : norm_vec_kernel<X, S, Y, E, SPLIT, false>;
   const cudaError_t e = allow_smem(f, p.smem);
   if (e != cudaSuccess) return e;
   f<<<p.grid, p.threads, p.smem, s>>>(a);

@@ -51,7 +51,8 @@ cudaError_t launch_layernorm_backward(const NormArgs& a, const moe_layernorm_con
 // teams of `lanes` threads, each with rows of its own, and one copy of the parameters in shared memory.
 // Its rows are gridDim.x apart, a multiple of eight unless the stride is one, so that the phase is the
 // same for all of them and the parameters can lie at that phase.  SPLIT: a team is a power of two of a
-// warp's lanes; else it is whole warps with a barrier of their own.
+// warp's lanes; else it is whole warps with a barrier of their own.  ENDS: rows may begin or end within a
+// group; else every group lies in its row or past it.
 //
 // Each thread copies its own groups of the next rows asynchronously into its own slots of a ring in
 // shared memory, a.stages rows ahead: the bytes on their way do not depend on registers, and the
@@ -93,7 +94,7 @@ __device__ __forceinline__ void wait_stage(int stages) {   // the oldest of `sta
 template <int G, int P, bool SPLIT>
 struct Seat {
   int lanes, lane, team, groups, phase;
-  int64_t row, step;
+  int row, step;      // the team's first row, and from one to the next
   int turns;          // of its warp, the last of which may be past the last row for some teams (SPLIT)
   int e0[P];          // first element of each group, within the row
   bool whole[P], all; // whether each lies in the row, and all do
@@ -103,10 +104,10 @@ struct Seat {
     lane = threadIdx.x - team * lanes;
     groups = lanes * P;
     phase = first_phase;
-    row = blockIdx.x + static_cast<int64_t>(team) * gridDim.x;
-    step = static_cast<int64_t>(blockDim.x / lanes) * gridDim.x;
-    const int64_t first = SPLIT ? blockIdx.x + static_cast<int64_t>((threadIdx.x & ~31) / lanes) * gridDim.x : row;
-    turns = first < a.T ? static_cast<int>((a.T - first + step - 1) / step) : 0;
+    row = blockIdx.x + team * gridDim.x;
+    step = blockDim.x / lanes * gridDim.x;
+    const int first = SPLIT ? blockIdx.x + (threadIdx.x & ~31) / lanes * gridDim.x : row, T = static_cast<int>(a.T);
+    turns = first < T ? (T - first + step - 1) / step : 0;
     all = true;
 #pragma unroll
     for (int k = 0; k < P; ++k) {
@@ -117,20 +118,22 @@ struct Seat {
   }
 };
 
-// The rows of one operand on their way into a thread's slots of the ring, `stride` bytes apart.
-template <typename T, int G, int P, bool SPLIT>
+// A thread's groups of one operand: `at` is where the current row's lie in the ring, copies of later rows
+// begin from `next`.  The pieces are `stride` bytes apart.
+template <typename T, int G, int P, bool SPLIT, bool ENDS>
 struct Feed {
-  const T* next;      // element 0 of the row to be copied next
+  const T* next;      // element 0 of the thread's first group, in the row to be copied next
   int64_t step;       // elements to the team's row after it
   uint32_t stride;
   __device__ __forceinline__ Feed(const void* base, int64_t ld, const Seat<G, P, SPLIT>& s)
-      : next(static_cast<const T*>(base) + s.row * ld), step(s.step * ld),
+      : next(static_cast<const T*>(base) + s.row * ld + s.e0[0]), step(s.step * ld),
         stride(blockDim.x * static_cast<uint32_t>(G * sizeof(T))) {}
   __device__ __forceinline__ void copy(char* to, const Seat<G, P, SPLIT>& s, const NormArgs& a, const void* base, int64_t ld) {
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-      if (s.whole[k]) copy_whole<G>(to + k * stride, next + s.e0[k]);
-      else copy_end<G>(to + k * stride, next + s.e0[k], s.e0[k], a.d, extent_of(base, a.T, ld, a.d, sizeof(T)));
+      const T* src = next + k * G * s.lanes;
+      if (s.whole[k]) copy_whole<G>(to + k * stride, src);
+      else if (ENDS) copy_end<G>(to + k * stride, src, s.e0[k], a.d, extent_of(base, a.T, ld, a.d, sizeof(T)));
     }
     next += step;
   }
@@ -143,6 +146,20 @@ struct Feed {
   }
 };
 
+// A thread's groups of a result, row by row.
+template <typename T, int G, int P, bool SPLIT, bool ENDS>
+struct Sink {
+  T* row;
+  int64_t step;
+  __device__ __forceinline__ Sink(void* base, int64_t ld, const Seat<G, P, SPLIT>& s)
+      : row(static_cast<T*>(base) + s.row * ld + s.e0[0]), step(s.step * ld) {}
+  __device__ __forceinline__ void store(int k, const Seat<G, P, SPLIT>& s, int d, const float2 (&v)[G / 2]) {
+    T* dst = row + k * G * s.lanes;
+    if (s.whole[k]) store_whole(dst, v);
+    else if (ENDS) store_end(dst, s.e0[k], d, v);
+  }
+};
+
 template <bool SPLIT, int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], float* part, int& turn, int lanes, int lane, int team) {
   if (SPLIT) {
@@ -150,7 +167,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* part, int& turn, i
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
   } else {
-    team_sum<N>(v, part + (2 * team + turn) * N * 32, lane >> 5, lanes >> 5, 1 + team);
+    team_sum<N>(v, part + (2 * team + turn) * N * 16, lane >> 5, lanes >> 5, 1 + team);
     turn ^= 1;
   }
 }
@@ -164,7 +181,7 @@ constexpr size_t kSharedPerSm = 227 * 1024;
 struct Plan {
   int elements = 0;            // of a thread; 0: any layout
   int lanes = 0, threads = 0, stages = 0;
-  bool split = false;
+  bool split = false, ends = false;
   unsigned grid = 0;
   size_t smem = 0;
 };
@@ -189,6 +206,7 @@ Plan make_plan(const NormArgs& a, size_t bytes, int params, int64_t most, int re
   const int64_t sms = device_sm_count();
   auto lanes_of = [&](int elements) { return (groups + elements / G - 1) / (elements / G); };
   p.split = lanes_of(16) <= 32;
+  p.ends = phase || shift || a.d % G;
   int E, teams;
   if (p.split) {
     E = lanes_of(8) <= 32 ? 8 : 16;

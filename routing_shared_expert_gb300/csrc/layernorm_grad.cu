@@ -86,18 +86,19 @@ __global__ void __launch_bounds__(256) norm_join_kernel(NormArgs a) {
 // The backward pass in one reading of the rows; the columns' sums stay in registers over the CTA's rows
 // (B: those of db too) and go out once.  Between the two uses of a row its values stay in the ring.
 // With c = h - mean: dw sums (dy rstd) c, and dx = rstd (g - c1) - c (rstd^2 c2), c2 = rstd sum (g c) / d.
-template <typename H, typename S, typename DY, int E, bool SPLIT, bool B>
+template <typename H, typename S, typename DY, int E, bool SPLIT, bool ENDS, bool B>
 __global__ void __launch_bounds__(512) norm_grad_kernel(NormArgs a) {
   constexpr int G = kGroup<H, S, DY>, P = E / G, N = G / 2;
   extern __shared__ float4 smem[];
-  __shared__ float part[SPLIT ? 1 : kMaxTeams * 2 * 64];
+  __shared__ float part[SPLIT ? 1 : kMaxTeams * 2 * 32];
   const Seat<G, P, SPLIT> at(a, phase_of<G>(static_cast<const H*>(a.x) + blockIdx.x * a.ldx));
   const int d = a.d;
   const bool add = a.r && a.s;
   float* w = reinterpret_cast<float*>(smem);
-  Feed<H, G, P, SPLIT> fh(a.x, a.ldx, at);
-  Feed<DY, G, P, SPLIT> fy(a.y, a.ldy, at);
-  Feed<S, G, P, SPLIT> fs(a.r, a.ldr, at);
+  Feed<H, G, P, SPLIT, ENDS> fh(a.x, a.ldx, at);
+  Feed<DY, G, P, SPLIT, ENDS> fy(a.y, a.ldy, at);
+  Feed<S, G, P, SPLIT, ENDS> fs(a.r, a.ldr, at);
+  Sink<S, G, P, SPLIT, ENDS> dx(a.s, a.lds, at);
   // the ring: each thread's groups of h, then those of dy, then those of dsum
   constexpr uint32_t kH = G * sizeof(H), kY = G * sizeof(DY), kS = G * sizeof(S);
   char* const ring = reinterpret_cast<char*>(w + G * at.groups) + threadIdx.x * kH;
@@ -105,9 +106,10 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormArgs a) {
   const uint32_t at_s = P * (fh.stride + fy.stride) + threadIdx.x * kS - threadIdx.x * kH;
   const uint32_t stage_bytes = P * (fh.stride + fy.stride + (add ? fs.stride : 0));
   char* const ring_end = ring + a.stages * stage_bytes;
-  int64_t ahead = at.row;
+  const int T = static_cast<int>(a.T);
+  int ahead = at.row;
   auto fetch = [&](char* to) {
-    if (ahead < a.T) {
+    if (ahead < T) {
       fh.copy(to, at, a, a.x, a.ldx);
       fy.copy(to + at_y, at, a, a.y, a.ldy);
       if (add) fs.copy(to + at_s, at, a, a.r, a.ldr);
@@ -115,7 +117,14 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormArgs a) {
     ahead += at.step;
     cp_async_commit();
   };
-  for (char* to = ring; to != ring_end; to += stage_bytes) fetch(to);
+  for (char* to = ring; to != ring_end; to += stage_bytes) {
+    if (!ENDS && !at.all) {      // groups past the row are never copied
+      fh.clear(to, at, d);
+      fy.clear(to + at_y, at, d);
+      if (add) fs.clear(to + at_s, at, d);
+    }
+    fetch(to);
+  }
   if (a.w) stage_param<G>(w, a.w, a.w_dtype, at.groups, at.phase, d);
   __syncthreads();
   const float inv_d = 1.f / d;
@@ -125,22 +134,22 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormArgs a) {
   for (int k = 0; k < P; ++k)
 #pragma unroll
     for (int j = 0; j < N; ++j) acc_w[k][j] = acc_b[k][j] = both(0.f);
-  int64_t row = at.row;
+  int row = at.row;
   float mean = 0.f, r = 0.f;
-  if (row < a.T) {
+  if (row < T) {
     r = a.rstd[row];
     if (!a.rms) mean = a.mean[row];
   }
   char* from = ring;
   for (int it = 0; it < at.turns; ++it, row += at.step) {
-    const bool live = !SPLIT || row < a.T;
+    const bool live = !SPLIT || row < T;
     float next_mean = 0.f, next_r = 0.f;
-    if (row + at.step < a.T) {
+    if (row + at.step < T) {
       next_r = a.rstd[row + at.step];
       if (!a.rms) next_mean = a.mean[row + at.step];
     }
     wait_stage(a.stages);
-    if (!at.all || !live) {     // with dy = 0 outside the row nothing there counts
+    if ((ENDS && !at.all) || !live) {     // with dy = 0 outside the row nothing there counts
       fh.clear(from, at, live ? d : 0);
       fy.clear(from + at_y, at, live ? d : 0);
     }
@@ -178,7 +187,6 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormArgs a) {
       row_sum<SPLIT, 2>(v, part, turn, at.lanes, at.lane, at.team);
       if (live) {
         const float2 c1 = both(a.rms ? 0.f : -(v[0] * inv_d) * r), c2 = both(-(v[1] * r * inv_d) * r * r), rr = both(r);
-        S* dx = static_cast<S*>(a.s) + row * a.lds;
 #pragma unroll
         for (int k = 0; k < P; ++k) {
           float2 c[N], g[N], u[N];
@@ -195,9 +203,10 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormArgs a) {
 #pragma unroll
             for (int j = 0; j < N; ++j) g[j] = add2(g[j], u[j]);
           }
-          store_group(dx + at.e0[k], at.e0[k], d, at.whole[k], g);
+          dx.store(k, at, d, g);
         }
       }
+      dx.row += dx.step;
     }
     fetch(from);
     from += stage_bytes;
@@ -241,13 +250,17 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormArgs a) {
 
 // ---------------------------------------------------------------------- launch --
 
-template <typename X, typename S, typename Y, int E, bool SPLIT>
-cudaError_t launch_grad(const NormArgs& a, const Plan& p, cudaStream_t s) {
-  const auto f = a.db ? norm_grad_kernel<X, S, Y, E, SPLIT, true> : norm_grad_kernel<X, S, Y, E, SPLIT, false>;
+template <typename X, typename S, typename Y, int E, bool SPLIT, bool ENDS>
+cudaError_t launch_grad_b(const NormArgs& a, const Plan& p, cudaStream_t s) {
+  const auto f = a.db ? norm_grad_kernel<X, S, Y, E, SPLIT, ENDS, true> : norm_grad_kernel<X, S, Y, E, SPLIT, ENDS, false>;
   const cudaError_t e = allow_smem(f, p.smem);
   if (e != cudaSuccess) return e;
   f<<<p.grid, p.threads, p.smem, s>>>(a);
   return cudaGetLastError();
+}
+template <typename X, typename S, typename Y, int E, bool SPLIT>
+cudaError_t launch_grad(const NormArgs& a, const Plan& p, cudaStream_t s) {
+  return p.ends ? launch_grad_b<X, S, Y, E, SPLIT, true>(a, p, s) : launch_grad_b<X, S, Y, E, SPLIT, false>(a, p, s);
 }
 
 template <typename X, typename S, typename Y>

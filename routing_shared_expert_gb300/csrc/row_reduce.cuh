@@ -16,8 +16,8 @@ __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// Sums of N values over the warps of a team, the same in every thread.  `part` holds N * 32 floats of the
-// team's own; its calls alternate between two of them, so that one barrier per sum is enough.
+// Sums of N values over the warps of a team, 16 at most, the same in every thread.  `part` holds N * 16
+// floats of the team's own; its calls alternate between two of them, so that one barrier per sum is enough.
 template <int N>
 __device__ __forceinline__ void team_sum(float (&v)[N], float* part, int warp, int warps, int barrier) {
   const int lane = threadIdx.x & 31;
@@ -25,18 +25,17 @@ __device__ __forceinline__ void team_sum(float (&v)[N], float* part, int warp, i
   for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
   if (lane == 0)
 #pragma unroll
-    for (int i = 0; i < N; ++i) part[i * 32 + warp] = v[i];
+    for (int i = 0; i < N; ++i) part[i * 16 + warp] = v[i];
   named_barrier(barrier, warps * 32);
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = lane < warps ? part[i * 32 + lane] : 0.f;
-  for (int o = warps > 16 ? 16 : warps > 8 ? 8 : warps > 4 ? 4 : 2; o > 0; o >>= 1)
+  for (int i = 0; i < N; ++i) v[i] = (lane & 15) < warps ? part[i * 16 + (lane & 15)] : 0.f;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, v[i], 0);
 }
 
-// The same over the whole CTA.
+// The same over the whole CTA of at most 512 threads.
 template <int N>
 __device__ __forceinline__ void block_sum(float (&v)[N], float* part) {
   team_sum<N>(v, part, threadIdx.x >> 5, blockDim.x >> 5, 0);

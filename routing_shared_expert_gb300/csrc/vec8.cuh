@@ -91,20 +91,16 @@ __device__ __forceinline__ void read_group(const char* src, const float*, float2
 __device__ __forceinline__ void read_group(const char* src, const float*, float2 (&v)[4]) {}   // never called
 // Stores the part of a group that lies in the row (dst: element e0).
 template <typename T>
-__device__ __noinline__ void store_end(T* dst, int e0, int d, float2 a, float2 b) {
+__device__ __noinline__ void store_end4(T* dst, int e0, int d, float2 a, float2 b) {
   const float v[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     if (e0 + j >= 0 && e0 + j < d) dst[j] = from_f32<T>(v[j]);
 }
 template <typename T, int N>
-__device__ __forceinline__ void store_group(T* dst, int e0, int d, bool whole, const float2 (&v)[N]) {
-  if (whole) {
-    store_whole(dst, v);
-  } else {
-    store_end(dst, e0, d, v[0], v[1]);
-    if (N == 4) store_end(dst + 4, e0 + 4, d, v[N - 2], v[N - 1]);
-  }
+__device__ __forceinline__ void store_end(T* dst, int e0, int d, const float2 (&v)[N]) {
+  store_end4(dst, e0, d, v[0], v[1]);
+  if (N == 4) store_end4(dst + 4, e0 + 4, d, v[N - 2], v[N - 1]);
 }
 
 }  // namespace moe

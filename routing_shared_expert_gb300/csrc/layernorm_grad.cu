@@ -84,10 +84,12 @@ __global__ void __launch_bounds__(256) norm_join_kernel(NormArgs a) {
 }
 
 // The backward pass in one reading of the rows; the columns' sums stay in registers over the CTA's rows
-// (B: those of db too) and go out once.  Between the two uses of a row its values stay in the ring.
-// With c = h - mean: dw sums (dy rstd) c, and dx = rstd (g - c1) - c (rstd^2 c2), c2 = rstd sum (g c) / d.
-template <typename H, typename S, typename DY, int E, bool SPLIT, bool ENDS, bool B>
-__global__ void __launch_bounds__(512) norm_grad_kernel(NormArgs a) {
+// (B: those of db too) and go out once.  With c = h - mean and p = dy c:
+//   dw = sum p rstd,  dx = rstd (g - c1) - c (rstd^2 c2),  c1 = sum (dy w) / d,  c2 = rstd sum (p w) / d.
+// RMS: no mean and no c1, one sum per row instead of two (db of RMS rows runs the other form).  Between its two
+// uses a row stays in registers where a thread has 16 elements of it, else in the ring.
+template <typename H, typename S, typename DY, int E, bool SPLIT, bool ENDS, bool RMS, bool B>
+__global__ void __launch_bounds__(RMS && E <= 16 ? 640 : 512) norm_grad_kernel(NormArgs a) {
   constexpr int G = kGroup<H, S, DY>, P = E / G, N = G / 2;
   extern __shared__ float4 smem[];
   __shared__ float part[SPLIT ? 1 : kMaxTeams * 2 * 32];
@@ -138,7 +140,7 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormArgs a) {
   float mean = 0.f, r = 0.f;
   if (row < T) {
     r = a.rstd[row];
-    if (!a.rms) mean = a.mean[row];
+    if (!RMS && !a.rms) mean = a.mean[row];
   }
   char* from = ring;
   for (int it = 0; it < at.turns; ++it, row += at.step) {
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormArgs a) {
     float next_mean = 0.f, next_r = 0.f;
     if (row + at.step < T) {
       next_r = a.rstd[row + at.step];
-      if (!a.rms) next_mean = a.mean[row + at.step];
+      if (!RMS && !a.rms) next_mean = a.mean[row + at.step];
     }
     wait_stage(a.stages);
     if ((ENDS && !at.all) || !live) {     // with dy = 0 outside the row nothing there counts
@@ -157,47 +159,57 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormArgs a) {
     auto values = [&](int k, float2 (&c)[N], float2 (&dy)[N]) {
       fh.read(from, k, c);
       fy.read(from + at_y, k, dy);
+      if (!RMS)
 #pragma unroll
-      for (int j = 0; j < N; ++j) c[j] = add2(c[j], both(-mean));
+        for (int j = 0; j < N; ++j) c[j] = add2(c[j], both(-mean));
     };
+    constexpr bool KEEP = E <= 16;
+    float2 kc[KEEP ? P : 1][N], kg[KEEP ? P : 1][N];
     float2 sg = both(0.f), sgc = both(0.f);
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-      float2 c[N], g[N];
+      float2 (&c)[N] = kc[KEEP ? k : 0];
+      float2 (&g)[N] = kg[KEEP ? k : 0];
       values(k, c, g);
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        acc_w[k][j] = fma2(mul2(g[j], both(r)), c[j], acc_w[k][j]);
-        if (B) acc_b[k][j] = add2(acc_b[k][j], g[j]);
-      }
+      float2 u[N], p[N];
       if (a.w) {
-        float2 u[N];
         param_group(w, at.groups, k * at.lanes + at.lane, u);
+      } else {
 #pragma unroll
-        for (int j = 0; j < N; ++j) g[j] = mul2(g[j], u[j]);
+        for (int j = 0; j < N; ++j) u[j] = both(1.f);
       }
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        sg = add2(sg, g[j]);
-        sgc = fma2(g[j], c[j], sgc);
+        p[j] = mul2(g[j], c[j]);
+        acc_w[k][j] = fma2(p[j], both(r), acc_w[k][j]);
+        if (B) acc_b[k][j] = add2(acc_b[k][j], g[j]);
+        sgc = fma2(p[j], u[j], sgc);
+        if (!RMS) sg = fma2(g[j], u[j], sg);
+        if (KEEP) g[j] = mul2(g[j], u[j]);
       }
     }
     if (a.s) {
-      float v[2] = {sg.x + sg.y, sgc.x + sgc.y};
-      row_sum<SPLIT, 2>(v, part, turn, at.lanes, at.lane, at.team);
+      float v[RMS ? 1 : 2];
+      v[0] = sgc.x + sgc.y;
+      if (!RMS) v[RMS ? 0 : 1] = sg.x + sg.y;
+      row_sum<SPLIT, RMS ? 1 : 2>(v, part, turn, at.lanes, at.lane, at.team);
       if (live) {
-        const float2 c1 = both(a.rms ? 0.f : -(v[0] * inv_d) * r), c2 = both(-(v[1] * r * inv_d) * r * r), rr = both(r);
+        const float2 c1 = both(RMS || a.rms ? 0.f : -(v[RMS ? 0 : 1] * inv_d) * r), c2 = both(-(v[0] * r * inv_d) * r * r);
 #pragma unroll
         for (int k = 0; k < P; ++k) {
-          float2 c[N], g[N], u[N];
-          values(k, c, g);
-          if (a.w) {
-            param_group(w, at.groups, k * at.lanes + at.lane, u);
+          float2 (&c)[N] = kc[KEEP ? k : 0];
+          float2 (&g)[N] = kg[KEEP ? k : 0];
+          float2 u[N];
+          if (!KEEP) {
+            values(k, c, g);
+            if (a.w) {
+              param_group(w, at.groups, k * at.lanes + at.lane, u);
 #pragma unroll
-            for (int j = 0; j < N; ++j) g[j] = mul2(g[j], u[j]);
+              for (int j = 0; j < N; ++j) g[j] = mul2(g[j], u[j]);
+            }
           }
 #pragma unroll
-          for (int j = 0; j < N; ++j) g[j] = fma2(c[j], c2, fma2(g[j], rr, c1));
+          for (int j = 0; j < N; ++j) g[j] = fma2(c[j], c2, RMS ? mul2(g[j], both(r)) : fma2(g[j], both(r), c1));
           if (add) {
             fs.read(from + at_s, k, u);
 #pragma unroll
@@ -252,7 +264,9 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormArgs a) {
 
 template <typename X, typename S, typename Y, int E, bool SPLIT, bool ENDS>
 cudaError_t launch_grad_b(const NormArgs& a, const Plan& p, cudaStream_t s) {
-  const auto f = a.db ? norm_grad_kernel<X, S, Y, E, SPLIT, ENDS, true> : norm_grad_kernel<X, S, Y, E, SPLIT, ENDS, false>;
+  const auto f = a.db    ? norm_grad_kernel<X, S, Y, E, SPLIT, ENDS, false, true>
+                 : a.rms ? norm_grad_kernel<X, S, Y, E, SPLIT, ENDS, true, false>
+                         : norm_grad_kernel<X, S, Y, E, SPLIT, ENDS, false, false>;
   const cudaError_t e = allow_smem(f, p.smem);
   if (e != cudaSuccess) return e;
   f<<<p.grid, p.threads, p.smem, s>>>(a);
@@ -266,7 +280,7 @@ cudaError_t launch_grad(const NormArgs& a, const Plan& p, cudaStream_t s) {
 template <typename X, typename S, typename Y>
 cudaError_t launch_backward(NormArgs a, cudaStream_t s) {
   const unsigned cols = static_cast<unsigned>((a.d + 31) / 32);
-  const Plan p = make_plan<X, S, Y>(a, sizeof(X) + sizeof(Y) + (a.r && a.s ? sizeof(S) : 0), 1, a.slots, 512);
+  const Plan p = make_plan<X, S, Y>(a, sizeof(X) + sizeof(Y) + (a.r && a.s ? sizeof(S) : 0), 1, a.slots, a.rms && !a.db ? 640 : 512);
   a.lanes = p.lanes;
   a.stages = p.stages;
   cudaError_t e = cudaSuccess;

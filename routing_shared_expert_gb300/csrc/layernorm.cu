@@ -53,6 +53,7 @@ __global__ void __launch_bounds__(E == 32 ? 512 : 1024) norm_vec_kernel(NormArgs
   constexpr int G = kGroup<X, S, Y>, P = E / G, N = G / 2;
   extern __shared__ float4 smem[];
   __shared__ float part[SPLIT ? 1 : kMaxTeams * 2 * 16];
+  launch_dependents();
   const Seat<G, P, SPLIT> at(a, phase_of<G>(static_cast<const X*>(a.x) + blockIdx.x * a.ldx));
   const int d = a.d;
   const bool add = a.r != nullptr;
@@ -78,10 +79,11 @@ __global__ void __launch_bounds__(E == 32 ? 512 : 1024) norm_vec_kernel(NormArgs
     ahead += at.step;
     cp_async_commit();
   };
+  wait_for_previous();
   for (char* to = ring; to != ring_end; to += stage_bytes) {
-    if (!ENDS && !at.all) {      // groups past the row are never copied
-      x.clear(to, at, d);
-      if (add) r.clear(to + at_r, at, d);
+    if (!at.all) {      // groups past the row are never copied
+      x.clear(to);
+      if (add) r.clear(to + at_r);
     }
     fetch(to);
   }
@@ -95,9 +97,13 @@ __global__ void __launch_bounds__(E == 32 ? 512 : 1024) norm_vec_kernel(NormArgs
   for (int it = 0; it < at.turns; ++it, row += at.step) {
     const bool live = !SPLIT || row < T;
     wait_stage(a.stages);
-    if ((ENDS && !at.all) || !live) {
-      x.clear(from, at, live ? d : 0);
-      if (add) r.clear(from + at_r, at, live ? d : 0);
+    if (ENDS && at.parts) {
+      x.clear_parts(from, at, d);
+      if (add) r.clear_parts(from + at_r, at, d);
+    }
+    if (!live) {
+      x.clear(from);
+      if (add) r.clear(from + at_r);
     }
     float2 h[P][N];
 #pragma unroll
@@ -182,19 +188,18 @@ cudaError_t launch_vec(const NormArgs& a, const Plan& p, cudaStream_t s) {
   const auto f = p.ends ? norm_vec_kernel<X, S, Y, E, SPLIT, true> : norm_vec_kernel<X, S, Y, E, SPLIT, false>;
   const cudaError_t e = allow_smem(f, p.smem);
   if (e != cudaSuccess) return e;
-  f<<<p.grid, p.threads, p.smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_over(f, dim3(p.grid), p.threads, p.smem, s, a);
 }
 
 template <typename X, typename S, typename Y>
 cudaError_t launch_forward(NormArgs a, cudaStream_t s) {
   const Plan p = make_plan<X, S, Y>(a, sizeof(X) + (a.r ? sizeof(S) : 0), (a.w != nullptr) + (a.b != nullptr),
-                                    int64_t{1} << 30, 1024);
+                                    int64_t{1} << 30, 1024, 32);
   a.lanes = p.lanes;
   a.stages = p.stages;
   if (p.elements == 8) return launch_vec<X, S, Y, 8, true>(a, p, s);
   if (p.elements == 16) return p.split ? launch_vec<X, S, Y, 16, true>(a, p, s) : launch_vec<X, S, Y, 16, false>(a, p, s);
-  if (p.elements == 32) return launch_vec<X, S, Y, 32, false>(a, p, s);
+  if (p.elements == 32) return p.split ? launch_vec<X, S, Y, 32, true>(a, p, s) : launch_vec<X, S, Y, 32, false>(a, p, s);
   norm_any_kernel<X, S, Y><<<static_cast<unsigned>(a.T), 256, 0, s>>>(a);
   return cudaGetLastError();
 }

@@ -75,9 +75,16 @@ __device__ __forceinline__ void param_group(const float* p, int groups, int q, f
 }
 template <int G>
 __device__ __forceinline__ void stage_param(float* dst, const void* src, int32_t dtype, int groups, int phase, int d) {
-  for (int i = threadIdx.x; i < G * groups; i += blockDim.x) {
-    const int c = i - phase, q = i / G, j = i % G;
-    dst[j / 4 * 4 * groups + 4 * q + j % 4] = c >= 0 && c < d ? load_param(src, dtype, c, 0.f) : 0.f;
+  for (int q = threadIdx.x; q < groups; q += blockDim.x) {
+    float v[G];
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      const int c = G * q + j - phase;
+      v[j] = c >= 0 && c < d ? load_param(src, dtype, c, 0.f) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < G; j += 4)
+      reinterpret_cast<float4*>(dst)[j / 4 * groups + q] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
   }
 }
 template <int G, typename T>
@@ -97,7 +104,9 @@ struct Seat {
   int row, step;      // the team's first row, and from one to the next
   int turns;          // of its warp, the last of which may be past the last row for some teams (SPLIT)
   int e0[P];          // first element of each group, within the row
-  bool whole[P], all; // whether each lies in the row, and all do
+  bool whole[P];      // whether each lies in the row,
+  bool part[P];       // over one of its ends (ENDS only),
+  bool all, parts;    // whether all lie in it, and whether any lies over an end
   __device__ __forceinline__ Seat(const NormArgs& a, int first_phase) {
     lanes = a.lanes;
     team = threadIdx.x / lanes;
@@ -109,11 +118,14 @@ struct Seat {
     const int first = SPLIT ? blockIdx.x + (threadIdx.x & ~31) / lanes * gridDim.x : row, T = static_cast<int>(a.T);
     turns = first < T ? (T - first + step - 1) / step : 0;
     all = true;
+    parts = false;
 #pragma unroll
     for (int k = 0; k < P; ++k) {
       e0[k] = G * (k * lanes + lane) - phase;
       whole[k] = e0[k] >= 0 && e0[k] + G <= a.d;
+      part[k] = !whole[k] && e0[k] + G > 0 && e0[k] < a.d;
       all = all && whole[k];
+      parts = parts || part[k];
     }
   }
 };
@@ -133,13 +145,19 @@ struct Feed {
     for (int k = 0; k < P; ++k) {
       const T* src = next + k * G * s.lanes;
       if (s.whole[k]) copy_whole<G>(to + k * stride, src);
-      else if (ENDS) copy_end<G>(to + k * stride, src, s.e0[k], a.d, extent_of(base, a.T, ld, a.d, sizeof(T)));
+      else if (ENDS && s.part[k]) copy_end<G>(to + k * stride, src, s.e0[k], a.d, extent_of(base, a.T, ld, a.d, sizeof(T)));
     }
     next += step;
   }
-  __device__ __forceinline__ void clear(char* at, const Seat<G, P, SPLIT>& s, int d) {
+  // Zeros in the copied groups' places outside the row; in all places of groups that are never copied.
+  __device__ __forceinline__ void clear_parts(char* at, const Seat<G, P, SPLIT>& s, int d) {
 #pragma unroll
-    for (int k = 0; k < P; ++k) clear_end<G, T>(at + k * stride, s.e0[k], d);
+    for (int k = 0; k < P; ++k)
+      if (s.part[k]) clear_end<G, T>(at + k * stride, s.e0[k], d);
+  }
+  __device__ __forceinline__ void clear(char* at) {
+#pragma unroll
+    for (int k = 0; k < P; ++k) clear_end<G, T>(at + k * stride, 0, 0);
   }
   __device__ __forceinline__ void read(const char* at, int k, float2 (&v)[G / 2]) const {
     read_group(at + k * stride, static_cast<const T*>(nullptr), v);
@@ -156,7 +174,7 @@ struct Sink {
   __device__ __forceinline__ void store(int k, const Seat<G, P, SPLIT>& s, int d, const float2 (&v)[G / 2]) {
     T* dst = row + k * G * s.lanes;
     if (s.whole[k]) store_whole(dst, v);
-    else if (ENDS) store_end(dst, s.e0[k], d, v);
+    else if (ENDS && s.part[k]) store_end(dst, s.e0[k], d, v);
   }
 };
 
@@ -193,9 +211,10 @@ bool same_phase(const void* p, int64_t ld, int64_t rows, int G, int64_t phase, i
 }
 
 // bytes: of one element of all operands that are read; params: fp32 rows of parameters in shared memory;
-// most: CTAs at most; resident: threads of a CTA and of an SM that the kernels' registers leave room for.
+// most: CTAs at most; resident: threads of a CTA and of an SM that the kernels' registers leave room for;
+// split: elements of a lane up to which a row goes to a warp's lanes.
 template <typename X, typename S, typename Y>
-Plan make_plan(const NormArgs& a, size_t bytes, int params, int64_t most, int resident) {
+Plan make_plan(const NormArgs& a, size_t bytes, int params, int64_t most, int resident, int split) {
   Plan p;
   constexpr int G = kGroup<X, S, Y>;
   const int64_t phase = reinterpret_cast<uintptr_t>(a.x) / sizeof(X) % G, shift = a.T > 1 ? a.ldx % G : 0;
@@ -205,14 +224,15 @@ Plan make_plan(const NormArgs& a, size_t bytes, int params, int64_t most, int re
   const int groups = static_cast<int>((a.d + (shift ? G - 1 : phase) + G - 1) / G);   // of any row
   const int64_t sms = device_sm_count();
   auto lanes_of = [&](int elements) { return (groups + elements / G - 1) / (elements / G); };
-  p.split = lanes_of(16) <= 32;
+  p.split = lanes_of(split) <= 32;
   p.ends = phase || shift || a.d % G;
   int E, teams;
   if (p.split) {
-    E = lanes_of(8) <= 32 ? 8 : 16;
+    E = lanes_of(8) <= 32 ? 8 : lanes_of(16) <= 32 ? 16 : 32;
     p.lanes = 32;
     while (p.lanes / 2 >= lanes_of(E)) p.lanes /= 2;
     teams = 256 / p.lanes;
+    if (E == 32) resident = 512;
   } else {
     E = lanes_of(16) <= kMaxLanes ? 16 : 32;
     p.lanes = (lanes_of(E) + 31) / 32 * 32;
@@ -239,6 +259,22 @@ Plan make_plan(const NormArgs& a, size_t bytes, int params, int64_t most, int re
   if (shift) ctas = std::max<int64_t>(8, ctas / 8 * 8);
   p.grid = static_cast<unsigned>(ctas);
   return p;
+}
+
+// A launch that may begin under the one before it: its kernel waits before it looks at any operand.
+template <typename A>
+cudaError_t launch_over(void (*f)(A), dim3 grid, int threads, size_t smem, cudaStream_t s, const A& a) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(static_cast<unsigned>(threads));
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, f, a);
 }
 
 // The limit of a kernel's shared memory, raised where the plan needs more than every kernel has (48 KB, the

@@ -59,28 +59,26 @@ __global__ void __launch_bounds__(256) norm_columns_any_kernel(NormArgs a) {
   }
 }
 
-// The slots' partial sums of dw (blockIdx.y 0) and db (1), in order: each of 8 groups takes a run
-// of slots for 32 columns.
-__global__ void __launch_bounds__(256) norm_join_kernel(NormArgs a) {
-  __shared__ float part[8][32];
+// The slots' partial sums of dw (blockIdx.y 0) and db (1), in order: each of 32 warps takes a run of
+// slots for 32 columns.
+__global__ void __launch_bounds__(1024) norm_join_kernel(NormArgs a) {
+  __shared__ float part[32][33];
   float* out = blockIdx.y == 0 ? a.dw : a.db;
+  wait_for_previous();
   if (!out) return;
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
+  const int per = (a.slots + 31) / 32, s0 = g * per, s1 = min(a.slots, s0 + per);
   float v = 0.f;
   if (c < a.d) {
-    const int per = (a.slots + 7) / 8;
-    const int s1 = min(a.slots, (g + 1) * per);
-    for (int s = g * per; s < s1; ++s) v += a.partial[(static_cast<int64_t>(s) * 2 + blockIdx.y) * a.d + c];
+    const float* p = a.partial + (static_cast<int64_t>(s0) * 2 + blockIdx.y) * a.d + c;
+#pragma unroll 5
+    for (int s = s0; s < s1; ++s, p += 2 * static_cast<int64_t>(a.d)) v += *p;
   }
   part[g][lane] = v;
   __syncthreads();
-  if (g == 0 && c < a.d) {
-    float t = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t += part[i][lane];
-    out[c] = t;
-  }
+  v = warp_sum(part[lane][g]);
+  if (lane == 0 && blockIdx.x * 32 + g < a.d) out[blockIdx.x * 32 + g] = v;
 }
 
 // The backward pass in one reading of the rows; the columns' sums stay in registers over the CTA's rows
@@ -93,6 +91,7 @@ __global__ void __launch_bounds__(RMS && E <= 16 ? 640 : 512) norm_grad_kernel(N
   constexpr int G = kGroup<H, S, DY>, P = E / G, N = G / 2;
   extern __shared__ float4 smem[];
   __shared__ float part[SPLIT ? 1 : kMaxTeams * 2 * 32];
+  launch_dependents();
   const Seat<G, P, SPLIT> at(a, phase_of<G>(static_cast<const H*>(a.x) + blockIdx.x * a.ldx));
   const int d = a.d;
   const bool add = a.r && a.s;
@@ -119,11 +118,12 @@ __global__ void __launch_bounds__(RMS && E <= 16 ? 640 : 512) norm_grad_kernel(N
     ahead += at.step;
     cp_async_commit();
   };
+  wait_for_previous();
   for (char* to = ring; to != ring_end; to += stage_bytes) {
-    if (!ENDS && !at.all) {      // groups past the row are never copied
-      fh.clear(to, at, d);
-      fy.clear(to + at_y, at, d);
-      if (add) fs.clear(to + at_s, at, d);
+    if (!at.all) {      // groups past the row are never copied
+      fh.clear(to);
+      fy.clear(to + at_y);
+      if (add) fs.clear(to + at_s);
     }
     fetch(to);
   }
@@ -151,9 +151,13 @@ __global__ void __launch_bounds__(RMS && E <= 16 ? 640 : 512) norm_grad_kernel(N
       if (!RMS && !a.rms) next_mean = a.mean[row + at.step];
     }
     wait_stage(a.stages);
-    if ((ENDS && !at.all) || !live) {     // with dy = 0 outside the row nothing there counts
-      fh.clear(from, at, live ? d : 0);
-      fy.clear(from + at_y, at, live ? d : 0);
+    if (ENDS && at.parts) {     // with dy = 0 outside the row nothing there counts
+      fh.clear_parts(from, at, d);
+      fy.clear_parts(from + at_y, at, d);
+    }
+    if (!live) {
+      fh.clear(from);
+      fy.clear(from + at_y);
     }
     // c and dy of group k
     auto values = [&](int k, float2 (&c)[N], float2 (&dy)[N]) {
@@ -228,35 +232,38 @@ __global__ void __launch_bounds__(RMS && E <= 16 ? 640 : 512) norm_grad_kernel(N
   }
   if (!a.dw && !a.db) return;
   float* out = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * d;
-  // the teams in order; of a warp's own rows (SPLIT) first its lanes
+  // every team's sums (SPLIT: every warp's, its rows by its lanes first) to where the ring was, added in order
   const int mine = SPLIT ? threadIdx.x >> 5 : at.team, seats = SPLIT ? blockDim.x >> 5 : blockDim.x / at.lanes;
-  float* join = w;
+  const int width = G * at.groups;
+  float* join = w + width;
   for (int half = 0; half < (B ? 2 : 1); ++half) {
+    if (SPLIT)
 #pragma unroll
-    for (int k = 0; k < P; ++k)
+      for (int k = 0; k < P; ++k)
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        if (half) acc_w[k][j] = acc_b[k][j];
-        if (SPLIT)
+        for (int j = 0; j < N; ++j) {
+          float2& v = half ? acc_b[k][j] : acc_w[k][j];
           for (int o = at.lanes; o < 32; o <<= 1) {
-            acc_w[k][j].x += __shfl_xor_sync(0xffffffffu, acc_w[k][j].x, o);
-            acc_w[k][j].y += __shfl_xor_sync(0xffffffffu, acc_w[k][j].y, o);
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
           }
-      }
-    for (int i = 0; i < seats; ++i) {
-      __syncthreads();
-      if (mine == i && (!SPLIT || (threadIdx.x & 31) < at.lanes))
-#pragma unroll
-        for (int k = 0; k < P; ++k)
-#pragma unroll
-          for (int j = 0; j < G; ++j) {
-            const int c = at.e0[k] + j;
-            const float z = j & 1 ? acc_w[k][j / 2].y : acc_w[k][j / 2].x;
-            if (c >= 0 && c < d) join[c] = i == 0 ? z : join[c] + z;
-          }
-    }
+        }
     __syncthreads();
-    for (int c = threadIdx.x; c < d; c += blockDim.x) out[half * d + c] = join[c];
+    if (!SPLIT || (threadIdx.x & 31) < at.lanes)
+#pragma unroll
+      for (int k = 0; k < P; ++k)
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+          const float2 lo = half ? acc_b[k][j] : acc_w[k][j], hi = half ? acc_b[k][j + 1] : acc_w[k][j + 1];
+          *reinterpret_cast<float4*>(join + mine * width + G * (k * at.lanes + at.lane) + 2 * j) =
+              make_float4(lo.x, lo.y, hi.x, hi.y);
+        }
+    __syncthreads();
+    for (int c = threadIdx.x; c < d; c += blockDim.x) {
+      float v = join[c + at.phase];
+      for (int i = 1; i < seats; ++i) v += join[i * width + c + at.phase];
+      out[half * d + c] = v;
+    }
   }
 }
 
@@ -269,8 +276,7 @@ cudaError_t launch_grad_b(const NormArgs& a, const Plan& p, cudaStream_t s) {
                          : norm_grad_kernel<X, S, Y, E, SPLIT, ENDS, false, false>;
   const cudaError_t e = allow_smem(f, p.smem);
   if (e != cudaSuccess) return e;
-  f<<<p.grid, p.threads, p.smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_over(f, dim3(p.grid), p.threads, p.smem, s, a);
 }
 template <typename X, typename S, typename Y, int E, bool SPLIT>
 cudaError_t launch_grad(const NormArgs& a, const Plan& p, cudaStream_t s) {
@@ -280,23 +286,23 @@ cudaError_t launch_grad(const NormArgs& a, const Plan& p, cudaStream_t s) {
 template <typename X, typename S, typename Y>
 cudaError_t launch_backward(NormArgs a, cudaStream_t s) {
   const unsigned cols = static_cast<unsigned>((a.d + 31) / 32);
-  const Plan p = make_plan<X, S, Y>(a, sizeof(X) + sizeof(Y) + (a.r && a.s ? sizeof(S) : 0), 1, a.slots, a.rms && !a.db ? 640 : 512);
+  const Plan p = make_plan<X, S, Y>(a, sizeof(X) + sizeof(Y) + (a.r && a.s ? sizeof(S) : 0), 1, a.slots, a.rms && !a.db ? 640 : 512, 16);
   a.lanes = p.lanes;
   a.stages = p.stages;
-  cudaError_t e = cudaSuccess;
   if (p.elements) {
+    cudaError_t e;
     if (p.elements == 8) e = launch_grad<X, S, Y, 8, true>(a, p, s);
     else if (p.elements == 16) e = p.split ? launch_grad<X, S, Y, 16, true>(a, p, s) : launch_grad<X, S, Y, 16, false>(a, p, s);
     else e = launch_grad<X, S, Y, 32, false>(a, p, s);
     if (e != cudaSuccess) return e;
     a.slots = static_cast<int32_t>(p.grid);
-    if (a.dw || a.db) norm_join_kernel<<<dim3(cols, 2), 256, 0, s>>>(a);
-    return cudaGetLastError();
+    return a.dw || a.db ? launch_over(norm_join_kernel, dim3(cols, 2), 1024, 0, s, a) : cudaSuccess;
   }
   // the column sums first: dx may overwrite h or dy
   if (a.dw || a.db) {
     norm_columns_any_kernel<X, Y><<<dim3(cols, static_cast<unsigned>(a.slots)), 256, 0, s>>>(a);
-    norm_join_kernel<<<dim3(cols, 2), 256, 0, s>>>(a);
+    const cudaError_t e = launch_over(norm_join_kernel, dim3(cols, 2), 1024, 0, s, a);
+    if (e != cudaSuccess) return e;
   }
   if (a.s) norm_dx_any_kernel<X, Y, S><<<static_cast<unsigned>(a.T), 256, 0, s>>>(a);
   return cudaGetLastError();

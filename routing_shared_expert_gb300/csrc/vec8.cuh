@@ -60,7 +60,6 @@ __device__ __forceinline__ void copy_whole(char* dst, const T* src) {
 // element only at the tensor's own ends.
 template <int G, typename T>
 __device__ __noinline__ void copy_end(char* dst, const T* src, int e0, int d, Extent t) {
-  if (e0 + G <= 0 || e0 >= d) return;
   const uintptr_t a = reinterpret_cast<uintptr_t>(src);
   if (a >= t.lo && a + G * sizeof(T) <= t.hi) {
     copy_whole<G>(dst, src);

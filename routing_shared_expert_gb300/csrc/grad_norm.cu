@@ -7,6 +7,8 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "launch.h"
+#include "vec8.cuh"
 
 namespace moe {
 namespace {
@@ -17,19 +19,26 @@ struct Entry {
   int64_t rows, cols, ldi, ldo;
   int64_t first;          // number of the tensor's first chunk
   int32_t dtype;
+  int16_t lead;           // elements between a 32-byte (fp32) or 16-byte (bf16) boundary and the first one
+  int16_t vec;            // kReads: gradients in groups of eight elements; kWrites: results too
 };
+constexpr int16_t kReads = 1, kWrites = 2;
 
-constexpr int kEntries = 56;          // tensors of one launch: the table is its argument (< 4 KB)
-constexpr int kThreads = 256;
-constexpr int64_t kChunk = 8192;      // elements
-constexpr int kSlots = 152 * 8;       // CTAs, at most: one partial sum each
+// Tensors of one launch: the table is its argument.  56 of them fit into 4 KB; longer lists take a
+// table of up to 32 KB.
+constexpr int kShortTable = 56, kLongTable = 500;
+constexpr int kThreads = 256, kGroups = 4;
+constexpr int64_t kChunk = kThreads * kGroups * 8;      // elements
+constexpr int kPerSm = 4;
+constexpr int kSlots = 152 * kPerSm;  // CTAs, at most: one partial sum each
 constexpr size_t kTicketOffset = 64, kPartialOffset = 256;
 constexpr size_t kWorkspace = kPartialOffset + kSlots * sizeof(double);
 
+template <int N>
 struct Table {
-  Entry e[kEntries];
-  int32_t n;
   int64_t chunks;
+  int32_t n;
+  Entry e[N];
 };
 
 struct NormSums {
@@ -41,18 +50,50 @@ struct NormSums {
   int32_t last;           // slots to join after this launch; 0: another launch follows
 };
 
-__device__ __forceinline__ const Entry& entry_of(const Table& t, int64_t chunk) {
-  int lo = 0, hi = t.n;   // the last tensor whose first chunk is not after this one
+__device__ __forceinline__ float load_elem(const void* p, int32_t dtype, int64_t i) {
+  return dtype == MOE_F32 ? static_cast<const float*>(p)[i] : to_f32(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+__device__ __forceinline__ void store_elem(void* p, int32_t dtype, int64_t i, float v) {
+  if (dtype == MOE_F32) static_cast<float*>(p)[i] = v;
+  else static_cast<__nv_bfloat16*>(p)[i] = from_f32<__nv_bfloat16>(v);
+}
+
+// The tensor that a chunk belongs to: the last one whose first chunk is not after it.
+template <int N>
+__device__ __forceinline__ int entry_of(const Table<N>& t, int64_t chunk) {
+  int lo = 0, hi = t.n;
   while (hi - lo > 1) {
     const int m = (lo + hi) / 2;
     if (t.e[m].first <= chunk) lo = m;
     else hi = m;
   }
-  return t.e[lo];
+  return lo;
 }
 
-__device__ __forceinline__ float load_elem(const void* p, int32_t dtype, int64_t i) {
-  return dtype == MOE_F32 ? static_cast<const float*>(p)[i] : to_f32(static_cast<const __nv_bfloat16*>(p)[i]);
+// Eight values as they lie in memory: 32 bytes of fp32, 16 of bf16.
+struct Words {
+  uint32_t w[8];
+};
+__device__ __forceinline__ Words load_words(const float* p) {
+  Words r;
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]),
+                 "=r"(r.w[7])
+               : "l"(p)
+               : "memory");
+  return r;
+}
+__device__ __forceinline__ Words load_words(const __nv_bfloat16* p) {
+  Words r;
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
+               : "l"(p)
+               : "memory");
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ float2 pair(const Words& r, int i) {
+  return sizeof(T) == 4 ? make_float2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1])) : unpack2(r.w[i]);
 }
 
 __device__ __forceinline__ double block_sum_f64(double v, double* part) {
@@ -65,20 +106,69 @@ __device__ __forceinline__ double block_sum_f64(double v, double* part) {
   return v;
 }
 
-__global__ void __launch_bounds__(kThreads) grad_square_kernel(const __grid_constant__ Table t, NormSums s) {
-  __shared__ double part[2][kThreads / 32];
-  __shared__ bool join;
-  float acc = 0.f;
-  for (int64_t chunk = blockIdx.x; chunk < t.chunks; chunk += gridDim.x) {
-    const Entry& e = entry_of(t, chunk);
-    const int64_t n = e.rows * e.cols, i0 = (chunk - e.first) * kChunk, i1 = min(n, i0 + kChunk);
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) {
-      const int64_t row = e.rows == 1 ? 0 : i / e.cols;
-      const float v = load_elem(e.in, e.dtype, row * e.ldi + (i - row * e.cols));
-      acc += v * v;
+// The groups of a chunk: group q of the tensor is its elements 8 q - lead .. 8 q - lead + 7.  f(words, address
+// of the result) takes whole groups, g(i) the elements of groups over the tensor's ends.  Of a dense chunk
+// inside its tensor each thread loads all its groups before any is used.
+template <typename T, typename F, typename G>
+__device__ __forceinline__ void walk_chunk(const Entry& e, int64_t chunk, const F& f, const G& g) {
+  const int64_t n = e.rows * e.cols, i0 = (chunk - e.first) * kChunk - e.lead;
+  const T* in = static_cast<const T*>(e.in);
+  const int mine = 8 * threadIdx.x;
+  if (e.rows == 1 && i0 >= 0 && i0 + kChunk <= n) {
+    Words w[kGroups];
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) w[k] = load_words(in + i0 + mine + 8 * k * kThreads);
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) f(w[k], i0 + mine + 8 * k * kThreads);
+    return;
+  }
+#pragma unroll 1
+  for (int k = 0; k < kGroups; ++k) {
+    const int64_t i = i0 + mine + 8 * k * kThreads;
+    if (i >= 0 && i + 8 <= n) {
+      const int64_t row = e.rows == 1 ? 0 : i / e.cols, col = i - row * e.cols;
+      f(load_words(in + row * e.ldi + col), row * e.ldo + col);
+    } else {
+      for (int64_t j = max(i, int64_t{0}); j < min(i + 8, n); ++j) g(j);
     }
   }
-  const double sum = block_sum_f64(acc, part[0]);
+}
+
+// One reading of every gradient: 32 bytes per lane and load, four loads on their way.
+// Bound by HBM.
+template <int N>
+__global__ void __launch_bounds__(kThreads, kPerSm) grad_square_kernel(const __grid_constant__ Table<N> t, NormSums s) {
+  __shared__ double part[2][kThreads / 32];
+  __shared__ bool join;
+  launch_dependents();
+  float2 acc[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
+  int at = entry_of(t, blockIdx.x);
+  wait_for_previous();
+  for (int64_t chunk = blockIdx.x; chunk < t.chunks; chunk += gridDim.x) {
+    while (at + 1 < t.n && t.e[at + 1].first <= chunk) ++at;
+    const Entry& e = t.e[at];
+    auto one = [&](int64_t i) {
+      const int64_t row = e.rows == 1 ? 0 : i / e.cols;
+      const float v = load_elem(e.in, e.dtype, row * e.ldi + (i - row * e.cols));
+      acc[0].x += v * v;
+    };
+    if (!(e.vec & kReads)) {
+      const int64_t i0 = (chunk - e.first) * kChunk, i1 = min(e.rows * e.cols, i0 + kChunk);
+      for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) one(i);
+    } else if (e.dtype == MOE_F32) {
+      walk_chunk<float>(e, chunk, [&](const Words& w, int64_t) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = fma2(pair<float>(w, j), pair<float>(w, j), acc[j]);
+      }, one);
+    } else {
+      walk_chunk<__nv_bfloat16>(e, chunk, [&](const Words& w, int64_t) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = fma2(pair<__nv_bfloat16>(w, j), pair<__nv_bfloat16>(w, j), acc[j]);
+      }, one);
+    }
+  }
+  const float2 lo = add2(acc[0], acc[1]), hi = add2(acc[2], acc[3]), all = add2(lo, hi);
+  const double sum = block_sum_f64(static_cast<double>(all.x) + static_cast<double>(all.y), part[0]);
   if (threadIdx.x == 0) {
     s.partial[blockIdx.x] = sum + (blockIdx.x < s.used ? s.partial[blockIdx.x] : 0.0);
     __threadfence();
@@ -101,17 +191,47 @@ __global__ void __launch_bounds__(kThreads) grad_square_kernel(const __grid_cons
   }
 }
 
-__global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ Table t, const float* norm) {
+__device__ __forceinline__ void store_scaled(float* p, const Words& w, float c) {
+  float2 v[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = mul2(pair<float>(w, j), both(c));
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0].x), "f"(v[0].y),
+               "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y)
+               : "memory");
+}
+__device__ __forceinline__ void store_scaled(__nv_bfloat16* p, const Words& w, float c) {
+  float2 v[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = mul2(pair<__nv_bfloat16>(w, j), both(c));
+  store_whole(p, v);
+}
+
+// The chunks last to first: what the norm's reading left in L2 is read again before it is replaced.
+template <int N>
+__global__ void __launch_bounds__(kThreads, kPerSm) grad_scale_kernel(const __grid_constant__ Table<N> t, const float* norm) {
+  launch_dependents();
+  int at = entry_of(t, t.chunks - 1 - blockIdx.x);
+  wait_for_previous();
   const float coef = norm[1];
-  for (int64_t chunk = blockIdx.x; chunk < t.chunks; chunk += gridDim.x) {
-    const Entry& e = entry_of(t, chunk);
+  for (int64_t k = blockIdx.x; k < t.chunks; k += gridDim.x) {
+    const int64_t chunk = t.chunks - 1 - k;
+    while (at > 0 && t.e[at].first > chunk) --at;
+    const Entry& e = t.e[at];
     if (coef == 1.f && e.in == e.out) continue;
-    const int64_t n = e.rows * e.cols, i0 = (chunk - e.first) * kChunk, i1 = min(n, i0 + kChunk);
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) {
+    auto one = [&](int64_t i) {
       const int64_t row = e.rows == 1 ? 0 : i / e.cols, col = i - row * e.cols;
-      const float v = coef * load_elem(e.in, e.dtype, row * e.ldi + col);
-      if (e.dtype == MOE_F32) static_cast<float*>(e.out)[row * e.ldo + col] = v;
-      else static_cast<__nv_bfloat16*>(e.out)[row * e.ldo + col] = from_f32<__nv_bfloat16>(v);
+      store_elem(e.out, e.dtype, row * e.ldo + col, coef * load_elem(e.in, e.dtype, row * e.ldi + col));
+    };
+    if (!(e.vec & kWrites)) {
+      const int64_t base = e.vec & kReads ? e.lead : 0;      // the norm's chunks, which may begin before the tensor
+      const int64_t i0 = (chunk - e.first) * kChunk - base, i1 = min(e.rows * e.cols, i0 + kChunk);
+      for (int64_t i = max(i0, int64_t{0}) + threadIdx.x; i < i1; i += kThreads) one(i);
+    } else if (e.dtype == MOE_F32) {
+      walk_chunk<float>(e, chunk, [&](const Words& w, int64_t i) { store_scaled(static_cast<float*>(e.out) + i, w, coef); },
+                        one);
+    } else {
+      walk_chunk<__nv_bfloat16>(
+          e, chunk, [&](const Words& w, int64_t i) { store_scaled(static_cast<__nv_bfloat16*>(e.out) + i, w, coef); }, one);
     }
   }
 }
@@ -120,14 +240,14 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
 
 constexpr int64_t kMaxElements = int64_t{1} << 40;
 
-struct Extent {
+struct Reach {
   uintptr_t lo, hi;       // bytes spanned
   uint64_t pitch, width;  // bytes between rows (0: one row) and of a row
   int32_t tensor;
   bool written;
 };
 
-bool share_memory(const Extent& a, const Extent& b) {
+bool share_memory(const Reach& a, const Reach& b) {
   if (a.lo >= b.hi || b.lo >= a.hi) return false;
   if (a.pitch == 0 || a.pitch != b.pitch) return true;
   // columns of rows of one matrix: apart when they are apart within a row
@@ -162,7 +282,7 @@ moe_status check_tensor(const moe_tensor& t, Entry& e, bool out) {
   return MOE_OK;
 }
 
-Extent extent_of(const void* p, const Entry& e, int64_t ld, int32_t i, bool written) {
+Reach reach_of(const void* p, const Entry& e, int64_t ld, int32_t i, bool written) {
   const uint64_t b = size_of(e.dtype);
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
   return {lo, lo + ((e.rows - 1) * ld + e.cols) * b, e.rows > 1 ? ld * b : 0, e.cols * b, i, written};
@@ -170,17 +290,17 @@ Extent extent_of(const void* p, const Entry& e, int64_t ld, int32_t i, bool writ
 
 // Whether tensors that are written share memory with each other or with one that is read.
 bool overlap(const std::vector<Entry>& list) {
-  std::vector<Extent> x, open;
+  std::vector<Reach> x, open;
   for (size_t i = 0; i < list.size(); ++i) {
     const Entry& e = list[i];
     const bool same = e.in == e.out && e.ldi == e.ldo;
-    x.push_back(extent_of(e.out, e, e.ldo, static_cast<int32_t>(i), true));
-    if (!same) x.push_back(extent_of(e.in, e, e.ldi, static_cast<int32_t>(i), false));
+    x.push_back(reach_of(e.out, e, e.ldo, static_cast<int32_t>(i), true));
+    if (!same) x.push_back(reach_of(e.in, e, e.ldi, static_cast<int32_t>(i), false));
   }
-  std::sort(x.begin(), x.end(), [](const Extent& a, const Extent& b) { return a.lo < b.lo; });
-  for (const Extent& e : x) {
+  std::sort(x.begin(), x.end(), [](const Reach& a, const Reach& b) { return a.lo < b.lo; });
+  for (const Reach& e : x) {
     size_t k = 0;
-    for (const Extent& o : open) {
+    for (const Reach& o : open) {
       if (o.hi <= e.lo) continue;
       if ((o.written || e.written) && share_memory(o, e)) return true;
       open[k++] = o;
@@ -189,6 +309,40 @@ bool overlap(const std::vector<Entry>& list) {
     open.push_back(e);
   }
   return false;
+}
+
+template <int N>
+cudaError_t launch_lists(const std::vector<Entry>& list, NormSums sums, bool clip, cudaStream_t s) {
+  const size_t n = list.size();
+  Table<N> t;
+  auto fill = [&](size_t at) {
+    t.n = static_cast<int32_t>(std::min<size_t>(N, n - at));
+    t.chunks = 0;
+    for (int32_t i = 0; i < t.n; ++i) {
+      t.e[i] = list[at + i];
+      t.e[i].first = t.chunks;
+      t.chunks += (t.e[i].lead + t.e[i].rows * t.e[i].cols + kChunk - 1) / kChunk;
+    }
+    return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>({t.chunks, kSlots, int64_t{kPerSm} * device_sm_count()})));
+  };
+  size_t at = 0;
+  do {   // a list without elements has one launch too, for the norm of nothing
+    const unsigned grid = fill(at);
+    at += t.n;
+    const int32_t slots = std::max(sums.used, static_cast<int32_t>(grid));
+    if (at >= n) sums.last = slots;
+    const cudaError_t e = launch_over(grad_square_kernel<N>, dim3(grid), kThreads, 0, s, t, sums);
+    if (e != cudaSuccess) return e;
+    sums.used = slots;
+  } while (at < n);
+  if (!clip) return cudaSuccess;
+  // the tables last to first, as the chunks
+  for (size_t tables = (n + N - 1) / N; tables > 0; --tables) {
+    const unsigned grid = fill((tables - 1) * N);
+    const cudaError_t e = launch_over(grad_scale_kernel<N>, dim3(grid), kThreads, 0, s, t, static_cast<const float*>(sums.norm));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 moe_status run_norm(const moe_tensor* grads, const moe_tensor* out, int32_t count, double max_norm, float* norm,
@@ -216,6 +370,15 @@ moe_status run_norm(const moe_tensor* grads, const moe_tensor* out, int32_t coun
       e.rows = 1;
       e.ldi = e.ldo = e.cols;
     }
+    // in groups: dense from any element on, or rows that begin and end on groups
+    const int64_t align = e.dtype == MOE_F32 ? 32 : 16, b = static_cast<int64_t>(size_of(e.dtype));
+    const int64_t lead = static_cast<int64_t>(reinterpret_cast<uintptr_t>(e.in) % align) / b;
+    if (e.rows == 1 || (lead == 0 && e.cols % 8 == 0 && e.ldi % 8 == 0)) {
+      e.lead = static_cast<int16_t>(lead);
+      e.vec = kReads;
+      if (static_cast<int64_t>(reinterpret_cast<uintptr_t>(e.out) % align) / b == lead && (e.rows == 1 || e.ldo % 8 == 0))
+        e.vec |= kWrites;
+    }
     list.push_back(e);
   }
   if (reinterpret_cast<uintptr_t>(norm) & 3u || reinterpret_cast<uintptr_t>(workspace) & 255u)
@@ -228,33 +391,9 @@ moe_status run_norm(const moe_tensor* grads, const moe_tensor* out, int32_t coun
   sums.ticket = reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + kTicketOffset);
   sums.norm = norm;
   sums.max_norm = max_norm;
-  const size_t n = list.size();
-  auto fill = [&](size_t at, Table& t) {
-    t.n = static_cast<int32_t>(std::min<size_t>(kEntries, n - at));
-    t.chunks = 0;
-    for (int32_t i = 0; i < t.n; ++i) {
-      t.e[i] = list[at + i];
-      t.e[i].first = t.chunks;
-      t.chunks += (t.e[i].rows * t.e[i].cols + kChunk - 1) / kChunk;
-    }
-    return static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(t.chunks, kSlots)));
-  };
-  size_t at = 0;
-  do {   // a list without elements has one launch too, for the norm of nothing
-    Table t{};
-    const int32_t grid = fill(at, t);
-    at += t.n;
-    if (at >= n) sums.last = std::max(sums.used, grid);
-    grad_square_kernel<<<grid, kThreads, 0, s>>>(t, sums);
-    sums.used = std::max(sums.used, grid);
-  } while (at < n);
-  if (clip)
-    for (at = 0; at < n; at += kEntries) {
-      Table t{};
-      const int32_t grid = fill(at, t);
-      grad_scale_kernel<<<grid, kThreads, 0, s>>>(t, norm);
-    }
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  const cudaError_t e = list.size() <= kShortTable ? launch_lists<kShortTable>(list, sums, clip, s)
+                                                   : launch_lists<kLongTable>(list, sums, clip, s);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status guarded(const moe_tensor* grads, const moe_tensor* out, int32_t count, double max_norm, float* norm,

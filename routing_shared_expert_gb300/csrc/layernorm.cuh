@@ -11,6 +11,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "launch.h"
 #include "row_reduce.cuh"
 #include "vec8.cuh"
 
@@ -259,22 +260,6 @@ Plan make_plan(const NormArgs& a, size_t bytes, int params, int64_t most, int re
   if (shift) ctas = std::max<int64_t>(8, ctas / 8 * 8);
   p.grid = static_cast<unsigned>(ctas);
   return p;
-}
-
-// A launch that may begin under the one before it: its kernel waits before it looks at any operand.
-template <typename A>
-cudaError_t launch_over(void (*f)(A), dim3 grid, int threads, size_t smem, cudaStream_t s, const A& a) {
-  cudaLaunchConfig_t c{};
-  c.gridDim = grid;
-  c.blockDim = dim3(static_cast<unsigned>(threads));
-  c.dynamicSmemBytes = smem;
-  c.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = attr;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, f, a);
 }
 
 // The limit of a kernel's shared memory, raised where the plan needs more than every kernel has (48 KB, the

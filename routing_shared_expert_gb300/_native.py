@@ -8,6 +8,7 @@ this module fails.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from ctypes import POINTER, c_char_p, c_double, c_float, c_int32, c_int64, c_size_t, c_void_p
@@ -817,26 +818,47 @@ def alloc_grad_norm_workspace(device="cuda", stream=None):
     return ws
 
 
-def _tensor_list(name, tensors, dev):
+def _rows_words(name, t):
+    """(rows, cols, row stride) of a tensor that is not contiguous."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1) or t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: contiguous tensors, or matrices of contiguous rows with memory of their own, are "
+                         f"expected, got strides {t.stride()} of {tuple(t.shape)}")
+    return t.shape[0], t.shape[1], t.stride(0)
+
+
+def _tensor_list(tensors, dev):
     """The tensors as an array of moe_tensor, five 64-bit words each."""
-    words = []
+    words, kind = [], _TORCH_DTYPES.get
     for t in tensors:
-        dtype = _TORCH_DTYPES.get(t.dtype)
+        dtype = kind(t.dtype)
         if dtype is None or t.get_device() != dev:
-            raise ValueError(f"{name}: fp32 or bf16 tensors on device {dev} are expected, got {t.dtype} on {t.device}")
-        if t.dim() == 2 and t.shape[0] > 1 and t.shape[1] > 0:
-            rows, cols = t.shape
-            s0, s1 = t.stride()
-            if (s1 != 1 and cols > 1) or s0 < cols:
-                raise ValueError(f"{name}: contiguous rows with memory of their own are expected, got strides "
-                                 f"{t.stride()} of {tuple(t.shape)}")
-            words += (t.data_ptr(), rows, cols, s0, dtype)
-        elif t.is_contiguous():
+            raise ValueError(f"grads: fp32 or bf16 tensors on device {dev} are expected, got {t.dtype} on {t.device}")
+        if t.is_contiguous():
             words += (t.data_ptr(), 1, t.numel(), 0, dtype)
         else:
-            raise ValueError(f"{name}: contiguous tensors, or matrices of contiguous rows, are expected, got "
-                             f"strides {t.stride()} of {tuple(t.shape)}")
-    return (c_int64 * len(words))(*words)
+            words += (t.data_ptr(), *_rows_words("grads", t), dtype)
+    return array.array("q", words)
+
+
+def _tensor_lists(tensors, outs, dev):
+    """The same for two lists of equal shapes and types."""
+    words, more, kind = [], [], _TORCH_DTYPES.get
+    for t, o in zip(tensors, outs):
+        torch_dtype = t.dtype
+        dtype = kind(torch_dtype)
+        if dtype is None or t.get_device() != dev:
+            raise ValueError(f"grads: fp32 or bf16 tensors on device {dev} are expected, got {t.dtype} on {t.device}")
+        if o.dtype is not torch_dtype or o.get_device() != dev or o.shape != t.shape:
+            raise ValueError(f"out: {tuple(t.shape)} of {t.dtype} on device {dev} is expected, got {tuple(o.shape)} "
+                             f"of {o.dtype} on {o.device}")
+        if t.is_contiguous() and o.is_contiguous():
+            n = t.numel()
+            words += (t.data_ptr(), 1, n, 0, dtype)
+            more += (o.data_ptr(), 1, n, 0, dtype)
+        else:       # both by their rows
+            words += (t.data_ptr(), *_rows_words("grads", t), dtype)
+            more += (o.data_ptr(), *_rows_words("out", o), dtype)
+    return array.array("q", words), array.array("q", more)
 
 
 def _norm_operands(norm, workspace):
@@ -849,7 +871,8 @@ def moe_grad_norm(grads, norm, workspace, max_norm=float("inf"), stream=None):
     """norm (fp32 [2]) = the 2-norm over all elements of the tensors of ``grads``, and
     min(1, max_norm / (norm + 1e-6)), the factor that clips it to ``max_norm``."""
     dev, pn, pw, nw = _norm_operands(norm, workspace)
-    _check("moe_grad_norm", _lib.moe_grad_norm(_tensor_list("grads", grads, dev), len(grads), max_norm, pn, pw, nw,
+    g = _tensor_list(grads, dev)
+    _check("moe_grad_norm", _lib.moe_grad_norm(g.buffer_info()[0], len(grads), max_norm, pn, pw, nw,
                                                _raw_stream(stream, dev)))
 
 
@@ -857,10 +880,9 @@ def moe_clip_grad_norm(grads, max_norm, out, norm, workspace, stream=None):
     """moe_grad_norm, then every gradient times norm[1]: into the tensors of ``out``, or in place where it is
     None."""
     dev, pn, pw, nw = _norm_operands(norm, workspace)
-    po = None
-    if out is not None:
-        if [(t.shape, t.dtype) for t in out] != [(t.shape, t.dtype) for t in grads]:
-            raise ValueError("out: the shapes and types of grads are expected")
-        po = _tensor_list("out", out, dev)
-    _check("moe_clip_grad_norm", _lib.moe_clip_grad_norm(_tensor_list("grads", grads, dev), po, len(grads), max_norm,
-                                                         pn, pw, nw, _raw_stream(stream, dev)))
+    if out is not None and len(out) != len(grads):
+        raise ValueError(f"out: {len(grads)} tensors are expected, got {len(out)}")
+    g, o = (_tensor_list(grads, dev), None) if out is None else _tensor_lists(grads, out, dev)
+    _check("moe_clip_grad_norm", _lib.moe_clip_grad_norm(
+        g.buffer_info()[0], None if o is None else o.buffer_info()[0], len(grads), max_norm, pn, pw, nw,
+        _raw_stream(stream, dev)))

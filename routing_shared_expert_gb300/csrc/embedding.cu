@@ -1,130 +1,94 @@
-// Token embedding: out_t = scale table[id_t], and the gradient of the table by tokens,
-// dtable_v = scale sum_{t: id_t = v} dout_t, summed in fp32 in a fixed order.
-#include <cmath>
-
-#include "common.cuh"
-#include "internal.h"
+// Token embedding: the lookup, and the checks and entry points of both passes.
+//
+//   out_t = scale table[id_t],   dtable_v = scale sum_{t: id_t = v} dout_t
+#include "embedding.cuh"
 
 namespace moe {
 namespace {
 
-struct EmbedArgs {
-  const void* ids;
-  const void* src;       // table, or dout
-  void* dst;             // out, or dtable
-  int64_t T, V, ldt, ldo;
-  int32_t d, accumulate;
-  float scale;
-  int32_t* status;
-};
+// A warp per token and slice of kSlice columns, its four loads of eight values per lane on their way at
+// once.  Bound by HBM where rows are long: the rows of frequent tokens come from L2.  ALIGNED: rows of the table
+// and of out begin on groups of eight and end on one; else the groups are those of out, and the
+// table's values are moved into place.
+constexpr int kSlice = 1024;
 
-// The token's row, -1 for none; a number outside the table is reported by the callers that pass a
-// status word.
-template <typename I>
-__device__ __forceinline__ int64_t token_row(const I* ids, int64_t t, int64_t V, int32_t* status) {
-  const int64_t v = ids[t];
-  if (v >= 0 && v < V) return v;
-  if (v != -1) set_status(status, MOE_ERR_DEVICE_BOUNDS);
-  return -1;
-}
-
-template <typename I, typename W, typename Y>
-__global__ void __launch_bounds__(128) embed_any_kernel(EmbedArgs a) {
-  const int64_t t = blockIdx.x;
-  const int64_t v = token_row(static_cast<const I*>(a.ids), t, a.V, a.status);
+template <typename I, typename W, typename Y, bool ALIGNED>
+__global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a, int slices, int64_t items) {
+  launch_dependents();
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32;
+  if (item >= items) return;
+  const int64_t t = item / slices;
+  const int lane = threadIdx.x & 31, c0 = static_cast<int>(item - t * slices) * kSlice;
+  wait_for_previous();
+  const int64_t v = token_row(static_cast<const I*>(a.ids), t, a.V, lane == 0 ? a.status : nullptr);
   Y* out = static_cast<Y*>(a.dst) + t * a.ldo;
   const W* row = static_cast<const W*>(a.src) + (v < 0 ? 0 : v) * a.ldt;
-  for (int c = threadIdx.x; c < a.d; c += blockDim.x)
-    out[c] = from_f32<Y>(v < 0 ? 0.f : to_f32(row[c]) * a.scale);
-}
-
-// Gradient without a sort: a CTA owns kScanRows rows of the table and 256 columns, reads every
-// token number, keeps those of its rows in order, and adds their gradients up in shared memory,
-// a thread per column.
-constexpr int kScanRows = 32, kScanIds = 8 * 256;
-
-template <typename I, typename Y, typename W>
-__global__ void __launch_bounds__(256) embed_scan_kernel(EmbedArgs a) {
-  __shared__ float acc[kScanRows][256];
-  __shared__ int32_t list_t[kScanIds];
-  __shared__ uint8_t list_v[kScanIds];
-  __shared__ int32_t warp_n[8];
-  __shared__ uint32_t seen;
-  const int64_t v0 = static_cast<int64_t>(blockIdx.x) * kScanRows;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + tid;
-  int32_t* status = blockIdx.x == 0 && blockIdx.y == 0 ? a.status : nullptr;
-  for (int r = 0; r < kScanRows; ++r) acc[r][tid] = 0.f;
-  if (tid == 0) seen = 0;
-  for (int64_t t0 = 0; t0 < a.T; t0 += kScanIds) {
-    // eight neighbouring tokens per thread, so that the list is in the tokens' order
-    uint32_t hits = 0;
-    int row[8];
+  const float2 scale = both(a.scale);
+  if (ALIGNED) {
+    uint32_t w[4][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int64_t t = t0 + tid * 8 + j;
-      const int64_t v = t < a.T ? token_row(static_cast<const I*>(a.ids), t, a.V, status) : -1;
-      row[j] = static_cast<int>(v - v0);
-      if (v >= v0 && v < v0 + kScanRows) hits |= 1u << j;
-    }
-    int n = __popc(hits), before = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += u;
-    }
-    __syncthreads();   // the last tile's list and counts are used up
-    if (lane == 31) warp_n[warp] = before;
-    __syncthreads();
-    int at = before - n, total = 0;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      if (w < warp) at += warp_n[w];
-      total += warp_n[w];
+    for (int k = 0; k < 4; ++k) {
+      const int c = c0 + 8 * (k * 32 + lane);
+      if (c < a.d && v >= 0) load8(row + c, w[k]);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (hits >> j & 1) {
-        list_t[at] = static_cast<int32_t>(t0 + tid * 8 + j);
-        list_v[at++] = static_cast<uint8_t>(row[j]);
-        atomicOr(&seen, 1u << row[j]);
+    for (int k = 0; k < 4; ++k) {
+      const int c = c0 + 8 * (k * 32 + lane);
+      if (c >= a.d) break;
+      float2 u[4];
+      unpack8<W>(w[k], u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[j] = v < 0 ? both(0.f) : mul2(u[j], scale);
+      store8(out + c, u);
+    }
+  } else {
+    const int phase = static_cast<int>(reinterpret_cast<uintptr_t>(out) / sizeof(Y)) & 7;
+    const Span span = span_of(a.src, a.V, a.ldt, a.d, sizeof(W));
+    // the last slice takes the groups that the phase pushes past its end
+    const int end = c0 + kSlice >= a.d ? a.d + phase : c0 + kSlice;
+    for (int g = c0 + 8 * lane; g < end; g += 256) {
+      const int e0 = g - phase;
+      float2 u[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
+      if (v >= 0) take_any(row + e0, e0, a.d, span, u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[j] = mul2(u[j], scale);
+      if (e0 >= 0 && e0 + 8 <= a.d) {
+        store8(out + e0, u);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (e0 + j >= 0 && e0 + j < a.d) out[e0 + j] = from_f32<Y>(j & 1 ? u[j / 2].y : u[j / 2].x);
       }
-    __syncthreads();
-    if (c < a.d)
-      for (int i = 0; i < total; ++i)
-        acc[list_v[i]][tid] += to_f32(static_cast<const Y*>(a.src)[list_t[i] * a.ldo + c]);
-  }
-  __syncthreads();
-  if (c >= a.d) return;
-  for (int r = 0; r < kScanRows && v0 + r < a.V; ++r) {
-    W* out = static_cast<W*>(a.dst) + (v0 + r) * a.ldt + c;
-    const float v = acc[r][tid] * a.scale;
-    if (!a.accumulate) *out = from_f32<W>(v);
-    else if (seen >> r & 1) *out = from_f32<W>(to_f32(*out) + v);
+    }
   }
 }
 
 // ---------------------------------------------------------------------- launch --
 
+template <typename T>
+bool groups_of_eight(const void* p, int64_t ld, int32_t d) {
+  return reinterpret_cast<uintptr_t>(p) % (8 * sizeof(T)) == 0 && ld % 8 == 0 && d % 8 == 0;
+}
+
 template <typename I, typename W, typename Y>
-cudaError_t launch_embed(const EmbedArgs& a, bool backward, cudaStream_t s) {
-  if (!backward) {
-    embed_any_kernel<I, W, Y><<<static_cast<unsigned>(a.T), 128, 0, s>>>(a);
-  } else {
-    const dim3 grid(static_cast<unsigned>((a.V + kScanRows - 1) / kScanRows), static_cast<unsigned>((a.d + 255) / 256));
-    embed_scan_kernel<I, Y, W><<<grid, 256, 0, s>>>(a);
-  }
-  return cudaGetLastError();
+cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t s) {
+  const int slices = (a.d + kSlice - 1) / kSlice;
+  const int64_t items = a.T * slices;
+  const unsigned grid = static_cast<unsigned>((items + 7) / 8);
+  return groups_of_eight<W>(a.src, a.ldt, a.d) && groups_of_eight<Y>(a.dst, a.ldo, a.d)
+             ? launch_over(embed_kernel<I, W, Y, true>, dim3(grid), 256, 0, s, a, slices, items)
+             : launch_over(embed_kernel<I, W, Y, false>, dim3(grid), 256, 0, s, a, slices, items);
 }
 template <typename I, typename W>
-cudaError_t launch_embed_out(const EmbedArgs& a, const moe_embedding_config& c, bool backward, cudaStream_t s) {
-  return c.out_dtype == MOE_F32 ? launch_embed<I, W, float>(a, backward, s)
-                                : launch_embed<I, W, __nv_bfloat16>(a, backward, s);
+cudaError_t launch_out(const EmbedArgs& a, const moe_embedding_config& c, cudaStream_t s) {
+  return c.out_dtype == MOE_F32 ? launch_embed<I, W, float>(a, s) : launch_embed<I, W, __nv_bfloat16>(a, s);
 }
 template <typename I>
-cudaError_t launch_embed_table(const EmbedArgs& a, const moe_embedding_config& c, bool backward, cudaStream_t s) {
-  return c.table_dtype == MOE_F32 ? launch_embed_out<I, float>(a, c, backward, s)
-                                  : launch_embed_out<I, __nv_bfloat16>(a, c, backward, s);
+cudaError_t launch_table(const EmbedArgs& a, const moe_embedding_config& c, cudaStream_t s) {
+  return c.table_dtype == MOE_F32 ? launch_out<I, float>(a, c, s) : launch_out<I, __nv_bfloat16>(a, c, s);
+}
+cudaError_t launch_forward(const EmbedArgs& a, const moe_embedding_config& c, cudaStream_t s) {
+  return c.ids_int64 ? launch_table<int64_t>(a, c, s) : launch_table<int32_t>(a, c, s);
 }
 
 // ---------------------------------------------------------------------- checks --
@@ -138,7 +102,7 @@ uintptr_t size_of(int32_t t) { return t == MOE_F32 ? 4 : 2; }
 bool embed_sizes_ok(int64_t T, int64_t V, int32_t d) {
   return T >= 0 && T <= kMaxTokens && V >= 1 && V <= kMaxVocab && d >= 1 && d <= kMaxWidth;
 }
-size_t embed_workspace(int64_t, int64_t, int32_t) { return 256; }
+size_t embed_workspace(int64_t T, int64_t V, int32_t d) { return 256 + embedding_scratch(T, V, d); }
 
 moe_status run_embed(const moe_embedding_config* c, const void* ids, const void* src, void* dst,
                      bool backward, int32_t accumulate, void* workspace, size_t bytes, cudaStream_t s) {
@@ -157,7 +121,7 @@ moe_status run_embed(const moe_embedding_config* c, const void* ids, const void*
   if (!aligned_to(ids, c->ids_int64 ? 8 : 4) || !aligned_to(src, size_of(backward ? c->out_dtype : c->table_dtype)) ||
       !aligned_to(dst, size_of(backward ? c->table_dtype : c->out_dtype)) || !aligned_to(workspace, 256))
     return MOE_ERR_MISALIGNED;
-  if (bytes < embed_workspace(c->T, c->V, c->d)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (bytes < (backward ? embed_workspace(c->T, c->V, c->d) : 256)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if (c->T == 0 && accumulate) return MOE_OK;
   EmbedArgs a{};
   a.ids = ids;
@@ -171,8 +135,8 @@ moe_status run_embed(const moe_embedding_config* c, const void* ids, const void*
   a.accumulate = accumulate;
   a.scale = c->scale;
   a.status = static_cast<int32_t*>(workspace);
-  const cudaError_t e = c->ids_int64 ? launch_embed_table<int64_t>(a, *c, backward, s)
-                                     : launch_embed_table<int32_t>(a, *c, backward, s);
+  a.scratch = static_cast<char*>(workspace) + 256;
+  const cudaError_t e = backward ? launch_embedding_backward(a, *c, s) : launch_forward(a, *c, s);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

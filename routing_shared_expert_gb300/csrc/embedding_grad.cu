@@ -1,0 +1,623 @@
+// Gradient of the token embedding's table: dtable_v = scale sum_{t: id_t = v} dout_t, in fp32 and in a fixed
+// order, zeros (or what was there) for rows without a token.
+//
+// The tokens are sorted by their row, stably, so that a row's tokens are neighbours in ascending order.
+// The sorted list is cut into chunks of 32 tokens: a warp adds a chunk's gradients up over a slice of columns,
+// run by run, and writes the rows whose run lies within the chunk.  A run over a chunk's end (a frequent
+// token) leaves partial sums, which a second launch adds in the chunks' order.  Other CTAs of the same
+// launch write the zeros.
+#include "embedding.cuh"
+
+namespace moe {
+namespace {
+
+// ------------------------------------------------------------------------- sort --
+// Radix sort by digits of up to nine bits from the lowest, each pass stable.  A tile is the tokens of one CTA.
+
+constexpr int kDigits = 512, kSortThreads = 512, kSortWarps = kSortThreads / 32, kItems = 4;
+constexpr int kTile = kSortThreads * kItems;      // tokens at a time
+constexpr int kMaxTiles = 128;
+
+struct SortArgs {
+  const void* ids;
+  int64_t V;
+  int32_t T;
+  int32_t tile;           // tokens of a CTA, a multiple of kTile
+  int32_t tiles;
+  int32_t shift, bits;    // of this pass's digit
+  int32_t next_shift, next_bits;   // of the next pass's, 0 bits after the last
+  const int2* in;         // (row, token) of earlier passes; NULL: the token numbers
+  int2* out;
+  int32_t* hist;          // [tiles][kDigits] tokens of each digit in each tile of `in`
+  int32_t* next_hist;     // the same of `out`, zero at the launch
+  int32_t* status;
+};
+
+template <typename I>
+__device__ __forceinline__ int2 sort_item(const SortArgs& a, int i, int32_t* status) {
+  if (a.in) return a.in[i];
+  const int64_t v = token_row(static_cast<const I*>(a.ids), i, a.V, status);
+  return make_int2(static_cast<int>(v < 0 ? a.V : v), i);      // no token: behind the last row
+}
+
+// Digits of each tile, and zeros for the counts of the next pass.
+template <typename I>
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a) {
+  __shared__ int32_t n[kDigits];
+  launch_dependents();
+  wait_for_previous();
+  n[threadIdx.x] = 0;
+  if (a.next_bits) a.next_hist[blockIdx.x * kDigits + threadIdx.x] = 0;
+  __syncthreads();
+  const int t0 = blockIdx.x * a.tile, t1 = min(a.T, t0 + a.tile);
+  for (int i = t0 + threadIdx.x; i < t1; i += kSortThreads)
+    atomicAdd(n + (sort_item<I>(a, i, a.status).x >> a.shift & ((1 << a.bits) - 1)), 1);
+  __syncthreads();
+  a.hist[blockIdx.x * kDigits + threadIdx.x] = n[threadIdx.x];
+}
+
+// The sum of v over the threads before this one.
+__device__ __forceinline__ int exclusive_scan(int v, int32_t* part) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += u;
+  }
+  if (lane == 31) part[warp] = s;
+  __syncthreads();
+  int w = lane < kSortWarps ? part[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < kSortWarps; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += u;
+  }
+  const int before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+  return s - v + (warp > 0 ? before : 0);
+}
+
+// Where the items of up to kTile neighbours go: item j of a thread is number warp * 128 + 32 j + lane.  `base` holds
+// where each digit's next item goes and is moved on.
+struct RankSpace {
+  alignas(16) int32_t warp_n[kSortWarps][kDigits];
+  int32_t base[kDigits];
+  int32_t part[kSortWarps];
+};
+__device__ __forceinline__ void place_items(RankSpace& r, const int (&digit)[kItems], const bool (&on)[kItems],
+                                            int (&to)[kItems]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = lane; i < kDigits; i += 32) r.warp_n[warp][i] = 0;
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < kItems; ++j) {
+    const unsigned peers = __match_any_sync(0xffffffffu, on[j] ? digit[j] : -1 - lane);
+    const int before = on[j] ? r.warp_n[warp][digit[j]] : 0;
+    to[j] = before + __popc(peers & ((1u << lane) - 1));
+    __syncwarp();
+    if (on[j] && (peers & ((1u << lane) - 1)) == 0) r.warp_n[warp][digit[j]] = before + __popc(peers);
+    __syncwarp();
+  }
+  __syncthreads();
+  int at = r.base[threadIdx.x];
+#pragma unroll
+  for (int w = 0; w < kSortWarps; ++w) {
+    const int n = r.warp_n[w][threadIdx.x];
+    r.warp_n[w][threadIdx.x] = at;
+    at += n;
+  }
+  r.base[threadIdx.x] = at;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kItems; ++j)
+    if (on[j]) to[j] += r.warp_n[warp][digit[j]];
+  __syncthreads();
+}
+
+template <typename I>
+__global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(SortArgs a) {
+  __shared__ RankSpace r;
+  launch_dependents();
+  wait_for_previous();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // this tile's share of each digit begins behind the lower digits and the earlier tiles
+  int before = 0, all = 0;
+#pragma unroll 8
+  for (int t = 0; t < a.tiles; ++t) {
+    const int n = a.hist[t * kDigits + threadIdx.x];
+    if (t < static_cast<int>(blockIdx.x)) before += n;
+    all += n;
+  }
+  const int lower = exclusive_scan(all, r.part);
+  r.base[threadIdx.x] = lower + before;
+  const int t0 = blockIdx.x * a.tile, t1 = min(a.T, t0 + a.tile);
+  for (int i0 = t0; i0 < t1; i0 += kTile) {
+    int2 item[kItems];
+    int digit[kItems], to[kItems];
+    bool on[kItems];
+#pragma unroll
+    for (int j = 0; j < kItems; ++j) {
+      const int i = i0 + warp * 32 * kItems + 32 * j + lane;
+      on[j] = i < t1;
+      item[j] = on[j] ? sort_item<I>(a, i, nullptr) : make_int2(0, 0);
+      digit[j] = item[j].x >> a.shift & ((1 << a.bits) - 1);
+    }
+    __syncthreads();
+    place_items(r, digit, on, to);
+#pragma unroll
+    for (int j = 0; j < kItems; ++j)
+      if (on[j]) {
+        a.out[to[j]] = item[j];
+        if (a.next_bits)
+          atomicAdd(a.next_hist + to[j] / a.tile * kDigits + (item[j].x >> a.next_shift & ((1 << a.next_bits) - 1)), 1);
+      }
+  }
+}
+
+// All passes for at most kTile tokens, in shared memory.
+template <typename I>
+__global__ void __launch_bounds__(kSortThreads) sort_small_kernel(SortArgs a) {
+  __shared__ RankSpace r;
+  static_assert(sizeof(r.warp_n) >= kTile * sizeof(int2), "the counts' place holds the list between passes");
+  int2* list = reinterpret_cast<int2*>(r.warp_n);
+  launch_dependents();
+  wait_for_previous();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int2 item[kItems];
+  int digit[kItems], to[kItems];
+  bool on[kItems];
+#pragma unroll
+  for (int j = 0; j < kItems; ++j) {
+    const int i = warp * 32 * kItems + 32 * j + lane;
+    on[j] = i < a.T;
+    item[j] = on[j] ? sort_item<I>(a, i, a.status) : make_int2(0, 0);
+  }
+  for (int shift = 0; shift < a.bits; shift += 9) {      // bits: of a whole row number
+    r.base[threadIdx.x] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kItems; ++j) {
+      digit[j] = item[j].x >> shift & (kDigits - 1);
+      if (on[j]) atomicAdd(r.base + digit[j], 1);
+    }
+    __syncthreads();
+    const int n = r.base[threadIdx.x], lower = exclusive_scan(n, r.part);
+    r.base[threadIdx.x] = lower;
+    __syncthreads();
+    place_items(r, digit, on, to);
+#pragma unroll
+    for (int j = 0; j < kItems; ++j)
+      if (on[j]) list[to[j]] = item[j];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kItems; ++j)
+      if (on[j]) item[j] = list[warp * 32 * kItems + 32 * j + lane];
+    __syncthreads();
+  }
+#pragma unroll
+  for (int j = 0; j < kItems; ++j)
+    if (on[j]) a.out[warp * 32 * kItems + 32 * j + lane] = item[j];
+}
+
+// ------------------------------------------------------------------------- sums --
+
+constexpr int kChunk = 32, kColumns = 256;      // tokens and columns of a warp
+constexpr int kZeroRows = 128;                  // rows of a CTA that writes zeros
+
+struct SumArgs {
+  EmbedArgs e;
+  const int2* list;        // (row, token), sorted; row V behind the last: no token
+  float* partial;          // [chunks][2][d]: of the run that enters a chunk, of the one that leaves it
+  int32_t T, chunks, slices;
+  unsigned sum_ctas;       // of the launch; the others write zeros
+};
+
+// One slice of a table row: v times the scale, or added to what it holds.
+template <typename W, bool ALIGNED>
+__device__ __forceinline__ void write_row(const EmbedArgs& a, int64_t row, int c, const float2 (&v)[4]) {
+  W* p = static_cast<W*>(a.dst) + row * a.ldt + c;
+  float2 u[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) u[j] = mul2(v[j], both(a.scale));
+  if (ALIGNED) {
+    if (a.accumulate) {
+      uint32_t w[8];
+      float2 h[4];
+      load8(p, w);
+      unpack8<W>(w, h);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[j] = add2(h[j], u[j]);
+    }
+    store8(p, u);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j < a.d) {
+        const float z = j & 1 ? u[j / 2].y : u[j / 2].x;
+        p[j] = from_f32<W>(a.accumulate ? to_f32(p[j]) + z : z);
+      }
+  }
+}
+template <bool ALIGNED>
+__device__ __forceinline__ void write_partial(float* p, int c, int d, const float2 (&v)[4]) {
+  if (ALIGNED) {
+    store8(p + c, v);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (c + j < d) p[c + j] = j & 1 ? v[j / 2].y : v[j / 2].x;
+}
+
+template <typename Y, typename W, bool ALIGNED>
+__device__ __forceinline__ void sum_chunk(const SumArgs& s, int chunk, int c) {
+  const EmbedArgs& a = s.e;
+  const int lane = threadIdx.x & 31;
+  const int i0 = chunk * kChunk, n = min(kChunk, s.T - i0);
+  const int2 mine = lane < n ? s.list[i0 + lane] : make_int2(static_cast<int>(a.V), 0);
+  const int entering = i0 > 0 ? s.list[i0 - 1].x : -1, leaving = i0 + n < s.T ? s.list[i0 + n].x : -1;
+  const bool on = c < a.d;
+  const Span span = span_of(a.src, a.T, a.ldo, a.d, sizeof(Y));
+  float2 acc[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
+  bool first = true;       // of the chunk's runs
+  int row = __shfl_sync(0xffffffffu, mine.x, 0);
+  constexpr int kAhead = 8;
+  for (int b = 0; b < kChunk && row < a.V; b += kAhead) {
+    float2 v[kAhead][4];
+    int rows[kAhead];
+    if (ALIGNED) {
+      uint32_t w[kAhead][8];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        rows[j] = __shfl_sync(0xffffffffu, mine.x, b + j);
+        const int t = __shfl_sync(0xffffffffu, mine.y, b + j);
+        if (rows[j] < a.V && on) load8(static_cast<const Y*>(a.src) + t * a.ldo + c, w[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) unpack8<Y>(w[j], v[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        rows[j] = __shfl_sync(0xffffffffu, mine.x, b + j);
+        const int t = __shfl_sync(0xffffffffu, mine.y, b + j);
+        if (rows[j] < a.V && on) take_any(static_cast<const Y*>(a.src) + t * a.ldo + c, c, a.d, span, v[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (rows[j] != row) {        // the run ends before this token
+        if (on) {
+          if (first && row == entering) write_partial<ALIGNED>(s.partial + static_cast<int64_t>(chunk) * 2 * a.d, c, a.d, acc);
+          else write_row<W, ALIGNED>(a, row, c, acc);
+        }
+        first = false;
+        row = rows[j];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = both(0.f);
+      }
+      if (row >= a.V) break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = add2(acc[i], v[j][i]);
+    }
+  }
+  if (row >= a.V || !on) return;
+  const bool enters = first && row == entering;
+  if (enters || row == leaving) write_partial<ALIGNED>(s.partial + (static_cast<int64_t>(chunk) * 2 + (enters ? 0 : 1)) * a.d, c, a.d, acc);
+  else write_row<W, ALIGNED>(a, row, c, acc);
+}
+
+// The first of the list's places from lo on whose row is not below v.
+__device__ __forceinline__ int lower_bound(const int2* list, int lo, int hi, int64_t v) {
+  while (lo < hi) {
+    const int m = lo + (hi - lo) / 2;
+    if (list[m].x < v) lo = m + 1;
+    else hi = m;
+  }
+  return lo;
+}
+
+template <typename W, bool ALIGNED>
+__device__ __forceinline__ void write_zeros(const SumArgs& s, int64_t v0) {
+  __shared__ bool none[kZeroRows];
+  const EmbedArgs& a = s.e;
+  if (threadIdx.x < kZeroRows) {
+    const int64_t v = v0 + threadIdx.x;
+    const int at = v < a.V ? lower_bound(s.list, 0, s.T, v) : 0;
+    none[threadIdx.x] = v < a.V && (at == s.T || s.list[at].x != v);
+  }
+  __syncthreads();
+  const float2 zero[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
+  for (int r = threadIdx.x >> 5; r < kZeroRows; r += blockDim.x >> 5) {
+    if (!none[r]) continue;
+    W* p = static_cast<W*>(a.dst) + (v0 + r) * a.ldt;
+    if (ALIGNED)
+      for (int c = 8 * (threadIdx.x & 31); c < a.d; c += 256) store8(p + c, zero);
+    else
+      for (int c = threadIdx.x & 31; c < a.d; c += 32) p[c] = from_f32<W>(0.f);
+  }
+}
+
+template <typename Y, typename W, bool ALIGNED>
+__global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs s) {
+  launch_dependents();
+  wait_for_previous();
+  if (blockIdx.x >= s.sum_ctas) {
+    write_zeros<W, ALIGNED>(s, static_cast<int64_t>(blockIdx.x - s.sum_ctas) * kZeroRows);
+    return;
+  }
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int chunk = static_cast<int>(item / s.slices);
+  if (chunk >= s.chunks) return;
+  sum_chunk<Y, W, ALIGNED>(s, chunk, static_cast<int>(item - static_cast<int64_t>(chunk) * s.slices) * kColumns + 8 * (threadIdx.x & 31));
+}
+
+// Runs over several chunks: the sum of the chunk that a run begins in and of those that it enters, in order.  A CTA
+// looks through 32 chunks for runs that begin there, its warps each add a stretch of a run's partial sums up.
+template <typename W, bool ALIGNED>
+__global__ void __launch_bounds__(256) embed_join_kernel(SumArgs s) {
+  __shared__ float part[8][kColumns + 8];
+  wait_for_previous();
+  const EmbedArgs& a = s.e;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.y * kColumns + 8 * lane;
+  const int chunk = blockIdx.x * 32 + lane;
+  const int last = chunk * kChunk + kChunk - 1;
+  bool begins = false;
+  int row = 0;
+  if (last + 1 < s.T) {
+    row = s.list[last].x;
+    const int first = chunk * kChunk;
+    begins = row < a.V && s.list[last + 1].x == row &&
+             (s.list[first].x != row || first == 0 || s.list[first - 1].x != row);
+  }
+  unsigned todo = __ballot_sync(0xffffffffu, begins);
+  while (todo) {
+    const int k = __ffs(todo) - 1;
+    todo &= todo - 1;
+    const int from = blockIdx.x * 32 + k, v = __shfl_sync(0xffffffffu, row, k);
+    const int end = lower_bound(s.list, from * kChunk + kChunk, s.T, static_cast<int64_t>(v) + 1);   // behind the run
+    const int to = (end - 1) / kChunk;                      // the last chunk that it enters
+    const int per = (to - from + 1 + 7) / 8, b0 = from + warp * per, b1 = min(to + 1, b0 + per);
+    float2 acc[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
+#pragma unroll 4
+    for (int b = b0; b < b1; ++b) {
+      const float* p = s.partial + (static_cast<int64_t>(b) * 2 + (b == from ? 1 : 0)) * a.d + c;
+      float2 u[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
+      if (ALIGNED) {
+        uint32_t w[8];
+        if (c < a.d) {
+          load8(p, w);
+          unpack8<float>(w, u);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          u[j] = make_float2(c + 2 * j < a.d ? p[2 * j] : 0.f, c + 2 * j + 1 < a.d ? p[2 * j + 1] : 0.f);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] = add2(acc[j], u[j]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(&part[warp][8 * lane + 2 * j]) = acc[j];
+    __syncthreads();
+    if (warp == 0 && c < a.d) {
+      float2 sum[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sum[j] = *reinterpret_cast<const float2*>(&part[0][8 * lane + 2 * j]);
+#pragma unroll
+        for (int w = 1; w < 8; ++w) sum[j] = add2(sum[j], *reinterpret_cast<const float2*>(&part[w][8 * lane + 2 * j]));
+      }
+      write_row<W, ALIGNED>(a, v, c, sum);
+    }
+  }
+}
+
+// Gradient without a sort: a CTA owns kScanRows rows of the table and 256 columns, reads every
+// token number, keeps those of its rows in order, and adds their gradients up in shared memory,
+// a thread per column.
+constexpr int kScanRows = 32, kScanIds = 8 * 256;
+
+template <typename I, typename Y, typename W>
+__global__ void __launch_bounds__(256) embed_scan_kernel(EmbedArgs a) {
+  launch_dependents();
+  __shared__ float acc[kScanRows][256];
+  __shared__ int32_t list_t[kScanIds];
+  __shared__ uint8_t list_v[kScanIds];
+  __shared__ int32_t warp_n[8];
+  __shared__ uint32_t seen;
+  const int64_t v0 = static_cast<int64_t>(blockIdx.x) * kScanRows;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + tid;
+  int32_t* status = blockIdx.x == 0 && blockIdx.y == 0 ? a.status : nullptr;
+  for (int r = 0; r < kScanRows; ++r) acc[r][tid] = 0.f;
+  if (tid == 0) seen = 0;
+  wait_for_previous();
+  for (int64_t t0 = 0; t0 < a.T; t0 += kScanIds) {
+    // eight neighbouring tokens per thread, so that the list is in the tokens' order
+    uint32_t hits = 0;
+    int row[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t t = t0 + tid * 8 + j;
+      const int64_t v = t < a.T ? token_row(static_cast<const I*>(a.ids), t, a.V, status) : -1;
+      row[j] = static_cast<int>(v - v0);
+      if (v >= v0 && v < v0 + kScanRows) hits |= 1u << j;
+    }
+    int n = __popc(hits), before = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += u;
+    }
+    __syncthreads();   // the last tile's list and counts are used up
+    if (lane == 31) warp_n[warp] = before;
+    __syncthreads();
+    int at = before - n, total = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      if (w < warp) at += warp_n[w];
+      total += warp_n[w];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (hits >> j & 1) {
+        list_t[at] = static_cast<int32_t>(t0 + tid * 8 + j);
+        list_v[at++] = static_cast<uint8_t>(row[j]);
+        atomicOr(&seen, 1u << row[j]);
+      }
+    __syncthreads();
+    if (c < a.d)
+      for (int i = 0; i < total; ++i)
+        acc[list_v[i]][tid] += to_f32(static_cast<const Y*>(a.src)[list_t[i] * a.ldo + c]);
+  }
+  __syncthreads();
+  if (c >= a.d) return;
+  for (int r = 0; r < kScanRows && v0 + r < a.V; ++r) {
+    W* out = static_cast<W*>(a.dst) + (v0 + r) * a.ldt + c;
+    const float v = acc[r][tid] * a.scale;
+    if (!a.accumulate) *out = from_f32<W>(v);
+    else if (seen >> r & 1) *out = from_f32<W>(to_f32(*out) + v);
+  }
+}
+
+// ---------------------------------------------------------------------- launch --
+
+size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
+
+int bits_of(int64_t v) {
+  int b = 1;
+  while (v >> b) ++b;
+  return b;
+}
+
+// How many tokens the table's rows are looked through for, row block by row block, instead of being sorted: while
+// all CTAs together read few token numbers.
+bool scans(int64_t T, int64_t V, int32_t d) {
+  const int64_t ctas = (V + kScanRows - 1) / kScanRows * ((d + 255) / 256);
+  return T <= 2048 && T * ctas <= (1 << 20);
+}
+
+struct GradLayout {
+  bool scan;
+  int32_t tiles, tile, chunks;
+  size_t list[2], hist[2], partial, total;
+};
+GradLayout grad_layout(int64_t T, int64_t V, int32_t d) {
+  GradLayout l{};
+  l.scan = T == 0 || scans(T, V, d);
+  if (l.scan) return l;
+  const int64_t per = (T + kMaxTiles - 1) / kMaxTiles;
+  l.tile = static_cast<int32_t>((per + kTile - 1) / kTile * kTile);
+  l.tiles = static_cast<int32_t>((T + l.tile - 1) / l.tile);
+  l.chunks = static_cast<int32_t>((T + kChunk - 1) / kChunk);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = up256(o + bytes);
+    return at;
+  };
+  for (int i = 0; i < 2; ++i) {
+    l.list[i] = take(static_cast<size_t>(T) * 8);
+    l.hist[i] = take(static_cast<size_t>(l.tiles) * kDigits * 4);
+  }
+  l.partial = take(static_cast<size_t>(l.chunks) * 2 * static_cast<size_t>(d) * 4);
+  l.total = o;
+  return l;
+}
+
+// The sorted list of (row, token).
+template <typename I>
+cudaError_t sort_tokens(const EmbedArgs& a, const GradLayout& l, const int2** list, cudaStream_t s) {
+  SortArgs p{};
+  p.ids = a.ids;
+  p.V = a.V;
+  p.T = static_cast<int32_t>(a.T);
+  p.tile = l.tile;
+  p.tiles = l.tiles;
+  p.status = a.status;
+  const int bits = bits_of(a.V);
+  int2* lists[2] = {reinterpret_cast<int2*>(a.scratch + l.list[0]), reinterpret_cast<int2*>(a.scratch + l.list[1])};
+  int32_t* hists[2] = {reinterpret_cast<int32_t*>(a.scratch + l.hist[0]), reinterpret_cast<int32_t*>(a.scratch + l.hist[1])};
+  if (a.T <= kTile) {
+    p.bits = bits;
+    p.out = lists[0];
+    *list = lists[0];
+    return launch_over(sort_small_kernel<I>, dim3(1), kSortThreads, 0, s, p);
+  }
+  const int passes = (bits + 8) / 9, width = (bits + passes - 1) / passes;
+  cudaError_t e = cudaSuccess;
+  for (int k = 0; k < passes && e == cudaSuccess; ++k) {
+    p.shift = k * width;
+    p.bits = std::min(width, bits - p.shift);
+    p.next_shift = p.shift + width;
+    p.next_bits = k + 1 < passes ? std::min(width, bits - p.next_shift) : 0;
+    p.in = k ? lists[(k - 1) % 2] : nullptr;
+    p.out = lists[k % 2];
+    p.hist = hists[k % 2];
+    p.next_hist = hists[(k + 1) % 2];
+    if (k != 1) {      // the counts of the second pass are kept by the first
+      const int next = p.next_bits;
+      if (k) p.next_bits = 0;
+      e = launch_over(sort_count_kernel<I>, dim3(static_cast<unsigned>(l.tiles)), kSortThreads, 0, s, p);
+      p.next_bits = k ? 0 : next;
+    } else {
+      p.next_bits = 0;
+    }
+    if (e == cudaSuccess) e = launch_over(sort_pass_kernel<I>, dim3(static_cast<unsigned>(l.tiles)), kSortThreads, 0, s, p);
+    *list = p.out;
+  }
+  return e;
+}
+
+template <typename Y, typename W, bool ALIGNED>
+cudaError_t launch_sums(const SumArgs& p, cudaStream_t s) {
+  const unsigned zeros = p.e.accumulate ? 0u : static_cast<unsigned>((p.e.V + kZeroRows - 1) / kZeroRows);
+  const cudaError_t e = launch_over(embed_sum_kernel<Y, W, ALIGNED>, dim3(p.sum_ctas + zeros), 256, 0, s, p);
+  if (e != cudaSuccess || p.chunks < 2) return e;
+  return launch_over(embed_join_kernel<W, ALIGNED>, dim3(static_cast<unsigned>((p.chunks + 31) / 32), static_cast<unsigned>(p.slices)),
+                     256, 0, s, p);
+}
+
+template <typename T>
+bool groups_of_eight(const void* p, int64_t ld, int32_t d) {
+  return reinterpret_cast<uintptr_t>(p) % (8 * sizeof(T)) == 0 && ld % 8 == 0 && d % 8 == 0;
+}
+
+template <typename I, typename Y, typename W>
+cudaError_t launch_grad(const EmbedArgs& a, cudaStream_t s) {
+  const GradLayout l = grad_layout(a.T, a.V, a.d);
+  if (l.scan) {
+    const dim3 grid(static_cast<unsigned>((a.V + kScanRows - 1) / kScanRows), static_cast<unsigned>((a.d + 255) / 256));
+    return launch_over(embed_scan_kernel<I, Y, W>, grid, 256, 0, s, a);
+  }
+  SumArgs p{};
+  const cudaError_t e = sort_tokens<I>(a, l, &p.list, s);
+  if (e != cudaSuccess) return e;
+  p.e = a;
+  p.partial = reinterpret_cast<float*>(a.scratch + l.partial);
+  p.T = static_cast<int32_t>(a.T);
+  p.chunks = l.chunks;
+  p.slices = (a.d + kColumns - 1) / kColumns;
+  p.sum_ctas = static_cast<unsigned>((static_cast<int64_t>(p.chunks) * p.slices + 7) / 8);
+  return groups_of_eight<Y>(a.src, a.ldo, a.d) && groups_of_eight<W>(a.dst, a.ldt, a.d) ? launch_sums<Y, W, true>(p, s)
+                                                                                        : launch_sums<Y, W, false>(p, s);
+}
+template <typename I, typename Y>
+cudaError_t launch_table(const EmbedArgs& a, const moe_embedding_config& c, cudaStream_t s) {
+  return c.table_dtype == MOE_F32 ? launch_grad<I, Y, float>(a, s) : launch_grad<I, Y, __nv_bfloat16>(a, s);
+}
+template <typename I>
+cudaError_t launch_out(const EmbedArgs& a, const moe_embedding_config& c, cudaStream_t s) {
+  return c.out_dtype == MOE_F32 ? launch_table<I, float>(a, c, s) : launch_table<I, __nv_bfloat16>(a, c, s);
+}
+
+}  // namespace
+
+size_t embedding_scratch(int64_t T, int64_t V, int32_t d) { return grad_layout(T, V, d).total; }
+
+cudaError_t launch_embedding_backward(const EmbedArgs& a, const moe_embedding_config& c, cudaStream_t s) {
+  return c.ids_int64 ? launch_out<int64_t>(a, c, s) : launch_out<int32_t>(a, c, s);
+}
+
+}  // namespace moe

@@ -4,12 +4,76 @@
 // The tokens are sorted by their row, stably, so that a row's tokens are neighbours in ascending order.
 // The sorted list is cut into chunks of 32 tokens: a warp adds a chunk's gradients up over a slice of columns,
 // run by run, and writes the rows whose run lies within the chunk.  A run over a chunk's end (a frequent
-// token) leaves partial sums, which a second launch adds in the chunks' order.  Other CTAs of the same
-// launch write the zeros.
+// token) leaves partial sums, which a second launch adds in the chunks' order.  The rows without a token get
+// their zeros from other CTAs of the sort's launches, which leave HBM idle, and of the sums'.
 #include "embedding.cuh"
 
 namespace moe {
 namespace {
+
+// ------------------------------------------------------------------------ zeros --
+
+constexpr int kZeroRows = 128;                  // rows of a CTA that writes zeros
+
+// Which rows of the table have no token: from one bit per row, or (no bits) from the token numbers themselves.
+struct Zeros {
+  const uint32_t* has;     // [(V + 31) / 32], set for rows with a token
+  void* table;
+  int64_t ldt, V;
+  int64_t from;            // first row of this launch's share
+  unsigned ctas;           // CTAs of kZeroRows rows that write it
+  int32_t d, bf16, aligned;
+};
+
+__device__ __forceinline__ void fill_zero_rows(const Zeros& z, int64_t v0, const uint32_t (&has)[kZeroRows / 32]) {
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  const int64_t size = z.bf16 ? 2 : 4, bytes = z.d * size;
+#pragma unroll
+  for (int i = 0; i < kZeroRows / 32; ++i)
+    for (int r = threadIdx.x >> 5; r < 32 && v0 + 32 * i + r < z.V; r += warps) {
+      if (has[i] >> r & 1) continue;
+      char* p = static_cast<char*>(z.table) + (v0 + 32 * i + r) * z.ldt * size;
+      if (z.aligned)      // rows of whole 16-byte pieces
+        for (int64_t c = 16 * lane; c < bytes; c += 512) *reinterpret_cast<uint4*>(p + c) = make_uint4(0u, 0u, 0u, 0u);
+      else if (z.bf16)
+        for (int64_t c = lane; c < z.d; c += 32) reinterpret_cast<uint16_t*>(p)[c] = 0;
+      else
+        for (int64_t c = lane; c < z.d; c += 32) reinterpret_cast<uint32_t*>(p)[c] = 0u;
+    }
+}
+
+// The zeros of rows [from + kZeroRows cta, ...).
+__device__ __forceinline__ void zeros_by_bits(const Zeros& z, unsigned cta) {
+  const int64_t v0 = z.from + static_cast<int64_t>(cta) * kZeroRows;
+  uint32_t has[kZeroRows / 32];
+#pragma unroll
+  for (int i = 0; i < kZeroRows / 32; ++i) has[i] = v0 + 32 * i < z.V ? z.has[v0 / 32 + i] : 0u;
+  fill_zero_rows(z, v0, has);
+}
+template <typename I>
+__device__ __forceinline__ void zeros_by_tokens(const Zeros& z, unsigned cta, const I* ids, int T) {
+  __shared__ uint32_t seen[kZeroRows / 32];
+  const int64_t v0 = z.from + static_cast<int64_t>(cta) * kZeroRows;
+  if (threadIdx.x < kZeroRows / 32) seen[threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll 4
+  for (int i = threadIdx.x; i < T; i += blockDim.x) {
+    const int64_t r = static_cast<int64_t>(ids[i]) - v0;
+    if (r >= 0 && r < kZeroRows) atomicOr(seen + (r >> 5), 1u << (r & 31));
+  }
+  __syncthreads();
+  uint32_t has[kZeroRows / 32];
+#pragma unroll
+  for (int i = 0; i < kZeroRows / 32; ++i) has[i] = seen[i];
+  fill_zero_rows(z, v0, has);
+}
+
+__global__ void __launch_bounds__(256) clear_bits_kernel(uint32_t* has, int64_t words) {
+  launch_dependents();
+  wait_for_previous();
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < words; i += static_cast<int64_t>(gridDim.x) * blockDim.x)
+    has[i] = 0u;
+}
 
 // ------------------------------------------------------------------------- sort --
 // Radix sort by digits of up to nine bits from the lowest, each pass stable.  A tile is the tokens of one CTA.
@@ -31,6 +95,8 @@ struct SortArgs {
   int32_t* hist;          // [tiles][kDigits] tokens of each digit in each tile of `in`
   int32_t* next_hist;     // the same of `out`, zero at the launch
   int32_t* status;
+  uint32_t* has;          // bits to set, or NULL
+  Zeros zeros;            // what CTAs past the tiles write
 };
 
 template <typename I>
@@ -50,8 +116,14 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a) {
   if (a.next_bits) a.next_hist[blockIdx.x * kDigits + threadIdx.x] = 0;
   __syncthreads();
   const int t0 = blockIdx.x * a.tile, t1 = min(a.T, t0 + a.tile);
-  for (int i = t0 + threadIdx.x; i < t1; i += kSortThreads)
-    atomicAdd(n + (sort_item<I>(a, i, a.status).x >> a.shift & ((1 << a.bits) - 1)), 1);
+  for (int i = t0 + threadIdx.x; i < t1; i += kSortThreads) {
+    const int v = sort_item<I>(a, i, a.status).x;
+    atomicAdd(n + (v >> a.shift & ((1 << a.bits) - 1)), 1);
+    if (a.has && v < a.V) {
+      const uint32_t bit = 1u << (v & 31);
+      if (!(a.has[v >> 5] & bit)) atomicOr(a.has + (v >> 5), bit);    // frequent tokens' bits are there already
+    }
+  }
   __syncthreads();
   a.hist[blockIdx.x * kDigits + threadIdx.x] = n[threadIdx.x];
 }
@@ -119,6 +191,10 @@ __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(SortArgs a) {
   __shared__ RankSpace r;
   launch_dependents();
   wait_for_previous();
+  if (blockIdx.x >= static_cast<unsigned>(a.tiles)) {
+    zeros_by_bits(a.zeros, blockIdx.x - a.tiles);
+    return;
+  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // this tile's share of each digit begins behind the lower digits and the earlier tiles
   int before = 0, all = 0;
@@ -154,7 +230,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(SortArgs a) {
   }
 }
 
-// All passes for at most kTile tokens, in shared memory.
+// All passes for at most kTile tokens, in the first CTA's shared memory; the others write all zeros.
 template <typename I>
 __global__ void __launch_bounds__(kSortThreads) sort_small_kernel(SortArgs a) {
   __shared__ RankSpace r;
@@ -162,6 +238,10 @@ __global__ void __launch_bounds__(kSortThreads) sort_small_kernel(SortArgs a) {
   int2* list = reinterpret_cast<int2*>(r.warp_n);
   launch_dependents();
   wait_for_previous();
+  if (blockIdx.x > 0) {
+    zeros_by_tokens(a.zeros, blockIdx.x - 1, static_cast<const I*>(a.ids), a.T);
+    return;
+  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int2 item[kItems];
   int digit[kItems], to[kItems];
@@ -202,14 +282,13 @@ __global__ void __launch_bounds__(kSortThreads) sort_small_kernel(SortArgs a) {
 // ------------------------------------------------------------------------- sums --
 
 constexpr int kChunk = 32, kColumns = 256;      // tokens and columns of a warp
-constexpr int kZeroRows = 128;                  // rows of a CTA that writes zeros
-
 struct SumArgs {
   EmbedArgs e;
   const int2* list;        // (row, token), sorted; row V behind the last: no token
   float* partial;          // [chunks][2][d]: of the run that enters a chunk, of the one that leaves it
   int32_t T, chunks, slices;
-  unsigned sum_ctas;       // of the launch; the others write zeros
+  unsigned sum_ctas;       // of the launch, beside those that write zeros
+  Zeros zeros;
 };
 
 // One slice of a table row: v times the scale, or added to what it holds.
@@ -242,11 +321,11 @@ template <bool ALIGNED>
 __device__ __forceinline__ void write_partial(float* p, int c, int d, const float2 (&v)[4]) {
   if (ALIGNED) {
     store8(p + c, v);
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (c + j < d) p[c + j] = j & 1 ? v[j / 2].y : v[j / 2].x;
+    for (int j = 0; j < 8; ++j)
+      if (c + j < d) p[c + j] = j & 1 ? v[j / 2].y : v[j / 2].x;
+  }
 }
 
 template <typename Y, typename W, bool ALIGNED>
@@ -306,110 +385,102 @@ __device__ __forceinline__ void sum_chunk(const SumArgs& s, int chunk, int c) {
   else write_row<W, ALIGNED>(a, row, c, acc);
 }
 
-// The first of the list's places from lo on whose row is not below v.
-__device__ __forceinline__ int lower_bound(const int2* list, int lo, int hi, int64_t v) {
-  while (lo < hi) {
-    const int m = lo + (hi - lo) / 2;
-    if (list[m].x < v) lo = m + 1;
-    else hi = m;
-  }
-  return lo;
-}
-
-template <typename W, bool ALIGNED>
-__device__ __forceinline__ void write_zeros(const SumArgs& s, int64_t v0) {
-  __shared__ bool none[kZeroRows];
-  const EmbedArgs& a = s.e;
-  if (threadIdx.x < kZeroRows) {
-    const int64_t v = v0 + threadIdx.x;
-    const int at = v < a.V ? lower_bound(s.list, 0, s.T, v) : 0;
-    none[threadIdx.x] = v < a.V && (at == s.T || s.list[at].x != v);
-  }
-  __syncthreads();
-  const float2 zero[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
-  for (int r = threadIdx.x >> 5; r < kZeroRows; r += blockDim.x >> 5) {
-    if (!none[r]) continue;
-    W* p = static_cast<W*>(a.dst) + (v0 + r) * a.ldt;
-    if (ALIGNED)
-      for (int c = 8 * (threadIdx.x & 31); c < a.d; c += 256) store8(p + c, zero);
-    else
-      for (int c = threadIdx.x & 31; c < a.d; c += 32) p[c] = from_f32<W>(0.f);
-  }
-}
-
 template <typename Y, typename W, bool ALIGNED>
 __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs s) {
   launch_dependents();
   wait_for_previous();
-  if (blockIdx.x >= s.sum_ctas) {
-    write_zeros<W, ALIGNED>(s, static_cast<int64_t>(blockIdx.x - s.sum_ctas) * kZeroRows);
+  // the CTAs that write zeros spread evenly among those that read
+  const int64_t before = static_cast<int64_t>(blockIdx.x) * s.zeros.ctas / gridDim.x;
+  if ((static_cast<int64_t>(blockIdx.x) + 1) * s.zeros.ctas / gridDim.x > before) {
+    zeros_by_bits(s.zeros, static_cast<unsigned>(before));
     return;
   }
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int64_t item = (static_cast<int64_t>(blockIdx.x) - before) * 8 + (threadIdx.x >> 5);
   const int chunk = static_cast<int>(item / s.slices);
   if (chunk >= s.chunks) return;
   sum_chunk<Y, W, ALIGNED>(s, chunk, static_cast<int>(item - static_cast<int64_t>(chunk) * s.slices) * kColumns + 8 * (threadIdx.x & 31));
 }
 
-// Runs over several chunks: the sum of the chunk that a run begins in and of those that it enters, in order.  A CTA
-// looks through 32 chunks for runs that begin there, its warps each add a stretch of a run's partial sums up.
+// Partial sums of chunks [b0, b1) of the run that begins in chunk `from`, in order.
+template <bool ALIGNED>
+__device__ __forceinline__ void add_partials(const SumArgs& s, int from, int b0, int b1, int c, float2 (&acc)[4]) {
+  const int d = s.e.d;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) acc[j] = both(0.f);
+  if (c >= d) return;
+#pragma unroll 8
+  for (int b = b0; b < b1; ++b) {
+    const float* p = s.partial + (static_cast<int64_t>(b) * 2 + (b == from ? 1 : 0)) * d + c;
+    float2 u[4];
+    if (ALIGNED) {
+      uint32_t w[8];
+      load8(p, w);
+      unpack8<float>(w, u);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        u[j] = make_float2(c + 2 * j < d ? p[2 * j] : 0.f, c + 2 * j + 1 < d ? p[2 * j + 1] : 0.f);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = add2(acc[j], u[j]);
+  }
+}
+
+// Runs over several chunks: the sum of the chunk that a run begins in and of those that it enters, in order.  A warp
+// looks whether a run begins in its chunk and goes on, and adds runs of up to kAlone chunks up by itself; longer
+// ones are cut into eight stretches for the CTA's warps.
+constexpr int kAlone = 32;
+
 template <typename W, bool ALIGNED>
 __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs s) {
   __shared__ float part[8][kColumns + 8];
+  __shared__ int long_row[8], long_end[8];
   wait_for_previous();
   const EmbedArgs& a = s.e;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.y * kColumns + 8 * lane;
-  const int chunk = blockIdx.x * 32 + lane;
-  const int last = chunk * kChunk + kChunk - 1;
-  bool begins = false;
-  int row = 0;
-  if (last + 1 < s.T) {
-    row = s.list[last].x;
-    const int first = chunk * kChunk;
-    begins = row < a.V && s.list[last + 1].x == row &&
-             (s.list[first].x != row || first == 0 || s.list[first - 1].x != row);
+  const int chunk = blockIdx.x * 8 + warp, first = chunk * kChunk, next = first + kChunk;
+  int row = -1, end = 0;           // the run's row, and the chunk behind the last that it enters
+  if (next < s.T) {
+    const int v = s.list[next - 1].x;
+    if (v < a.V && s.list[next].x == v && (first == 0 || s.list[first - 1].x != v || s.list[first].x != v)) row = v;
   }
-  unsigned todo = __ballot_sync(0xffffffffu, begins);
-  while (todo) {
-    const int k = __ffs(todo) - 1;
-    todo &= todo - 1;
-    const int from = blockIdx.x * 32 + k, v = __shfl_sync(0xffffffffu, row, k);
-    const int end = lower_bound(s.list, from * kChunk + kChunk, s.T, static_cast<int64_t>(v) + 1);   // behind the run
-    const int to = (end - 1) / kChunk;                      // the last chunk that it enters
-    const int per = (to - from + 1 + 7) / 8, b0 = from + warp * per, b1 = min(to + 1, b0 + per);
-    float2 acc[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
-#pragma unroll 4
-    for (int b = b0; b < b1; ++b) {
-      const float* p = s.partial + (static_cast<int64_t>(b) * 2 + (b == from ? 1 : 0)) * a.d + c;
-      float2 u[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
-      if (ALIGNED) {
-        uint32_t w[8];
-        if (c < a.d) {
-          load8(p, w);
-          unpack8<float>(w, u);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          u[j] = make_float2(c + 2 * j < a.d ? p[2 * j] : 0.f, c + 2 * j + 1 < a.d ? p[2 * j + 1] : 0.f);
+  if (row >= 0) {
+    for (end = chunk + 1;; end += 32) {      // 32 chunks at a time: the last item of each that the run fills
+      const int at = min((end + lane) * kChunk + kChunk, s.T) - 1;
+      const unsigned fills = __ballot_sync(0xffffffffu, end + lane < s.chunks && s.list[at].x == row);
+      if (fills != 0xffffffffu) {
+        end += __popc(fills);
+        break;
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] = add2(acc[j], u[j]);
     }
-    __syncthreads();
+    if (end < s.chunks && s.list[end * kChunk].x == row) ++end;      // it ends within this one
+  }
+  const bool alone = row >= 0 && end - chunk <= kAlone;
+  if (lane == 0) {
+    long_row[warp] = row >= 0 && !alone ? row : -1;
+    long_end[warp] = end;
+  }
+  float2 acc[4];
+  if (alone) {
+    add_partials<ALIGNED>(s, chunk, chunk, end, c, acc);
+    if (c < a.d) write_row<W, ALIGNED>(a, row, c, acc);
+  }
+  __syncthreads();
+  for (int k = 0; k < 8; ++k) {
+    if (long_row[k] < 0) continue;
+    const int from = blockIdx.x * 8 + k, to = long_end[k], per = (to - from + 7) / 8, b0 = from + warp * per;
+    add_partials<ALIGNED>(s, from, min(b0, to), min(to, b0 + per), c, acc);
 #pragma unroll
     for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(&part[warp][8 * lane + 2 * j]) = acc[j];
     __syncthreads();
     if (warp == 0 && c < a.d) {
-      float2 sum[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        sum[j] = *reinterpret_cast<const float2*>(&part[0][8 * lane + 2 * j]);
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int w = 1; w < 8; ++w) sum[j] = add2(sum[j], *reinterpret_cast<const float2*>(&part[w][8 * lane + 2 * j]));
-      }
-      write_row<W, ALIGNED>(a, v, c, sum);
+        for (int w = 1; w < 8; ++w) acc[j] = add2(acc[j], *reinterpret_cast<const float2*>(&part[w][8 * lane + 2 * j]));
+      write_row<W, ALIGNED>(a, long_row[k], c, acc);
     }
+    __syncthreads();
   }
 }
 
@@ -468,8 +539,15 @@ __global__ void __launch_bounds__(256) embed_scan_kernel(EmbedArgs a) {
       }
     __syncthreads();
     if (c < a.d)
-      for (int i = 0; i < total; ++i)
-        acc[list_v[i]][tid] += to_f32(static_cast<const Y*>(a.src)[list_t[i] * a.ldo + c]);
+      for (int i0 = 0; i0 < total; i0 += 8) {      // eight loads on their way
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          v[i] = i0 + i < total ? to_f32(static_cast<const Y*>(a.src)[list_t[i0 + i] * a.ldo + c]) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i0 + i < total) acc[list_v[i0 + i]][tid] += v[i];
+      }
   }
   __syncthreads();
   if (c >= a.d) return;
@@ -501,7 +579,7 @@ bool scans(int64_t T, int64_t V, int32_t d) {
 struct GradLayout {
   bool scan;
   int32_t tiles, tile, chunks;
-  size_t list[2], hist[2], partial, total;
+  size_t list[2], hist[2], has, partial, total;
 };
 GradLayout grad_layout(int64_t T, int64_t V, int32_t d) {
   GradLayout l{};
@@ -521,14 +599,27 @@ GradLayout grad_layout(int64_t T, int64_t V, int32_t d) {
     l.list[i] = take(static_cast<size_t>(T) * 8);
     l.hist[i] = take(static_cast<size_t>(l.tiles) * kDigits * 4);
   }
+  l.has = take(static_cast<size_t>((V + 31) / 32) * 4);
   l.partial = take(static_cast<size_t>(l.chunks) * 2 * static_cast<size_t>(d) * 4);
   l.total = o;
   return l;
 }
 
-// The sorted list of (row, token).
+// Bytes of zeros beside one pass of the sort: about what HBM takes during it.
+constexpr int64_t kZerosOfPass = 32 << 20;
+
+// The next share of the table's rows for the CTAs of one launch, `rows` at most.
+Zeros next_zeros(Zeros& z, int64_t rows) {
+  Zeros part = z;
+  const int64_t left = (z.V - z.from + kZeroRows - 1) / kZeroRows;
+  part.ctas = static_cast<unsigned>(std::min(left, (rows + kZeroRows - 1) / kZeroRows));
+  z.from += part.ctas * static_cast<int64_t>(kZeroRows);
+  return part;
+}
+
+// The sorted list of (row, token); zeros: of what is left when the sort is done.
 template <typename I>
-cudaError_t sort_tokens(const EmbedArgs& a, const GradLayout& l, const int2** list, cudaStream_t s) {
+cudaError_t sort_tokens(const EmbedArgs& a, const GradLayout& l, const int2** list, Zeros& zeros, cudaStream_t s) {
   SortArgs p{};
   p.ids = a.ids;
   p.V = a.V;
@@ -542,29 +633,33 @@ cudaError_t sort_tokens(const EmbedArgs& a, const GradLayout& l, const int2** li
   if (a.T <= kTile) {
     p.bits = bits;
     p.out = lists[0];
+    p.zeros = next_zeros(zeros, a.V);
     *list = lists[0];
-    return launch_over(sort_small_kernel<I>, dim3(1), kSortThreads, 0, s, p);
+    return launch_over(sort_small_kernel<I>, dim3(1 + p.zeros.ctas), kSortThreads, 0, s, p);
+  }
+  cudaError_t e = cudaSuccess;
+  if (zeros.from < a.V) {
+    const int64_t words = (a.V + 31) / 32;
+    p.has = reinterpret_cast<uint32_t*>(a.scratch + l.has);
+    e = launch_over(clear_bits_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(1024, (words + 255) / 256))), 256, 0, s, p.has, words);
   }
   const int passes = (bits + 8) / 9, width = (bits + passes - 1) / passes;
-  cudaError_t e = cudaSuccess;
+  const int64_t rows = kZerosOfPass / (zeros.d * (zeros.bf16 ? 2 : 4)) + 1;
   for (int k = 0; k < passes && e == cudaSuccess; ++k) {
     p.shift = k * width;
     p.bits = std::min(width, bits - p.shift);
     p.next_shift = p.shift + width;
-    p.next_bits = k + 1 < passes ? std::min(width, bits - p.next_shift) : 0;
+    // the counts of the second pass are kept by the first, those of later ones are taken anew
+    p.next_bits = k == 0 && passes > 1 ? std::min(width, bits - p.next_shift) : 0;
     p.in = k ? lists[(k - 1) % 2] : nullptr;
     p.out = lists[k % 2];
     p.hist = hists[k % 2];
     p.next_hist = hists[(k + 1) % 2];
-    if (k != 1) {      // the counts of the second pass are kept by the first
-      const int next = p.next_bits;
-      if (k) p.next_bits = 0;
-      e = launch_over(sort_count_kernel<I>, dim3(static_cast<unsigned>(l.tiles)), kSortThreads, 0, s, p);
-      p.next_bits = k ? 0 : next;
-    } else {
-      p.next_bits = 0;
-    }
-    if (e == cudaSuccess) e = launch_over(sort_pass_kernel<I>, dim3(static_cast<unsigned>(l.tiles)), kSortThreads, 0, s, p);
+    if (k != 1) e = launch_over(sort_count_kernel<I>, dim3(static_cast<unsigned>(l.tiles)), kSortThreads, 0, s, p);
+    p.has = nullptr;
+    p.zeros = next_zeros(zeros, rows);
+    if (e == cudaSuccess)
+      e = launch_over(sort_pass_kernel<I>, dim3(static_cast<unsigned>(l.tiles) + p.zeros.ctas), kSortThreads, 0, s, p);
     *list = p.out;
   }
   return e;
@@ -572,10 +667,9 @@ cudaError_t sort_tokens(const EmbedArgs& a, const GradLayout& l, const int2** li
 
 template <typename Y, typename W, bool ALIGNED>
 cudaError_t launch_sums(const SumArgs& p, cudaStream_t s) {
-  const unsigned zeros = p.e.accumulate ? 0u : static_cast<unsigned>((p.e.V + kZeroRows - 1) / kZeroRows);
-  const cudaError_t e = launch_over(embed_sum_kernel<Y, W, ALIGNED>, dim3(p.sum_ctas + zeros), 256, 0, s, p);
+  const cudaError_t e = launch_over(embed_sum_kernel<Y, W, ALIGNED>, dim3(p.sum_ctas + p.zeros.ctas), 256, 0, s, p);
   if (e != cudaSuccess || p.chunks < 2) return e;
-  return launch_over(embed_join_kernel<W, ALIGNED>, dim3(static_cast<unsigned>((p.chunks + 31) / 32), static_cast<unsigned>(p.slices)),
+  return launch_over(embed_join_kernel<W, ALIGNED>, dim3(static_cast<unsigned>((p.chunks + 7) / 8), static_cast<unsigned>(p.slices)),
                      256, 0, s, p);
 }
 
@@ -592,8 +686,18 @@ cudaError_t launch_grad(const EmbedArgs& a, cudaStream_t s) {
     return launch_over(embed_scan_kernel<I, Y, W>, grid, 256, 0, s, a);
   }
   SumArgs p{};
-  const cudaError_t e = sort_tokens<I>(a, l, &p.list, s);
+  Zeros zeros{};
+  zeros.has = reinterpret_cast<const uint32_t*>(a.scratch + l.has);
+  zeros.table = a.dst;
+  zeros.ldt = a.ldt;
+  zeros.V = a.V;
+  zeros.from = a.accumulate ? a.V : 0;
+  zeros.d = a.d;
+  zeros.bf16 = sizeof(W) == 2;
+  zeros.aligned = reinterpret_cast<uintptr_t>(a.dst) % 16 == 0 && a.ldt * sizeof(W) % 16 == 0 && a.d * sizeof(W) % 16 == 0;
+  const cudaError_t e = sort_tokens<I>(a, l, &p.list, zeros, s);
   if (e != cudaSuccess) return e;
+  p.zeros = next_zeros(zeros, a.V);
   p.e = a;
   p.partial = reinterpret_cast<float*>(a.scratch + l.partial);
   p.T = static_cast<int32_t>(a.T);

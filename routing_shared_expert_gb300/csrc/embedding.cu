@@ -7,41 +7,55 @@ namespace moe {
 namespace {
 
 // A warp per token and slice of kSlice columns, its four loads of eight values per lane on their way at
-// once.  Bound by HBM where rows are long: the rows of frequent tokens come from L2.  ALIGNED: rows of the table
-// and of out begin on groups of eight and end on one; else the groups are those of out, and the
-// table's values are moved into place.
+// once; of rows of at most 256 columns (SHORT, ALIGNED ones) the four loads and a row's unused lanes go to further tokens.
+// Bound by HBM where rows are long: the rows of frequent tokens come from L2.  ALIGNED: rows of the table and
+// of out begin on groups of eight and end on one; else the groups are those of out, and the table's values
+// are moved into place.
 constexpr int kSlice = 1024;
 
-template <typename I, typename W, typename Y, bool ALIGNED>
+template <typename I, typename W, typename Y, bool ALIGNED, bool SHORT>
 __global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a, int slices, int64_t items) {
   launch_dependents();
   const int64_t item = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32;
   if (item >= items) return;
-  const int64_t t = item / slices;
-  const int lane = threadIdx.x & 31, c0 = static_cast<int>(item - t * slices) * kSlice;
-  wait_for_previous();
-  const int64_t v = token_row(static_cast<const I*>(a.ids), t, a.V, lane == 0 ? a.status : nullptr);
-  Y* out = static_cast<Y*>(a.dst) + t * a.ldo;
-  const W* row = static_cast<const W*>(a.src) + (v < 0 ? 0 : v) * a.ldt;
+  const int lane = threadIdx.x & 31;
   const float2 scale = both(a.scale);
+  wait_for_previous();
   if (ALIGNED) {
+    // load k: columns from c on of token t[k].  SHORT: `slices` tokens to a warp's width
+    const int lanes = SHORT ? 32 / slices : 32;
+    const int64_t t0 = SHORT ? item * (4 * slices) + lane / lanes : item / slices;
+    const int c0 = SHORT ? 8 * (lane & (lanes - 1)) : static_cast<int>(item - t0 * slices) * kSlice + 8 * lane;
+    int64_t v[4];
+#pragma unroll
+    for (int k = 0; k < (SHORT ? 4 : 1); ++k) {
+      const int64_t t = t0 + k * slices;
+      v[k] = !SHORT || t < a.T ? token_row(static_cast<const I*>(a.ids), t, a.V, c0 == 0 ? a.status : nullptr) : -1;
+    }
     uint32_t w[4][8];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int c = c0 + 8 * (k * 32 + lane);
-      if (c < a.d && v >= 0) load8(row + c, w[k]);
+      const int64_t row = v[SHORT ? k : 0];
+      const int c = SHORT ? c0 : c0 + 256 * k;
+      if (c < a.d && row >= 0) load8(static_cast<const W*>(a.src) + row * a.ldt + c, w[k]);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int c = c0 + 8 * (k * 32 + lane);
-      if (c >= a.d) break;
+      const int64_t t = SHORT ? t0 + k * slices : t0;
+      const int c = SHORT ? c0 : c0 + 256 * k;
+      if (c >= a.d || (SHORT && t >= a.T)) break;
       float2 u[4];
       unpack8<W>(w[k], u);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) u[j] = v < 0 ? both(0.f) : mul2(u[j], scale);
-      store8(out + c, u);
+      for (int j = 0; j < 4; ++j) u[j] = v[SHORT ? k : 0] < 0 ? both(0.f) : mul2(u[j], scale);
+      store8(static_cast<Y*>(a.dst) + t * a.ldo + c, u);
     }
   } else {
+    const int64_t t = item / slices;
+    const int c0 = static_cast<int>(item - t * slices) * kSlice;
+    const int64_t v = token_row(static_cast<const I*>(a.ids), t, a.V, lane == 0 ? a.status : nullptr);
+    Y* out = static_cast<Y*>(a.dst) + t * a.ldo;
+    const W* row = static_cast<const W*>(a.src) + (v < 0 ? 0 : v) * a.ldt;
     const int phase = static_cast<int>(reinterpret_cast<uintptr_t>(out) / sizeof(Y)) & 7;
     const Span span = span_of(a.src, a.V, a.ldt, a.d, sizeof(W));
     // the last slice takes the groups that the phase pushes past its end
@@ -72,12 +86,20 @@ bool groups_of_eight(const void* p, int64_t ld, int32_t d) {
 
 template <typename I, typename W, typename Y>
 cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t s) {
+  const bool aligned = groups_of_eight<W>(a.src, a.ldt, a.d) && groups_of_eight<Y>(a.dst, a.ldo, a.d);
+  // several tokens to a warp where there are warps enough for all SMs
+  if (aligned && a.d <= 256 && a.T >= 4096) {
+    int lanes = 32;
+    while (8 * (lanes / 2) >= a.d) lanes /= 2;
+    const int tokens = 32 / lanes;
+    const int64_t items = (a.T + 4 * tokens - 1) / (4 * tokens);
+    return launch_over(embed_kernel<I, W, Y, true, true>, dim3(static_cast<unsigned>((items + 7) / 8)), 256, 0, s, a, tokens, items);
+  }
   const int slices = (a.d + kSlice - 1) / kSlice;
   const int64_t items = a.T * slices;
-  const unsigned grid = static_cast<unsigned>((items + 7) / 8);
-  return groups_of_eight<W>(a.src, a.ldt, a.d) && groups_of_eight<Y>(a.dst, a.ldo, a.d)
-             ? launch_over(embed_kernel<I, W, Y, true>, dim3(grid), 256, 0, s, a, slices, items)
-             : launch_over(embed_kernel<I, W, Y, false>, dim3(grid), 256, 0, s, a, slices, items);
+  const dim3 grid(static_cast<unsigned>((items + 7) / 8));
+  return aligned ? launch_over(embed_kernel<I, W, Y, true, false>, grid, 256, 0, s, a, slices, items)
+                 : launch_over(embed_kernel<I, W, Y, false, false>, grid, 256, 0, s, a, slices, items);
 }
 template <typename I, typename W>
 cudaError_t launch_out(const EmbedArgs& a, const moe_embedding_config& c, cudaStream_t s) {

@@ -13,59 +13,52 @@ namespace {
 
 // ------------------------------------------------------------------------ zeros --
 
-constexpr int kZeroRows = 128;                  // rows of a CTA that writes zeros
+constexpr int kMaxZeroRows = 128;   // of a CTA that writes zeros
 
 // Which rows of the table have no token: from one bit per row, or (no bits) from the token numbers themselves.
 struct Zeros {
   const uint32_t* has;     // [(V + 31) / 32], set for rows with a token
   void* table;
   int64_t ldt, V;
-  int64_t from;            // first row of this launch's share
-  unsigned ctas;           // CTAs of kZeroRows rows that write it
+  int64_t from;            // first row of this launch's share, a multiple of eight
+  unsigned ctas;           // CTAs that write it
+  int32_t rows;            // of each, a multiple of eight
   int32_t d, bf16, aligned;
 };
 
-__device__ __forceinline__ void fill_zero_rows(const Zeros& z, int64_t v0, const uint32_t (&has)[kZeroRows / 32]) {
-  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+// Zeros for row v by one warp.
+__device__ __forceinline__ void zero_row(const Zeros& z, int64_t v) {
+  const int lane = threadIdx.x & 31;
   const int64_t size = z.bf16 ? 2 : 4, bytes = z.d * size;
-#pragma unroll
-  for (int i = 0; i < kZeroRows / 32; ++i)
-    for (int r = threadIdx.x >> 5; r < 32 && v0 + 32 * i + r < z.V; r += warps) {
-      if (has[i] >> r & 1) continue;
-      char* p = static_cast<char*>(z.table) + (v0 + 32 * i + r) * z.ldt * size;
-      if (z.aligned)      // rows of whole 16-byte pieces
-        for (int64_t c = 16 * lane; c < bytes; c += 512) *reinterpret_cast<uint4*>(p + c) = make_uint4(0u, 0u, 0u, 0u);
-      else if (z.bf16)
-        for (int64_t c = lane; c < z.d; c += 32) reinterpret_cast<uint16_t*>(p)[c] = 0;
-      else
-        for (int64_t c = lane; c < z.d; c += 32) reinterpret_cast<uint32_t*>(p)[c] = 0u;
-    }
+  char* p = static_cast<char*>(z.table) + v * z.ldt * size;
+  if (z.aligned)      // rows of whole 16-byte pieces
+    for (int64_t c = 16 * lane; c < bytes; c += 512) *reinterpret_cast<uint4*>(p + c) = make_uint4(0u, 0u, 0u, 0u);
+  else if (z.bf16)
+    for (int64_t c = lane; c < z.d; c += 32) reinterpret_cast<uint16_t*>(p)[c] = 0;
+  else
+    for (int64_t c = lane; c < z.d; c += 32) reinterpret_cast<uint32_t*>(p)[c] = 0u;
 }
 
-// The zeros of rows [from + kZeroRows cta, ...).
+// The zeros of the rows of one CTA of a share.
 __device__ __forceinline__ void zeros_by_bits(const Zeros& z, unsigned cta) {
-  const int64_t v0 = z.from + static_cast<int64_t>(cta) * kZeroRows;
-  uint32_t has[kZeroRows / 32];
-#pragma unroll
-  for (int i = 0; i < kZeroRows / 32; ++i) has[i] = v0 + 32 * i < z.V ? z.has[v0 / 32 + i] : 0u;
-  fill_zero_rows(z, v0, has);
+  const int64_t v0 = z.from + static_cast<int64_t>(cta) * z.rows, v1 = min(z.V, v0 + z.rows);
+  for (int64_t v = v0 + (threadIdx.x >> 5); v < v1; v += blockDim.x >> 5)
+    if (!(z.has[v >> 5] >> (v & 31) & 1)) zero_row(z, v);
 }
 template <typename I>
 __device__ __forceinline__ void zeros_by_tokens(const Zeros& z, unsigned cta, const I* ids, int T) {
-  __shared__ uint32_t seen[kZeroRows / 32];
-  const int64_t v0 = z.from + static_cast<int64_t>(cta) * kZeroRows;
-  if (threadIdx.x < kZeroRows / 32) seen[threadIdx.x] = 0;
+  __shared__ uint32_t seen[kMaxZeroRows / 32];
+  const int64_t v0 = z.from + static_cast<int64_t>(cta) * z.rows, v1 = min(z.V, v0 + z.rows);
+  if (threadIdx.x < kMaxZeroRows / 32) seen[threadIdx.x] = 0;
   __syncthreads();
 #pragma unroll 4
   for (int i = threadIdx.x; i < T; i += blockDim.x) {
     const int64_t r = static_cast<int64_t>(ids[i]) - v0;
-    if (r >= 0 && r < kZeroRows) atomicOr(seen + (r >> 5), 1u << (r & 31));
+    if (r >= 0 && r < z.rows) atomicOr(seen + (r >> 5), 1u << (r & 31));
   }
   __syncthreads();
-  uint32_t has[kZeroRows / 32];
-#pragma unroll
-  for (int i = 0; i < kZeroRows / 32; ++i) has[i] = seen[i];
-  fill_zero_rows(z, v0, has);
+  for (int64_t v = v0 + (threadIdx.x >> 5); v < v1; v += blockDim.x >> 5)
+    if (!(seen[(v - v0) >> 5] >> ((v - v0) & 31) & 1)) zero_row(z, v);
 }
 
 __global__ void __launch_bounds__(256) clear_bits_kernel(uint32_t* has, int64_t words) {
@@ -287,7 +280,7 @@ struct SumArgs {
   const int2* list;        // (row, token), sorted; row V behind the last: no token
   float* partial;          // [chunks][2][d]: of the run that enters a chunk, of the one that leaves it
   int32_t T, chunks, slices;
-  unsigned sum_ctas;       // of the launch, beside those that write zeros
+  unsigned sum_ctas;       // of the launch; those behind them write zeros
   Zeros zeros;
 };
 
@@ -389,13 +382,11 @@ template <typename Y, typename W, bool ALIGNED>
 __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs s) {
   launch_dependents();
   wait_for_previous();
-  // the CTAs that write zeros spread evenly among those that read
-  const int64_t before = static_cast<int64_t>(blockIdx.x) * s.zeros.ctas / gridDim.x;
-  if ((static_cast<int64_t>(blockIdx.x) + 1) * s.zeros.ctas / gridDim.x > before) {
-    zeros_by_bits(s.zeros, static_cast<unsigned>(before));
+  if (blockIdx.x >= s.sum_ctas) {
+    zeros_by_bits(s.zeros, blockIdx.x - s.sum_ctas);
     return;
   }
-  const int64_t item = (static_cast<int64_t>(blockIdx.x) - before) * 8 + (threadIdx.x >> 5);
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int chunk = static_cast<int>(item / s.slices);
   if (chunk >= s.chunks) return;
   sum_chunk<Y, W, ALIGNED>(s, chunk, static_cast<int>(item - static_cast<int64_t>(chunk) * s.slices) * kColumns + 8 * (threadIdx.x & 31));
@@ -611,9 +602,9 @@ constexpr int64_t kZerosOfPass = 32 << 20;
 // The next share of the table's rows for the CTAs of one launch, `rows` at most.
 Zeros next_zeros(Zeros& z, int64_t rows) {
   Zeros part = z;
-  const int64_t left = (z.V - z.from + kZeroRows - 1) / kZeroRows;
-  part.ctas = static_cast<unsigned>(std::min(left, (rows + kZeroRows - 1) / kZeroRows));
-  z.from += part.ctas * static_cast<int64_t>(kZeroRows);
+  const int64_t left = (z.V - z.from + z.rows - 1) / z.rows;
+  part.ctas = static_cast<unsigned>(std::max<int64_t>(0, std::min(left, (rows + z.rows - 1) / z.rows)));
+  z.from += part.ctas * static_cast<int64_t>(z.rows);
   return part;
 }
 
@@ -644,7 +635,7 @@ cudaError_t sort_tokens(const EmbedArgs& a, const GradLayout& l, const int2** li
     e = launch_over(clear_bits_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(1024, (words + 255) / 256))), 256, 0, s, p.has, words);
   }
   const int passes = (bits + 8) / 9, width = (bits + passes - 1) / passes;
-  const int64_t rows = kZerosOfPass / (zeros.d * (zeros.bf16 ? 2 : 4)) + 1;
+  const int64_t rows = kZerosOfPass / (static_cast<int64_t>(zeros.d) * (zeros.bf16 ? 2 : 4)) + 1;
   for (int k = 0; k < passes && e == cudaSuccess; ++k) {
     p.shift = k * width;
     p.bits = std::min(width, bits - p.shift);
@@ -694,6 +685,8 @@ cudaError_t launch_grad(const EmbedArgs& a, cudaStream_t s) {
   zeros.from = a.accumulate ? a.V : 0;
   zeros.d = a.d;
   zeros.bf16 = sizeof(W) == 2;
+  // a CTA's rows: about 64 KB of them, so that a share spreads over the SMs; at least one for each of its warps
+  zeros.rows = static_cast<int32_t>(std::min<int64_t>(kMaxZeroRows, std::max<int64_t>(8, (64 << 10) / (static_cast<int64_t>(a.d) * sizeof(W)) / 8 * 8)));
   zeros.aligned = reinterpret_cast<uintptr_t>(a.dst) % 16 == 0 && a.ldt * sizeof(W) % 16 == 0 && a.d * sizeof(W) % 16 == 0;
   const cudaError_t e = sort_tokens<I>(a, l, &p.list, zeros, s);
   if (e != cudaSuccess) return e;

@@ -64,7 +64,8 @@ def check(moe, T, V, d, spread="zipf", table="f32", out="bf16", scale=1.0, ids_d
 SIZES = [(1, 1, 1), (1, 7, 8), (2, 3, 5), (5, 100, 64), (31, 10, 33), (32, 1000, 256), (33, 1000, 257), (300, 1000, 256),
          (257, 4097, 96), (1000, 50, 40), (2049, 300, 130), (4095, 5000, 64), (4096, 70000, 24), (4097, 5000, 64),
          (8192, 100, 72), (9001, 66000, 40), (20000, 3001, 136), (40000, 131073, 16), (70001, 513, 8), (131072, 2, 32),
-         (150000, 200000, 9), (513, 300, 2051), (6000, 900, 2560)]
+         (150000, 200000, 9), (513, 300, 2051), (6000, 900, 2560),
+         (5001, 300, 8), (4999, 300, 128), (7000, 40, 136), (9000, 3000, 256), (4100, 600000, 8), (4096, 300, 16)]
 
 
 @pytest.mark.parametrize("T,V,d", SIZES)

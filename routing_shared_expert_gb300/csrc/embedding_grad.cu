@@ -15,9 +15,9 @@ namespace {
 
 constexpr int kMaxZeroRows = 128;   // of a CTA that writes zeros
 
-// Which rows of the table have no token: from one bit per row, or (no bits) from the token numbers themselves.
+// Which rows of the table have no token: from a mark per row, or (few tokens) from the token numbers themselves.
 struct Zeros {
-  const uint32_t* has;     // [(V + 31) / 32], set for rows with a token
+  const uint8_t* has;      // [V], 1 for rows with a token
   void* table;
   int64_t ldt, V;
   int64_t from;            // first row of this launch's share, a multiple of eight
@@ -40,10 +40,10 @@ __device__ __forceinline__ void zero_row(const Zeros& z, int64_t v) {
 }
 
 // The zeros of the rows of one CTA of a share.
-__device__ __forceinline__ void zeros_by_bits(const Zeros& z, unsigned cta) {
+__device__ __forceinline__ void zeros_by_marks(const Zeros& z, unsigned cta) {
   const int64_t v0 = z.from + static_cast<int64_t>(cta) * z.rows, v1 = min(z.V, v0 + z.rows);
   for (int64_t v = v0 + (threadIdx.x >> 5); v < v1; v += blockDim.x >> 5)
-    if (!(z.has[v >> 5] >> (v & 31) & 1)) zero_row(z, v);
+    if (!z.has[v]) zero_row(z, v);
 }
 template <typename I>
 __device__ __forceinline__ void zeros_by_tokens(const Zeros& z, unsigned cta, const I* ids, int T) {
@@ -61,11 +61,11 @@ __device__ __forceinline__ void zeros_by_tokens(const Zeros& z, unsigned cta, co
     if (!(seen[(v - v0) >> 5] >> ((v - v0) & 31) & 1)) zero_row(z, v);
 }
 
-__global__ void __launch_bounds__(256) clear_bits_kernel(uint32_t* has, int64_t words) {
+__global__ void __launch_bounds__(256) clear_marks_kernel(uint4* has, int64_t n) {
   launch_dependents();
   wait_for_previous();
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < words; i += static_cast<int64_t>(gridDim.x) * blockDim.x)
-    has[i] = 0u;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * blockDim.x)
+    has[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // ------------------------------------------------------------------------- sort --
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(256) clear_bits_kernel(uint32_t* has, int64_t 
 
 constexpr int kDigits = 512, kSortThreads = 512, kSortWarps = kSortThreads / 32, kItems = 4;
 constexpr int kTile = kSortThreads * kItems;      // tokens at a time
-constexpr int kMaxTiles = 128;
+constexpr int kMaxTiles = 64;
 
 struct SortArgs {
   const void* ids;
@@ -88,7 +88,7 @@ struct SortArgs {
   int32_t* hist;          // [tiles][kDigits] tokens of each digit in each tile of `in`
   int32_t* next_hist;     // the same of `out`, zero at the launch
   int32_t* status;
-  uint32_t* has;          // bits to set, or NULL
+  uint8_t* has;           // marks to set, or NULL
   Zeros zeros;            // what CTAs past the tiles write
 };
 
@@ -103,18 +103,20 @@ __device__ __forceinline__ int2 sort_item(const SortArgs& a, int i, int32_t* sta
 template <typename I>
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a) {
   __shared__ int32_t n[kDigits];
+  __shared__ int32_t marked[2048];      // rows that this CTA has marked lately: a frequent one's mark is not stored at each token
   launch_dependents();
   wait_for_previous();
   n[threadIdx.x] = 0;
+  for (int i = threadIdx.x; i < 2048; i += kSortThreads) marked[i] = -1;
   if (a.next_bits) a.next_hist[blockIdx.x * kDigits + threadIdx.x] = 0;
   __syncthreads();
   const int t0 = blockIdx.x * a.tile, t1 = min(a.T, t0 + a.tile);
   for (int i = t0 + threadIdx.x; i < t1; i += kSortThreads) {
     const int v = sort_item<I>(a, i, a.status).x;
     atomicAdd(n + (v >> a.shift & ((1 << a.bits) - 1)), 1);
-    if (a.has && v < a.V) {
-      const uint32_t bit = 1u << (v & 31);
-      if (!(a.has[v >> 5] & bit)) atomicOr(a.has + (v >> 5), bit);    // frequent tokens' bits are there already
+    if (a.has && v < a.V && marked[v & 2047] != v) {
+      marked[v & 2047] = v;
+      a.has[v] = 1;
     }
   }
   __syncthreads();
@@ -185,13 +187,13 @@ __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(SortArgs a) {
   launch_dependents();
   wait_for_previous();
   if (blockIdx.x >= static_cast<unsigned>(a.tiles)) {
-    zeros_by_bits(a.zeros, blockIdx.x - a.tiles);
+    zeros_by_marks(a.zeros, blockIdx.x - a.tiles);
     return;
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // this tile's share of each digit begins behind the lower digits and the earlier tiles
   int before = 0, all = 0;
-#pragma unroll 8
+#pragma unroll 16
   for (int t = 0; t < a.tiles; ++t) {
     const int n = a.hist[t * kDigits + threadIdx.x];
     if (t < static_cast<int>(blockIdx.x)) before += n;
@@ -383,7 +385,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs s) {
   launch_dependents();
   wait_for_previous();
   if (blockIdx.x >= s.sum_ctas) {
-    zeros_by_bits(s.zeros, blockIdx.x - s.sum_ctas);
+    zeros_by_marks(s.zeros, blockIdx.x - s.sum_ctas);
     return;
   }
   const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -427,13 +429,20 @@ __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs s) {
   __shared__ float part[8][kColumns + 8];
   __shared__ int long_row[8], long_end[8];
   wait_for_previous();
+  const unsigned groups = (s.chunks + 7) / 8;
+  if (blockIdx.x >= groups * s.slices) {
+    zeros_by_marks(s.zeros, blockIdx.x - groups * s.slices);
+    return;
+  }
   const EmbedArgs& a = s.e;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.y * kColumns + 8 * lane;
-  const int chunk = blockIdx.x * 8 + warp, first = chunk * kChunk, next = first + kChunk;
+  const int group = blockIdx.x % groups, slice = blockIdx.x / groups;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = slice * kColumns + 8 * lane;
+  const int chunk = group * 8 + warp, first = chunk * kChunk, next = first + kChunk;
   int row = -1, end = 0;           // the run's row, and the chunk behind the last that it enters
   if (next < s.T) {
-    const int v = s.list[next - 1].x;
-    if (v < a.V && s.list[next].x == v && (first == 0 || s.list[first - 1].x != v || s.list[first].x != v)) row = v;
+    const int before = first > 0 ? s.list[first - 1].x : -1, head = s.list[first].x, tail = s.list[next - 1].x,
+              after = s.list[next].x;
+    if (tail < a.V && after == tail && (before != tail || head != tail)) row = tail;
   }
   if (row >= 0) {
     for (end = chunk + 1;; end += 32) {      // 32 chunks at a time: the last item of each that the run fills
@@ -459,7 +468,7 @@ __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs s) {
   __syncthreads();
   for (int k = 0; k < 8; ++k) {
     if (long_row[k] < 0) continue;
-    const int from = blockIdx.x * 8 + k, to = long_end[k], per = (to - from + 7) / 8, b0 = from + warp * per;
+    const int from = group * 8 + k, to = long_end[k], per = (to - from + 7) / 8, b0 = from + warp * per;
     add_partials<ALIGNED>(s, from, min(b0, to), min(to, b0 + per), c, acc);
 #pragma unroll
     for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(&part[warp][8 * lane + 2 * j]) = acc[j];
@@ -560,11 +569,12 @@ int bits_of(int64_t v) {
   return b;
 }
 
-// How many tokens the table's rows are looked through for, row block by row block, instead of being sorted: while
-// all CTAs together read few token numbers.
+// Whether every block of the table's rows looks through the tokens, instead of their being sorted: while they are so
+// few that one CTA can add a frequent one up, and all CTAs together read few token numbers (300 tokens to
+// 1000 x 256: 6.2 us; 2000 tokens to 500 x 1024 45 us, sorted 18).
 bool scans(int64_t T, int64_t V, int32_t d) {
   const int64_t ctas = (V + kScanRows - 1) / kScanRows * ((d + 255) / 256);
-  return T <= 2048 && T * ctas <= (1 << 20);
+  return T <= 512 && T * ctas <= (1 << 20);
 }
 
 struct GradLayout {
@@ -590,14 +600,15 @@ GradLayout grad_layout(int64_t T, int64_t V, int32_t d) {
     l.list[i] = take(static_cast<size_t>(T) * 8);
     l.hist[i] = take(static_cast<size_t>(l.tiles) * kDigits * 4);
   }
-  l.has = take(static_cast<size_t>((V + 31) / 32) * 4);
+  l.has = take(static_cast<size_t>(V + 15) / 16 * 16);
   l.partial = take(static_cast<size_t>(l.chunks) * 2 * static_cast<size_t>(d) * 4);
   l.total = o;
   return l;
 }
 
-// Bytes of zeros beside one pass of the sort: about what HBM takes during it.
-constexpr int64_t kZerosOfPass = 32 << 20;
+// Bytes of zeros beside one pass of the sort, and beside the join: about what HBM takes during it.
+constexpr int64_t kZerosBeside = 48 << 20;
+int64_t rows_beside(const Zeros& z) { return kZerosBeside / (static_cast<int64_t>(z.d) * (z.bf16 ? 2 : 4)) + 1; }
 
 // The next share of the table's rows for the CTAs of one launch, `rows` at most.
 Zeros next_zeros(Zeros& z, int64_t rows) {
@@ -630,12 +641,12 @@ cudaError_t sort_tokens(const EmbedArgs& a, const GradLayout& l, const int2** li
   }
   cudaError_t e = cudaSuccess;
   if (zeros.from < a.V) {
-    const int64_t words = (a.V + 31) / 32;
-    p.has = reinterpret_cast<uint32_t*>(a.scratch + l.has);
-    e = launch_over(clear_bits_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(1024, (words + 255) / 256))), 256, 0, s, p.has, words);
+    const int64_t pieces = (a.V + 15) / 16;
+    p.has = reinterpret_cast<uint8_t*>(a.scratch + l.has);
+    e = launch_over(clear_marks_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(1024, (pieces + 255) / 256))), 256, 0, s,
+                    reinterpret_cast<uint4*>(p.has), pieces);
   }
   const int passes = (bits + 8) / 9, width = (bits + passes - 1) / passes;
-  const int64_t rows = kZerosOfPass / (static_cast<int64_t>(zeros.d) * (zeros.bf16 ? 2 : 4)) + 1;
   for (int k = 0; k < passes && e == cudaSuccess; ++k) {
     p.shift = k * width;
     p.bits = std::min(width, bits - p.shift);
@@ -648,7 +659,7 @@ cudaError_t sort_tokens(const EmbedArgs& a, const GradLayout& l, const int2** li
     p.next_hist = hists[(k + 1) % 2];
     if (k != 1) e = launch_over(sort_count_kernel<I>, dim3(static_cast<unsigned>(l.tiles)), kSortThreads, 0, s, p);
     p.has = nullptr;
-    p.zeros = next_zeros(zeros, rows);
+    p.zeros = next_zeros(zeros, rows_beside(zeros));
     if (e == cudaSuccess)
       e = launch_over(sort_pass_kernel<I>, dim3(static_cast<unsigned>(l.tiles) + p.zeros.ctas), kSortThreads, 0, s, p);
     *list = p.out;
@@ -657,11 +668,12 @@ cudaError_t sort_tokens(const EmbedArgs& a, const GradLayout& l, const int2** li
 }
 
 template <typename Y, typename W, bool ALIGNED>
-cudaError_t launch_sums(const SumArgs& p, cudaStream_t s) {
+cudaError_t launch_sums(SumArgs p, const Zeros& beside_join, cudaStream_t s) {
   const cudaError_t e = launch_over(embed_sum_kernel<Y, W, ALIGNED>, dim3(p.sum_ctas + p.zeros.ctas), 256, 0, s, p);
   if (e != cudaSuccess || p.chunks < 2) return e;
-  return launch_over(embed_join_kernel<W, ALIGNED>, dim3(static_cast<unsigned>((p.chunks + 7) / 8), static_cast<unsigned>(p.slices)),
-                     256, 0, s, p);
+  p.zeros = beside_join;
+  const unsigned ctas = static_cast<unsigned>((p.chunks + 7) / 8) * static_cast<unsigned>(p.slices);
+  return launch_over(embed_join_kernel<W, ALIGNED>, dim3(ctas + p.zeros.ctas), 256, 0, s, p);
 }
 
 template <typename T>
@@ -678,7 +690,7 @@ cudaError_t launch_grad(const EmbedArgs& a, cudaStream_t s) {
   }
   SumArgs p{};
   Zeros zeros{};
-  zeros.has = reinterpret_cast<const uint32_t*>(a.scratch + l.has);
+  zeros.has = reinterpret_cast<const uint8_t*>(a.scratch + l.has);
   zeros.table = a.dst;
   zeros.ldt = a.ldt;
   zeros.V = a.V;
@@ -690,15 +702,18 @@ cudaError_t launch_grad(const EmbedArgs& a, cudaStream_t s) {
   zeros.aligned = reinterpret_cast<uintptr_t>(a.dst) % 16 == 0 && a.ldt * sizeof(W) % 16 == 0 && a.d * sizeof(W) % 16 == 0;
   const cudaError_t e = sort_tokens<I>(a, l, &p.list, zeros, s);
   if (e != cudaSuccess) return e;
-  p.zeros = next_zeros(zeros, a.V);
+  // what is left: a share for the join, when it is launched, and the rest beside the sums
+  const int64_t left = a.V - zeros.from, late = l.chunks > 1 ? std::min(left, rows_beside(zeros)) : 0;
+  p.zeros = next_zeros(zeros, left - late);
+  const Zeros beside_join = next_zeros(zeros, a.V);
   p.e = a;
   p.partial = reinterpret_cast<float*>(a.scratch + l.partial);
   p.T = static_cast<int32_t>(a.T);
   p.chunks = l.chunks;
   p.slices = (a.d + kColumns - 1) / kColumns;
   p.sum_ctas = static_cast<unsigned>((static_cast<int64_t>(p.chunks) * p.slices + 7) / 8);
-  return groups_of_eight<Y>(a.src, a.ldo, a.d) && groups_of_eight<W>(a.dst, a.ldt, a.d) ? launch_sums<Y, W, true>(p, s)
-                                                                                        : launch_sums<Y, W, false>(p, s);
+  return groups_of_eight<Y>(a.src, a.ldo, a.d) && groups_of_eight<W>(a.dst, a.ldt, a.d) ? launch_sums<Y, W, true>(p, beside_join, s)
+                                                                                        : launch_sums<Y, W, false>(p, beside_join, s);
 }
 template <typename I, typename Y>
 cudaError_t launch_table(const EmbedArgs& a, const moe_embedding_config& c, cudaStream_t s) {

@@ -23,7 +23,7 @@ struct Zeros {
   int64_t from;            // first row of this launch's share, a multiple of eight
   unsigned ctas;           // CTAs that write it
   int32_t rows;            // of each, a multiple of eight
-  int32_t d, bf16, aligned;
+  int32_t d, bf16;
 };
 
 // Zeros for row v by one warp.
@@ -31,12 +31,14 @@ __device__ __forceinline__ void zero_row(const Zeros& z, int64_t v) {
   const int lane = threadIdx.x & 31;
   const int64_t size = z.bf16 ? 2 : 4, bytes = z.d * size;
   char* p = static_cast<char*>(z.table) + v * z.ldt * size;
-  if (z.aligned)      // rows of whole 16-byte pieces
-    for (int64_t c = 16 * lane; c < bytes; c += 512) *reinterpret_cast<uint4*>(p + c) = make_uint4(0u, 0u, 0u, 0u);
-  else if (z.bf16)
-    for (int64_t c = lane; c < z.d; c += 32) reinterpret_cast<uint16_t*>(p)[c] = 0;
-  else
-    for (int64_t c = lane; c < z.d; c += 32) reinterpret_cast<uint32_t*>(p)[c] = 0u;
+  // whole 16-byte pieces, and what lies before and behind them element by element
+  const int64_t head = min(bytes, static_cast<int64_t>(-reinterpret_cast<uintptr_t>(p) & 15)), body = (bytes - head) & ~int64_t{15};
+  for (int64_t c = head + 16 * lane; c < head + body; c += 512) *reinterpret_cast<uint4*>(p + c) = make_uint4(0u, 0u, 0u, 0u);
+  const int64_t at = lane < 16 ? lane * size : head + body + (lane - 16) * size;
+  if (at < (lane < 16 ? head : bytes)) {
+    if (z.bf16) *reinterpret_cast<uint16_t*>(p + at) = 0;
+    else *reinterpret_cast<uint32_t*>(p + at) = 0u;
+  }
 }
 
 // The zeros of the rows of one CTA of a share.
@@ -286,14 +288,17 @@ struct SumArgs {
   Zeros zeros;
 };
 
-// One slice of a table row: v times the scale, or added to what it holds.
+// One slice of a table row, by a whole warp: v (columns c to c + 7 of each lane) times the scale, or added to what
+// the row holds.  Rows that do not begin on groups of eight take the values through `turn`, 256 floats of the
+// warp's own, so that neighbouring lanes store neighbouring values.
 template <typename W, bool ALIGNED>
-__device__ __forceinline__ void write_row(const EmbedArgs& a, int64_t row, int c, const float2 (&v)[4]) {
+__device__ __forceinline__ void write_row(const EmbedArgs& a, int64_t row, int c, const float2 (&v)[4], float* turn) {
   W* p = static_cast<W*>(a.dst) + row * a.ldt + c;
   float2 u[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) u[j] = mul2(v[j], both(a.scale));
   if (ALIGNED) {
+    if (c >= a.d) return;
     if (a.accumulate) {
       uint32_t w[8];
       float2 h[4];
@@ -304,27 +309,37 @@ __device__ __forceinline__ void write_row(const EmbedArgs& a, int64_t row, int c
     }
     store8(p, u);
   } else {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c + j < a.d) {
-        const float z = j & 1 ? u[j / 2].y : u[j / 2].x;
-        p[j] = from_f32<W>(a.accumulate ? to_f32(p[j]) + z : z);
-      }
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(turn + 8 * lane + 2 * j) = u[j];
+    __syncwarp();
+    p -= 8 * lane;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = 32 * j + lane;
+      if (c - 8 * lane + i < a.d) p[i] = from_f32<W>(a.accumulate ? to_f32(p[i]) + turn[i] : turn[i]);
+    }
+    __syncwarp();
   }
 }
 template <bool ALIGNED>
-__device__ __forceinline__ void write_partial(float* p, int c, int d, const float2 (&v)[4]) {
+__device__ __forceinline__ void write_partial(float* p, int c, int d, const float2 (&v)[4], float* turn) {
   if (ALIGNED) {
-    store8(p + c, v);
+    if (c < d) store8(p + c, v);
   } else {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(turn + 8 * lane + 2 * j) = v[j];
+    __syncwarp();
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (c + j < d) p[c + j] = j & 1 ? v[j / 2].y : v[j / 2].x;
+      if (c - 8 * lane + 32 * j + lane < d) p[c - 8 * lane + 32 * j + lane] = turn[32 * j + lane];
+    __syncwarp();
   }
 }
 
 template <typename Y, typename W, bool ALIGNED>
-__device__ __forceinline__ void sum_chunk(const SumArgs& s, int chunk, int c) {
+__device__ __forceinline__ void sum_chunk(const SumArgs& s, int chunk, int c, float* turn) {
   const EmbedArgs& a = s.e;
   const int lane = threadIdx.x & 31;
   const int i0 = chunk * kChunk, n = min(kChunk, s.T - i0);
@@ -360,10 +375,8 @@ __device__ __forceinline__ void sum_chunk(const SumArgs& s, int chunk, int c) {
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (rows[j] != row) {        // the run ends before this token
-        if (on) {
-          if (first && row == entering) write_partial<ALIGNED>(s.partial + static_cast<int64_t>(chunk) * 2 * a.d, c, a.d, acc);
-          else write_row<W, ALIGNED>(a, row, c, acc);
-        }
+        if (first && row == entering) write_partial<ALIGNED>(s.partial + static_cast<int64_t>(chunk) * 2 * a.d, c, a.d, acc, turn);
+        else write_row<W, ALIGNED>(a, row, c, acc, turn);
         first = false;
         row = rows[j];
 #pragma unroll
@@ -374,14 +387,17 @@ __device__ __forceinline__ void sum_chunk(const SumArgs& s, int chunk, int c) {
       for (int i = 0; i < 4; ++i) acc[i] = add2(acc[i], v[j][i]);
     }
   }
-  if (row >= a.V || !on) return;
+  if (row >= a.V) return;
   const bool enters = first && row == entering;
-  if (enters || row == leaving) write_partial<ALIGNED>(s.partial + (static_cast<int64_t>(chunk) * 2 + (enters ? 0 : 1)) * a.d, c, a.d, acc);
-  else write_row<W, ALIGNED>(a, row, c, acc);
+  if (enters || row == leaving)
+    write_partial<ALIGNED>(s.partial + (static_cast<int64_t>(chunk) * 2 + (enters ? 0 : 1)) * a.d, c, a.d, acc, turn);
+  else
+    write_row<W, ALIGNED>(a, row, c, acc, turn);
 }
 
 template <typename Y, typename W, bool ALIGNED>
 __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs s) {
+  __shared__ float turn[ALIGNED ? 1 : 8][ALIGNED ? 1 : kColumns];
   launch_dependents();
   wait_for_previous();
   if (blockIdx.x >= s.sum_ctas) {
@@ -391,7 +407,8 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs s) {
   const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int chunk = static_cast<int>(item / s.slices);
   if (chunk >= s.chunks) return;
-  sum_chunk<Y, W, ALIGNED>(s, chunk, static_cast<int>(item - static_cast<int64_t>(chunk) * s.slices) * kColumns + 8 * (threadIdx.x & 31));
+  sum_chunk<Y, W, ALIGNED>(s, chunk, static_cast<int>(item - static_cast<int64_t>(chunk) * s.slices) * kColumns + 8 * (threadIdx.x & 31),
+                           turn[ALIGNED ? 0 : threadIdx.x >> 5]);
 }
 
 // Partial sums of chunks [b0, b1) of the run that begins in chunk `from`, in order.
@@ -463,7 +480,7 @@ __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs s) {
   float2 acc[4];
   if (alone) {
     add_partials<ALIGNED>(s, chunk, chunk, end, c, acc);
-    if (c < a.d) write_row<W, ALIGNED>(a, row, c, acc);
+    write_row<W, ALIGNED>(a, row, c, acc, part[warp]);
   }
   __syncthreads();
   for (int k = 0; k < 8; ++k) {
@@ -473,12 +490,12 @@ __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs s) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(&part[warp][8 * lane + 2 * j]) = acc[j];
     __syncthreads();
-    if (warp == 0 && c < a.d) {
+    if (warp == 0) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int w = 1; w < 8; ++w) acc[j] = add2(acc[j], *reinterpret_cast<const float2*>(&part[w][8 * lane + 2 * j]));
-      write_row<W, ALIGNED>(a, long_row[k], c, acc);
+      write_row<W, ALIGNED>(a, long_row[k], c, acc, part[0]);
     }
     __syncthreads();
   }
@@ -699,7 +716,6 @@ cudaError_t launch_grad(const EmbedArgs& a, cudaStream_t s) {
   zeros.bf16 = sizeof(W) == 2;
   // a CTA's rows: about 64 KB of them, so that a share spreads over the SMs; at least one for each of its warps
   zeros.rows = static_cast<int32_t>(std::min<int64_t>(kMaxZeroRows, std::max<int64_t>(8, (64 << 10) / (static_cast<int64_t>(a.d) * sizeof(W)) / 8 * 8)));
-  zeros.aligned = reinterpret_cast<uintptr_t>(a.dst) % 16 == 0 && a.ldt * sizeof(W) % 16 == 0 && a.d * sizeof(W) % 16 == 0;
   const cudaError_t e = sort_tokens<I>(a, l, &p.list, zeros, s);
   if (e != cudaSuccess) return e;
   // what is left: a share for the join, when it is launched, and the rest beside the sums

@@ -350,28 +350,23 @@ __device__ __forceinline__ void sum_chunk(const SumArgs& s, int chunk, int c, fl
   float2 acc[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
   bool first = true;       // of the chunk's runs
   int row = __shfl_sync(0xffffffffu, mine.x, 0);
-  constexpr int kAhead = 8;
+  constexpr int kAhead = ALIGNED ? 8 : 4;      // tokens on their way
   for (int b = 0; b < kChunk && row < a.V; b += kAhead) {
-    float2 v[kAhead][4];
     int rows[kAhead];
-    if (ALIGNED) {
-      uint32_t w[kAhead][8];
+    const Y* p[kAhead];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        rows[j] = __shfl_sync(0xffffffffu, mine.x, b + j);
-        const int t = __shfl_sync(0xffffffffu, mine.y, b + j);
-        if (rows[j] < a.V && on) load8(static_cast<const Y*>(a.src) + t * a.ldo + c, w[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) unpack8<Y>(w[j], v[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        rows[j] = __shfl_sync(0xffffffffu, mine.x, b + j);
-        const int t = __shfl_sync(0xffffffffu, mine.y, b + j);
-        if (rows[j] < a.V && on) take_any(static_cast<const Y*>(a.src) + t * a.ldo + c, c, a.d, span, v[j]);
-      }
+    for (int j = 0; j < kAhead; ++j) {
+      rows[j] = __shfl_sync(0xffffffffu, mine.x, b + j);
+      p[j] = static_cast<const Y*>(a.src) + __shfl_sync(0xffffffffu, mine.y, b + j) * a.ldo + c;
     }
+    uint32_t w[ALIGNED ? kAhead : 1][8];
+    Raw8 raw[ALIGNED ? 1 : kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (rows[j] < a.V && on) {
+        if (ALIGNED) load8(p[j], w[ALIGNED ? j : 0]);
+        else raw[ALIGNED ? 0 : j] = load8_raw(p[j], span);
+      }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (rows[j] != row) {        // the run ends before this token
@@ -383,8 +378,17 @@ __device__ __forceinline__ void sum_chunk(const SumArgs& s, int chunk, int c, fl
         for (int i = 0; i < 4; ++i) acc[i] = both(0.f);
       }
       if (row >= a.V) break;
+      float2 v[4];
+      if (ALIGNED) {
+        unpack8<Y>(w[ALIGNED ? j : 0], v);
+      } else {
+        float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (on) take8(raw[ALIGNED ? 0 : j], p[j], min(8, a.d - c), u);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = add2(acc[i], v[j][i]);
+        for (int i = 0; i < 4; ++i) v[i] = make_float2(u[2 * i], u[2 * i + 1]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = add2(acc[i], v[i]);
     }
   }
   if (row >= a.V) return;
@@ -396,7 +400,7 @@ __device__ __forceinline__ void sum_chunk(const SumArgs& s, int chunk, int c, fl
 }
 
 template <typename Y, typename W, bool ALIGNED>
-__global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs s) {
+__global__ void __launch_bounds__(256, 2) embed_sum_kernel(SumArgs s) {
   __shared__ float turn[ALIGNED ? 1 : 8][ALIGNED ? 1 : kColumns];
   launch_dependents();
   wait_for_previous();

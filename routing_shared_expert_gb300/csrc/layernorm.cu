@@ -52,7 +52,7 @@ template <typename X, typename S, typename Y, int E, bool SPLIT, bool ENDS>
 __global__ void __launch_bounds__(E == 32 ? 512 : 1024) norm_vec_kernel(NormArgs a) {
   constexpr int G = kGroup<X, S, Y>, P = E / G, N = G / 2;
   extern __shared__ float4 smem[];
-  __shared__ float part[SPLIT ? 1 : kMaxTeams * 2 * 16];
+  __shared__ float part[SPLIT ? 1 : kMaxTeams * 2 * 32];
   launch_dependents();
   const Seat<G, P, SPLIT> at(a, phase_of<G>(static_cast<const X*>(a.x) + blockIdx.x * a.ldx));
   const int d = a.d;
@@ -73,8 +73,8 @@ __global__ void __launch_bounds__(E == 32 ? 512 : 1024) norm_vec_kernel(NormArgs
   int ahead = at.row;
   auto fetch = [&](char* to) {
     if (ahead < T) {
-      x.copy(to, at, a, a.x, a.ldx);
-      if (add) r.copy(to + at_r, at, a, a.r, a.ldr);
+      x.copy(to, at, ahead, T);
+      if (add) r.copy(to + at_r, at, ahead, T);
     }
     ahead += at.step;
     cp_async_commit();
@@ -97,10 +97,6 @@ __global__ void __launch_bounds__(E == 32 ? 512 : 1024) norm_vec_kernel(NormArgs
   for (int it = 0; it < at.turns; ++it, row += at.step) {
     const bool live = !SPLIT || row < T;
     wait_stage(a.stages);
-    if (ENDS && at.parts) {
-      x.clear_parts(from, at, d);
-      if (add) r.clear_parts(from + at_r, at, d);
-    }
     if (!live) {
       x.clear(from);
       if (add) r.clear(from + at_r);
@@ -108,14 +104,14 @@ __global__ void __launch_bounds__(E == 32 ? 512 : 1024) norm_vec_kernel(NormArgs
     float2 h[P][N];
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-      x.read(from, k, h[k]);
+      x.read(from, k, at, h[k]);
       if (add) {
         float2 v[N];
-        r.read(from + at_r, k, v);
+        r.read(from + at_r, k, at, v);
 #pragma unroll
         for (int j = 0; j < N; ++j) h[k][j] = add2(h[k][j], v[j]);
         if (a.s) {
-          if (live) sum.store(k, at, d, h[k]);
+          if (live) sum.store(k, at, h[k]);
           round_to<S>(h[k]);     // normalised is the sum as stored
         }
       }
@@ -133,17 +129,15 @@ __global__ void __launch_bounds__(E == 32 ? 512 : 1024) norm_vec_kernel(NormArgs
 #pragma unroll
         for (int j = 0; j < N; ++j) total = add2(total, h[k][j]);
       v[0] = total.x + total.y;
-      row_sum<SPLIT, 1>(v, part, turn, at.lanes, at.lane, at.team);
+      row_sum<SPLIT, 1, 32>(v, part, turn, at.lanes, at.lane, at.team);
       mean = v[0] * inv_d;
 #pragma unroll
       for (int k = 0; k < P; ++k) {
 #pragma unroll
         for (int j = 0; j < N; ++j) h[k][j] = add2(h[k][j], both(ENDS || at.whole[k] ? -mean : 0.f));
         if (ENDS && !at.whole[k]) {
-          asm volatile("");      // a branch that few threads take, not selections in all of them
-#pragma unroll
-          for (int j = 0; j < G; ++j)
-            if (at.e0[k] + j < 0 || at.e0[k] + j >= d) (j & 1 ? h[k][j / 2].y : h[k][j / 2].x) = 0.f;
+          asm volatile("");
+          keep(h[k], at.mask[k]);
         }
       }
     }
@@ -153,7 +147,7 @@ __global__ void __launch_bounds__(E == 32 ? 512 : 1024) norm_vec_kernel(NormArgs
 #pragma unroll
       for (int j = 0; j < N; ++j) sq = fma2(h[k][j], h[k][j], sq);
     v[0] = sq.x + sq.y;
-    row_sum<SPLIT, 1>(v, part, turn, at.lanes, at.lane, at.team);
+    row_sum<SPLIT, 1, 32>(v, part, turn, at.lanes, at.lane, at.team);
     const float rstd = rsqrtf(v[0] * inv_d + a.eps);
     if (!live) continue;      // its last turn
     if (at.lane == 0) {
@@ -175,7 +169,7 @@ __global__ void __launch_bounds__(E == 32 ? 512 : 1024) norm_vec_kernel(NormArgs
 #pragma unroll
         for (int j = 0; j < N; ++j) h[k][j] = add2(h[k][j], u[j]);
       }
-      y.store(k, at, d, h[k]);
+      y.store(k, at, h[k]);
     }
     y.row += y.step;
   }
@@ -194,12 +188,12 @@ cudaError_t launch_vec(const NormArgs& a, const Plan& p, cudaStream_t s) {
 template <typename X, typename S, typename Y>
 cudaError_t launch_forward(NormArgs a, cudaStream_t s) {
   const Plan p = make_plan<X, S, Y>(a, sizeof(X) + (a.r ? sizeof(S) : 0), (a.w != nullptr) + (a.b != nullptr),
-                                    int64_t{1} << 30, 1024, 32);
+                                    int64_t{1} << 30, 1024, 32, 1025);
   a.lanes = p.lanes;
   a.stages = p.stages;
   if (p.elements == 8) return launch_vec<X, S, Y, 8, true>(a, p, s);
   if (p.elements == 16) return p.split ? launch_vec<X, S, Y, 16, true>(a, p, s) : launch_vec<X, S, Y, 16, false>(a, p, s);
-  if (p.elements == 32) return p.split ? launch_vec<X, S, Y, 32, true>(a, p, s) : launch_vec<X, S, Y, 32, false>(a, p, s);
+  if (p.elements == 32 && p.split) return launch_vec<X, S, Y, 32, true>(a, p, s);
   norm_any_kernel<X, S, Y><<<static_cast<unsigned>(a.T), 256, 0, s>>>(a);
   return cudaGetLastError();
 }
@@ -216,6 +210,15 @@ cudaError_t launch_forward_any_type(const NormArgs& a, const moe_layernorm_confi
   const int32_t stream = a.r ? c.stream_dtype : c.x_dtype;    // without a residual: the form of x alone
   return c.x_dtype == MOE_F32 ? launch_s<float>(a, stream, c.y_dtype, s)
                               : launch_s<__nv_bfloat16>(a, stream, c.y_dtype, s);
+}
+
+cudaError_t launch_backward_any_type(const NormArgs& a, const moe_layernorm_config& c, cudaStream_t s) {
+  const int32_t stream = a.s ? c.stream_dtype : c.x_dtype;    // without dx: the form of h and dy alone
+  if (c.x_dtype == MOE_F32)
+    return c.y_dtype == MOE_F32 ? launch_layernorm_grad<float, float>(a, stream, s)
+                                : launch_layernorm_grad<float, __nv_bfloat16>(a, stream, s);
+  return c.y_dtype == MOE_F32 ? launch_layernorm_grad<__nv_bfloat16, float>(a, stream, s)
+                              : launch_layernorm_grad<__nv_bfloat16, __nv_bfloat16>(a, stream, s);
 }
 
 // ---------------------------------------------------------------------- checks --
@@ -336,7 +339,7 @@ moe_status moe_layernorm_backward(const moe_layernorm_config* cfg, const void* h
   a.db = dbias;
   a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + 256);
   a.slots = norm_slots(a.T, a.d);
-  return launch_layernorm_backward(a, *cfg, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launch_backward_any_type(a, *cfg, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -42,8 +42,9 @@ __device__ __forceinline__ float load_param(const void* p, int32_t dtype, int32_
   return dtype == MOE_F32 ? static_cast<const float*>(p)[c] : to_f32(static_cast<const __nv_bfloat16*>(p)[c]);
 }
 
-// The gradients (layernorm_grad.cu).
-cudaError_t launch_layernorm_backward(const NormArgs& a, const moe_layernorm_config& c, cudaStream_t s);
+// The gradients of rows h of X with dy of Y, dsum and dx of the given type (layernorm_grad.cuh).
+template <typename X, typename Y>
+cudaError_t launch_layernorm_grad(const NormArgs& a, int32_t stream_dtype, cudaStream_t s);
 
 // --------------------------------------------------------------- rows in groups --
 // Rows whose operands all start at the same place within a group of G elements (aligned tensors
@@ -76,12 +77,20 @@ __device__ __forceinline__ void param_group(const float* p, int groups, int q, f
 }
 template <int G>
 __device__ __forceinline__ void stage_param(float* dst, const void* src, int32_t dtype, int groups, int phase, int d) {
+  const bool pieces = (reinterpret_cast<uintptr_t>(src) & 15) == 0 && phase == 0;    // 16 bytes at a time
+#pragma unroll 4
   for (int q = threadIdx.x; q < groups; q += blockDim.x) {
     float v[G];
+    const int c0 = G * q - phase;
+    if (pieces && c0 + G <= d && dtype == MOE_F32) {
 #pragma unroll
-    for (int j = 0; j < G; ++j) {
-      const int c = G * q + j - phase;
-      v[j] = c >= 0 && c < d ? load_param(src, dtype, c, 0.f) : 0.f;
+      for (int j = 0; j < G; j += 4) {
+        const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(src) + c0 + j);
+        v[j] = u.x, v[j + 1] = u.y, v[j + 2] = u.z, v[j + 3] = u.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < G; ++j) v[j] = c0 + j >= 0 && c0 + j < d ? load_param(src, dtype, c0 + j, 0.f) : 0.f;
     }
 #pragma unroll
     for (int j = 0; j < G; j += 4)
@@ -93,7 +102,8 @@ __device__ __forceinline__ int phase_of(const T* row) {
   return static_cast<int>(reinterpret_cast<uintptr_t>(row) / sizeof(T)) & (G - 1);
 }
 __device__ __forceinline__ void wait_stage(int stages) {   // the oldest of `stages` copies has landed
-  if (stages == 2) cp_async_wait<1>();
+  if (stages == 1) cp_async_wait<0>();
+  else if (stages == 2) cp_async_wait<1>();
   else if (stages == 3) cp_async_wait<2>();
   else cp_async_wait<3>();
 }
@@ -104,10 +114,11 @@ struct Seat {
   int lanes, lane, team, groups, phase;
   int row, step;      // the team's first row, and from one to the next
   int turns;          // of its warp, the last of which may be past the last row for some teams (SPLIT)
-  int e0[P];          // first element of each group, within the row
-  bool whole[P];      // whether each lies in the row,
-  bool part[P];       // over one of its ends (ENDS only),
-  bool all, parts;    // whether all lie in it, and whether any lies over an end
+  int e0;             // first element of the first group within the row, the others G * lanes further
+  unsigned mask[P];   // which elements of each group lie in the row
+  bool whole[P];      // all of them,
+  bool part[P];       // some but not all (ENDS only)
+  bool all;           // whether all groups are whole
   __device__ __forceinline__ Seat(const NormArgs& a, int first_phase) {
     lanes = a.lanes;
     team = threadIdx.x / lanes;
@@ -118,50 +129,55 @@ struct Seat {
     step = blockDim.x / lanes * gridDim.x;
     const int first = SPLIT ? blockIdx.x + (threadIdx.x & ~31) / lanes * gridDim.x : row, T = static_cast<int>(a.T);
     turns = first < T ? (T - first + step - 1) / step : 0;
+    e0 = G * lane - phase;
     all = true;
-    parts = false;
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-      e0[k] = G * (k * lanes + lane) - phase;
-      whole[k] = e0[k] >= 0 && e0[k] + G <= a.d;
-      part[k] = !whole[k] && e0[k] + G > 0 && e0[k] < a.d;
+      mask[k] = 0;
+#pragma unroll
+      for (int j = 0; j < G; ++j)
+        if (column(k) + j >= 0 && column(k) + j < a.d) mask[k] |= 1u << j;
+      whole[k] = column(k) >= 0 && column(k) + G <= a.d;
+      part[k] = !whole[k] && mask[k] != 0;
       all = all && whole[k];
-      parts = parts || part[k];
     }
   }
+  __device__ __forceinline__ int column(int k) const { return e0 + k * G * lanes; }
 };
 
 // A thread's groups of one operand: `at` is where the current row's lie in the ring, copies of later rows
 // begin from `next`.  The pieces are `stride` bytes apart.
-template <typename T, int G, int P, bool SPLIT, bool ENDS>
+template <typename T_, int G, int P, bool SPLIT, bool ENDS>
 struct Feed {
-  const T* next;      // element 0 of the thread's first group, in the row to be copied next
+  const T_* next;      // element 0 of the thread's first group, in the row to be copied next
   int64_t step;       // elements to the team's row after it
   uint32_t stride;
   __device__ __forceinline__ Feed(const void* base, int64_t ld, const Seat<G, P, SPLIT>& s)
-      : next(static_cast<const T*>(base) + s.row * ld + s.e0[0]), step(s.step * ld),
-        stride(blockDim.x * static_cast<uint32_t>(G * sizeof(T))) {}
-  __device__ __forceinline__ void copy(char* to, const Seat<G, P, SPLIT>& s, const NormArgs& a, const void* base, int64_t ld) {
+      : next(static_cast<const T_*>(base) + s.row * ld + s.e0), step(s.step * ld),
+        stride(blockDim.x * static_cast<uint32_t>(G * sizeof(T_))) {}
+  // The row's groups begin their way.  One over an end of the row is copied whole, the neighbouring row's values
+  // with it, but for the tensor's own ends: the first row's beginning and the last one's end.
+  __device__ __forceinline__ void copy(char* to, const Seat<G, P, SPLIT>& s, int at, int T) {
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-      const T* src = next + k * G * s.lanes;
-      if (s.whole[k]) copy_whole<G>(to + k * stride, src);
-      else if (ENDS && s.part[k]) copy_end<G>(to + k * stride, src, s.e0[k], a.d, extent_of(base, a.T, ld, a.d, sizeof(T)));
+      const T_* src = next + k * G * s.lanes;
+      const bool inside = ENDS && s.part[k] && (at > 0 || s.mask[k] & 1) && (at < T - 1 || s.mask[k] >> (G - 1));
+      if (s.whole[k] || inside) copy_whole<G>(to + k * stride, src);
+      else if (ENDS && s.part[k]) copy_masked<G>(to + k * stride, src, s.mask[k]);
     }
     next += step;
   }
-  // Zeros in the copied groups' places outside the row; in all places of groups that are never copied.
-  __device__ __forceinline__ void clear_parts(char* at, const Seat<G, P, SPLIT>& s, int d) {
-#pragma unroll
-    for (int k = 0; k < P; ++k)
-      if (s.part[k]) clear_end<G, T>(at + k * stride, s.e0[k], d);
-  }
   __device__ __forceinline__ void clear(char* at) {
 #pragma unroll
-    for (int k = 0; k < P; ++k) clear_end<G, T>(at + k * stride, 0, 0);
+    for (int k = 0; k < P; ++k) clear_group<G, T_>(at + k * stride);
   }
-  __device__ __forceinline__ void read(const char* at, int k, float2 (&v)[G / 2]) const {
-    read_group(at + k * stride, static_cast<const T*>(nullptr), v);
+  // Group k, with zeros outside the row.
+  __device__ __forceinline__ void read(const char* at, int k, const Seat<G, P, SPLIT>& s, float2 (&v)[G / 2]) const {
+    read_group(at + k * stride, static_cast<const T_*>(nullptr), v);
+    if (ENDS && s.part[k]) {
+      asm volatile("");      // a branch that few threads take, not selections in all of them
+      keep(v, s.mask[k]);
+    }
   }
 };
 
@@ -171,29 +187,28 @@ struct Sink {
   T* row;
   int64_t step;
   __device__ __forceinline__ Sink(void* base, int64_t ld, const Seat<G, P, SPLIT>& s)
-      : row(static_cast<T*>(base) + s.row * ld + s.e0[0]), step(s.step * ld) {}
-  __device__ __forceinline__ void store(int k, const Seat<G, P, SPLIT>& s, int d, const float2 (&v)[G / 2]) {
+      : row(static_cast<T*>(base) + s.row * ld + s.e0), step(s.step * ld) {}
+  __device__ __forceinline__ void store(int k, const Seat<G, P, SPLIT>& s, const float2 (&v)[G / 2]) {
     T* dst = row + k * G * s.lanes;
     if (s.whole[k]) store_whole(dst, v);
-    else if (ENDS && s.part[k]) store_end(dst, s.e0[k], d, v);
+    else if (ENDS && s.part[k]) store_masked(dst, s.mask[k], v);
   }
 };
 
-template <bool SPLIT, int N>
+template <bool SPLIT, int N, int W>
 __device__ __forceinline__ void row_sum(float (&v)[N], float* part, int& turn, int lanes, int lane, int team) {
   if (SPLIT) {
     for (int o = lanes / 2; o > 0; o >>= 1)
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
   } else {
-    team_sum<N>(v, part + (2 * team + turn) * N * 16, lane >> 5, lanes >> 5, 1 + team);
+    team_sum<N, W>(v, part + (2 * team + turn) * N * W, lane >> 5, lanes >> 5, 1 + team);
     turn ^= 1;
   }
 }
 
 // ------------------------------------------------------------------ launch plan --
 
-constexpr int kMaxLanes = 512;
 constexpr size_t kSharedPerSm = 227 * 1024;
 
 // How rows are taken in groups of eight, if they can be.
@@ -213,9 +228,10 @@ bool same_phase(const void* p, int64_t ld, int64_t rows, int G, int64_t phase, i
 
 // bytes: of one element of all operands that are read; params: fp32 rows of parameters in shared memory;
 // most: CTAs at most; resident: threads of a CTA and of an SM that the kernels' registers leave room for;
-// split: elements of a lane up to which a row goes to a warp's lanes.
+// split: elements of a lane up to which a row goes to a warp's lanes; wide: lanes of 16 elements from which on a
+// thread takes 32.
 template <typename X, typename S, typename Y>
-Plan make_plan(const NormArgs& a, size_t bytes, int params, int64_t most, int resident, int split) {
+Plan make_plan(const NormArgs& a, size_t bytes, int params, int64_t most, int resident, int split, int wide) {
   Plan p;
   constexpr int G = kGroup<X, S, Y>;
   const int64_t phase = reinterpret_cast<uintptr_t>(a.x) / sizeof(X) % G, shift = a.T > 1 ? a.ldx % G : 0;
@@ -235,9 +251,9 @@ Plan make_plan(const NormArgs& a, size_t bytes, int params, int64_t most, int re
     teams = 256 / p.lanes;
     if (E == 32) resident = 512;
   } else {
-    E = lanes_of(16) <= kMaxLanes ? 16 : 32;
+    E = lanes_of(16) < wide ? 16 : 32;
     p.lanes = (lanes_of(E) + 31) / 32 * 32;
-    if (p.lanes > kMaxLanes) return p;
+    if (p.lanes > (E == 32 ? 512 : 1024)) return p;
     if (E == 32) resident = 512;
     // rows for every SM before several for one
     teams = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kMaxTeams, resident / p.lanes, (a.T + sms - 1) / sms})));
@@ -246,12 +262,17 @@ Plan make_plan(const NormArgs& a, size_t bytes, int params, int64_t most, int re
   int per_sm = std::max(1, resident / (teams * p.lanes));
   const size_t fixed = static_cast<size_t>(p.lanes) * E * 4 * params, stage = static_cast<size_t>(p.lanes) * E * bytes;
   auto need = [&] { return per_sm * (fixed + static_cast<size_t>(teams) * p.stages * stage + 6 * 1024); };
+  // rows ahead: up to four, no more than a team has
+  const int64_t rows = (a.T + per_sm * sms * teams - 1) / (per_sm * sms * teams);
+  const int ahead = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(4, rows)));
   for (;;) {
-    for (p.stages = 4; p.stages > 2 && need() > kSharedPerSm;) --p.stages;
+    for (p.stages = ahead; p.stages > 2 && need() > kSharedPerSm;) --p.stages;
     if (need() <= kSharedPerSm) break;
     if (per_sm > 1) --per_sm;
     else if (teams > 1 && !p.split) --teams;
+    else if (p.stages > 1) p.stages = 1;
     else return p;
+    if (p.stages == 1 && need() <= kSharedPerSm) break;
   }
   p.threads = teams * p.lanes;
   p.smem = fixed + static_cast<size_t>(teams) * p.stages * stage;

@@ -1,4 +1,6 @@
-// Gradients of the normalisation of rows.
+// Gradients of the normalisation of rows; the kernels of one pair of types of h and dy are compiled by one file each.
+#pragma once
+
 #include "layernorm.cuh"
 
 namespace moe {
@@ -111,9 +113,9 @@ __global__ void __launch_bounds__(RMS && E <= 16 ? 640 : 512) norm_grad_kernel(N
   int ahead = at.row;
   auto fetch = [&](char* to) {
     if (ahead < T) {
-      fh.copy(to, at, a, a.x, a.ldx);
-      fy.copy(to + at_y, at, a, a.y, a.ldy);
-      if (add) fs.copy(to + at_s, at, a, a.r, a.ldr);
+      fh.copy(to, at, ahead, T);
+      fy.copy(to + at_y, at, ahead, T);
+      if (add) fs.copy(to + at_s, at, ahead, T);
     }
     ahead += at.step;
     cp_async_commit();
@@ -151,18 +153,14 @@ __global__ void __launch_bounds__(RMS && E <= 16 ? 640 : 512) norm_grad_kernel(N
       if (!RMS && !a.rms) next_mean = a.mean[row + at.step];
     }
     wait_stage(a.stages);
-    if (ENDS && at.parts) {     // with dy = 0 outside the row nothing there counts
-      fh.clear_parts(from, at, d);
-      fy.clear_parts(from + at_y, at, d);
-    }
     if (!live) {
       fh.clear(from);
       fy.clear(from + at_y);
     }
     // c and dy of group k
     auto values = [&](int k, float2 (&c)[N], float2 (&dy)[N]) {
-      fh.read(from, k, c);
-      fy.read(from + at_y, k, dy);
+      fh.read(from, k, at, c);
+      fy.read(from + at_y, k, at, dy);     // with dy = 0 outside the row nothing there counts
       if (!RMS)
 #pragma unroll
         for (int j = 0; j < N; ++j) c[j] = add2(c[j], both(-mean));
@@ -196,7 +194,7 @@ __global__ void __launch_bounds__(RMS && E <= 16 ? 640 : 512) norm_grad_kernel(N
       float v[RMS ? 1 : 2];
       v[0] = sgc.x + sgc.y;
       if (!RMS) v[RMS ? 0 : 1] = sg.x + sg.y;
-      row_sum<SPLIT, RMS ? 1 : 2>(v, part, turn, at.lanes, at.lane, at.team);
+      row_sum<SPLIT, RMS ? 1 : 2, 16>(v, part, turn, at.lanes, at.lane, at.team);
       if (live) {
         const float2 c1 = both(RMS || a.rms ? 0.f : -(v[RMS ? 0 : 1] * inv_d) * r), c2 = both(-(v[0] * r * inv_d) * r * r);
 #pragma unroll
@@ -215,11 +213,11 @@ __global__ void __launch_bounds__(RMS && E <= 16 ? 640 : 512) norm_grad_kernel(N
 #pragma unroll
           for (int j = 0; j < N; ++j) g[j] = fma2(c[j], c2, RMS ? mul2(g[j], both(r)) : fma2(g[j], both(r), c1));
           if (add) {
-            fs.read(from + at_s, k, u);
+            fs.read(from + at_s, k, at, u);
 #pragma unroll
             for (int j = 0; j < N; ++j) g[j] = add2(g[j], u[j]);
           }
-          dx.store(k, at, d, g);
+          dx.store(k, at, g);
         }
       }
       dx.row += dx.step;
@@ -286,7 +284,11 @@ cudaError_t launch_grad(const NormArgs& a, const Plan& p, cudaStream_t s) {
 template <typename X, typename S, typename Y>
 cudaError_t launch_backward(NormArgs a, cudaStream_t s) {
   const unsigned cols = static_cast<unsigned>((a.d + 31) / 32);
-  const Plan p = make_plan<X, S, Y>(a, sizeof(X) + sizeof(Y) + (a.r && a.s ? sizeof(S) : 0), 1, a.slots, a.rms && !a.db ? 640 : 512, 16);
+  // With two sums a row, many long rows go faster with 32 elements a thread (32768 x 4096: 128 us against 142), few ones
+  // slower (64 x 4096: 8.6 against 6.3); with one sum there is no difference (8192 x 7168).
+  const bool rms = a.rms && !a.db;
+  const int wide = !rms && a.T >= 16 * device_sm_count() ? 256 : 513;
+  const Plan p = make_plan<X, S, Y>(a, sizeof(X) + sizeof(Y) + (a.r && a.s ? sizeof(S) : 0), 1, a.slots, rms ? 640 : 512, 16, wide);
   a.lanes = p.lanes;
   a.stages = p.stages;
   if (p.elements) {
@@ -308,21 +310,12 @@ cudaError_t launch_backward(NormArgs a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <typename X, typename S>
-cudaError_t launch_y(const NormArgs& a, int32_t y, cudaStream_t s) {
-  return y == MOE_F32 ? launch_backward<X, S, float>(a, s) : launch_backward<X, S, __nv_bfloat16>(a, s);
-}
-template <typename X>
-cudaError_t launch_s(const NormArgs& a, int32_t st, int32_t y, cudaStream_t s) {
-  return st == MOE_F32 ? launch_y<X, float>(a, y, s) : launch_y<X, __nv_bfloat16>(a, y, s);
-}
-
 }  // namespace
 
-cudaError_t launch_layernorm_backward(const NormArgs& a, const moe_layernorm_config& c, cudaStream_t s) {
-  const int32_t stream = a.s ? c.stream_dtype : c.x_dtype;    // without dx: the form of h and dy alone
-  return c.x_dtype == MOE_F32 ? launch_s<float>(a, stream, c.y_dtype, s)
-                              : launch_s<__nv_bfloat16>(a, stream, c.y_dtype, s);
+// The gradients of rows h of X with dy of Y, dsum and dx of the given type.
+template <typename X, typename Y>
+cudaError_t launch_layernorm_grad(const NormArgs& a, int32_t stream_dtype, cudaStream_t s) {
+  return stream_dtype == MOE_F32 ? launch_backward<X, float, Y>(a, s) : launch_backward<X, __nv_bfloat16, Y>(a, s);
 }
 
 }  // namespace moe

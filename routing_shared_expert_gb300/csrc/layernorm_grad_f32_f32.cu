@@ -1,0 +1,6 @@
+// Gradients of the normalisation of fp32 rows for fp32 dy.
+#include "layernorm_grad.cuh"
+
+namespace moe {
+template cudaError_t launch_layernorm_grad<float, float>(const NormArgs&, int32_t, cudaStream_t);
+}  // namespace moe

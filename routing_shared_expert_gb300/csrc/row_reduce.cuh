@@ -16,19 +16,23 @@ __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// Sums of N values over the warps of a team, 16 at most, the same in every thread.  `part` holds N * 16
+// Sums of N values over the warps of a team, W at most, the same in every thread.  `part` holds N * W
 // floats of the team's own; its calls alternate between two of them, so that one barrier per sum is enough.
-template <int N>
+template <int N, int W>
 __device__ __forceinline__ void team_sum(float (&v)[N], float* part, int warp, int warps, int barrier) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
   if (lane == 0)
 #pragma unroll
-    for (int i = 0; i < N; ++i) part[i * 16 + warp] = v[i];
+    for (int i = 0; i < N; ++i) part[i * W + warp] = v[i];
   named_barrier(barrier, warps * 32);
+  const int at = warps > 16 ? lane : lane & 15;
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = (lane & 15) < warps ? part[i * 16 + (lane & 15)] : 0.f;
+  for (int i = 0; i < N; ++i) v[i] = at < warps ? part[i * W + at] : 0.f;
+  if (W > 16 && warps > 16)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1)
 #pragma unroll
@@ -38,7 +42,7 @@ __device__ __forceinline__ void team_sum(float (&v)[N], float* part, int warp, i
 // The same over the whole CTA of at most 512 threads.
 template <int N>
 __device__ __forceinline__ void block_sum(float (&v)[N], float* part) {
-  team_sum<N>(v, part, threadIdx.x >> 5, blockDim.x >> 5, 0);
+  team_sum<N, 16>(v, part, threadIdx.x >> 5, blockDim.x >> 5, 0);
 }
 
 }  // namespace moe

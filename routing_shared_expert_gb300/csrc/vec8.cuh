@@ -39,15 +39,6 @@ __device__ __forceinline__ void round_to(float2 (&v)[N]) {
     for (int i = 0; i < N; ++i) v[i] = unpack2(pack_bf16x2(v[i].x, v[i].y));
 }
 
-// The bytes of a tensor with rows ld elements apart: what may be read.
-struct Extent {
-  uintptr_t lo, hi;
-};
-__device__ __forceinline__ Extent extent_of(const void* p, int64_t rows, int64_t ld, int64_t cols, int elem) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return {a, a + static_cast<uintptr_t>(((rows - 1) * ld + cols) * elem)};
-}
-
 // Begins the copy of a group that lies in its row.
 template <int G, typename T>
 __device__ __forceinline__ void copy_whole(char* dst, const T* src) {
@@ -55,25 +46,26 @@ __device__ __forceinline__ void copy_whole(char* dst, const T* src) {
   if (G * sizeof(T) == 16) cp_async16(smem_u32(dst), src, 16);
   else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
-// The same of elements [e0, e0 + G) of a row of d that reach over one of its ends (src: element e0).  The
-// group is aligned to its size and copied whole, the neighbouring row's values with it, and element by
-// element only at the tensor's own ends.
+// The same of the elements of a group that `mask` has, for the groups at a tensor's own ends, whose other
+// elements may not be read.
 template <int G, typename T>
-__device__ __noinline__ void copy_end(char* dst, const T* src, int e0, int d, Extent t) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(src);
-  if (a >= t.lo && a + G * sizeof(T) <= t.hi) {
-    copy_whole<G>(dst, src);
-    return;
-  }
-#pragma unroll 1
-  for (int j = max(0, -e0); j < min(G, d - e0); ++j) reinterpret_cast<T*>(dst)[j] = src[j];
+__device__ __noinline__ void copy_masked(char* dst, const T* src, unsigned mask) {
+  T v[G];
+#pragma unroll
+  for (int j = 0; j < G; ++j) v[j] = mask >> j & 1 ? src[j] : from_f32<T>(0.f);
+#pragma unroll
+  for (int j = 0; j < G; ++j) reinterpret_cast<T*>(dst)[j] = v[j];
 }
-// Zeros in the places of a copied group that lie outside the row.
 template <int G, typename T>
-__device__ __noinline__ void clear_end(char* at, int e0, int d) {
-#pragma unroll 1
-  for (int j = 0; j < G; ++j)
-    if (e0 + j < 0 || e0 + j >= d) reinterpret_cast<T*>(at)[j] = from_f32<T>(0.f);
+__device__ __forceinline__ void clear_group(char* at) {
+  if (G * sizeof(T) == 16) *reinterpret_cast<uint4*>(at) = make_uint4(0u, 0u, 0u, 0u);
+  else *reinterpret_cast<uint2*>(at) = make_uint2(0u, 0u);
+}
+// Zeros where the mask has none.
+template <int N>
+__device__ __forceinline__ void keep(float2 (&v)[N], unsigned mask) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) v[j] = make_float2(mask >> 2 * j & 1 ? v[j].x : 0.f, mask >> 2 * j & 2 ? v[j].y : 0.f);
 }
 __device__ __forceinline__ void read_group(const char* src, const __nv_bfloat16*, float2 (&v)[4]) {
   const uint4 u = *reinterpret_cast<const uint4*>(src);
@@ -88,18 +80,14 @@ __device__ __forceinline__ void read_group(const char* src, const float*, float2
   v[0] = make_float2(u.x, u.y), v[1] = make_float2(u.z, u.w);
 }
 __device__ __forceinline__ void read_group(const char* src, const float*, float2 (&v)[4]) {}   // never called
-// Stores the part of a group that lies in the row (dst: element e0).
-template <typename T>
-__device__ __noinline__ void store_end4(T* dst, int e0, int d, float2 a, float2 b) {
-  const float v[4] = {a.x, a.y, b.x, b.y};
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (e0 + j >= 0 && e0 + j < d) dst[j] = from_f32<T>(v[j]);
-}
+// Stores the elements that the mask has.
 template <typename T, int N>
-__device__ __forceinline__ void store_end(T* dst, int e0, int d, const float2 (&v)[N]) {
-  store_end4(dst, e0, d, v[0], v[1]);
-  if (N == 4) store_end4(dst + 4, e0 + 4, d, v[N - 2], v[N - 1]);
+__device__ __forceinline__ void store_masked(T* dst, unsigned mask, const float2 (&v)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    if (mask >> 2 * j & 1) dst[2 * j] = from_f32<T>(v[j].x);
+    if (mask >> 2 * j & 2) dst[2 * j + 1] = from_f32<T>(v[j].y);
+  }
 }
 
 }  // namespace moe

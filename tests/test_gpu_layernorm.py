@@ -107,7 +107,8 @@ def check(moe, T, d, kind="layer", x="bf16", stream=None, y="bf16", w="f32", bia
 
 SIZES = [(1, 1), (1, 2), (2, 7), (3, 8), (5, 31), (9, 32), (1, 2048), (2, 129), (33, 64), (17, 255), (130, 256),
          (40, 257), (21, 1000), (700, 96), (65, 1023), (19, 1024), (11, 1025), (7, 2049), (37, 4095), (10, 4096), (13, 7168),
-         (6, 8200), (5, 16384), (4, 16385), (3, 20003), (2, 65536), (1500, 40), (3000, 8), (613, 520)]
+         (6, 8200), (5, 16384), (4, 16385), (3, 20003), (2, 65536), (1500, 40), (3000, 8), (613, 520),
+         (2, 16384), (3, 8640), (1, 5760), (17, 3387), (16, 905), (5, 841), (37, 379), (2000, 227), (400, 13760), (1, 16383)]
 
 
 @pytest.mark.parametrize("T,d", SIZES)

@@ -19,8 +19,8 @@ struct Entry {
   int64_t rows, cols, ldi, ldo;
   int64_t first;          // number of the tensor's first chunk
   int32_t dtype;
-  int16_t lead;           // elements between a 32-byte (fp32) or 16-byte (bf16) boundary and the first one
-  int16_t vec;            // kReads: gradients in groups of eight elements; kWrites: results too
+  int16_t lead;           // elements between a 32-byte boundary and the first one
+  int16_t vec;            // kReads: gradients in groups of 32 bytes; kWrites: results too
 };
 constexpr int16_t kReads = 1, kWrites = 2;
 
@@ -28,7 +28,8 @@ constexpr int16_t kReads = 1, kWrites = 2;
 // table of up to 32 KB.
 constexpr int kShortTable = 56, kLongTable = 500;
 constexpr int kThreads = 256, kGroups = 4;
-constexpr int64_t kChunk = kThreads * kGroups * 8;      // elements
+constexpr int64_t kChunkBytes = kThreads * kGroups * 32;
+__host__ __device__ constexpr int64_t chunk_of(int32_t dtype) { return kChunkBytes / (dtype == MOE_F32 ? 4 : 2); }   // elements
 constexpr int kPerSm = 4;
 constexpr int kSlots = 152 * kPerSm;  // CTAs, at most: one partial sum each
 constexpr size_t kTicketOffset = 64, kPartialOffset = 256;
@@ -70,11 +71,11 @@ __device__ __forceinline__ int entry_of(const Table<N>& t, int64_t chunk) {
   return lo;
 }
 
-// Eight values as they lie in memory: 32 bytes of fp32, 16 of bf16.
+// A group as it lies in memory: 32 bytes, eight fp32 or 16 bf16.
 struct Words {
   uint32_t w[8];
 };
-__device__ __forceinline__ Words load_words(const float* p) {
+__device__ __forceinline__ Words load_words(const void* p) {
   Words r;
   asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]),
@@ -83,17 +84,10 @@ __device__ __forceinline__ Words load_words(const float* p) {
                : "memory");
   return r;
 }
-__device__ __forceinline__ Words load_words(const __nv_bfloat16* p) {
-  Words r;
-  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
-               : "l"(p)
+__device__ __forceinline__ void store_words(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
-  return r;
-}
-template <typename T>
-__device__ __forceinline__ float2 pair(const Words& r, int i) {
-  return sizeof(T) == 4 ? make_float2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1])) : unpack2(r.w[i]);
 }
 
 __device__ __forceinline__ double block_sum_f64(double v, double* part) {
@@ -106,30 +100,48 @@ __device__ __forceinline__ double block_sum_f64(double v, double* part) {
   return v;
 }
 
-// The groups of a chunk: group q of the tensor is its elements 8 q - lead .. 8 q - lead + 7.  f(words, address
-// of the result) takes whole groups, g(i) the elements of groups over the tensor's ends.  Of a dense chunk
-// inside its tensor each thread loads all its groups before any is used.
-template <typename T, typename F, typename G>
-__device__ __forceinline__ void walk_chunk(const Entry& e, int64_t chunk, const F& f, const G& g) {
-  const int64_t n = e.rows * e.cols, i0 = (chunk - e.first) * kChunk - e.lead;
-  const T* in = static_cast<const T*>(e.in);
-  const int mine = 8 * threadIdx.x;
-  if (e.rows == 1 && i0 >= 0 && i0 + kChunk <= n) {
+// The groups of a chunk: group q of the tensor is its elements G q - lead .. G q - lead + G - 1.  f(words, address
+// of the result) takes whole groups, g(i) the elements of groups over the tensor's ends.  Of a dense tensor each
+// thread loads all its groups before any is used; a chunk inside the tensor, apart, needs no bounds.
+template <typename T, typename F, typename H>
+__device__ __forceinline__ void walk_chunk(const Entry& e, int64_t chunk, const F& f, const H& g) {
+  constexpr int G = 32 / sizeof(T), kElements = static_cast<int>(kChunkBytes / sizeof(T));
+  const int64_t n = e.rows * e.cols, i0 = (chunk - e.first) * kElements - e.lead;
+  const T* in = static_cast<const T*>(e.in) + i0;
+  const int mine = G * threadIdx.x;
+  if (e.rows == 1 && i0 >= 0 && i0 + kElements <= n) {
     Words w[kGroups];
 #pragma unroll
-    for (int k = 0; k < kGroups; ++k) w[k] = load_words(in + i0 + mine + 8 * k * kThreads);
+    for (int k = 0; k < kGroups; ++k) w[k] = load_words(in + mine + G * k * kThreads);
 #pragma unroll
-    for (int k = 0; k < kGroups; ++k) f(w[k], i0 + mine + 8 * k * kThreads);
-    return;
-  }
+    for (int k = 0; k < kGroups; ++k) f(w[k], i0 + mine + G * k * kThreads);
+  } else if (e.rows == 1) {
+    // of the chunk's elements those of the tensor, and of those the whole groups
+    const int lo = i0 < 0 ? static_cast<int>(-i0) : 0, hi = static_cast<int>(min(n - i0, int64_t{kElements}));
+    const int first = min((lo + G - 1) / G * G, hi), last = max(first, hi / G * G);
+    Words w[kGroups];
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      const int i = mine + G * k * kThreads;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[k].w[j] = 0u;
+      if (i >= first && i < last) w[k] = load_words(in + i);
+    }
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      const int i = mine + G * k * kThreads;
+      if (i >= first && i < last) f(w[k], i0 + i);
+    }
+    const int j = threadIdx.x;
+    if (j < first - lo) g(i0 + lo + j);
+    if (j < hi - last) g(i0 + last + j);
+  } else {
 #pragma unroll 1
-  for (int k = 0; k < kGroups; ++k) {
-    const int64_t i = i0 + mine + 8 * k * kThreads;
-    if (i >= 0 && i + 8 <= n) {
-      const int64_t row = e.rows == 1 ? 0 : i / e.cols, col = i - row * e.cols;
-      f(load_words(in + row * e.ldi + col), row * e.ldo + col);
-    } else {
-      for (int64_t j = max(i, int64_t{0}); j < min(i + 8, n); ++j) g(j);
+    for (int k = 0; k < kGroups; ++k) {      // rows that begin and end on groups
+      const int64_t i = i0 + mine + G * k * kThreads;
+      if (i + G > n) break;
+      const int64_t row = i / e.cols, col = i - row * e.cols;
+      f(load_words(static_cast<const T*>(e.in) + row * e.ldi + col), row * e.ldo + col);
     }
   }
 }
@@ -153,17 +165,20 @@ __global__ void __launch_bounds__(kThreads, kPerSm) grad_square_kernel(const __g
       acc[0].x += v * v;
     };
     if (!(e.vec & kReads)) {
-      const int64_t i0 = (chunk - e.first) * kChunk, i1 = min(e.rows * e.cols, i0 + kChunk);
+      const int64_t i0 = (chunk - e.first) * chunk_of(e.dtype), i1 = min(e.rows * e.cols, i0 + chunk_of(e.dtype));
       for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) one(i);
     } else if (e.dtype == MOE_F32) {
       walk_chunk<float>(e, chunk, [&](const Words& w, int64_t) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = fma2(pair<float>(w, j), pair<float>(w, j), acc[j]);
+        for (int j = 0; j < 4; ++j) {
+          const float2 v = make_float2(__uint_as_float(w.w[2 * j]), __uint_as_float(w.w[2 * j + 1]));
+          acc[j] = fma2(v, v, acc[j]);
+        }
       }, one);
     } else {
       walk_chunk<__nv_bfloat16>(e, chunk, [&](const Words& w, int64_t) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = fma2(pair<__nv_bfloat16>(w, j), pair<__nv_bfloat16>(w, j), acc[j]);
+        for (int j = 0; j < 8; ++j) acc[j & 3] = fma2(unpack2(w.w[j]), unpack2(w.w[j]), acc[j & 3]);
       }, one);
     }
   }
@@ -191,19 +206,18 @@ __global__ void __launch_bounds__(kThreads, kPerSm) grad_square_kernel(const __g
   }
 }
 
-__device__ __forceinline__ void store_scaled(float* p, const Words& w, float c) {
-  float2 v[4];
+__device__ __forceinline__ void store_scaled(float* p, Words w, float c) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = mul2(pair<float>(w, j), both(c));
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0].x), "f"(v[0].y),
-               "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y)
-               : "memory");
+  for (int j = 0; j < 8; ++j) w.w[j] = __float_as_uint(__uint_as_float(w.w[j]) * c);
+  store_words(p, w.w);
 }
-__device__ __forceinline__ void store_scaled(__nv_bfloat16* p, const Words& w, float c) {
-  float2 v[4];
+__device__ __forceinline__ void store_scaled(__nv_bfloat16* p, Words w, float c) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = mul2(pair<__nv_bfloat16>(w, j), both(c));
-  store_whole(p, v);
+  for (int j = 0; j < 8; ++j) {
+    const float2 v = mul2(unpack2(w.w[j]), both(c));
+    w.w[j] = pack_bf16x2(v.x, v.y);
+  }
+  store_words(p, w.w);
 }
 
 // The chunks last to first: what the norm's reading left in L2 is read again before it is replaced.
@@ -223,8 +237,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) grad_scale_kernel(const __gr
       store_elem(e.out, e.dtype, row * e.ldo + col, coef * load_elem(e.in, e.dtype, row * e.ldi + col));
     };
     if (!(e.vec & kWrites)) {
-      const int64_t base = e.vec & kReads ? e.lead : 0;      // the norm's chunks, which may begin before the tensor
-      const int64_t i0 = (chunk - e.first) * kChunk - base, i1 = min(e.rows * e.cols, i0 + kChunk);
+      const int64_t i0 = (chunk - e.first) * chunk_of(e.dtype) - e.lead, i1 = min(e.rows * e.cols, i0 + chunk_of(e.dtype));
       for (int64_t i = max(i0, int64_t{0}) + threadIdx.x; i < i1; i += kThreads) one(i);
     } else if (e.dtype == MOE_F32) {
       walk_chunk<float>(e, chunk, [&](const Words& w, int64_t i) { store_scaled(static_cast<float*>(e.out) + i, w, coef); },
@@ -315,19 +328,24 @@ template <int N>
 cudaError_t launch_lists(const std::vector<Entry>& list, NormSums sums, bool clip, cudaStream_t s) {
   const size_t n = list.size();
   Table<N> t;
-  auto fill = [&](size_t at) {
+  auto fill = [&](size_t at, bool reads) {
     t.n = static_cast<int32_t>(std::min<size_t>(N, n - at));
     t.chunks = 0;
     for (int32_t i = 0; i < t.n; ++i) {
       t.e[i] = list[at + i];
+      if (reads && t.e[i].ldi == t.e[i].cols) {      // a dense gradient, whatever its result is: the same sums
+        t.e[i].cols *= t.e[i].rows;
+        t.e[i].rows = 1;
+      }
       t.e[i].first = t.chunks;
-      t.chunks += (t.e[i].lead + t.e[i].rows * t.e[i].cols + kChunk - 1) / kChunk;
+      const int64_t size = chunk_of(t.e[i].dtype);
+      t.chunks += (t.e[i].lead + t.e[i].rows * t.e[i].cols + size - 1) / size;
     }
     return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>({t.chunks, kSlots, int64_t{kPerSm} * device_sm_count()})));
   };
   size_t at = 0;
   do {   // a list without elements has one launch too, for the norm of nothing
-    const unsigned grid = fill(at);
+    const unsigned grid = fill(at, true);
     at += t.n;
     const int32_t slots = std::max(sums.used, static_cast<int32_t>(grid));
     if (at >= n) sums.last = slots;
@@ -338,7 +356,7 @@ cudaError_t launch_lists(const std::vector<Entry>& list, NormSums sums, bool cli
   if (!clip) return cudaSuccess;
   // the tables last to first, as the chunks
   for (size_t tables = (n + N - 1) / N; tables > 0; --tables) {
-    const unsigned grid = fill((tables - 1) * N);
+    const unsigned grid = fill((tables - 1) * N, false);
     const cudaError_t e = launch_over(grad_scale_kernel<N>, dim3(grid), kThreads, 0, s, t, static_cast<const float*>(sums.norm));
     if (e != cudaSuccess) return e;
   }
@@ -371,14 +389,13 @@ moe_status run_norm(const moe_tensor* grads, const moe_tensor* out, int32_t coun
       e.ldi = e.ldo = e.cols;
     }
     // in groups: dense from any element on, or rows that begin and end on groups
-    const int64_t align = e.dtype == MOE_F32 ? 32 : 16, b = static_cast<int64_t>(size_of(e.dtype));
-    const int64_t lead = static_cast<int64_t>(reinterpret_cast<uintptr_t>(e.in) % align) / b;
-    if (e.rows == 1 || (lead == 0 && e.cols % 8 == 0 && e.ldi % 8 == 0)) {
-      e.lead = static_cast<int16_t>(lead);
-      e.vec = kReads;
-      if (static_cast<int64_t>(reinterpret_cast<uintptr_t>(e.out) % align) / b == lead && (e.rows == 1 || e.ldo % 8 == 0))
-        e.vec |= kWrites;
-    }
+    const int64_t b = static_cast<int64_t>(size_of(e.dtype)), G = 32 / b;
+    const int64_t lead = static_cast<int64_t>(reinterpret_cast<uintptr_t>(e.in) % 32) / b,
+                  lead_out = static_cast<int64_t>(reinterpret_cast<uintptr_t>(e.out) % 32) / b;
+    const bool rows = lead == 0 && e.cols % G == 0 && e.ldi % G == 0;
+    if (e.ldi == e.cols) e.lead = static_cast<int16_t>(lead);
+    if (e.ldi == e.cols || rows) e.vec = kReads;
+    if (lead_out == lead && (e.rows == 1 || (rows && e.ldo % G == 0))) e.vec |= kWrites;
     list.push_back(e);
   }
   if (reinterpret_cast<uintptr_t>(norm) & 3u || reinterpret_cast<uintptr_t>(workspace) & 255u)

@@ -288,90 +288,94 @@ struct SumArgs {
   Zeros zeros;
 };
 
-// One slice of a table row, by a whole warp: v (columns c to c + 7 of each lane) times the scale, or added to what
-// the row holds.  Rows that do not begin on groups of eight take the values through `turn`, 256 floats of the
-// warp's own, so that neighbouring lanes store neighbouring values.
-template <typename W, bool ALIGNED>
-__device__ __forceinline__ void write_row(const EmbedArgs& a, int64_t row, int c, const float2 (&v)[4], float* turn) {
-  W* p = static_cast<W*>(a.dst) + row * a.ldt + c;
-  float2 u[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) u[j] = mul2(v[j], both(a.scale));
-  if (ALIGNED) {
-    if (c >= a.d) return;
-    if (a.accumulate) {
-      uint32_t w[8];
-      float2 h[4];
-      load8(p, w);
-      unpack8<W>(w, h);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) u[j] = add2(h[j], u[j]);
-    }
-    store8(p, u);
-  } else {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(turn + 8 * lane + 2 * j) = u[j];
-    __syncwarp();
-    p -= 8 * lane;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int i = 32 * j + lane;
-      if (c - 8 * lane + i < a.d) p[i] = from_f32<W>(a.accumulate ? to_f32(p[i]) + turn[i] : turn[i]);
-    }
-    __syncwarp();
-  }
-}
+// A lane's eight columns of a warp's slice, which begins at column c0: neighbours where rows begin on groups of
+// eight (ALIGNED), else 32 apart, so that neighbouring lanes read and write neighbouring values.
 template <bool ALIGNED>
-__device__ __forceinline__ void write_partial(float* p, int c, int d, const float2 (&v)[4], float* turn) {
-  if (ALIGNED) {
-    if (c < d) store8(p + c, v);
-  } else {
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ int column(int c0, int j) {
+  const int lane = threadIdx.x & 31;
+  return ALIGNED ? c0 + 8 * lane + j : c0 + 32 * j + lane;
+}
+__device__ __forceinline__ float& value(float2 (&v)[4], int j) { return j & 1 ? v[j / 2].y : v[j / 2].x; }
+
+template <typename T, bool ALIGNED>
+struct Slice {      // as it is loaded
+  uint32_t w[8];
+  __device__ __forceinline__ void load(const T* row, int c0, int d) {
+    if (ALIGNED) {
+      if (column<true>(c0, 0) < d) load8(row + column<true>(c0, 0), w);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(turn + 8 * lane + 2 * j) = v[j];
-    __syncwarp();
+      for (int j = 0; j < 8; ++j) {
+        const int c = column<false>(c0, j);
+        if (sizeof(T) == 4) w[j] = c < d ? *reinterpret_cast<const uint32_t*>(row + c) : 0u;
+        else w[j] = c < d ? *reinterpret_cast<const uint16_t*>(row + c) : 0u;
+      }
+    }
+  }
+  __device__ __forceinline__ void unpack(float2 (&v)[4]) const {
+    if (ALIGNED) {
+      unpack8<T>(w, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) value(v, j) = __uint_as_float(sizeof(T) == 4 ? w[j] : w[j] << 16);
+    }
+  }
+};
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ void store_slice(T* row, int c0, int d, float2 (&v)[4]) {
+  if (ALIGNED) {
+    if (column<true>(c0, 0) < d) store8(row + column<true>(c0, 0), v);
+  } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (c - 8 * lane + 32 * j + lane < d) p[c - 8 * lane + 32 * j + lane] = turn[32 * j + lane];
-    __syncwarp();
+      if (column<false>(c0, j) < d) row[column<false>(c0, j)] = from_f32<T>(value(v, j));
   }
 }
 
+// One slice of a table row: v times the scale, or added to what the row holds.
+template <typename W, bool ALIGNED>
+__device__ __forceinline__ void write_row(const EmbedArgs& a, int64_t row, int c0, const float2 (&v)[4]) {
+  W* p = static_cast<W*>(a.dst) + row * a.ldt;
+  float2 u[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) u[j] = mul2(v[j], both(a.scale));
+  if (a.accumulate) {
+    Slice<W, ALIGNED> held;
+    float2 h[4];
+    held.load(p, c0, a.d);
+    held.unpack(h);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) u[j] = add2(h[j], u[j]);
+  }
+  store_slice<W, ALIGNED>(p, c0, a.d, u);
+}
+
 template <typename Y, typename W, bool ALIGNED>
-__device__ __forceinline__ void sum_chunk(const SumArgs& s, int chunk, int c, float* turn) {
+__device__ __forceinline__ void sum_chunk(const SumArgs& s, int chunk, int c0) {
   const EmbedArgs& a = s.e;
   const int lane = threadIdx.x & 31;
   const int i0 = chunk * kChunk, n = min(kChunk, s.T - i0);
   const int2 mine = lane < n ? s.list[i0 + lane] : make_int2(static_cast<int>(a.V), 0);
   const int entering = i0 > 0 ? s.list[i0 - 1].x : -1, leaving = i0 + n < s.T ? s.list[i0 + n].x : -1;
-  const bool on = c < a.d;
-  const Span span = span_of(a.src, a.T, a.ldo, a.d, sizeof(Y));
+  float* const partial = s.partial + static_cast<int64_t>(chunk) * 2 * a.d;
   float2 acc[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
   bool first = true;       // of the chunk's runs
   int row = __shfl_sync(0xffffffffu, mine.x, 0);
-  constexpr int kAhead = ALIGNED ? 8 : 4;      // tokens on their way
+  constexpr int kAhead = 8;      // tokens on their way
   for (int b = 0; b < kChunk && row < a.V; b += kAhead) {
+    Slice<Y, ALIGNED> w[kAhead];
     int rows[kAhead];
-    const Y* p[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       rows[j] = __shfl_sync(0xffffffffu, mine.x, b + j);
-      p[j] = static_cast<const Y*>(a.src) + __shfl_sync(0xffffffffu, mine.y, b + j) * a.ldo + c;
+      const int t = __shfl_sync(0xffffffffu, mine.y, b + j);
+      if (rows[j] < a.V) w[j].load(static_cast<const Y*>(a.src) + t * a.ldo, c0, a.d);
     }
-    uint32_t w[ALIGNED ? kAhead : 1][8];
-    Raw8 raw[ALIGNED ? 1 : kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-      if (rows[j] < a.V && on) {
-        if (ALIGNED) load8(p[j], w[ALIGNED ? j : 0]);
-        else raw[ALIGNED ? 0 : j] = load8_raw(p[j], span);
-      }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (rows[j] != row) {        // the run ends before this token
-        if (first && row == entering) write_partial<ALIGNED>(s.partial + static_cast<int64_t>(chunk) * 2 * a.d, c, a.d, acc, turn);
-        else write_row<W, ALIGNED>(a, row, c, acc, turn);
+        if (first && row == entering) store_slice<float, ALIGNED>(partial, c0, a.d, acc);
+        else write_row<W, ALIGNED>(a, row, c0, acc);
         first = false;
         row = rows[j];
 #pragma unroll
@@ -379,29 +383,19 @@ __device__ __forceinline__ void sum_chunk(const SumArgs& s, int chunk, int c, fl
       }
       if (row >= a.V) break;
       float2 v[4];
-      if (ALIGNED) {
-        unpack8<Y>(w[ALIGNED ? j : 0], v);
-      } else {
-        float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (on) take8(raw[ALIGNED ? 0 : j], p[j], min(8, a.d - c), u);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = make_float2(u[2 * i], u[2 * i + 1]);
-      }
+      w[j].unpack(v);
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i] = add2(acc[i], v[i]);
     }
   }
   if (row >= a.V) return;
   const bool enters = first && row == entering;
-  if (enters || row == leaving)
-    write_partial<ALIGNED>(s.partial + (static_cast<int64_t>(chunk) * 2 + (enters ? 0 : 1)) * a.d, c, a.d, acc, turn);
-  else
-    write_row<W, ALIGNED>(a, row, c, acc, turn);
+  if (enters || row == leaving) store_slice<float, ALIGNED>(partial + (enters ? 0 : a.d), c0, a.d, acc);
+  else write_row<W, ALIGNED>(a, row, c0, acc);
 }
 
 template <typename Y, typename W, bool ALIGNED>
 __global__ void __launch_bounds__(256, 2) embed_sum_kernel(SumArgs s) {
-  __shared__ float turn[ALIGNED ? 1 : 8][ALIGNED ? 1 : kColumns];
   launch_dependents();
   wait_for_previous();
   if (blockIdx.x >= s.sum_ctas) {
@@ -411,32 +405,28 @@ __global__ void __launch_bounds__(256, 2) embed_sum_kernel(SumArgs s) {
   const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int chunk = static_cast<int>(item / s.slices);
   if (chunk >= s.chunks) return;
-  sum_chunk<Y, W, ALIGNED>(s, chunk, static_cast<int>(item - static_cast<int64_t>(chunk) * s.slices) * kColumns + 8 * (threadIdx.x & 31),
-                           turn[ALIGNED ? 0 : threadIdx.x >> 5]);
+  sum_chunk<Y, W, ALIGNED>(s, chunk, static_cast<int>(item - static_cast<int64_t>(chunk) * s.slices) * kColumns);
 }
 
 // Partial sums of chunks [b0, b1) of the run that begins in chunk `from`, in order.
 template <bool ALIGNED>
-__device__ __forceinline__ void add_partials(const SumArgs& s, int from, int b0, int b1, int c, float2 (&acc)[4]) {
+__device__ __forceinline__ void add_partials(const SumArgs& s, int from, int b0, int b1, int c0, float2 (&acc)[4]) {
   const int d = s.e.d;
 #pragma unroll
   for (int j = 0; j < 4; ++j) acc[j] = both(0.f);
-  if (c >= d) return;
-#pragma unroll 8
-  for (int b = b0; b < b1; ++b) {
-    const float* p = s.partial + (static_cast<int64_t>(b) * 2 + (b == from ? 1 : 0)) * d + c;
-    float2 u[4];
-    if (ALIGNED) {
-      uint32_t w[8];
-      load8(p, w);
-      unpack8<float>(w, u);
-    } else {
+  for (int b = b0; b < b1; b += 8) {
+    Slice<float, ALIGNED> w[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        u[j] = make_float2(c + 2 * j < d ? p[2 * j] : 0.f, c + 2 * j + 1 < d ? p[2 * j + 1] : 0.f);
-    }
+    for (int k = 0; k < 8; ++k)
+      if (b + k < b1) w[k].load(s.partial + (static_cast<int64_t>(b + k) * 2 + (b + k == from ? 1 : 0)) * d, c0, d);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] = add2(acc[j], u[j]);
+    for (int k = 0; k < 8; ++k)
+      if (b + k < b1) {
+        float2 u[4];
+        w[k].unpack(u);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = add2(acc[j], u[j]);
+      }
   }
 }
 
@@ -447,7 +437,7 @@ constexpr int kAlone = 32;
 
 template <typename W, bool ALIGNED>
 __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs s) {
-  __shared__ float part[8][kColumns + 8];
+  __shared__ float2 part[8][4][32];
   __shared__ int long_row[8], long_end[8];
   wait_for_previous();
   const unsigned groups = (s.chunks + 7) / 8;
@@ -457,7 +447,7 @@ __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs s) {
   }
   const EmbedArgs& a = s.e;
   const int group = blockIdx.x % groups, slice = blockIdx.x / groups;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = slice * kColumns + 8 * lane;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = slice * kColumns;
   const int chunk = group * 8 + warp, first = chunk * kChunk, next = first + kChunk;
   int row = -1, end = 0;           // the run's row, and the chunk behind the last that it enters
   if (next < s.T) {
@@ -483,23 +473,23 @@ __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs s) {
   }
   float2 acc[4];
   if (alone) {
-    add_partials<ALIGNED>(s, chunk, chunk, end, c, acc);
-    write_row<W, ALIGNED>(a, row, c, acc, part[warp]);
+    add_partials<ALIGNED>(s, chunk, chunk, end, c0, acc);
+    write_row<W, ALIGNED>(a, row, c0, acc);
   }
   __syncthreads();
   for (int k = 0; k < 8; ++k) {
     if (long_row[k] < 0) continue;
     const int from = group * 8 + k, to = long_end[k], per = (to - from + 7) / 8, b0 = from + warp * per;
-    add_partials<ALIGNED>(s, from, min(b0, to), min(to, b0 + per), c, acc);
+    add_partials<ALIGNED>(s, from, min(b0, to), min(to, b0 + per), c0, acc);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(&part[warp][8 * lane + 2 * j]) = acc[j];
+    for (int j = 0; j < 4; ++j) part[warp][j][lane] = acc[j];
     __syncthreads();
     if (warp == 0) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int w = 1; w < 8; ++w) acc[j] = add2(acc[j], *reinterpret_cast<const float2*>(&part[w][8 * lane + 2 * j]));
-      write_row<W, ALIGNED>(a, long_row[k], c, acc, part[0]);
+        for (int w = 1; w < 8; ++w) acc[j] = add2(acc[j], part[w][j][lane]);
+      write_row<W, ALIGNED>(a, long_row[k], c0, acc);
     }
     __syncthreads();
   }

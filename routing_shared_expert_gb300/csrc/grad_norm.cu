@@ -17,16 +17,15 @@ struct Entry {
   const void* in;
   void* out;
   int64_t rows, cols, ldi, ldo;
-  int64_t first;          // number of the tensor's first chunk
   int32_t dtype;
   int16_t lead;           // elements between a 32-byte boundary and the first one
   int16_t vec;            // kReads: gradients in groups of 32 bytes; kWrites: results too
 };
 constexpr int16_t kReads = 1, kWrites = 2;
 
-// Tensors of one launch: the table is its argument.  56 of them fit into 4 KB; longer lists take a
-// table of up to 32 KB.
-constexpr int kShortTable = 56, kLongTable = 500;
+// Tensors of one launch: the table is its argument.  60 of them fit into 4 KB; longer lists take a table
+// of up to 32 KB.
+constexpr int kShortTable = 60, kLongTable = 500;
 constexpr int kThreads = 256, kGroups = 4;
 constexpr int64_t kChunkBytes = kThreads * kGroups * 32;
 __host__ __device__ constexpr int64_t chunk_of(int32_t dtype) { return kChunkBytes / (dtype == MOE_F32 ? 4 : 2); }   // elements
@@ -37,8 +36,8 @@ constexpr size_t kWorkspace = kPartialOffset + kSlots * sizeof(double);
 
 template <int N>
 struct Table {
-  int64_t chunks;
-  int32_t n;
+  int32_t chunks, n;
+  int32_t first[N];       // number of each tensor's first chunk
   Entry e[N];
 };
 
@@ -61,11 +60,11 @@ __device__ __forceinline__ void store_elem(void* p, int32_t dtype, int64_t i, fl
 
 // The tensor that a chunk belongs to: the last one whose first chunk is not after it.
 template <int N>
-__device__ __forceinline__ int entry_of(const Table<N>& t, int64_t chunk) {
+__device__ __forceinline__ int entry_of(const Table<N>& t, int chunk) {
   int lo = 0, hi = t.n;
   while (hi - lo > 1) {
     const int m = (lo + hi) / 2;
-    if (t.e[m].first <= chunk) lo = m;
+    if (t.first[m] <= chunk) lo = m;
     else hi = m;
   }
   return lo;
@@ -104,9 +103,9 @@ __device__ __forceinline__ double block_sum_f64(double v, double* part) {
 // of the result) takes whole groups, g(i) the elements of groups over the tensor's ends.  Of a dense tensor each
 // thread loads all its groups before any is used; a chunk inside the tensor, apart, needs no bounds.
 template <typename T, typename F, typename H>
-__device__ __forceinline__ void walk_chunk(const Entry& e, int64_t chunk, const F& f, const H& g) {
+__device__ __forceinline__ void walk_chunk(const Entry& e, int chunk, const F& f, const H& g) {
   constexpr int G = 32 / sizeof(T), kElements = static_cast<int>(kChunkBytes / sizeof(T));
-  const int64_t n = e.rows * e.cols, i0 = (chunk - e.first) * kElements - e.lead;
+  const int64_t n = e.rows * e.cols, i0 = static_cast<int64_t>(chunk) * kElements - e.lead;
   const T* in = static_cast<const T*>(e.in) + i0;
   const int mine = G * threadIdx.x;
   if (e.rows == 1 && i0 >= 0 && i0 + kElements <= n) {
@@ -154,18 +153,22 @@ __global__ void __launch_bounds__(kThreads, kPerSm) grad_square_kernel(const __g
   __shared__ bool join;
   launch_dependents();
   float2 acc[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
-  int at = entry_of(t, blockIdx.x);
+  // a CTA's chunks are neighbours: few tensors each
+  const int c0 = static_cast<int>(static_cast<int64_t>(t.chunks) * blockIdx.x / gridDim.x),
+            c1 = static_cast<int>(static_cast<int64_t>(t.chunks) * (blockIdx.x + 1) / gridDim.x);
+  int at = entry_of(t, c0);
   wait_for_previous();
-  for (int64_t chunk = blockIdx.x; chunk < t.chunks; chunk += gridDim.x) {
-    while (at + 1 < t.n && t.e[at + 1].first <= chunk) ++at;
+  for (int c = c0; c < c1; ++c) {
+    while (at + 1 < t.n && t.first[at + 1] <= c) ++at;
     const Entry& e = t.e[at];
+    const int chunk = c - t.first[at];
     auto one = [&](int64_t i) {
       const int64_t row = e.rows == 1 ? 0 : i / e.cols;
       const float v = load_elem(e.in, e.dtype, row * e.ldi + (i - row * e.cols));
       acc[0].x += v * v;
     };
     if (!(e.vec & kReads)) {
-      const int64_t i0 = (chunk - e.first) * chunk_of(e.dtype), i1 = min(e.rows * e.cols, i0 + chunk_of(e.dtype));
+      const int64_t i0 = chunk * chunk_of(e.dtype), i1 = min(e.rows * e.cols, i0 + chunk_of(e.dtype));
       for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) one(i);
     } else if (e.dtype == MOE_F32) {
       walk_chunk<float>(e, chunk, [&](const Words& w, int64_t) {
@@ -220,24 +223,26 @@ __device__ __forceinline__ void store_scaled(__nv_bfloat16* p, Words w, float c)
   store_words(p, w.w);
 }
 
-// The chunks last to first: what the norm's reading left in L2 is read again before it is replaced.
+// Each CTA's chunks last to first: what the norm's reading left in L2 is read again before it is replaced.
 template <int N>
 __global__ void __launch_bounds__(kThreads, kPerSm) grad_scale_kernel(const __grid_constant__ Table<N> t, const float* norm) {
   launch_dependents();
-  int at = entry_of(t, t.chunks - 1 - blockIdx.x);
+  const int c0 = static_cast<int>(static_cast<int64_t>(t.chunks) * blockIdx.x / gridDim.x),
+            c1 = static_cast<int>(static_cast<int64_t>(t.chunks) * (blockIdx.x + 1) / gridDim.x);
+  int at = entry_of(t, c1 - 1);
   wait_for_previous();
   const float coef = norm[1];
-  for (int64_t k = blockIdx.x; k < t.chunks; k += gridDim.x) {
-    const int64_t chunk = t.chunks - 1 - k;
-    while (at > 0 && t.e[at].first > chunk) --at;
+  for (int c = c1 - 1; c >= c0; --c) {
+    while (t.first[at] > c) --at;
     const Entry& e = t.e[at];
+    const int chunk = c - t.first[at];
     if (coef == 1.f && e.in == e.out) continue;
     auto one = [&](int64_t i) {
       const int64_t row = e.rows == 1 ? 0 : i / e.cols, col = i - row * e.cols;
       store_elem(e.out, e.dtype, row * e.ldo + col, coef * load_elem(e.in, e.dtype, row * e.ldi + col));
     };
     if (!(e.vec & kWrites)) {
-      const int64_t i0 = (chunk - e.first) * chunk_of(e.dtype) - e.lead, i1 = min(e.rows * e.cols, i0 + chunk_of(e.dtype));
+      const int64_t i0 = chunk * chunk_of(e.dtype) - e.lead, i1 = min(e.rows * e.cols, i0 + chunk_of(e.dtype));
       for (int64_t i = max(i0, int64_t{0}) + threadIdx.x; i < i1; i += kThreads) one(i);
     } else if (e.dtype == MOE_F32) {
       walk_chunk<float>(e, chunk, [&](const Words& w, int64_t i) { store_scaled(static_cast<float*>(e.out) + i, w, coef); },
@@ -330,18 +335,19 @@ cudaError_t launch_lists(const std::vector<Entry>& list, NormSums sums, bool cli
   Table<N> t;
   auto fill = [&](size_t at, bool reads) {
     t.n = static_cast<int32_t>(std::min<size_t>(N, n - at));
-    t.chunks = 0;
+    int64_t chunks = 0;
     for (int32_t i = 0; i < t.n; ++i) {
       t.e[i] = list[at + i];
       if (reads && t.e[i].ldi == t.e[i].cols) {      // a dense gradient, whatever its result is: the same sums
         t.e[i].cols *= t.e[i].rows;
         t.e[i].rows = 1;
       }
-      t.e[i].first = t.chunks;
+      t.first[i] = static_cast<int32_t>(chunks);
       const int64_t size = chunk_of(t.e[i].dtype);
-      t.chunks += (t.e[i].lead + t.e[i].rows * t.e[i].cols + size - 1) / size;
+      chunks += (t.e[i].lead + t.e[i].rows * t.e[i].cols + size - 1) / size;
     }
-    return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>({t.chunks, kSlots, int64_t{kPerSm} * device_sm_count()})));
+    t.chunks = static_cast<int32_t>(chunks);     // 2^40 elements at most: 2^27 chunks, and one more per tensor
+    return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>({chunks, kSlots, int64_t{kPerSm} * device_sm_count()})));
   };
   size_t at = 0;
   do {   // a list without elements has one launch too, for the norm of nothing

@@ -414,13 +414,14 @@ __device__ __forceinline__ void add_partials(const SumArgs& s, int from, int b0,
   const int d = s.e.d;
 #pragma unroll
   for (int j = 0; j < 4; ++j) acc[j] = both(0.f);
-  for (int b = b0; b < b1; b += 8) {
-    Slice<float, ALIGNED> w[8];
+  constexpr int kAhead = 4;
+  for (int b = b0; b < b1; b += kAhead) {
+    Slice<float, ALIGNED> w[kAhead];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < kAhead; ++k)
       if (b + k < b1) w[k].load(s.partial + (static_cast<int64_t>(b + k) * 2 + (b + k == from ? 1 : 0)) * d, c0, d);
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < kAhead; ++k)
       if (b + k < b1) {
         float2 u[4];
         w[k].unpack(u);

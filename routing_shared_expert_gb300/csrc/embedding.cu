@@ -7,8 +7,8 @@ namespace moe {
 namespace {
 
 // A warp per token and slice of kSlice columns, its four loads of eight values per lane on their way at
-// once; of rows of at most 256 columns (SHORT, ALIGNED ones) the four loads and a row's unused lanes go to further tokens.
-// Bound by HBM where rows are long: the rows of frequent tokens come from L2.  ALIGNED: rows of the table and
+// once; of rows of at most 256 columns (SHORT) the four loads, and a row's unused lanes where rows are aligned, go to
+// further tokens.  Bound by HBM where rows are long: the rows of frequent tokens come from L2.  ALIGNED: rows of the table and
 // of out begin on groups of eight and end on one; else the groups are those of out, and the table's values
 // are moved into place.
 constexpr int kSlice = 1024;
@@ -50,6 +50,26 @@ __global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a, int slices, int
       for (int j = 0; j < 4; ++j) u[j] = v[SHORT ? k : 0] < 0 ? both(0.f) : mul2(u[j], scale);
       store8(static_cast<Y*>(a.dst) + t * a.ldo + c, u);
     }
+  } else if (SHORT) {
+    Slice<W, false> w[4];
+    int64_t v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t t = item * 4 + k;
+      v[k] = t < a.T ? token_row(static_cast<const I*>(a.ids), t, a.V, lane == 0 ? a.status : nullptr) : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (v[k] >= 0) w[k].load(static_cast<const W*>(a.src) + v[k] * a.ldt, 0, a.d);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (item * 4 + k >= a.T) break;
+      float2 u[4];
+      w[k].unpack(u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[j] = v[k] < 0 ? both(0.f) : mul2(u[j], scale);
+      store_slice<Y, false>(static_cast<Y*>(a.dst) + (item * 4 + k) * a.ldo, 0, a.d, u);
+    }
   } else {
     const int64_t t = item / slices;
     const int c0 = static_cast<int>(item - t * slices) * kSlice;
@@ -88,12 +108,14 @@ template <typename I, typename W, typename Y>
 cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t s) {
   const bool aligned = groups_of_eight<W>(a.src, a.ldt, a.d) && groups_of_eight<Y>(a.dst, a.ldo, a.d);
   // several tokens to a warp where there are warps enough for all SMs
-  if (aligned && a.d <= 256 && a.T >= 4096) {
+  if (a.d <= kColumns && a.T >= 4096) {
     int lanes = 32;
-    while (8 * (lanes / 2) >= a.d) lanes /= 2;
+    while (aligned && 8 * (lanes / 2) >= a.d) lanes /= 2;
     const int tokens = 32 / lanes;
     const int64_t items = (a.T + 4 * tokens - 1) / (4 * tokens);
-    return launch_over(embed_kernel<I, W, Y, true, true>, dim3(static_cast<unsigned>((items + 7) / 8)), 256, 0, s, a, tokens, items);
+    const dim3 grid(static_cast<unsigned>((items + 7) / 8));
+    return aligned ? launch_over(embed_kernel<I, W, Y, true, true>, grid, 256, 0, s, a, tokens, items)
+                   : launch_over(embed_kernel<I, W, Y, false, true>, grid, 256, 0, s, a, 1, items);
   }
   const int slices = (a.d + kSlice - 1) / kSlice;
   const int64_t items = a.T * slices;

@@ -69,6 +69,52 @@ __device__ __forceinline__ void unpack8(const uint32_t (&w)[8], float2 (&v)[4]) 
     v[j] = sizeof(T) == 4 ? make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1])) : unpack2(w[j]);
 }
 
+constexpr int kColumns = 256;      // of a warp at a time
+
+// A lane's eight columns of a warp's slice, which begins at column c0: neighbours where rows begin on groups of
+// eight (ALIGNED), else 32 apart, so that neighbouring lanes read and write neighbouring values.
+template <bool ALIGNED>
+__device__ __forceinline__ int column(int c0, int j) {
+  const int lane = threadIdx.x & 31;
+  return ALIGNED ? c0 + 8 * lane + j : c0 + 32 * j + lane;
+}
+__device__ __forceinline__ float& value(float2 (&v)[4], int j) { return j & 1 ? v[j / 2].y : v[j / 2].x; }
+
+template <typename T, bool ALIGNED>
+struct Slice {      // as it is loaded
+  uint32_t w[8];
+  __device__ __forceinline__ void load(const T* row, int c0, int d) {
+    if (ALIGNED) {
+      if (column<true>(c0, 0) < d) load8(row + column<true>(c0, 0), w);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = column<false>(c0, j);
+        if (sizeof(T) == 4) w[j] = c < d ? *reinterpret_cast<const uint32_t*>(row + c) : 0u;
+        else w[j] = c < d ? *reinterpret_cast<const uint16_t*>(row + c) : 0u;
+      }
+    }
+  }
+  __device__ __forceinline__ void unpack(float2 (&v)[4]) const {
+    if (ALIGNED) {
+      unpack8<T>(w, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) value(v, j) = __uint_as_float(sizeof(T) == 4 ? w[j] : w[j] << 16);
+    }
+  }
+};
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ void store_slice(T* row, int c0, int d, float2 (&v)[4]) {
+  if (ALIGNED) {
+    if (column<true>(c0, 0) < d) store8(row + column<true>(c0, 0), v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (column<false>(c0, j) < d) row[column<false>(c0, j)] = from_f32<T>(value(v, j));
+  }
+}
+
 // The gradient of the table (embedding_grad.cu), and the scratch memory that it takes.
 size_t embedding_scratch(int64_t T, int64_t V, int32_t d);
 cudaError_t launch_embedding_backward(const EmbedArgs& a, const moe_embedding_config& c, cudaStream_t s);

@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_small_kernel(SortArgs a) {
 
 // ------------------------------------------------------------------------- sums --
 
-constexpr int kChunk = 32, kColumns = 256;      // tokens and columns of a warp
+constexpr int kChunk = 32;      // tokens of a warp
 struct SumArgs {
   EmbedArgs e;
   const int2* list;        // (row, token), sorted; row V behind the last: no token
@@ -287,50 +287,6 @@ struct SumArgs {
   unsigned sum_ctas;       // of the launch; those behind them write zeros
   Zeros zeros;
 };
-
-// A lane's eight columns of a warp's slice, which begins at column c0: neighbours where rows begin on groups of
-// eight (ALIGNED), else 32 apart, so that neighbouring lanes read and write neighbouring values.
-template <bool ALIGNED>
-__device__ __forceinline__ int column(int c0, int j) {
-  const int lane = threadIdx.x & 31;
-  return ALIGNED ? c0 + 8 * lane + j : c0 + 32 * j + lane;
-}
-__device__ __forceinline__ float& value(float2 (&v)[4], int j) { return j & 1 ? v[j / 2].y : v[j / 2].x; }
-
-template <typename T, bool ALIGNED>
-struct Slice {      // as it is loaded
-  uint32_t w[8];
-  __device__ __forceinline__ void load(const T* row, int c0, int d) {
-    if (ALIGNED) {
-      if (column<true>(c0, 0) < d) load8(row + column<true>(c0, 0), w);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int c = column<false>(c0, j);
-        if (sizeof(T) == 4) w[j] = c < d ? *reinterpret_cast<const uint32_t*>(row + c) : 0u;
-        else w[j] = c < d ? *reinterpret_cast<const uint16_t*>(row + c) : 0u;
-      }
-    }
-  }
-  __device__ __forceinline__ void unpack(float2 (&v)[4]) const {
-    if (ALIGNED) {
-      unpack8<T>(w, v);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) value(v, j) = __uint_as_float(sizeof(T) == 4 ? w[j] : w[j] << 16);
-    }
-  }
-};
-template <typename T, bool ALIGNED>
-__device__ __forceinline__ void store_slice(T* row, int c0, int d, float2 (&v)[4]) {
-  if (ALIGNED) {
-    if (column<true>(c0, 0) < d) store8(row + column<true>(c0, 0), v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (column<false>(c0, j) < d) row[column<false>(c0, j)] = from_f32<T>(value(v, j));
-  }
-}
 
 // One slice of a table row: v times the scale, or added to what the row holds.
 template <typename W, bool ALIGNED>

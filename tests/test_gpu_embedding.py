@@ -65,7 +65,8 @@ SIZES = [(1, 1, 1), (1, 7, 8), (2, 3, 5), (5, 100, 64), (31, 10, 33), (32, 1000,
          (257, 4097, 96), (1000, 50, 40), (2049, 300, 130), (4095, 5000, 64), (4096, 70000, 24), (4097, 5000, 64),
          (8192, 100, 72), (9001, 66000, 40), (20000, 3001, 136), (40000, 131073, 16), (70001, 513, 8), (131072, 2, 32),
          (150000, 200000, 9), (513, 300, 2051), (6000, 900, 2560),
-         (5001, 300, 8), (4999, 300, 128), (7000, 40, 136), (9000, 3000, 256), (4100, 600000, 8), (4096, 300, 16)]
+         (5001, 300, 8), (4999, 300, 128), (7000, 40, 136), (9000, 3000, 256), (4100, 600000, 8), (4096, 300, 16),
+         (5003, 70, 1), (4999, 300, 33), (6001, 200, 255)]
 
 
 @pytest.mark.parametrize("T,V,d", SIZES)

@@ -8,7 +8,14 @@
 Every product, the dropout, the balance loss and all gradients run in the library; torch holds the
 buffers, forms the difference to the target and applies plain gradient descent.
 
-    python examples/train_block.py [--steps 20] [--tokens 512]
+With --embedded the block is fed by token numbers, normalised in front of each half, and its gradients are clipped
+to a global norm:
+
+    x   = sqrt(d) table[ids]
+    h   = x + (norm_1(x) W_o^T + b_o)
+    out = h + dropout(MoE(norm_2(h)))
+
+    python examples/train_block.py [--steps 20] [--tokens 512] [--embedded]
 """
 import argparse
 import os
@@ -71,7 +78,7 @@ class Block:
         # the sum over a token's features in place of the mean keeps gradients within bf16's reach
         grads = self.backward(diff / self.spec.T)
         for name, grad in grads.items():
-            w = getattr(self, name, None) if name in ("W_o", "b_o") else self.weights[name]
+            w = self.weights[name] if name in self.weights else getattr(self, name)
             w.sub_(self.lr * grad.view(w.shape))
         self.rng[1] += 1          # another mask next time
         return loss, self.bal.clone()
@@ -81,14 +88,71 @@ class Block:
                    abs(self.moe.moe_read_status(self.proj_ws)), abs(self.moe.moe_read_status(self.bal_ws)))
 
 
+class EmbeddedBlock(Block):
+    """The block on token numbers, with normalised halves and clipped gradients."""
+
+    def __init__(self, spec, seq_len, vocab=1000, max_norm=1.0, eps=1e-6, seed=0, device="cuda", **kw):
+        super().__init__(spec, seq_len, seed=seed, device=device, **kw)
+        moe, T, d = self.moe, spec.T, spec.d_model
+        self.eps, self.max_norm, self.scale = eps, max_norm, d ** 0.5
+        g = torch.Generator(device=device).manual_seed(seed + 2)
+        self.ids = torch.randint(0, vocab, (T,), generator=g, device=device)
+        self.ids[-1] = -1            # a padded place: a row of zeros, no gradient
+        self.table = torch.randn((vocab, d), generator=g, device=device) * d ** -0.5
+        self.norm_1, self.norm_2 = torch.ones(d, device=device), torch.ones(d, device=device)
+        f32, bf16 = dict(device=device), dict(dtype=torch.bfloat16, device=device)
+        self.xn, self.hn = torch.empty((T, d), **bf16), torch.empty((T, d), **bf16)
+        self.rstd_1, self.rstd_2 = torch.empty(T, **f32), torch.empty(T, **f32)
+        self.dh32, self.de = torch.empty((T, d), **f32), torch.empty((T, d), **bf16)
+        self.dnorm_1, self.dnorm_2 = torch.empty(d, **f32), torch.empty(d, **f32)
+        self.dtable, self.grad_norm = torch.empty_like(self.table), torch.empty(2, **f32)
+        self.emb_ws = moe.alloc_embedding_workspace(T, vocab, d, device)
+        self.norm_ws = moe.alloc_layernorm_workspace(T, d, device)
+        self.clip_ws = moe.alloc_grad_norm_workspace(device)
+
+    def forward(self):
+        m = self.moe
+        m.moe_embedding_forward(self.ids, self.table, self.scale, self.x, self.emb_ws)
+        m.moe_layernorm_forward(self.x, None, self.norm_1, None, self.eps, None, self.xn, None, self.rstd_1, kind="rms")
+        m.moe_linear_forward(self.proj, self.xn, self.W_o, self.b_o, self.x, None, self.h, self.proj_ws)
+        m.moe_layernorm_forward(self.h, None, self.norm_2, None, self.eps, None, self.hn, None, self.rstd_2, kind="rms")
+        y = self.layer.forward(self.hn)
+        m.moe_dropout_add(y, self.h, self.p, self.rng, self.out)
+        m.moe_balance_loss(self.layer.cfg, self.layer.out["logits"], self.layer.out["topk_idx"], None, self.seq_len,
+                           self.coef_balance, self.coef_z, None, None, None, self.bal, self.dlogits, self.bal_ws)
+        return self.out
+
+    def backward(self, dout):
+        """Gradients of every weight for the gradient dout of out and the balance loss, clipped together."""
+        m = self.moe
+        m.moe_dropout_backward(dout, self.p, self.rng, self.dy)
+        grads = dict(self.layer.backward(self.hn, self.dy, router_grad=True, dlogits=self.dlogits))
+        # the stream's own gradient passes beside the layer and joins behind the normalisation
+        m.moe_layernorm_backward(self.h, self.norm_2, None, self.rstd_2, grads.pop("dx"), dout, self.dh32, self.dnorm_2,
+                                 None, self.norm_ws, kind="rms")
+        dh = self.dh32.bfloat16()
+        m.moe_linear_backward(self.proj, self.xn, self.W_o, None, dh, self.dx, self.dW_o, self.db_o, self.proj_ws)
+        m.moe_layernorm_backward(self.x, self.norm_1, None, self.rstd_1, self.dx, dh, self.de, self.dnorm_1, None,
+                                 self.norm_ws, kind="rms")
+        m.moe_embedding_backward(self.ids, self.de, self.scale, self.dtable, self.emb_ws)
+        grads = {**{k[1:]: v for k, v in grads.items()}, "W_o": self.dW_o, "b_o": self.db_o, "norm_1": self.dnorm_1,
+                 "norm_2": self.dnorm_2, "table": self.dtable}
+        m.moe_clip_grad_norm(list(grads.values()), self.max_norm, None, self.grad_norm, self.clip_ws)
+        return grads
+
+    def status(self):
+        return max(super().status(), *(abs(self.moe.moe_read_status(w)) for w in (self.emb_ws, self.norm_ws, self.clip_ws)))
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--steps", type=int, default=20)
     ap.add_argument("--tokens", type=int, default=512)
+    ap.add_argument("--embedded", action="store_true")
     a = ap.parse_args(argv)
     from workloads import CONFIGS
     spec = CONFIGS["olmo"].replace(T=a.tokens, d_model=256, d_expert=128, d_shared=128, N=16, K=2, alpha=2.0)
-    block = Block(spec, seq_len=128)
+    block = (EmbeddedBlock if a.embedded else Block)(spec, seq_len=128)
     losses = []
     for i in range(a.steps):
         loss, bal = block.step()

@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(SortArgs a) {
     place_items(r, digit, on, to);
 #pragma unroll
     for (int j = 0; j < kItems; ++j)
-      if (on[j]) {
+      if (on[j] && to[j] < a.T) {      // token numbers that change under the call stay within the list
         a.out[to[j]] = item[j];
         if (a.next_bits)
           atomicAdd(a.next_hist + to[j] / a.tile * kDigits + (item[j].x >> a.next_shift & ((1 << a.next_bits) - 1)), 1);
@@ -311,7 +311,8 @@ __device__ __forceinline__ void sum_chunk(const SumArgs& s, int chunk, int c0) {
   const EmbedArgs& a = s.e;
   const int lane = threadIdx.x & 31;
   const int i0 = chunk * kChunk, n = min(kChunk, s.T - i0);
-  const int2 mine = lane < n ? s.list[i0 + lane] : make_int2(static_cast<int>(a.V), 0);
+  int2 mine = lane < n ? s.list[i0 + lane] : make_int2(static_cast<int>(a.V), 0);
+  if (mine.x < 0 || static_cast<unsigned>(mine.y) >= static_cast<unsigned>(s.T)) mine = make_int2(static_cast<int>(a.V), 0);
   const int entering = i0 > 0 ? s.list[i0 - 1].x : -1, leaving = i0 + n < s.T ? s.list[i0 + n].x : -1;
   float* const partial = s.partial + static_cast<int64_t>(chunk) * 2 * a.d;
   float2 acc[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};

@@ -268,11 +268,15 @@ Plan make_plan(const NormArgs& a, size_t bytes, int params, int64_t most, int re
   for (;;) {
     for (p.stages = ahead; p.stages > 2 && need() > kSharedPerSm;) --p.stages;
     if (need() <= kSharedPerSm) break;
-    if (per_sm > 1) --per_sm;
-    else if (teams > 1 && !p.split) --teams;
-    else if (p.stages > 1) p.stages = 1;
-    else return p;
-    if (p.stages == 1 && need() <= kSharedPerSm) break;
+    if (per_sm > 1) {
+      --per_sm;
+    } else if (teams > 1 && !p.split) {
+      --teams;
+    } else {      // one row at a time, or none
+      p.stages = 1;
+      if (need() > kSharedPerSm) return p;
+      break;
+    }
   }
   p.threads = teams * p.lanes;
   p.smem = fixed + static_cast<size_t>(teams) * p.stages * stage;

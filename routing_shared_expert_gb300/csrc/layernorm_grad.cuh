@@ -85,7 +85,8 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(NormArgs a) {
 
 // The backward pass in one reading of the rows; the columns' sums stay in registers over the CTA's rows
 // (B: those of db too) and go out once.  With c = h - mean and p = dy c:
-//   dw = sum p rstd,  dx = rstd (g - c1) - c (rstd^2 c2),  c1 = sum (dy w) / d,  c2 = rstd sum (p w) / d.
+//   dw = sum p rstd,  dx = rstd (g - c1 - c (rstd c2)),  c1 = sum (dy w) / d,  c2 = rstd sum (p w) / d
+// (rstd^2 alone is never formed: it may leave fp32's range where the products do not).
 // RMS: no mean and no c1, one sum per row instead of two (db of RMS rows runs the other form).  Between its two
 // uses a row stays in registers where a thread has 16 elements of it, else in the ring.
 template <typename H, typename S, typename DY, int E, bool SPLIT, bool ENDS, bool RMS, bool B>
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(RMS && E <= 16 ? 640 : 512) norm_grad_kernel(N
       if (!RMS) v[RMS ? 0 : 1] = sg.x + sg.y;
       row_sum<SPLIT, RMS ? 1 : 2, 16>(v, part, turn, at.lanes, at.lane, at.team);
       if (live) {
-        const float2 c1 = both(RMS || a.rms ? 0.f : -(v[RMS ? 0 : 1] * inv_d) * r), c2 = both(-(v[0] * r * inv_d) * r * r);
+        const float2 c1 = both(RMS || a.rms ? 0.f : -(v[RMS ? 0 : 1] * inv_d) * r), c2 = both(-(v[0] * r * inv_d) * r), rr = both(r);
 #pragma unroll
         for (int k = 0; k < P; ++k) {
           float2 (&c)[N] = kc[KEEP ? k : 0];
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(RMS && E <= 16 ? 640 : 512) norm_grad_kernel(N
             }
           }
 #pragma unroll
-          for (int j = 0; j < N; ++j) g[j] = fma2(c[j], c2, RMS ? mul2(g[j], both(r)) : fma2(g[j], both(r), c1));
+          for (int j = 0; j < N; ++j) g[j] = fma2(mul2(c[j], c2), rr, RMS ? mul2(g[j], rr) : fma2(g[j], rr, c1));
           if (add) {
             fs.read(from + at_s, k, at, u);
 #pragma unroll

@@ -149,6 +149,32 @@ def test_in_place(moe, alias, T, d):
     check(moe, T, d, "rms", "bf16", "bf16", "bf16", alias=alias, save_sum=alias != "y=x")
 
 
+@pytest.mark.parametrize("d", [16384, 16383, 13000, 12001])
+def test_long_fp32_rows(moe, d):
+    """Rows whose operands fill, or do not fit, a processor's shared memory."""
+    for T in (3, 400):
+        check(moe, T, d, "layer", "f32", "f32", "f32")
+        check(moe, T, d, "rms", "f32", "f32", "bf16")
+
+
+def test_tiny_values_without_eps(moe):
+    """rstd of 1e18 and above: its square leaves fp32's range, the gradient's products with it do not."""
+    g = gen(11)
+    for kind in ("layer", "rms"):
+        h, dy = rand(g, 7, 300) * 1e-20, rand(g, 7, 300) * 1e-8
+        y, dx, rstd = torch.empty_like(h), torch.empty_like(h), torch.empty(7, device="cuda")
+        mean = torch.empty(7, device="cuda") if kind == "layer" else None
+        hd = h.double()
+        mu = hd.mean(1, keepdim=True) if kind == "layer" else 0
+        rstd.copy_(((hd - mu) ** 2).mean(1) ** -0.5)       # the forward pass would square 1e-20 in fp32
+        if mean is not None:
+            mean.copy_(hd.mean(1))
+        moe.moe_layernorm_backward(h, None, mean, rstd, dy, None, dx, None, None, moe.alloc_layernorm_workspace(7, 300), kind=kind)
+        want, bound = S.layernorm_backward(h, None, mean, rstd, dy, None, kind, torch.float32)["dx"]
+        assert torch.isfinite(dx).all()
+        near(dx, (want, bound), kind)
+
+
 def test_a_sum_that_is_not_stored(moe):
     check(moe, 31, 777, "layer", "bf16", "bf16", "f32", save_sum=False)
     check(moe, 31, 768, "rms", "f32", "bf16", "bf16", save_sum=False)

@@ -11,6 +11,7 @@ from __future__ import annotations
 import array
 import ctypes
 import os
+import struct
 from ctypes import POINTER, c_char_p, c_double, c_float, c_int32, c_int64, c_size_t, c_void_p
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -153,13 +154,14 @@ def _load():
                                 c_int32),
         "moe_dropout_add": ([POINTER(moe_dropout_config), P, P, P, P, P], c_int32),
         "moe_dropout_backward": ([POINTER(moe_dropout_config), P, P, P, P], c_int32),
-        "moe_layernorm_forward": ([POINTER(moe_layernorm_config), P, P, P, P, P, P, P, P, P], c_int32),
+        # the configurations of the calls below come packed by struct
+        "moe_layernorm_forward": ([P, P, P, P, P, P, P, P, P, P], c_int32),
         "moe_layernorm_workspace_size": ([c_int64, c_int32, POINTER(c_size_t)], c_int32),
-        "moe_layernorm_backward": ([POINTER(moe_layernorm_config), P, P, P, P, P, P, P, P, P, P, c_size_t, P],
+        "moe_layernorm_backward": ([P, P, P, P, P, P, P, P, P, P, P, c_size_t, P],
                                    c_int32),
         "moe_embedding_workspace_size": ([c_int64, c_int64, c_int32, POINTER(c_size_t)], c_int32),
-        "moe_embedding_forward": ([POINTER(moe_embedding_config), P, P, P, P, c_size_t, P], c_int32),
-        "moe_embedding_backward": ([POINTER(moe_embedding_config), P, P, P, c_int32, P, c_size_t, P], c_int32),
+        "moe_embedding_forward": ([P, P, P, P, P, c_size_t, P], c_int32),
+        "moe_embedding_backward": ([P, P, P, P, c_int32, P, c_size_t, P], c_int32),
         "moe_grad_norm_workspace_size": ([POINTER(c_size_t)], c_int32),
         "moe_grad_norm": ([P, c_int32, c_float, P, P, c_size_t, P], c_int32),
         "moe_clip_grad_norm": ([P, P, c_int32, c_float, P, P, c_size_t, P], c_int32),
@@ -630,6 +632,12 @@ def moe_balance_loss(cfg: moe_config, logits, topk_idx, token_mask, seq_len, coe
 
 # ---- around the block ------------------------------------------------------------------
 
+# moe_layernorm_config and moe_embedding_config as bytes: half the time of filling a ctypes structure
+_LAYERNORM = struct.Struct("@qiifiiiiqqqq")
+_EMBEDDING = struct.Struct("@qqiiiifqq")
+assert _LAYERNORM.size == ctypes.sizeof(moe_layernorm_config) and _EMBEDDING.size == ctypes.sizeof(moe_embedding_config)
+
+
 def _device_of(name, t) -> int:
     """Device number of the first tensor of a call, which has to be the current device's."""
     dev = t.get_device()
@@ -721,9 +729,9 @@ def moe_layernorm_forward(x, residual, weight, bias, eps, sum, y, mean, rstd, ki
         raise ValueError("sum: the type of the residual is expected")
     py, yt, ldy = _rows("y", y, dev, T, d)
     wt = _norm_param(weight, bias)
-    c = moe_layernorm_config(T, d, _enum(LAYERNORM_KINDS, kind), eps, xt, st, yt, wt, ldx, ldr, lds, ldy)
+    c = _LAYERNORM.pack(T, d, _enum(LAYERNORM_KINDS, kind), eps, xt, st, yt, wt, ldx, ldr, lds, ldy)
     _check("moe_layernorm_forward", _lib.moe_layernorm_forward(
-        ctypes.byref(c), px, pr, _flat("weight", weight, dev, d, wt), _flat("bias", bias, dev, d, wt), ps, py,
+        c, px, pr, _flat("weight", weight, dev, d, wt), _flat("bias", bias, dev, d, wt), ps, py,
         _flat("mean", mean, dev, T, 0), _flat("rstd", rstd, dev, T, 0), _raw_stream(stream, dev)))
 
 
@@ -746,10 +754,10 @@ def moe_layernorm_backward(h, weight, mean, rstd, dy, dsum, dx, dweight, dbias, 
     elif s2 != st:
         raise ValueError("dx: the type of dsum is expected")
     wt = _norm_param(weight, None)
-    c = moe_layernorm_config(T, d, _enum(LAYERNORM_KINDS, kind), 0.0, ht, st, yt, wt, ldh, ldr, lds, ldy)
+    c = _LAYERNORM.pack(T, d, _enum(LAYERNORM_KINDS, kind), 0.0, ht, st, yt, wt, ldh, ldr, lds, ldy)
     pw, nw = _workspace(workspace, dev)
     _check("moe_layernorm_backward", _lib.moe_layernorm_backward(
-        ctypes.byref(c), ph, _flat("weight", weight, dev, d, wt), _flat("mean", mean, dev, T, 0),
+        c, ph, _flat("weight", weight, dev, d, wt), _flat("mean", mean, dev, T, 0),
         _flat("rstd", rstd, dev, T, 0), py, pr, px, _flat("dweight", dweight, dev, d, 0),
         _flat("dbias", dbias, dev, d, 0), pw, nw, _raw_stream(stream, dev)))
 
@@ -786,7 +794,7 @@ def _embedding(ids, table, out, out_name, table_name, scale):
             raise ValueError(f"{out_name}: expected {tuple(ids.shape)} rows of {d}, got {tuple(out.shape)}")
         out = out.view(-1, out.shape[-1])
     po, ot, ldo = _rows(out_name, out, dev, T, d)
-    return moe_embedding_config(T, V, d, ids.dtype is torch.int64, tt, ot, scale, ldt, ldo), ids.data_ptr(), pt, po, dev
+    return _EMBEDDING.pack(T, V, d, ids.dtype is torch.int64, tt, ot, scale, ldt, ldo), ids.data_ptr(), pt, po, dev
 
 
 def moe_embedding_forward(ids, table, scale, out, workspace, stream=None):
@@ -795,7 +803,7 @@ def moe_embedding_forward(ids, table, scale, out, workspace, stream=None):
     MOE_ERR_DEVICE_BOUNDS for moe_read_status."""
     c, pi, pt, po, dev = _embedding(ids, table, out, "out", "table", scale)
     pw, nw = _workspace(workspace, dev)
-    _check("moe_embedding_forward", _lib.moe_embedding_forward(ctypes.byref(c), pi, pt, po, pw, nw,
+    _check("moe_embedding_forward", _lib.moe_embedding_forward(c, pi, pt, po, pw, nw,
                                                                _raw_stream(stream, dev)))
 
 
@@ -805,7 +813,7 @@ def moe_embedding_backward(ids, dout, scale, dtable, workspace, accumulate=False
     c, pi, pt, po, dev = _embedding(ids, dtable, dout, "dout", "dtable", scale)
     pw, nw = _workspace(workspace, dev)
     _check("moe_embedding_backward", _lib.moe_embedding_backward(
-        ctypes.byref(c), pi, po, pt, int(bool(accumulate)), pw, nw, _raw_stream(stream, dev)))
+        c, pi, po, pt, int(bool(accumulate)), pw, nw, _raw_stream(stream, dev)))
 
 
 def alloc_grad_norm_workspace(device="cuda", stream=None):

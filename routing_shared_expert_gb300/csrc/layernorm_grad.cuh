@@ -126,10 +126,10 @@ __global__ void __launch_bounds__(RMS && E <= 16 ? 640 : 512) norm_grad_kernel(N
   };
   wait_for_previous();
   for (char* to = ring; to != ring_end; to += stage_bytes) {
-    if (!at.all) {      // groups past the row are never copied
-      fh.clear(to);
-      fy.clear(to + at_y);
-      if (add) fs.clear(to + at_s);
+    if (!at.all) {
+      fh.clear_unused(to, at);
+      fy.clear_unused(to + at_y, at);
+      if (add) fs.clear_unused(to + at_s, at);
     }
     fetch(to);
   }

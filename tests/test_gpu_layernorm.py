@@ -310,6 +310,33 @@ def test_calls_repeat_bit_for_bit_and_in_a_graph_on_another_stream(moe):
     assert not torch.equal(dx, first[2])       # new inputs are read
 
 
+def test_graphs_of_few_rows_share_a_workspace(moe):
+    """Calls of several shapes, captured with one workspace and replayed in turn, leave it ready for one another."""
+    g = gen(9)
+    ws = moe.alloc_layernorm_workspace(300, 512)
+    calls = []
+    for T, d in ((5, 512), (31, 500), (1, 64), (300, 96), (260, 512)):
+        h, dy = rand(g, T, d), rand(g, T, d)
+        rstd, dw, db = torch.rand(T, device="cuda", generator=g) + 0.5, torch.empty(d, device="cuda"), torch.empty(d, device="cuda")
+        mean = torch.zeros(T, device="cuda")
+        args = (h, None, mean, rstd, dy, None, None, dw, db, ws)
+        moe.moe_layernorm_backward(*args)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            moe.moe_layernorm_backward(*args)
+        calls.append((graph, args))
+    for _ in range(2):
+        for graph, (h, _, mean, rstd, dy, _, _, dw, db, _) in calls + calls[::-1]:
+            dw.fill_(7.0)
+            db.fill_(7.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            want = S.layernorm_backward(h, None, mean, rstd, dy, None, "layer", torch.float32)
+            near(dw, want["dweight"], "dw")
+            near(db, want["dbias"], "db")
+    assert moe.moe_read_status(ws) == 0
+
+
 def test_no_rows(moe):
     x, v = torch.empty((0, 8), device="cuda"), torch.empty(0, device="cuda")
     dw, db = torch.ones(8, device="cuda"), torch.ones(8, device="cuda")

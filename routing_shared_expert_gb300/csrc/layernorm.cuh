@@ -169,12 +169,13 @@ struct Feed {
     }
     next += step;
   }
-  // Zeros in the places of groups past the row, which are never copied, or of all of a row that is not there.
+  // Zeros in the places of groups past the row, which are never copied.  (Where rows end on groups the masks stay out of
+  // it: with them the gradients of 32768 x 4096 took 134 us, not 129.)
   template <typename At>
   __device__ __forceinline__ void clear_unused(char* at, const At& s) {
 #pragma unroll
     for (int k = 0; k < P; ++k)
-      if (s.mask[k] == 0) clear_group<G, T_>(at + k * stride);
+      if (ENDS ? s.mask[k] == 0 : !s.whole[k]) clear_group<G, T_>(at + k * stride);
   }
   __device__ __forceinline__ void clear(char* at) {
 #pragma unroll

@@ -571,7 +571,8 @@ GradLayout grad_layout(int64_t T, int64_t V, int32_t d) {
   };
   for (int i = 0; i < 2; ++i) {
     l.list[i] = take(static_cast<size_t>(T) * 8);
-    l.hist[i] = take(static_cast<size_t>(l.tiles) * kDigits * 4);
+    // for as many tiles as any smaller T has, so that its workspace does for all of those
+    l.hist[i] = take(static_cast<size_t>(std::min<int64_t>(kMaxTiles, (T + kTile - 1) / kTile)) * kDigits * 4);
   }
   l.has = take(static_cast<size_t>(V + 15) / 16 * 16);
   l.partial = take(static_cast<size_t>(l.chunks) * 2 * static_cast<size_t>(d) * 4);

@@ -297,3 +297,14 @@ def test_tensors_on_the_host_or_another_device_are_refused(nat, monkeypatch):
     for t in (x, x.as_subclass(Elsewhere)):
         with pytest.raises(ValueError, match="device|CUDA"):
             nat.moe_layernorm_forward(t, None, None, None, 1e-5, None, t, None, None, stream=0)
+
+
+@pytest.mark.parametrize("d", [1, 64, 2560])
+def test_workspaces_hold_calls_of_fewer_tokens(nat, d):
+    """A workspace for T tokens is taken for every smaller number of them."""
+    tokens = [*range(0, 6000, 7), *range(6000, 60000, 517), *range(131000, 131200), *range(262100, 262200), 1 << 26]
+    for V in (1, 1000, 200000):
+        sizes = [nat.moe_embedding_workspace_size(T, V, d) for T in tokens]
+        assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+    sizes = [nat.moe_layernorm_workspace_size(T, d) for T in tokens]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))

@@ -2,9 +2,9 @@
 // order, zeros (or what was there) for rows without a token.
 //
 // The tokens are sorted by their row, stably, so that a row's tokens are neighbours in ascending order.
-// The sorted list is cut into chunks of 32 tokens: a warp adds a chunk's gradients up over a slice of columns,
-// run by run, and writes the rows whose run lies within the chunk.  A run over a chunk's end (a frequent
-// token) leaves partial sums, which a second launch adds in the chunks' order.  The rows without a token get
+// The sorted list is cut into chunks of 32 tokens (8, where they are few): a warp adds a chunk's gradients up over a
+// slice of columns, run by run, and writes the rows whose run lies within the chunk.  A run over a chunk's end (a
+// frequent token) leaves partial sums, which a second launch adds in the chunks' order.  The rows without a token get
 // their zeros from other CTAs of the sort's and the join's launches, which leave HBM idle, and of the sums'.
 // 32768 tokens to a fp32 table of 65536 x 2560: 136 us, 6.2 TB/s (the bytes at the copy rate 124 us): marks, counts and
 // two sort passes about 20 us, half of it covered by zeros, sums 90 us at 83 % of the DRAM peak, join 10 us.  Small or
@@ -282,12 +282,11 @@ __global__ void __launch_bounds__(kSortThreads) sort_small_kernel(SortArgs a) {
 
 // ------------------------------------------------------------------------- sums --
 
-constexpr int kChunk = 32;      // tokens of a warp
 struct SumArgs {
   EmbedArgs e;
   const int2* list;        // (row, token), sorted; row V behind the last: no token
   float* partial;          // [chunks][2][d]: of the run that enters a chunk, of the one that leaves it
-  int32_t T, chunks, slices;
+  int32_t T, chunk, chunks, slices;      // tokens; of a warp, 8 or 32; how many of those; parts of a row
   unsigned sum_ctas;       // of the launch; those behind them write zeros
   Zeros zeros;
 };
@@ -314,7 +313,7 @@ template <typename Y, typename W, bool ALIGNED>
 __device__ __forceinline__ void sum_chunk(const SumArgs& s, int chunk, int c0) {
   const EmbedArgs& a = s.e;
   const int lane = threadIdx.x & 31;
-  const int i0 = chunk * kChunk, n = min(kChunk, s.T - i0);
+  const int i0 = chunk * s.chunk, n = min(s.chunk, s.T - i0);
   int2 mine = lane < n ? s.list[i0 + lane] : make_int2(static_cast<int>(a.V), 0);
   if (mine.x < 0 || static_cast<unsigned>(mine.y) >= static_cast<unsigned>(s.T)) mine = make_int2(static_cast<int>(a.V), 0);
   const int entering = i0 > 0 ? s.list[i0 - 1].x : -1, leaving = i0 + n < s.T ? s.list[i0 + n].x : -1;
@@ -323,7 +322,7 @@ __device__ __forceinline__ void sum_chunk(const SumArgs& s, int chunk, int c0) {
   bool first = true;       // of the chunk's runs
   int row = __shfl_sync(0xffffffffu, mine.x, 0);
   constexpr int kAhead = 8;      // tokens on their way
-  for (int b = 0; b < kChunk && row < a.V; b += kAhead) {
+  for (int b = 0; b < s.chunk && row < a.V; b += kAhead) {
     Slice<Y, ALIGNED> w[kAhead];
     int rows[kAhead];
 #pragma unroll
@@ -375,7 +374,7 @@ __device__ __forceinline__ void add_partials(const SumArgs& s, int from, int b0,
   const int d = s.e.d;
 #pragma unroll
   for (int j = 0; j < 4; ++j) acc[j] = both(0.f);
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 8;
   for (int b = b0; b < b1; b += kAhead) {
     Slice<float, ALIGNED> w[kAhead];
 #pragma unroll
@@ -410,7 +409,7 @@ __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs s) {
   const EmbedArgs& a = s.e;
   const int group = blockIdx.x % groups, slice = blockIdx.x / groups;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = slice * kColumns;
-  const int chunk = group * 8 + warp, first = chunk * kChunk, next = first + kChunk;
+  const int chunk = group * 8 + warp, first = chunk * s.chunk, next = first + s.chunk;
   int row = -1, end = 0;           // the run's row, and the chunk behind the last that it enters
   if (next < s.T) {
     const int before = first > 0 ? s.list[first - 1].x : -1, head = s.list[first].x, tail = s.list[next - 1].x,
@@ -419,14 +418,14 @@ __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs s) {
   }
   if (row >= 0) {
     for (end = chunk + 1;; end += 32) {      // 32 chunks at a time: the last item of each that the run fills
-      const int at = min((end + lane) * kChunk + kChunk, s.T) - 1;
+      const int at = min((end + lane) * s.chunk + s.chunk, s.T) - 1;
       const unsigned fills = __ballot_sync(0xffffffffu, end + lane < s.chunks && s.list[at].x == row);
       if (fills != 0xffffffffu) {
         end += __popc(fills);
         break;
       }
     }
-    if (end < s.chunks && s.list[end * kChunk].x == row) ++end;      // it ends within this one
+    if (end < s.chunks && s.list[end * s.chunk].x == row) ++end;      // it ends within this one
   }
   const bool alone = row >= 0 && end - chunk <= kAlone;
   if (lane == 0) {
@@ -544,15 +543,24 @@ int bits_of(int64_t v) {
 
 // Whether every block of the table's rows looks through the tokens, instead of their being sorted: while they are so
 // few that one CTA can add a frequent one up, and all CTAs together read few token numbers (300 tokens to
-// 1000 x 256: 6.2 us; 2000 tokens to 500 x 1024 45 us, sorted 18).
+// 1000 x 256: 6.2 us; 2000 tokens to 500 x 1024 45 us, sorted 13).
 bool scans(int64_t T, int64_t V, int32_t d) {
   const int64_t ctas = (V + kScanRows - 1) / kScanRows * ((d + 255) / 256);
   return T <= 512 && T * ctas <= (1 << 20);
 }
 
+// Tokens of a warp.  Few tokens leave most of the GPU empty, and a warp that takes them one batch of loads after another
+// is what the launch waits for: 1200 tokens of 450 24 us with 8, 54 with 32; 9600 of 1024 30 and 35.  With the GPU
+// full the partial sums' traffic counts: 65536 of 64 37 and 31; 19200 of 4096 100 and 85.
+constexpr int kChunk = 32, kFewChunk = 8;
+constexpr int64_t kFewSlices = 152 * 2 * 16 * kFewChunk;      // tokens x slices of a row: twice the warps that are resident
+// A row with most of the tokens has a partial sum per chunk, and one CTA adds them up: 32768 tokens of one row 88 us with 8,
+// 42 with 32, while 19200 spread ones gain only 10 %.
+constexpr int64_t kFewTokens = 16384;
+
 struct GradLayout {
   bool scan;
-  int32_t tiles, tile, chunks;
+  int32_t tiles, tile, chunk, chunks;
   size_t list[2], hist[2], has, partial, total;
 };
 GradLayout grad_layout(int64_t T, int64_t V, int32_t d) {
@@ -562,7 +570,9 @@ GradLayout grad_layout(int64_t T, int64_t V, int32_t d) {
   const int64_t per = (T + kMaxTiles - 1) / kMaxTiles;
   l.tile = static_cast<int32_t>((per + kTile - 1) / kTile * kTile);
   l.tiles = static_cast<int32_t>((T + l.tile - 1) / l.tile);
-  l.chunks = static_cast<int32_t>((T + kChunk - 1) / kChunk);
+  const int64_t few = std::min(kFewTokens, kFewSlices / ((d + kColumns - 1) / kColumns));
+  l.chunk = T <= few ? kFewChunk : kChunk;
+  l.chunks = static_cast<int32_t>((T + l.chunk - 1) / l.chunk);
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -575,7 +585,9 @@ GradLayout grad_layout(int64_t T, int64_t V, int32_t d) {
     l.hist[i] = take(static_cast<size_t>(std::min<int64_t>(kMaxTiles, (T + kTile - 1) / kTile)) * kDigits * 4);
   }
   l.has = take(static_cast<size_t>(V + 15) / 16 * 16);
-  l.partial = take(static_cast<size_t>(l.chunks) * 2 * static_cast<size_t>(d) * 4);
+  // what any smaller T wants, too
+  const int64_t most = std::max((T + kChunk - 1) / kChunk, (std::min(T, few) + kFewChunk - 1) / kFewChunk);
+  l.partial = take(static_cast<size_t>(most) * 2 * static_cast<size_t>(d) * 4);
   l.total = o;
   return l;
 }
@@ -682,6 +694,7 @@ cudaError_t launch_grad(const EmbedArgs& a, cudaStream_t s) {
   p.e = a;
   p.partial = reinterpret_cast<float*>(a.scratch + l.partial);
   p.T = static_cast<int32_t>(a.T);
+  p.chunk = l.chunk;
   p.chunks = l.chunks;
   p.slices = (a.d + kColumns - 1) / kColumns;
   p.sum_ctas = static_cast<unsigned>((static_cast<int64_t>(p.chunks) * p.slices + 7) / 8);

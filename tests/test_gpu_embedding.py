@@ -25,6 +25,11 @@ def tokens(g, T, V, spread="zipf", dtype=torch.int64):
         ids = torch.full((T,), V // 2, device="cuda")
     elif spread == "sorted":
         ids = torch.arange(T, device="cuda") * V // max(T, 1)
+    elif spread == "runs":        # lengths about those that the sums are cut at
+        n = torch.tensor([64, 128, 63, 65, 8, 72, 1, 192, 127, 129, 32, 56, 2000, 7, 256, 640])
+        n = n.repeat(T // int(n.sum()) + 1)
+        ids = torch.repeat_interleave(torch.arange(len(n)) % V, n)[:T].cuda()
+        ids = ids[torch.randperm(T, generator=g, device="cuda")]
     elif spread == "none":
         ids = torch.full((T,), -1, device="cuda")
     elif spread == "uniform":
@@ -219,6 +224,33 @@ def test_one_workspace_for_calls_of_different_sizes(moe):
         ids, dout, dt = tokens(g, T, V), rand(g, T, d), torch.empty((V, d), device="cuda")
         moe.moe_embedding_backward(ids, dout, 1.0, dt, ws)
         near(dt, S.embedding_backward(ids, dout, 1.0, V, torch.float32), (T, V, d))
+
+
+@pytest.mark.parametrize("spread", ["zipf", "same", "sorted", "uniform", "runs"])
+@pytest.mark.parametrize("T,V,d", [(640, 300, 64), (4096, 900, 64), (4097, 900, 131), (16384, 500, 256), (16385, 500, 256),
+                                   (19456, 3000, 450), (12970, 300, 768), (12971, 300, 767), (39001, 1000, 48)])
+def test_about_the_length_of_the_chunks(moe, T, V, d, spread):
+    """Both lengths of what a warp adds up, on either side of where they change; nothing is written behind the
+    workspace's end."""
+    g = gen(T + d)
+    n = moe.moe_embedding_workspace_size(T, V, d)
+    ws = torch.full((n + 65536,), 0xA5, dtype=torch.uint8, device="cuda")
+    ws[:256] = moe.alloc_embedding_workspace(T, V, d)[:256]
+    ids, dout = tokens(g, T, V, spread), rand(g, T, d).bfloat16()
+    dt = torch.empty((V, d), device="cuda")
+    moe.moe_embedding_backward(ids, dout, 0.5, dt, ws[:n])
+    near(dt, S.embedding_backward(ids, dout, 0.5, V, torch.float32), "dtable")
+    assert moe.moe_read_status(ws) == 0 and bool((ws[n:] == 0xA5).all())
+
+
+def test_a_workspace_serves_fewer_tokens(moe):
+    g = gen(11)
+    V, d = 700, 520
+    ws = moe.alloc_embedding_workspace(140000, V, d)
+    for T in (140000, 131104, 131072, 12971, 12970, 4096, 2048, 513, 1):
+        ids, dout, dt = tokens(g, T, V), rand(g, T, d).bfloat16(), torch.empty((V, d), device="cuda")
+        moe.moe_embedding_backward(ids, dout, 1.0, dt, ws)
+        near(dt, S.embedding_backward(ids, dout, 1.0, V, torch.float32), T)
 
 
 def test_offsets_past_32_bits(moe):

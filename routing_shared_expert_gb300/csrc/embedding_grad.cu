@@ -151,45 +151,49 @@ __device__ __forceinline__ int exclusive_scan(int v, int32_t* part) {
 }
 
 // Where the items of up to kTile neighbours go: item j of a thread is number warp * 128 + 32 j + lane.  `base` holds
-// where each digit's next item goes and is moved on.
-struct RankSpace {
-  alignas(16) int32_t warp_n[kSortWarps][kDigits];
-  int32_t base[kDigits];
-  int32_t part[kSortWarps];
-};
-__device__ __forceinline__ void place_items(RankSpace& r, const int (&digit)[kItems], const bool (&on)[kItems],
-                                            int (&to)[kItems]) {
+// where each digit's next item goes and is moved on; NULL: these are all items, and the ranking's own counts say it.
+using WarpCounts = int32_t (&)[kSortWarps][kDigits];
+__device__ __forceinline__ void place_items(WarpCounts warp_n, int32_t* base, int32_t* part, const int (&digit)[kItems],
+                                            const bool (&on)[kItems], int (&to)[kItems]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int i = lane; i < kDigits; i += 32) r.warp_n[warp][i] = 0;
+  for (int i = lane; i < kDigits; i += 32) warp_n[warp][i] = 0;
   __syncwarp();
 #pragma unroll
   for (int j = 0; j < kItems; ++j) {
     const unsigned peers = __match_any_sync(0xffffffffu, on[j] ? digit[j] : -1 - lane);
-    const int before = on[j] ? r.warp_n[warp][digit[j]] : 0;
+    const int before = on[j] ? warp_n[warp][digit[j]] : 0;
     to[j] = before + __popc(peers & ((1u << lane) - 1));
     __syncwarp();
-    if (on[j] && (peers & ((1u << lane) - 1)) == 0) r.warp_n[warp][digit[j]] = before + __popc(peers);
+    if (on[j] && (peers & ((1u << lane) - 1)) == 0) warp_n[warp][digit[j]] = before + __popc(peers);
     __syncwarp();
   }
   __syncthreads();
-  int at = r.base[threadIdx.x];
+  int at;
+  if (base) {
+    at = base[threadIdx.x];
+  } else {
+    int all = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) all += warp_n[w][threadIdx.x];
+    at = exclusive_scan(all, part);
+  }
 #pragma unroll
   for (int w = 0; w < kSortWarps; ++w) {
-    const int n = r.warp_n[w][threadIdx.x];
-    r.warp_n[w][threadIdx.x] = at;
+    const int n = warp_n[w][threadIdx.x];
+    warp_n[w][threadIdx.x] = at;
     at += n;
   }
-  r.base[threadIdx.x] = at;
+  if (base) base[threadIdx.x] = at;
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < kItems; ++j)
-    if (on[j]) to[j] += r.warp_n[warp][digit[j]];
+    if (on[j]) to[j] += warp_n[warp][digit[j]];
   __syncthreads();
 }
 
 template <typename I>
 __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(SortArgs a) {
-  __shared__ RankSpace r;
+  __shared__ int32_t warp_n[kSortWarps][kDigits], base[kDigits], part[kSortWarps];
   launch_dependents();
   wait_for_previous();
   if (blockIdx.x >= static_cast<unsigned>(a.tiles)) {
@@ -205,8 +209,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(SortArgs a) {
     if (t < static_cast<int>(blockIdx.x)) before += n;
     all += n;
   }
-  const int lower = exclusive_scan(all, r.part);
-  r.base[threadIdx.x] = lower + before;
+  const int lower = exclusive_scan(all, part);
+  base[threadIdx.x] = lower + before;
   const int t0 = blockIdx.x * a.tile, t1 = min(a.T, t0 + a.tile);
   for (int i0 = t0; i0 < t1; i0 += kTile) {
     int2 item[kItems];
@@ -220,7 +224,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(SortArgs a) {
       digit[j] = item[j].x >> a.shift & ((1 << a.bits) - 1);
     }
     __syncthreads();
-    place_items(r, digit, on, to);
+    place_items(warp_n, base, part, digit, on, to);
 #pragma unroll
     for (int j = 0; j < kItems; ++j)
       if (on[j] && to[j] < a.T) {      // token numbers that change under the call stay within the list
@@ -234,50 +238,41 @@ __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(SortArgs a) {
 // All passes for at most kTile tokens, in the first CTA's shared memory; the others write all zeros.
 template <typename I>
 __global__ void __launch_bounds__(kSortThreads) sort_small_kernel(SortArgs a) {
-  __shared__ RankSpace r;
-  static_assert(sizeof(r.warp_n) >= kTile * sizeof(int2), "the counts' place holds the list between passes");
-  int2* list = reinterpret_cast<int2*>(r.warp_n);
+  __shared__ alignas(16) int32_t warp_n[kSortWarps][kDigits];
+  __shared__ int32_t part[kSortWarps];
+  static_assert(sizeof(warp_n) >= kTile * sizeof(int2), "the counts' place holds the list between passes");
+  int2* list = reinterpret_cast<int2*>(warp_n);
   launch_dependents();
   wait_for_previous();
   if (blockIdx.x > 0) {
     zeros_by_tokens(a.zeros, blockIdx.x - 1, static_cast<const I*>(a.ids), a.T);
     return;
   }
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int i0 = (threadIdx.x >> 5) * 32 * kItems + (threadIdx.x & 31);
   int2 item[kItems];
   int digit[kItems], to[kItems];
   bool on[kItems];
 #pragma unroll
   for (int j = 0; j < kItems; ++j) {
-    const int i = warp * 32 * kItems + 32 * j + lane;
-    on[j] = i < a.T;
-    item[j] = on[j] ? sort_item<I>(a, i, a.status) : make_int2(0, 0);
+    on[j] = i0 + 32 * j < a.T;
+    item[j] = on[j] ? sort_item<I>(a, i0 + 32 * j, a.status) : make_int2(0, 0);
   }
   for (int shift = 0; shift < a.bits; shift += 9) {      // bits: of a whole row number
-    r.base[threadIdx.x] = 0;
-    __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kItems; ++j) {
-      digit[j] = item[j].x >> shift & (kDigits - 1);
-      if (on[j]) atomicAdd(r.base + digit[j], 1);
-    }
-    __syncthreads();
-    const int n = r.base[threadIdx.x], lower = exclusive_scan(n, r.part);
-    r.base[threadIdx.x] = lower;
-    __syncthreads();
-    place_items(r, digit, on, to);
+    for (int j = 0; j < kItems; ++j) digit[j] = item[j].x >> shift & (kDigits - 1);
+    place_items(warp_n, nullptr, part, digit, on, to);
 #pragma unroll
     for (int j = 0; j < kItems; ++j)
       if (on[j]) list[to[j]] = item[j];
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kItems; ++j)
-      if (on[j]) item[j] = list[warp * 32 * kItems + 32 * j + lane];
+      if (on[j]) item[j] = list[i0 + 32 * j];
     __syncthreads();
   }
 #pragma unroll
   for (int j = 0; j < kItems; ++j)
-    if (on[j]) a.out[warp * 32 * kItems + 32 * j + lane] = item[j];
+    if (on[j]) a.out[i0 + 32 * j] = item[j];
 }
 
 // ------------------------------------------------------------------------- sums --
@@ -543,7 +538,7 @@ int bits_of(int64_t v) {
 
 // Whether every block of the table's rows looks through the tokens, instead of their being sorted: while they are so
 // few that one CTA can add a frequent one up, and all CTAs together read few token numbers (300 tokens to
-// 1000 x 256: 6.2 us; 2000 tokens to 500 x 1024 45 us, sorted 13).
+// 1000 x 256: 6.2 us; 2000 tokens to 500 x 1024 45 us, sorted 12).
 bool scans(int64_t T, int64_t V, int32_t d) {
   const int64_t ctas = (V + kScanRows - 1) / kScanRows * ((d + 255) / 256);
   return T <= 512 && T * ctas <= (1 << 20);

@@ -81,8 +81,8 @@ __global__ void __launch_bounds__(E == 32 || R == 2 ? 512 : 1024) norm_vec_kerne
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (ahead < T) {
-        x.copy(to + i * row_bytes, at, ahead, T);
-        if (add) r.copy(to + i * row_bytes + at_r, at, ahead, T);
+        x.copy(to + i * row_bytes, at, ahead, T, a.room);
+        if (add) r.copy(to + i * row_bytes + at_r, at, ahead, T, a.room);
       }
       ahead += at.step;
     }
@@ -243,6 +243,7 @@ cudaError_t launch_forward(NormArgs a, cudaStream_t s) {
   if (two) p = make_plan<X, S, Y>(a, bytes, params, int64_t{1} << 30, 512, 32, 513, 2);
   a.lanes = p.lanes;
   a.stages = p.stages;
+  a.room = room_of(a, false, kGroup<X, S, Y>);
   if (two && p.elements == 16) return launch_vec<X, S, Y, 16, false, kBf16 ? 2 : 1>(a, p, s);
   if (two && p.elements == 32 && p.split) return launch_vec<X, S, Y, 32, true, kBf16 ? 2 : 1>(a, p, s);
   if (p.elements == 8) return launch_vec<X, S, Y, 8, true>(a, p, s);

@@ -12,6 +12,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "launch.h"
+#include "row_ends.h"
 #include "row_reduce.cuh"
 #include "vec8.cuh"
 
@@ -35,6 +36,7 @@ struct NormArgs {
   int32_t rms, w_dtype;
   int32_t lanes;        // threads of a team, which takes a row at a time
   int32_t stages;       // turns whose rows are on their way, 1 to 4
+  int32_t room;         // rows at either end of the operands whose groups over a row's end are not copied whole
 };
 
 __device__ __forceinline__ float load_param(const void* p, int32_t dtype, int32_t c, float none) {
@@ -156,14 +158,14 @@ struct Feed {
   __device__ __forceinline__ Feed(const void* base, int64_t ld, const At& s)
       : next(static_cast<const T_*>(base) + s.row * ld + s.e0), step(s.step * ld),
         stride(blockDim.x * static_cast<uint32_t>(G * sizeof(T_))) {}
-  // The row's groups begin their way.  One over an end of the row is copied whole, the neighbouring row's values
-  // with it, but for the tensor's own ends: the first row's beginning and the last one's end.
+  // The row's groups begin their way.  One over an end of the row is copied whole, what lies beside the row with it,
+  // but for the groups that could leave the tensor (row_ends.h).
   template <typename At>
-  __device__ __forceinline__ void copy(char* to, const At& s, int at, int T) {
+  __device__ __forceinline__ void copy(char* to, const At& s, int at, int T, int room) {
 #pragma unroll
     for (int k = 0; k < P; ++k) {
       const T_* src = next + k * G * s.lanes;
-      const bool inside = ENDS && s.part[k] && (at > 0 || s.mask[k] & 1) && (at < T - 1 || s.mask[k] >> (G - 1));
+      const bool inside = ENDS && s.part[k] && copied_whole(at, T, room, s.mask[k], G);
       if (s.whole[k] || inside) copy_whole<G>(to + k * stride, src);
       else if (ENDS && s.part[k]) copy_masked<G>(to + k * stride, src, s.mask[k]);
     }
@@ -224,6 +226,14 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* part, int& turn, i
 // ------------------------------------------------------------------ launch plan --
 
 constexpr size_t kSharedPerSm = 227 * 1024;
+
+// Rows of room for the operands that are read in groups of G.
+inline int32_t room_of(const NormArgs& a, bool y_read, int G) {
+  int room = rows_of_room(a.ldx, G);
+  if (a.r) room = std::max(room, rows_of_room(a.ldr, G));
+  if (y_read) room = std::max(room, rows_of_room(a.ldy, G));
+  return room;
+}
 
 // How rows are taken in groups, if they can be.
 struct Plan {

@@ -117,9 +117,9 @@ __global__ void __launch_bounds__(RMS && E <= 16 ? 640 : 512) norm_grad_kernel(N
   int ahead = at.row;
   auto fetch = [&](char* to) {
     if (ahead < T) {
-      fh.copy(to, at, ahead, T);
-      fy.copy(to + at_y, at, ahead, T);
-      if (add) fs.copy(to + at_s, at, ahead, T);
+      fh.copy(to, at, ahead, T, a.room);
+      fy.copy(to + at_y, at, ahead, T, a.room);
+      if (add) fs.copy(to + at_s, at, ahead, T, a.room);
     }
     ahead += at.step;
     cp_async_commit();
@@ -298,6 +298,7 @@ cudaError_t launch_backward(NormArgs a, cudaStream_t s) {
     p = make_plan<X, S, Y>(a, bytes, 1, a.slots, 512, 16, 256);
   a.lanes = p.lanes;
   a.stages = p.stages;
+  a.room = room_of(a, true, kGroup<X, S, Y>);
   if (p.elements) {
     cudaError_t e;
     if (p.elements == 8) e = launch_grad<X, S, Y, 8, true>(a, p, s);

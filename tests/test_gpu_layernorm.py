@@ -137,6 +137,40 @@ def test_strides_and_offsets(moe, lds, off, d):
     check(moe, 19, d, "rms", "f32", "bf16", "f32", lds=lds, off=off)
 
 
+@pytest.mark.parametrize("d", [1, 2, 3, 4, 5, 6])
+@pytest.mark.parametrize("T", [2, 3, 5, 9, 40])
+def test_rows_narrower_than_a_group(moe, T, d):
+    for off in (0, 1, 5):
+        for ld in (d, d + 1, 8):
+            check(moe, T, d, "layer", "bf16", "bf16", "bf16", lds=(ld, ld, ld, ld), off=off)
+            check(moe, T, d, "rms", "f32", "f32", "f32", lds=(ld, ld, ld, ld), off=off)
+            check(moe, T, d, "rms", "f32", "bf16", "f32", lds=(ld, ld, ld, ld), off=off)
+
+
+@pytest.mark.parametrize("T,d", [(2, 1), (3, 2), (4, 3), (7, 5), (9, 6), (3, 257), (2, 4095)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_what_lies_around_the_rows_does_not_count(moe, T, d, dtype):
+    """The same results whether zeros or NaN lie before, behind and between the rows."""
+    g = gen(T + d)
+    x, dy, w = rand(g, T, d).to(dtype), rand(g, T, d).to(dtype), rand(g, d)
+    for off in range(4):
+        for ld in (d, d + 3):
+            seen = []
+            for fill in (0.0, math.nan):
+                X, DY = (torch.full((off + T * ld + 24,), fill, dtype=dtype, device="cuda") for _ in range(2))
+                X, DY = (b[off:off + T * ld].view(T, ld)[:, :d] for b in (X, DY))
+                X.copy_(x)
+                DY.copy_(dy)
+                y, dx = Rows(T, d, dtype, ld, off).v, Rows(T, d, dtype, ld, off).v
+                mean, rstd = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+                dw, db = torch.empty(d, device="cuda"), torch.empty(d, device="cuda")
+                moe.moe_layernorm_forward(X, None, w, None, 1e-5, None, y, mean, rstd)
+                moe.moe_layernorm_backward(X, w, mean, rstd, DY, None, dx, dw, db, moe.alloc_layernorm_workspace(T, d))
+                seen.append([t.clone() for t in (y, mean, rstd, dx, dw, db)])
+            for a, b in zip(*seen):
+                assert torch.equal(a, b) and torch.isfinite(a).all()
+
+
 def test_strided_long_rows(moe):
     check(moe, 23, 5000, "layer", "bf16", "f32", "bf16", lds=(5001, 5001, 5001, 5001), off=5)
     check(moe, 23, 5000, "layer", "bf16", "f32", "bf16", lds=(5008, 5016, 5024, 5032))

@@ -567,12 +567,17 @@ cudaError_t set_smem_once(const void* func, size_t bytes) {
   int dev = 0;
   cudaGetDevice(&dev);
   std::lock_guard<std::mutex> lock(mu);
-  SmemTable::Entry* e = table.find(func, dev);
-  if (e && e->bytes >= bytes) return cudaSuccess;
-  const cudaError_t err = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(bytes));
-  if (err == cudaSuccess && e) e->bytes = bytes;
-  return err;
+  return raise_limit<cudaError_t>(
+      table.find(func, dev), bytes,
+      [&](size_t* held) {
+        cudaFuncAttributes a;
+        const cudaError_t err = cudaFuncGetAttributes(&a, func);
+        if (err == cudaSuccess) *held = static_cast<size_t>(a.maxDynamicSharedSizeBytes);
+        return err;
+      },
+      [&](size_t wanted) {
+        return cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(wanted));
+      });
 }
 
 int device_sm_count() {

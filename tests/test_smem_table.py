@@ -43,3 +43,51 @@ def test_the_limit_setter_uses_it():
     with open(os.path.join(CSRC, "gemm_tc.cu")) as fh:
         body = re.search(r"cudaError_t set_smem_once\(.*?\n}\n", fh.read(), re.S).group(0)
     assert "SmemTable" in body and "[64]" not in body
+
+
+LIMITS = r"""
+#include "smem_table.h"
+#include <initializer_list>
+enum Error { kOk, kFailed };
+int main() {
+  // kernels of the library on eight devices: all have entries
+  static moe::SmemTable t;
+  for (int d = 0; d < 8; ++d)
+    for (int f = 0; f < KERNELS; ++f)
+      if (!t.find(reinterpret_cast<char*>(1 << 20) + 16 * f, d)) return 1;
+  // one kernel and its limit as the driver keeps it; with an entry and, the table full, without
+  moe::SmemTable::Entry own{nullptr, 0, 0};
+  for (auto* e : {&own, static_cast<moe::SmemTable::Entry*>(nullptr)}) {
+    size_t limit = 0;
+    int sets = 0;
+    auto get = [&](size_t* held) { return *held = limit, kOk; };
+    auto set = [&](size_t bytes) { return limit = bytes, ++sets, kOk; };
+    const size_t asked[] = {50000, 200000, 60000, 200000, 48000, 220000, 50000};
+    size_t most = 0;
+    for (size_t bytes : asked) {
+      if (moe::raise_limit<Error>(e, bytes, get, set) != kOk || limit < bytes || limit < most) return 2;
+      most = limit;
+    }
+    if (sets != 3) return 3;
+    // a refused limit stays an error at the next call too
+    auto refuse = [&](size_t) { return kFailed; };
+    for (int i = 0; i < 2; ++i)
+      if (moe::raise_limit<Error>(e, 230000, get, refuse) != kFailed || limit != 220000) return 4;
+  }
+  auto broken = [&](size_t*) { return kFailed; };
+  auto set = [&](size_t) { return kOk; };
+  return moe::raise_limit<Error>(nullptr, 1, broken, set) == kFailed ? 0 : 5;
+}
+"""
+
+
+def test_limits_never_fall(tmp_path):
+    """With 400 kernels on eight devices every one has an entry, and past a full table a smaller plan does not take
+    back what a larger one set."""
+    src, exe = tmp_path / "t.cpp", tmp_path / "t"
+    src.write_text(LIMITS.replace("KERNELS", "400"))
+    subprocess.run(["g++", "-O1", "-std=c++17", "-Wall", "-Werror", "-I", CSRC, str(src), "-o", str(exe)], check=True)
+    assert subprocess.run([str(exe)]).returncode == 0
+    with open(os.path.join(CSRC, "gemm_tc.cu")) as fh:
+        body = re.search(r"cudaError_t set_smem_once\(.*?\n}\n", fh.read(), re.S).group(0)
+    assert body.index("lock_guard") < body.index("raise_limit")

@@ -59,6 +59,7 @@ __global__ void __launch_bounds__(E == 32 || R == 2 ? 512 : 1024) norm_vec_kerne
   constexpr int G = kGroup<X, S, Y>, P = E / G, N = G / 2;
   extern __shared__ float4 smem[];
   __shared__ float part[SPLIT ? 1 : kMaxTeams * 2 * 32 * R];
+  static_assert(sizeof(part) <= kStaticSmem, "the launch counts on no more");
   launch_dependents();
   const Seat<G, P, SPLIT, R> at(a, phase_of<G>(static_cast<const X*>(a.x) + blockIdx.x * a.ldx));
   const int d = a.d;

@@ -63,6 +63,7 @@ cudaError_t launch_layernorm_grad(const NormArgs& a, int32_t stream_dtype, cudaS
 // ring needs no barrier.
 
 constexpr int kMaxTeams = 8;     // of whole warps: barriers 1 to 8
+constexpr size_t kStaticSmem = 4 * 1024;      // the kernels' own arrays, at most
 
 template <typename X, typename S, typename Y>
 constexpr int kGroup = sizeof(X) + sizeof(S) + sizeof(Y) == 6 ? 8 : 4;
@@ -225,7 +226,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* part, int& turn, i
 
 // ------------------------------------------------------------------ launch plan --
 
-constexpr size_t kSharedPerSm = 227 * 1024;
+constexpr size_t kSharedPerSm = 227 * 1024, kDefaultSmem = 48 * 1024;
 
 // Rows of room for the operands that are read in groups of G.
 inline int32_t room_of(const NormArgs& a, bool y_read, int G) {
@@ -285,7 +286,7 @@ Plan make_plan(const NormArgs& a, size_t bytes, int params, int64_t most, int re
   // as many CTAs to an SM as their registers let in, fewer teams or CTAs where the rings would be too short
   int per_sm = std::max(1, resident / (teams * p.lanes));
   const size_t fixed = static_cast<size_t>(p.lanes) * E * 4 * params, stage = static_cast<size_t>(p.lanes) * E * bytes * rows;
-  auto need = [&] { return per_sm * (fixed + static_cast<size_t>(teams) * p.stages * stage + 6 * 1024); };
+  auto need = [&] { return per_sm * (fixed + static_cast<size_t>(teams) * p.stages * stage + kStaticSmem + 2 * 1024); };
   // stages: up to four, no more than a team has turns
   const int64_t turns = (a.T + per_sm * sms * teams * rows - 1) / (per_sm * sms * teams * rows);
   const int ahead = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(4, turns)));
@@ -311,11 +312,11 @@ Plan make_plan(const NormArgs& a, size_t bytes, int params, int64_t most, int re
   return p;
 }
 
-// The limit of a kernel's shared memory, raised where the plan needs more than every kernel has (48 KB, the
-// kernel's own static arrays among them).
+// A kernel's limit of dynamic shared memory, raised where the plan's and the kernel's own arrays may together be more
+// than every kernel has without asking.
 template <typename F>
 cudaError_t allow_smem(F f, size_t bytes) {
-  return bytes > 47 * 1024 ? set_smem_once(reinterpret_cast<const void*>(f), bytes) : cudaSuccess;
+  return bytes + kStaticSmem > kDefaultSmem ? set_smem_once(reinterpret_cast<const void*>(f), bytes) : cudaSuccess;
 }
 
 }  // namespace moe

@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(RMS && E <= 16 ? 640 : 512) norm_grad_kernel(N
   constexpr int G = kGroup<H, S, DY>, P = E / G, N = G / 2;
   extern __shared__ float4 smem[];
   __shared__ float part[SPLIT ? 1 : kMaxTeams * 2 * 32];
+  static_assert(sizeof(part) <= kStaticSmem, "the launch counts on no more");
   launch_dependents();
   const Seat<G, P, SPLIT> at(a, phase_of<G>(static_cast<const H*>(a.x) + blockIdx.x * a.ldx));
   const int d = a.d;

@@ -91,3 +91,20 @@ def test_limits_never_fall(tmp_path):
     with open(os.path.join(CSRC, "gemm_tc.cu")) as fh:
         body = re.search(r"cudaError_t set_smem_once\(.*?\n}\n", fh.read(), re.S).group(0)
     assert body.index("lock_guard") < body.index("raise_limit")
+
+
+def test_the_kernels_own_arrays_count():
+    """The normalisation raises a kernel's limit wherever the plan's bytes and the kernel's own arrays can pass the 48 KB
+    that every kernel has; the arrays' size is held to what the launch counts on."""
+    def text(name):
+        with open(os.path.join(CSRC, name)) as fh:
+            return re.sub(r"//[^\n]*", "", fh.read())
+
+    plan = text("layernorm.cuh")
+    static = eval(re.search(r"kStaticSmem = ([\d* ]+);", plan).group(1))
+    default = eval(re.search(r"kDefaultSmem = ([\d* ]+);", plan).group(1))
+    assert (static, default) == (4096, 49152) and "bytes + kStaticSmem > kDefaultSmem ? set_smem_once" in plan
+    teams = int(re.search(r"kMaxTeams = (\d+)", plan).group(1))
+    for name, most in (("layernorm.cu", teams * 2 * 32 * 2 * 4), ("layernorm_grad.cuh", teams * 2 * 32 * 4)):
+        body = text(name)
+        assert most <= static and "static_assert(sizeof(part) <= kStaticSmem" in body

@@ -8,6 +8,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "launch.h"
+#include "share_memory.h"
 #include "vec8.cuh"
 
 namespace moe {
@@ -261,21 +262,6 @@ __global__ void __launch_bounds__(kThreads, kPerSm) grad_scale_kernel(const __gr
 
 constexpr int64_t kMaxElements = int64_t{1} << 40;
 
-struct Reach {
-  uintptr_t lo, hi;       // bytes spanned
-  uint64_t pitch, width;  // bytes between rows (0: one row) and of a row
-  int32_t tensor;
-  bool written;
-};
-
-bool share_memory(const Reach& a, const Reach& b) {
-  if (a.lo >= b.hi || b.lo >= a.hi) return false;
-  if (a.pitch == 0 || a.pitch != b.pitch) return true;
-  // columns of rows of one matrix: apart when they are apart within a row
-  const uint64_t gap = (b.lo >= a.lo ? b.lo - a.lo : a.pitch - (a.lo - b.lo) % a.pitch) % a.pitch;
-  return !(gap >= a.width && gap + b.width <= a.pitch);
-}
-
 bool elem_ok(const moe_tensor& t) {
   return (t.dtype == MOE_F32 || t.dtype == MOE_BF16) && t.rows >= 0 && t.cols >= 0;
 }
@@ -303,33 +289,16 @@ moe_status check_tensor(const moe_tensor& t, Entry& e, bool out) {
   return MOE_OK;
 }
 
-Reach reach_of(const void* p, const Entry& e, int64_t ld, int32_t i, bool written) {
-  const uint64_t b = size_of(e.dtype);
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return {lo, lo + ((e.rows - 1) * ld + e.cols) * b, e.rows > 1 ? ld * b : 0, e.cols * b, i, written};
-}
-
 // Whether tensors that are written share memory with each other or with one that is read.
 bool overlap(const std::vector<Entry>& list) {
-  std::vector<Reach> x, open;
-  for (size_t i = 0; i < list.size(); ++i) {
-    const Entry& e = list[i];
-    const bool same = e.in == e.out && e.ldi == e.ldo;
-    x.push_back(reach_of(e.out, e, e.ldo, static_cast<int32_t>(i), true));
-    if (!same) x.push_back(reach_of(e.in, e, e.ldi, static_cast<int32_t>(i), false));
+  std::vector<Reach> all;
+  all.reserve(2 * list.size());
+  for (const Entry& e : list) {
+    const uint64_t b = size_of(e.dtype);
+    all.push_back(reach_of(e.out, e.rows, e.cols * b, e.ldo * b, true));
+    if (e.in != e.out || e.ldi != e.ldo) all.push_back(reach_of(e.in, e.rows, e.cols * b, e.ldi * b, false));
   }
-  std::sort(x.begin(), x.end(), [](const Reach& a, const Reach& b) { return a.lo < b.lo; });
-  for (const Reach& e : x) {
-    size_t k = 0;
-    for (const Reach& o : open) {
-      if (o.hi <= e.lo) continue;
-      if ((o.written || e.written) && share_memory(o, e)) return true;
-      open[k++] = o;
-    }
-    open.resize(k);
-    open.push_back(e);
-  }
-  return false;
+  return any_written_is_shared(all);
 }
 
 template <int N>
@@ -409,8 +378,8 @@ moe_status run_norm(const moe_tensor* grads, const moe_tensor* out, int32_t coun
   }
   if (reinterpret_cast<uintptr_t>(norm) & 3u || reinterpret_cast<uintptr_t>(workspace) & 255u)
     return MOE_ERR_MISALIGNED;
-  if (bytes < kWorkspace) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if (clip && overlap(list)) return MOE_ERR_INVALID_ARG;
+  if (bytes < kWorkspace) return MOE_ERR_WORKSPACE_TOO_SMALL;
 
   NormSums sums{};
   sums.partial = reinterpret_cast<double*>(static_cast<char*>(workspace) + kPartialOffset);

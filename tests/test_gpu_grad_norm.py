@@ -75,6 +75,21 @@ def test_columns_of_one_matrix(moe):
     near(both, S.clip([before], 1.0)[0], "both")
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_tensors_in_the_gaps_of_another(moe, dtype):
+    """A matrix, and between its rows a single row and a matrix of another stride."""
+    both = rand(gen(3), 100, 256).to(dtype)
+    before = both.clone()
+    parts = lambda t: [t[:, :100], t[0:1, 100:], t[1::2, 101:200]]
+    norm, ws = torch.empty(2, device="cuda"), moe.alloc_grad_norm_workspace()
+    moe.moe_clip_grad_norm(parts(both), 1.0, None, norm, ws)
+    mine = torch.zeros_like(before, dtype=torch.bool)
+    for p, m, w in zip(parts(both), parts(mine), S.clip(parts(before), 1.0)):
+        near(p, w, "part")
+        m[:] = True
+    assert torch.equal(both[~mine], before[~mine])
+
+
 def test_shapes_of_any_rank_and_empty_tensors(moe):
     g = gen(2)
     ws = moe.alloc_grad_norm_workspace()

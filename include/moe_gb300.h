@@ -741,7 +741,8 @@ moe_status moe_grad_norm(const moe_tensor* grads, int32_t count, float max_norm,
 /* moe_grad_norm, then out_i = norm[1] g_i in fp32, rounded once.  out: HOST [count], shapes and types
  * of grads, or NULL: the gradients themselves are scaled, and stay untouched when norm[1] is 1.
  * No two tensors that the call writes, and none that it writes and another that it reads, may
- * share memory, out_i = grads_i (same address and stride) apart: MOE_ERR_INVALID_ARG.  Errors as above. */
+ * share memory, out_i = grads_i (same address and stride) apart, and norm lies in none of them:
+ * MOE_ERR_INVALID_ARG.  Errors as above. */
 moe_status moe_clip_grad_norm(const moe_tensor* grads, const moe_tensor* out, int32_t count,
                               float max_norm, float* norm, void* workspace, size_t workspace_bytes,
                               cudaStream_t stream);

@@ -289,8 +289,8 @@ moe_status check_tensor(const moe_tensor& t, Entry& e, bool out) {
   return MOE_OK;
 }
 
-// Whether tensors that are written share memory with each other or with one that is read.
-bool overlap(const std::vector<Entry>& list) {
+// What the tensors of a clipping call occupy.
+std::vector<Reach> reaches_of(const std::vector<Entry>& list) {
   std::vector<Reach> all;
   all.reserve(2 * list.size());
   for (const Entry& e : list) {
@@ -298,7 +298,7 @@ bool overlap(const std::vector<Entry>& list) {
     all.push_back(reach_of(e.out, e.rows, e.cols * b, e.ldo * b, true));
     if (e.in != e.out || e.ldi != e.ldo) all.push_back(reach_of(e.in, e.rows, e.cols * b, e.ldi * b, false));
   }
-  return any_written_is_shared(all);
+  return all;
 }
 
 template <int N>
@@ -378,8 +378,13 @@ moe_status run_norm(const moe_tensor* grads, const moe_tensor* out, int32_t coun
   }
   if (reinterpret_cast<uintptr_t>(norm) & 3u || reinterpret_cast<uintptr_t>(workspace) & 255u)
     return MOE_ERR_MISALIGNED;
-  if (clip && overlap(list)) return MOE_ERR_INVALID_ARG;
+  std::vector<Reach> reaches;
+  if (clip) reaches = reaches_of(list);
+  if (any_written_is_shared(reaches)) return MOE_ERR_INVALID_ARG;
   if (bytes < kWorkspace) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  // the norm is written before the gradients are read again
+  for (const Reach& r : reaches)
+    if (share_memory(r, reach_of(norm, 1, 8, 8, true))) return MOE_ERR_INVALID_ARG;
 
   NormSums sums{};
   sums.partial = reinterpret_cast<double*>(static_cast<char*>(workspace) + kPartialOffset);

@@ -72,10 +72,10 @@ def clip():
     ensure_built()
     from routing_shared_expert_gb300 import _native as nat
 
-    def call(grads, out=None):
+    def call(grads, out=None, norm=0x10000, size=256):
         lists = [(nat.moe_tensor * len(x))(*[nat.moe_tensor(*t) for t in x]) if x else None for x in (grads, out)]
-        return nat.library().moe_clip_grad_norm(*lists, len(grads), 1.0, ctypes.c_void_p(0x10000), ctypes.c_void_p(0x20000),
-                                                256, None)
+        return nat.library().moe_clip_grad_norm(*lists, len(grads), 1.0, ctypes.c_void_p(norm),
+                                                ctypes.c_void_p(0x20000), size, None)
     return call
 
 
@@ -109,3 +109,11 @@ def test_lists_that_share_memory_are_refused(clip, pair):
 def test_refused_whatever_the_workspace(clip):
     """The check of the list comes before that of the workspace, so that the cases above reach it."""
     assert clip([(A, 1, 8, 0, 0), (A, 1, 8, 0, 0)]) == -1
+
+
+def test_the_norm_lies_in_no_tensor(clip):
+    """It is written before the gradients are read for the second time."""
+    grads, out = [(A, 4, 8, 16, 0)], [(A + 0x1000, 4, 8, 16, 0)]
+    for norm in (A, A + 28, A - 4, A + 3 * 64 + 24, A + 0x1000, A + 0x1000 + 64):
+        assert clip(grads, out, norm, 1 << 40) == -1
+    assert clip(grads, None, A + 8, 1 << 40) == -1

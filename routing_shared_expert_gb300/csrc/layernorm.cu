@@ -225,7 +225,9 @@ __global__ void __launch_bounds__(E == 32 || R == 2 ? 512 : 1024) norm_vec_kerne
 
 template <typename X, typename S, typename Y, int E, bool SPLIT, int R = 1>
 cudaError_t launch_vec(const NormArgs& a, const Plan& p, cudaStream_t s) {
-  const auto f = p.ends ? norm_vec_kernel<X, S, Y, E, SPLIT, true, R> : norm_vec_kernel<X, S, Y, E, SPLIT, false, R>;
+  auto f = norm_vec_kernel<X, S, Y, E, SPLIT, false, R>;
+  if constexpr (R == 1)      // two rows at a time: those that end on groups alone
+    if (p.ends) f = norm_vec_kernel<X, S, Y, E, SPLIT, true, R>;
   const cudaError_t e = allow_smem(f, p.smem);
   if (e != cudaSuccess) return e;
   return launch_over(f, dim3(p.grid), p.threads, p.smem, s, a);

@@ -28,8 +28,6 @@ __device__ __forceinline__ void store_whole(__nv_bfloat16* p, const float2 (&v)[
 __device__ __forceinline__ void store_whole(float* p, const float2 (&v)[2]) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
 }
-// Never called: fp32 operands come in groups of four.
-__device__ __forceinline__ void store_whole(float* p, const float2 (&v)[4]) {}
 
 // The pairs rounded to T and back.
 template <typename T, int N>
@@ -79,7 +77,6 @@ __device__ __forceinline__ void read_group(const char* src, const float*, float2
   const float4 u = *reinterpret_cast<const float4*>(src);
   v[0] = make_float2(u.x, u.y), v[1] = make_float2(u.z, u.w);
 }
-__device__ __forceinline__ void read_group(const char* src, const float*, float2 (&v)[4]) {}   // never called
 // Stores the elements that the mask has.  In line: a call here is on the way of every row (16384 x 4095 76 us, called
 // 84), while one at a tensor's own ends above is not (in line 98: its instructions would be predicated ones in
 // every thread).

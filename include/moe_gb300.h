@@ -663,6 +663,8 @@ typedef struct moe_layernorm_config {
  * mean, rstd fp32 [T] or NULL (mean with RMS: MOE_ERR_INVALID_ARG).  Statistics and products in
  * fp32, the mean before the deviations, one rounding of y.  A row that holds an infinity or a NaN gives
  * what the formula gives; no other row is touched by it.
+ * Where rows begin and end on groups of eight values (addresses, strides and d), a row's results have the same
+ * bits whatever T is and wherever the row stands; elsewhere, and in the gradients, last bits may differ with T.
  * sum may be x or the residual itself and y may be x or the residual (when sum is not), each where
  * type and stride agree; no other buffers may overlap.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (rows past 2^40 elements), MOE_ERR_MISALIGNED,

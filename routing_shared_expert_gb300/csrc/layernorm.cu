@@ -60,6 +60,7 @@ __global__ void __launch_bounds__(E == 32 || R == 2 ? 512 : 1024) norm_vec_kerne
   extern __shared__ float4 smem[];
   __shared__ float part[SPLIT ? 1 : kMaxTeams * 2 * 32 * R];
   static_assert(sizeof(part) <= kStaticSmem, "the launch counts on no more");
+  static_assert(R == 1 || G == 8, "groups of four are taken a row at a time");
   launch_dependents();
   const Seat<G, P, SPLIT, R> at(a, phase_of<G>(static_cast<const X*>(a.x) + blockIdx.x * a.ldx));
   const int d = a.d;
@@ -186,20 +187,29 @@ __global__ void __launch_bounds__(E == 32 || R == 2 ? 512 : 1024) norm_vec_kerne
     }
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-      float2 u[N], t[N];
-      if (R == 2) {      // both parameters on their way at once (32768 x 4096: 88 us, one after the other 109)
-        if (a.w) param_group(w, at.groups, k * at.lanes + at.lane, u);
-        if (a.b) param_group(b, at.groups, k * at.lanes + at.lane, t);
+      if constexpr (G == 8) {
+        // Weight and bias in one rounding whether two rows are taken at a time or one, so that a row's bits do not depend
+        // on how many rows there are.  R = 2: both parameters on their way at once (32768 x 4096: 88 us, one after the
+        // other 109); R = 1: 64 registers leave room for half a group of each.
+        constexpr int M = R == 2 ? N : 2;
 #pragma unroll
-        for (int i = 0; i < R; ++i)
+        for (int part = 0; part < N; part += M) {
+          float2 u[M], t[M];
+          if (a.w) param_values(w, at.groups, k * at.lanes + at.lane, part, u);
+          if (a.b) param_values(b, at.groups, k * at.lanes + at.lane, part, t);
 #pragma unroll
-          for (int j = 0; j < N; ++j) {
-            h[i][k][j] = mul2(h[i][k][j], both(rstd[i]));
-            if (a.w && a.b) h[i][k][j] = fma2(h[i][k][j], u[j], t[j]);
-            else if (a.w) h[i][k][j] = mul2(h[i][k][j], u[j]);
-            else if (a.b) h[i][k][j] = add2(h[i][k][j], t[j]);
-          }
-      } else {           // 64 registers leave room for one of them
+          for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int j = 0; j < M; ++j) {
+              float2& v = h[i][k][part + j];
+              v = mul2(v, both(rstd[i]));
+              if (a.w && a.b) v = fma2(v, u[j], t[j]);
+              else if (a.w) v = mul2(v, u[j]);
+              else if (a.b) v = add2(v, t[j]);
+            }
+        }
+      } else {           // groups of four are taken a row at a time; both parameters at once 8192 x 7168 94 -> 101 us
+        float2 u[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) h[0][k][j] = mul2(h[0][k][j], both(rstd[0]));
         if (a.w) {

@@ -68,15 +68,19 @@ constexpr size_t kStaticSmem = 4 * 1024;      // the kernels' own arrays, at mos
 template <typename X, typename S, typename Y>
 constexpr int kGroup = sizeof(X) + sizeof(S) + sizeof(Y) == 6 ? 8 : 4;
 
-// Group q of a parameter in shared memory.  G = 8: the lower and the upper half of all groups lie apart, so
-// that neighbouring lanes' 16-byte reads are neighbours.
-__device__ __forceinline__ void param_group(const float* p, int groups, int q, float2 (&v)[2]) {
-  read_group(reinterpret_cast<const char*>(p + 4 * q), static_cast<const float*>(nullptr), v);
+// Pairs `from` .. from + M - 1 of group q of a parameter in shared memory.  G = 8: the lower and the upper half of all
+// groups lie apart, so that neighbouring lanes' 16-byte reads are neighbours.
+template <int M>
+__device__ __forceinline__ void param_values(const float* p, int groups, int q, int from, float2 (&v)[M]) {
+#pragma unroll
+  for (int i = 0; i < M; i += 2) {
+    const float4 u = reinterpret_cast<const float4*>(p)[(from + i) / 2 * groups + q];
+    v[i] = make_float2(u.x, u.y), v[i + 1] = make_float2(u.z, u.w);
+  }
 }
-__device__ __forceinline__ void param_group(const float* p, int groups, int q, float2 (&v)[4]) {
-  const float4 lo = reinterpret_cast<const float4*>(p)[q], hi = reinterpret_cast<const float4*>(p)[groups + q];
-  v[0] = make_float2(lo.x, lo.y), v[1] = make_float2(lo.z, lo.w);
-  v[2] = make_float2(hi.x, hi.y), v[3] = make_float2(hi.z, hi.w);
+template <int N>
+__device__ __forceinline__ void param_group(const float* p, int groups, int q, float2 (&v)[N]) {
+  param_values(p, groups, q, 0, v);
 }
 template <int G>
 __device__ __forceinline__ void stage_param(float* dst, const void* src, int32_t dtype, int groups, int phase, int d) {

@@ -371,6 +371,34 @@ def test_graphs_of_few_rows_share_a_workspace(moe):
     assert moe.moe_read_status(ws) == 0
 
 
+@pytest.mark.parametrize("x,stream,y", [("bf16", None, "bf16"), ("bf16", "bf16", "bf16"), ("f32", "bf16", "bf16"), ("f32", "f32", "f32")])
+@pytest.mark.parametrize("d", [8, 256, 520, 1024, 4096, 7168])
+def test_a_row_has_the_same_bits_in_every_call(moe, x, stream, y, d):
+    """Rows on groups of eight: a token's results do not depend on how many rows are normalised with it, nor on its place
+    among them."""
+    g = gen(d)
+    T = 6000
+    X, R = rand(g, T, d, shift=0.3).to(DT[x]), rand(g, T, d).to(DT[stream]) if stream else None
+    w, b = rand(g, d, scale=0.2, shift=1.0), rand(g, d, scale=0.2)
+
+    def call(rows, kind, bias):
+        x, r = X[rows], R[rows] if stream else None
+        out = dict(y=torch.empty_like(x, dtype=DT[y]), rstd=torch.empty(len(x), device="cuda"))
+        mean = out["mean"] = torch.zeros(len(x), device="cuda")
+        out["sum"] = torch.empty_like(r) if stream else mean
+        moe.moe_layernorm_forward(x, r, w, bias, 1e-5, out["sum"] if stream else None, out["y"],
+                                  mean if kind == "layer" else None, out["rstd"], kind=kind)
+        return out
+
+    order = torch.randperm(T, generator=g, device="cuda")
+    for kind in ("layer", "rms"):
+        for bias in (b, None):
+            whole = call(torch.arange(T, device="cuda"), kind, bias)
+            for part in (order, order[:1], order[:3], order[5:170], order[:1300]):
+                for name, got in call(part, kind, bias).items():
+                    assert torch.equal(got, whole[name][part]), (kind, bias is None, len(part), name)
+
+
 def test_no_rows(moe):
     x, v = torch.empty((0, 8), device="cuda"), torch.empty(0, device="cuda")
     dw, db = torch.ones(8, device="cuda"), torch.ones(8, device="cuda")

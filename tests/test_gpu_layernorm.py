@@ -292,6 +292,51 @@ def test_gradient_against_differences(moe, T, d, kind):
     assert bound < 0.05 * abs(float((dy.double() * step).norm())) + 1.0     # the bound says something
 
 
+@pytest.mark.parametrize("T,d", [(33, 200), (5, 2049), (300, 64), (3, 17000)])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+def test_gradients_against_differences_along_themselves(moe, T, d, kind):
+    """The forward kernel's difference quotients along the gradients: the slope is as large as it can be there, and what
+    is allowed between the two kernels, the roundings of y over the step and of the gradient, is under a fiftieth of it (at
+    most 0.011, from the oracles alone).
+
+    With rows of spread near 1 and steps of s = 2^-7 in units of it, a central difference is off by s^2 / 6 of the third
+    derivative, which is of the size of 15 |dy| per unit step: under 3e-4 of the slope, where |dx| is half of |dy| or more."""
+    g = gen(15)
+    h, dy = rand(g, T, d), rand(g, T, d)
+    w, b = rand(g, d, scale=0.2, shift=1.0), rand(g, d, scale=0.2)
+    mean = torch.empty(T, device="cuda") if kind == "layer" else None
+    y, rstd, dx = torch.empty_like(h), torch.empty(T, device="cuda"), torch.empty_like(h)
+    dw, db = torch.empty(d, device="cuda"), torch.empty(d, device="cuda")
+    moe.moe_layernorm_forward(h, None, w, b, 1e-5, None, y, mean, rstd, kind=kind)
+    moe.moe_layernorm_backward(h, w, mean, rstd, dy, None, dx, dw, db, moe.alloc_layernorm_workspace(T, d), kind=kind)
+    exact = S.layernorm(h, None, w, b, 1e-5, kind, None, torch.float32)
+    true_mean = exact["mean"][0] if kind == "layer" else None
+    want = S.layernorm_backward(h, w, true_mean, exact["rstd"][0], dy, None, kind, torch.float32)
+    # the kernel's statistics are off by their own bounds, and its gradients by what that makes
+    e_rel = 8 * float((exact["rstd"][1] / exact["rstd"][0]).max())
+    grown = {"dx": e_rel * (want["dx"][0].abs() + (rstd[:, None] * dy * w).abs().double()), "dbias": 0.0,
+             "dweight": e_rel * (dy.double().abs() * (1 + y.double().abs() + h.double().abs())).sum(0)}
+    for name, got in (("dx", dx), ("dweight", dw), ("dbias", db)):
+        G, e = want[name]
+        u = (G / G.square().mean().sqrt() * 2.0 ** -7).float()
+        sides = []
+        for sign in (1, -1):
+            x, w2, b2 = (t + sign * u if name == n else t for n, t in (("dx", h), ("dweight", w), ("dbias", b)))
+            moved = {"dx": x, "dweight": w2, "dbias": b2}[name]
+            out = torch.empty_like(y)
+            moe.moe_layernorm_forward(x, None, w2, b2, 1e-5, None, out, None, None, kind=kind)
+            sides.append((moved.double(), out.double(), *S.layernorm(x, None, w2, b2, 1e-5, kind, None, torch.float32)["y"]))
+        step = (sides[0][0] - sides[1][0]) / 2          # as the inputs hold it
+        slope = float(((sides[0][1] - sides[1][1]) / 2 * dy.double()).sum())
+        exact_slope = float(((sides[0][2] - sides[1][2]) / 2 * dy.double()).sum())
+        along = float((got.double() * step).sum())
+        # the oracles' own derivative and quotient
+        assert abs(float((G * step).sum()) - exact_slope) <= 1e-3 * exact_slope, name
+        bound = float(((sides[0][3] + sides[1][3]) / 2 * dy.double().abs()).sum()) + float(((e + grown[name]) * step.abs()).sum())
+        assert bound <= 0.02 * exact_slope, (name, bound, exact_slope)
+        assert abs(slope - along) <= bound + 1e-3 * exact_slope, (name, slope, along, bound)
+
+
 def test_parts_that_are_not_asked_for(moe):
     """Every subset of the results gives the values of the full call."""
     g = gen(6)

@@ -113,11 +113,6 @@ __global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a, int slices, int
 
 // ---------------------------------------------------------------------- launch --
 
-template <typename T>
-bool groups_of_eight(const void* p, int64_t ld, int32_t d) {
-  return reinterpret_cast<uintptr_t>(p) % (8 * sizeof(T)) == 0 && ld % 8 == 0 && d % 8 == 0;
-}
-
 template <typename I, typename W, typename Y>
 cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t s) {
   const bool aligned = groups_of_eight<W>(a.src, a.ldt, a.d) && groups_of_eight<Y>(a.dst, a.ldo, a.d);

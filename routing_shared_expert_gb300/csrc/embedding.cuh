@@ -115,6 +115,12 @@ __device__ __forceinline__ void store_slice(T* row, int c0, int d, float2 (&v)[4
   }
 }
 
+// Whether rows begin and end on groups of eight values (host).
+template <typename T>
+bool groups_of_eight(const void* p, int64_t ld, int32_t d) {
+  return reinterpret_cast<uintptr_t>(p) % (8 * sizeof(T)) == 0 && ld % 8 == 0 && d % 8 == 0;
+}
+
 // The gradient of the table (embedding_grad.cu), and the scratch memory that it takes.
 size_t embedding_scratch(int64_t T, int64_t V, int32_t d);
 cudaError_t launch_embedding_backward(const EmbedArgs& a, const moe_embedding_config& c, cudaStream_t s);

@@ -657,11 +657,6 @@ cudaError_t launch_sums(SumArgs p, const Zeros& beside_join, cudaStream_t s) {
   return launch_over(embed_join_kernel<W, ALIGNED>, dim3(ctas + p.zeros.ctas), 256, 0, s, p);
 }
 
-template <typename T>
-bool groups_of_eight(const void* p, int64_t ld, int32_t d) {
-  return reinterpret_cast<uintptr_t>(p) % (8 * sizeof(T)) == 0 && ld % 8 == 0 && d % 8 == 0;
-}
-
 template <typename I, typename Y, typename W>
 cudaError_t launch_grad(const EmbedArgs& a, cudaStream_t s) {
   const GradLayout l = grad_layout(a.T, a.V, a.d);

@@ -6,7 +6,8 @@
     loss = mean (out - target)^2 / 2 + balance loss and z-loss of the router
 
 Every product, the dropout, the balance loss and all gradients run in the library; torch holds the
-buffers, forms the difference to the target and applies plain gradient descent.
+buffers, forms the difference to the target, adds and converts the stream's gradient where two operators want it in
+different types, and applies plain gradient descent.
 
 With --embedded the block is fed by token numbers, normalised in front of each half, and its gradients are clipped
 to a global norm:

@@ -730,9 +730,9 @@ typedef struct moe_tensor {
 
 /* norm[0] = (sum over the tensors' elements of g^2)^(1/2), norm[1] = 1 where max_norm is infinite,
  * else min(1, max_norm / (norm + 1e-6)) (device fp32 [2]).  grads: HOST [count], count 0..2^20,
- * read before the call returns.  Squares and sums in fp32 in a fixed order, joined in fp64: an element
- * above 1.8e19 makes the norm infinite, squares below 1.2e-38 lose bits.  An infinity or a NaN in any
- * element shows in both numbers as the formula has it.  max_norm >= 0; a NaN is refused.
+ * read before the call returns.  Squares and sums in fp32 within a thread in a fixed order, joined in
+ * fp64: where a thread's squares add up past 3.4e38 (one element above 1.8e19 does) the norm is infinite, squares
+ * below 1.2e-38 lose bits.  An infinity or a NaN in any element shows in both numbers as the formula has it.  max_norm >= 0; a NaN is refused.
  * workspace: moe_grad_norm_workspace_size bytes, prepared by moe_workspace_init.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (a tensor or the list past 2^40 elements),
  * MOE_ERR_MISALIGNED, MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_CUDA. */

@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(256) norm_any_kernel(NormArgs a) {
 // 8192 x 7168 (fp32 + bf16 stream -> bf16): 88 us, 6.7 TB/s, bound by HBM (the bytes at the copy rate 86.5 us); rows
 // of bf16 alone are bound by the instructions of their sums and parameters: 32768 x 4096 with weight and bias 87 us,
 // 6.1 TB/s (one row at a time 101 us at 0.72 issue slots used).  Odd widths pay for the rows' ends and for
-// pieces across sectors: 16384 x 4095 76 us, 16384 x 4096 44.  One token of 2048: 2.6 us, the latency of one read.
+// pieces across sectors, and leave some of a warp's lanes idle: 16384 x 4095 73 us, 16384 x 4096 50.  One token of 2048: 2.6 us, the latency of one read.
 template <typename X, typename S, typename Y, int E, bool SPLIT, bool ENDS, int R>
 __global__ void __launch_bounds__(E == 32 || R == 2 ? 512 : 1024) norm_vec_kernel(NormArgs a) {
   constexpr int G = kGroup<X, S, Y>, P = E / G, N = G / 2;

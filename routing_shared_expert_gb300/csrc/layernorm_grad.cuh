@@ -92,6 +92,9 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(NormArgs a) {
 // 32768 x 4096 (LAYER, bf16): 128 us with the join, 6.3 TB/s, HBM and the issue slots (0.6 used) near their limits;
 // 8192 x 7168 in fp32 with dsum 139 us, 6.8 TB/s, bound by HBM; 8192 x 2560 (RMS, bf16, dsum) 32 us, of which the join
 // and the first and last rows are about 6.  Kept apart, the column sums would read h and dy again.
+// Far from that: odd widths, where one team is left to an SM (16384 x 4095 155 us, 16384 x 4096 73), and fp32 rows with
+// dsum that leave room for one stage (4096 x 8192 118 us, the bytes at the copy rate 79) or none (2048 x 13376, in the
+// general form above, 491 us; 2048 x 13312 96).
 template <typename H, typename S, typename DY, int E, bool SPLIT, bool ENDS, bool RMS, bool B>
 __global__ void __launch_bounds__(RMS && E <= 16 ? 640 : 512) norm_grad_kernel(NormArgs a) {
   constexpr int G = kGroup<H, S, DY>, P = E / G, N = G / 2;

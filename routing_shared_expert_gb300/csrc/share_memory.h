@@ -53,6 +53,7 @@ inline bool share_memory(Reach a, Reach b) {
   }
   const uint64_t P = b.pitch, reach = a.width + b.width - 2, from = a.lo + first * a.pitch + a.width - 1 - b.lo;
   if (reach >= P - 1) return true;
+  if (first == last || a.pitch == P) return from % P <= reach;     // one row, or rows that all lie alike
   return floor_sum(last - first + 1, P, a.pitch, from + P) != floor_sum(last - first + 1, P, a.pitch, from + P - reach - 1);
 }
 
